@@ -72,7 +72,8 @@ typedef enum {
     LATTICE_ERR_TIMEOUT = 4      /* a bounded device-side wait gave up        */
 } lattice_status;
 
-typedef enum { LATTICE_F32 = 0, LATTICE_BF16 = 1 } lattice_dtype;
+/* F16 is accepted by the gated recurrence and the block norms only. */
+typedef enum { LATTICE_F32 = 0, LATTICE_BF16 = 1, LATTICE_F16 = 2 } lattice_dtype;
 
 /* Objective (§3.1.1, eq. OSR): what each token writes into the slots.
  *   LATTICE_SIM  dot-product similarity objective, h_t = -x_t: slot i takes
@@ -265,6 +266,74 @@ lattice_status lattice_step(float *S, const void *x, lattice_dtype x_dtype, cons
  * q [B][H][m], y [B][H][d]. */
 lattice_status lattice_readout(const float *S, const void *q, lattice_dtype q_dtype, float *y,
                                int B, int H, int m, int d, void *stream);
+
+/* ---- Gated linear recurrence
+ *
+ * The linear recurrence that each slot of the chunked form runs (Eq. 17: s <- g s +
+ * kappa x), without the projection and the normaliser, for layers that mix both kinds of
+ * state: per (batch b, head h, channel j), for t = 1..len_b,
+ *     h_t = a_t h_{t-1} + s(a_t) x_t,     y_t = h_t.
+ * Gate:  LATTICE_GATE_VALUE  a = z, with |a| <= 1 (larger gates are not supported: the
+ *                            products of a run may overflow);
+ *        LATTICE_GATE_LOGIT  a = sigmoid(z)^tau, tau > 0. An infinite z is a gate of
+ *                            exactly 0 or 1.
+ * Write: LATTICE_WRITE_PLAIN s = 1; LATTICE_WRITE_LEAKY s = 1 - a; LATTICE_WRITE_UNIT
+ *        s = sqrt(max(0, 1 - a^2)), which keeps the variance of independent unit inputs.
+ *
+ * Layouts: x [B][T][H][d]; z [B][T][H][d], or [B][T][H] with z_per_head != 0 (then d in
+ * {16, 32, 64, 128}); h0, h_out [B][H][d] fp32, row-major; y [B][T][H][d] in x's type. x,
+ * z and dy may be slices of wider rows: their batch and token strides are given in
+ * elements (>= 0), a token's own H*d (or H) elements are contiguous. Every output is
+ * contiguous. x: fp32, bf16 or fp16; z: fp32 or x's type. Arithmetic and state are fp32
+ * whatever the types; y and the gradients are rounded once.
+ * Sizes: B, H, d >= 1, T >= 0; H*d and T up to 2^30.
+ * lengths (int32 [B], device, or NULL for T each) gives every sequence its own length,
+ * taken into 0..T. Tokens behind it are not read: their y and gradients are written as
+ * zero, and h_out is the state at the sequence's own end (h0 for a length of 0).
+ * Results do not depend on the run: every sum has a fixed order. */
+typedef enum { LATTICE_GATE_VALUE = 0, LATTICE_GATE_LOGIT = 1 } lattice_gate;
+typedef enum { LATTICE_WRITE_PLAIN = 0, LATTICE_WRITE_LEAKY = 1, LATTICE_WRITE_UNIT = 2 } lattice_write;
+
+/* Whole sequences. h0 may be NULL (0). h_out may be NULL or h0 (in place); y may be NULL
+ * when marks is given. marks (or NULL): device memory of lattice_gated_scan_marks_bytes,
+ * 16-byte aligned, filled with the state before every 16th token, for the backward pass.
+ * Outputs must not overlap inputs or each other (LATTICE_ERR_INVALID_ARG). Running a
+ * sequence in pieces, each from the state of the one before, gives the same recurrence. */
+lattice_status lattice_gated_scan_fwd(const void *x, lattice_dtype x_dtype,
+                                      long long x_batch_stride, long long x_token_stride,
+                                      const void *z, lattice_dtype z_dtype,
+                                      long long z_batch_stride, long long z_token_stride,
+                                      int z_per_head, const float *h0, float *h_out, void *y,
+                                      float *marks, const int *lengths, int B, int T, int H, int d,
+                                      lattice_gate gate, lattice_write write, float tau,
+                                      void *stream);
+
+/* Bytes of marks for this shape (0 for T = 0 or sizes the scan rejects). Host function. */
+size_t lattice_gated_scan_marks_bytes(int B, int T, int H, int d);
+
+/* Backward pass for L = sum_t dy_t . y_t + dh_T . h_len. x, z, lengths and the forms as in
+ * the forward call that filled marks (marks carries h0, which is therefore not an argument);
+ * dy in x's type, dh_T [B][H][d] fp32 or NULL (0). Writes dx (x's type), dz (z's type and
+ * shape; a gate per head collects its d channels) and dh0 [B][H][d] fp32, all contiguous and
+ * in full. Where s = 0 (|a| >= 1) the unit write passes no gradient to its gate. */
+lattice_status lattice_gated_scan_bwd(const void *x, lattice_dtype x_dtype,
+                                      long long x_batch_stride, long long x_token_stride,
+                                      const void *z, lattice_dtype z_dtype,
+                                      long long z_batch_stride, long long z_token_stride,
+                                      int z_per_head, const void *dy, long long dy_batch_stride,
+                                      long long dy_token_stride, const float *marks,
+                                      const float *dh_T, void *dx, void *dz, float *dh0,
+                                      const int *lengths, int B, int T, int H, int d,
+                                      lattice_gate gate, lattice_write write, float tau,
+                                      void *stream);
+
+/* One token: h_out = a h + s(a) x, y = h_out in x's type. h, h_out [B][H][d] fp32 (h_out ==
+ * h: in place); x [B][H][d], z [B][H][d] or [B][H], with batch strides as above. */
+lattice_status lattice_gated_step(const float *h, float *h_out, const void *x,
+                                  lattice_dtype x_dtype, long long x_batch_stride, const void *z,
+                                  lattice_dtype z_dtype, long long z_batch_stride, int z_per_head,
+                                  void *y, int B, int H, int d, lattice_gate gate,
+                                  lattice_write write, float tau, void *stream);
 
 /* Synchronises `stream`, returns LATTICE_ERR_TIMEOUT if any kernel since the
  * last call gave up a bounded wait (and clears the flag), LATTICE_ERR_CUDA if

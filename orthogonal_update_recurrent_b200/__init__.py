@@ -13,9 +13,14 @@ Tensors (row-major, contiguous, on one CUDA device):
     q   [B, T, H, m]  float32 or bfloat16      mu  [B, T, H]    float32
     eta [B, T, H]     float32 or None (=1)     S0  [B, H, m, d] float32
 Decode calls drop the T axis.
+
+Beside the state recurrence: the gated linear recurrence (gated_scan_fwd,
+gated_scan_bwd, gated_step). These also take float16, and rows that are slices of
+wider ones (their last axes contiguous).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -23,7 +28,8 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["LatticeError", "lib", "scan_fwd", "scan_bwd", "scan_bwd_workspace_bytes", "step",
-           "readout", "chunk_impl", "device_status", "selftest_bounded_wait", "LIB_PATH"]
+           "readout", "chunk_impl", "device_status", "selftest_bounded_wait", "LIB_PATH",
+           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_marks", "gated_step"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblattice.so")
 
@@ -72,6 +78,16 @@ def lib() -> ctypes.CDLL:
         L.lattice_chunk_impl.argtypes = [i, i, i, i, i, i, i]
         L.lattice_last_cuda_error.argtypes = []
         L.lattice_last_cuda_error.restype = ctypes.c_char_p
+        ll, f32 = ctypes.c_longlong, ctypes.c_float
+        L.lattice_gated_scan_fwd.argtypes = [vp, i, ll, ll, vp, i, ll, ll, i, fp, fp, vp, fp, vp, i, i, i, i, i, i,
+                                             f32, vp]
+        L.lattice_gated_scan_bwd.argtypes = [vp, i, ll, ll, vp, i, ll, ll, i, vp, ll, ll, fp, fp, vp, vp, fp, vp,
+                                             i, i, i, i, i, i, f32, vp]
+        L.lattice_gated_scan_marks_bytes.argtypes = [i, i, i, i]
+        L.lattice_gated_scan_marks_bytes.restype = ctypes.c_size_t
+        L.lattice_gated_step.argtypes = [fp, fp, vp, i, ll, vp, i, ll, i, vp, i, i, i, i, i, f32, vp]
+        for f in ("lattice_gated_scan_fwd", "lattice_gated_scan_bwd", "lattice_gated_step"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("lattice_scan_fwd", "lattice_scan_fwd_impl", "lattice_scan_fwd_ex", "lattice_scan_bwd",
                   "lattice_step", "lattice_readout", "lattice_selftest_bounded_wait",
                   "lattice_get_device_status", "lattice_version", "lattice_chunk_impl"):
@@ -82,6 +98,10 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _adr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -256,3 +276,150 @@ def selftest_bounded_wait(limit_ns: int = 1_000_000, stream=None) -> None:
     same stream then raises LatticeError with code ERR_TIMEOUT."""
     _raise(lib().lattice_selftest_bounded_wait(int(limit_ns), _stream(stream)),
            "lattice_selftest_bounded_wait")
+
+
+# ---------------------------------------------------------------- gated recurrence
+
+_DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_MARK = 16  # tokens between the states kept for the backward pass
+_GATE = {"value": 0, "logit": 1}
+_WRITE = {"plain": 0, "leaky": 1, "unit": 2}
+
+
+def _rows(t, name: str, shape, lead: int, dtypes, device):
+    """Checks a tensor whose first `lead` axes may be strided and whose other axes are
+    contiguous; returns the strides of the first `lead` axes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    strides = t.stride()
+    if not t.is_contiguous():
+        want = 1
+        for k in range(len(shape) - 1, lead - 1, -1):
+            if shape[k] != 1 and strides[k] != want:
+                raise ValueError(f"{name} must be contiguous in its last {len(shape) - lead} axes")
+            want *= shape[k]
+    return strides[:lead]
+
+
+def _whole(t, name: str, shape, dtypes, device):
+    """Checks a contiguous tensor; None passes."""
+    if t is None:
+        return
+    _rows(t, name, shape, 0, dtypes, device)
+
+
+def _place(device, stream):
+    """Where a call runs: on the tensors' device, its buffers allocated on the stream that
+    the kernels use, so that memory freed after the call is reused in that stream's order."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _gated_args(x, z, lead: int, lengths, gate: str, write: str):
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 2:
+        raise ValueError("x must be a tensor [B, T, H, d] (one token: [B, H, d])")
+    shape, device = x.shape, x.device
+    xs = _rows(x, "x", shape, lead, _FLOATS, device)
+    per_head = isinstance(z, torch.Tensor) and z.dim() == lead + 1
+    zs = _rows(z, "z", shape[:-1] if per_head else shape, lead, (x.dtype, torch.float32), device)
+    if lengths is not None:
+        _whole(lengths, "lengths", shape[:1], (torch.int32,), device)
+    if gate not in _GATE or write not in _WRITE:
+        raise ValueError(f"gate is one of {tuple(_GATE)}, write one of {tuple(_WRITE)}")
+    return xs, zs, per_head
+
+
+def gated_scan_marks(x: torch.Tensor) -> torch.Tensor:
+    """An empty buffer for the states that gated_scan_fwd leaves for gated_scan_bwd: the
+    state before every 16th token, [B, ceil(T/16), H, d] float32."""
+    B, T, H, d = x.shape
+    return torch.empty((B, (T + _MARK - 1) // _MARK, H, d), dtype=torch.float32, device=x.device)
+
+
+def gated_scan_fwd(x: torch.Tensor, z: torch.Tensor, h0: Optional[torch.Tensor] = None, *, gate: str = "logit",
+                   write: str = "leaky", tau: float = 1.0, lengths: Optional[torch.Tensor] = None,
+                   marks: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Gated linear recurrence h_t = a_t h_{t-1} + s(a_t) x_t over whole sequences, y_t = h_t.
+    x [B,T,H,d]; z [B,T,H,d], or [B,T,H] for one gate per head (d 16, 32, 64 or 128); both may
+    be slices of wider rows. z has x's dtype or float32. h0 [B,H,d] float32 or None (0).
+    gate "logit": a = sigmoid(z)**tau; "value": a = z, |a| <= 1. write "plain": s = 1;
+    "leaky": s = 1 - a; "unit": s = sqrt(1 - a*a). lengths int32 [B] or None (T): tokens behind
+    a sequence's length are not read and their y is 0. marks: a buffer of gated_scan_marks to
+    fill for gated_scan_bwd. h_out may be h0.
+    Returns (y [B,T,H,d] in x's dtype, h_T [B,H,d] float32, the state at each length)."""
+    xs, zs, per_head = _gated_args(x, z, 2, lengths, gate, write)
+    B, T, H, d = x.shape
+    dev, f32 = x.device, (torch.float32,)
+    _whole(h0, "h0", (B, H, d), f32, dev)
+    _whole(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), f32, dev)
+    _whole(h_out, "h_out", (B, H, d), f32, dev)
+    _whole(y, "y", x.shape, (x.dtype,), dev)
+    with _place(dev, stream):
+        if h_out is None:
+            h_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+        if y is None:
+            y = torch.empty((B, T, H, d), dtype=x.dtype, device=dev)
+        code = lib().lattice_gated_scan_fwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], z.data_ptr(), _DT[z.dtype], zs[0], zs[1], per_head, _adr(h0),
+            h_out.data_ptr(), y.data_ptr(), _adr(marks), _adr(lengths), B, T, H, d, _GATE[gate], _WRITE[write], tau,
+            _stream(stream))
+    _raise(code, "lattice_gated_scan_fwd")
+    return y, h_out
+
+
+def gated_scan_bwd(x: torch.Tensor, z: torch.Tensor, dy: torch.Tensor, marks: torch.Tensor, *,
+                   dh_T: Optional[torch.Tensor] = None, gate: str = "logit", write: str = "leaky", tau: float = 1.0,
+                   lengths: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward pass of gated_scan_fwd: gradients of L = sum_t dy_t . y_t + dh_T . h_T. x, z,
+    the forms, lengths and the filled marks are those of the forward call; dy has x's dtype
+    and may be strided as x. Returns a dict with dx (x's dtype), dz (z's dtype and shape) and
+    dh0 (float32); gradients of tokens behind a sequence's length are 0."""
+    xs, zs, per_head = _gated_args(x, z, 2, lengths, gate, write)
+    B, T, H, d = x.shape
+    dev, f32 = x.device, (torch.float32,)
+    dys = _rows(dy, "dy", x.shape, 2, (x.dtype,), dev)
+    _rows(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), 0, f32, dev)
+    _whole(dh_T, "dh_T", (B, H, d), f32, dev)
+    with _place(dev, stream):
+        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dz": torch.empty(z.shape, dtype=z.dtype, device=dev),
+               "dh0": torch.empty((B, H, d), dtype=torch.float32, device=dev)}
+        code = lib().lattice_gated_scan_bwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], z.data_ptr(), _DT[z.dtype], zs[0], zs[1], per_head, dy.data_ptr(),
+            dys[0], dys[1], marks.data_ptr(), _adr(dh_T), out["dx"].data_ptr(), out["dz"].data_ptr(),
+            out["dh0"].data_ptr(), _adr(lengths), B, T, H, d, _GATE[gate], _WRITE[write], tau, _stream(stream))
+    _raise(code, "lattice_gated_scan_bwd")
+    return out
+
+
+def gated_step(h: torch.Tensor, x: torch.Tensor, z: torch.Tensor, *, gate: str = "logit", write: str = "leaky",
+               tau: float = 1.0, h_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """One token of the gated recurrence: h [B,H,d] float32, x [B,H,d], z [B,H,d] or [B,H].
+    The state is updated in place, or written to h_out. Returns y [B,H,d] in x's dtype."""
+    xs, zs, per_head = _gated_args(x, z, 1, None, gate, write)
+    shape, dev = x.shape, x.device
+    B, H, d = shape
+    _rows(h, "h", shape, 0, (torch.float32,), dev)
+    _whole(h_out, "h_out", shape, (torch.float32,), dev)
+    _whole(y, "y", shape, (x.dtype,), dev)
+    with _place(dev, stream):
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
+        code = lib().lattice_gated_step(
+            h.data_ptr(), (h if h_out is None else h_out).data_ptr(), x.data_ptr(), _DT[x.dtype], xs[0], z.data_ptr(),
+            _DT[z.dtype], zs[0], per_head, y.data_ptr(), B, H, d, _GATE[gate], _WRITE[write], tau, _stream(stream))
+    _raise(code, "lattice_gated_step")
+    return y

@@ -93,4 +93,27 @@ inline size_t chunk_bwd_ws_floats(int B, int T, int H, int m, int D, int chunk) 
     return (size_t)B * H * chunk_bwd_ctas(m) * nc * kCbSlots * D;
 }
 
+// gated.cuh: gated linear recurrence
+constexpr int kGatedMark = 16;  // tokens between the states the forward pass leaves for the backward pass
+constexpr int kGatedMaxK = 8;   // CTAs of a cluster at most
+
+constexpr int kGatedMaxSize = 1 << 30;  // channels, and tokens: tile indices stay within int
+
+struct GatedArgs {
+    const void* x; const void* z;  // z: fp32 (z32) or x's type, per channel or per head (zhead)
+    const float* h0;               // may be null (=> 0)
+    float* h_out;                  // forward: may be null
+    void* y;                       // forward: may be null
+    float* marks;                  // forward: may be null
+    const int* lengths;            // may be null (=> T)
+    const void* dy; const float* dh_T;
+    void* dx; void* dz; float* dh0;
+    long long xbs, xts, zbs, zts, dybs, dyts;  // batch and token strides, in elements
+    int B, T, C, d;                // C = H*d channels
+    int ctiles, K, nmarks;         // channel tiles, CTAs per cluster, marks per sequence
+    float tau;
+    bool z32, zhead;
+    bool zwords;                   // 16-bit gates per head: every token's are whole 32-bit words
+};
+
 }  // namespace lattice

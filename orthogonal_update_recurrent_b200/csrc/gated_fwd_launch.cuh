@@ -1,0 +1,48 @@
+// gated_fwd_launch.cuh -- launches of the gated recurrence's forward and single-token kernels
+// (gated.cuh), instantiated per type of x in tu_gated_fwd_*.cu.
+#pragma once
+#include "gated_launch.cuh"
+
+namespace lattice {
+namespace gated {
+
+// Two channels per lane; runs of 16 tokens on 8 warps, two CTAs per SM (mid-size layer, bf16:
+// 72 us; runs of 8 on three CTAs 86 us: a run's exchange is then spread over half the
+// elements). fp32 rows are twice as wide, so runs of 8 keep the stages as large.
+template <class XT, int FORM, int ZM, bool VEC>
+lattice_status fwd(GatedArgs a, cudaStream_t st) {
+    constexpr int V = 2, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
+    a.ctiles = (a.C + 32 * V - 1) / (32 * V);
+    a.K = cluster_ctas(a, NW * R, MINB);
+    return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32,
+                  FwdLayout<XT, ZM, V, R, NW, NST>::bytes(a.K), st);
+}
+
+template <class XT, int FORM, int ZM, bool VEC>
+lattice_status step(const GatedArgs& a, cudaStream_t st) {
+    const long long threads = (long long)a.B * ((a.C + kStepVec - 1) / kStepVec), ctas = (threads + 255) / 256;
+    if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
+    gated_step_kernel<XT, ZM, FORM, VEC, kStepVec><<<(unsigned)ctas, 256, 0, st>>>(a);
+    return launch_status();
+}
+
+template <class XT>
+lattice_status launch_fwd(GatedArgs a, int form, bool vec, cudaStream_t st) {
+    return with_form(form, [&](auto f) {
+        return with_gates<XT>(a, vec, [&](auto zm, auto v) {
+            return fwd<XT, decltype(f)::value, decltype(zm)::value, decltype(v)::value>(a, st);
+        });
+    });
+}
+
+template <class XT>
+lattice_status launch_step(const GatedArgs& a, int form, bool vec, cudaStream_t st) {
+    return with_form(form, [&](auto f) {
+        return with_gates<XT>(a, vec, [&](auto zm, auto v) {
+            return step<XT, decltype(f)::value, decltype(zm)::value, decltype(v)::value>(a, st);
+        });
+    });
+}
+
+}  // namespace gated
+}  // namespace lattice

@@ -2,6 +2,8 @@
 // include/lattice.h): argument checks and kernel choice. The launches live in one
 // translation unit per kernel family (tu_*.cu, through launch.h).
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -105,6 +107,73 @@ lattice_status check_dims(int B, int H, int m, int d) {
     if ((long long)B * H > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
     if (!d_supported(d) || m > kMaxM) return LATTICE_ERR_UNSUPPORTED;
     return LATTICE_OK;
+}
+
+// ---- gated recurrence and block norms: fp16 is a type too, and rows may be strided
+size_t type_size(lattice_dtype t) { return t == LATTICE_F32 ? 4 : 2; }
+bool type_ok(lattice_dtype t) { return t == LATTICE_F32 || t == LATTICE_BF16 || t == LATTICE_F16; }
+
+// Bytes from the first to the last element of [B][T] rows of C elements with these strides;
+// false for a negative stride or an extent beyond 2^62 bytes.
+bool strided_span(const void* p, size_t size, long long B, long long T, long long C, long long bs, long long ts,
+                  Span* s) {
+    if (bs < 0 || ts < 0) return false;
+    const __int128 bytes = T < 1 ? 0 : ((__int128)(B - 1) * bs + (__int128)(T - 1) * ts + C) * size;
+    if (bytes > ((__int128)1 << 62)) return false;
+    *s = span(p, (size_t)bytes);
+    return true;
+}
+
+// Whether an output overlaps an input or another output. in_same == out_same: the one pair
+// that may be the same buffer.
+bool clash(const Span* ins, int ni, const Span* outs, int no, const void* in_same, const void* out_same) {
+    const uintptr_t same = in_same && in_same == out_same ? reinterpret_cast<uintptr_t>(in_same) : 0;
+    for (int i = 0; i < no; ++i) {
+        for (int k = 0; k < ni; ++k)
+            if (overlap(outs[i], ins[k]) &&
+                !(same && outs[i].lo == same && ins[k].lo == same && outs[i].hi == ins[k].hi))
+                return true;
+        for (int k = i + 1; k < no; ++k)
+            if (overlap(outs[i], outs[k])) return true;
+    }
+    return false;
+}
+
+lattice_status check_gated(lattice_dtype x_dtype, lattice_dtype z_dtype, int z_per_head, int B, int T, int H, int d,
+                           lattice_gate gate, lattice_write write, float tau) {
+    if (B < 1 || T < 0 || H < 1 || d < 1 || !type_ok(x_dtype) || !type_ok(z_dtype)) return LATTICE_ERR_INVALID_ARG;
+    if (gate != LATTICE_GATE_VALUE && gate != LATTICE_GATE_LOGIT) return LATTICE_ERR_INVALID_ARG;
+    if (write != LATTICE_WRITE_PLAIN && write != LATTICE_WRITE_LEAKY && write != LATTICE_WRITE_UNIT)
+        return LATTICE_ERR_INVALID_ARG;
+    if (gate == LATTICE_GATE_LOGIT && !(tau > 0.f && tau < 3.4e38f)) return LATTICE_ERR_INVALID_ARG;
+    if (z_dtype != LATTICE_F32 && z_dtype != x_dtype) return LATTICE_ERR_UNSUPPORTED;
+    if ((long long)H * d > kGatedMaxSize || T > kGatedMaxSize) return LATTICE_ERR_UNSUPPORTED;
+    if (z_per_head && !d_supported(d)) return LATTICE_ERR_UNSUPPORTED;
+    return LATTICE_OK;
+}
+
+int gated_form(lattice_gate gate, lattice_write write, float tau) {
+    return 3 * (gate == LATTICE_GATE_VALUE ? 0 : tau == 1.f ? 1 : 2) + (int)write;
+}
+
+// Whether the contiguous arrays of a gated call, whichever it has, and the channels suit
+// vectors of `bytes` bytes.
+bool gated_vec(const GatedArgs& a, size_t size, size_t bytes) {
+    return (size_t)a.C * size % bytes == 0 && aligned(a.y, bytes) && aligned(a.dx, bytes) && aligned(a.h0, 16) &&
+           aligned(a.h_out, 16) && aligned(a.dh_T, 16) && aligned(a.dh0, 16) && aligned(a.marks, 16);
+}
+// Whether the rows at p do.
+bool rows_vec(const void* p, size_t size, int B, int T, long long bs, long long ts, size_t bytes) {
+    return aligned(p, bytes) && (B == 1 || bs * size % bytes == 0) && (T <= 1 || ts * size % bytes == 0);
+}
+// Whether every token's 16-bit gates per head are whole 32-bit words.
+bool gate_words(const void* z, int H, long long bs, long long ts) {
+    return aligned(z, 4) && H % 2 == 0 && bs % 2 == 0 && ts % 2 == 0;
+}
+
+template <class F>
+lattice_status with_x(lattice_dtype t, F f) {
+    return t == LATTICE_F32 ? f(0.f) : t == LATTICE_BF16 ? f(__nv_bfloat16()) : f(__half());
 }
 
 }  // namespace
@@ -332,6 +401,116 @@ lattice_status lattice_scan_bwd(const void* x, lattice_dtype x_dtype, const floa
     return launch_bwd(a, d, static_cast<cudaStream_t>(stream));
 }
 
+lattice_status lattice_gated_scan_fwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride,
+                                      long long x_token_stride, const void* z, lattice_dtype z_dtype,
+                                      long long z_batch_stride, long long z_token_stride, int z_per_head,
+                                      const float* h0, float* h_out, void* y, float* marks, const int* lengths,
+                                      int B, int T, int H, int d, lattice_gate gate, lattice_write write,
+                                      float tau, void* stream) {
+    lattice_status s = check_gated(x_dtype, z_dtype, z_per_head, B, T, H, d, gate, write, tau);
+    if (s != LATTICE_OK) return s;
+    const long long C = (long long)H * d, Cz = z_per_head ? H : C, nm = (T + (long long)kGatedMark - 1) / kGatedMark;
+    Span sx, sz;
+    if (!strided_span(x, type_size(x_dtype), B, T, C, x_batch_stride, x_token_stride, &sx) ||
+        !strided_span(z, type_size(z_dtype), B, T, Cz, z_batch_stride, z_token_stride, &sz))
+        return LATTICE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !z || (!y && !marks))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(x, type_size(x_dtype)) || !aligned(z, type_size(z_dtype)) || !aligned(y, type_size(x_dtype)) ||
+        !aligned(h0, 4) || !aligned(h_out, 4) || !aligned(marks, 16) || !aligned(lengths, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    const size_t nh = (size_t)B * C * 4;
+    const Span ins[] = {sx, sz, span(h0, h0 ? nh : 0), span(lengths, lengths ? (size_t)B * 4 : 0)};
+    const Span outs[] = {span(h_out, h_out ? nh : 0), span(y, y ? (size_t)B * T * C * type_size(x_dtype) : 0),
+                         span(marks, marks ? (size_t)B * nm * C * 4 : 0)};
+    if (clash(ins, 4, outs, 3, h0, h_out)) return LATTICE_ERR_INVALID_ARG;
+    GatedArgs a = {};
+    a.x = x; a.z = z; a.h0 = h0; a.h_out = h_out; a.y = y; a.marks = marks; a.lengths = lengths;
+    a.xbs = x_batch_stride; a.xts = x_token_stride; a.zbs = z_batch_stride; a.zts = z_token_stride;
+    a.B = B; a.T = T; a.C = (int)C; a.d = d; a.nmarks = (int)nm; a.tau = tau;
+    a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
+    a.zwords = gate_words(z, H, a.zbs, a.zts);
+    const bool vec = gated_vec(a, type_size(x_dtype), 16) && rows_vec(x, type_size(x_dtype), B, T, a.xbs, a.xts, 16) &&
+                     (a.zhead || rows_vec(z, type_size(z_dtype), B, T, a.zbs, a.zts, 16));
+    return with_x(x_dtype, [&](auto t) {
+        return gated::launch_fwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
+    });
+}
+
+size_t lattice_gated_scan_marks_bytes(int B, int T, int H, int d) {
+    if (B < 1 || T < 0 || H < 1 || d < 1 || (long long)H * d > kGatedMaxSize || T > kGatedMaxSize) return 0;
+    return (size_t)B * ((T + (size_t)kGatedMark - 1) / kGatedMark) * H * d * 4;
+}
+
+lattice_status lattice_gated_scan_bwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride,
+                                      long long x_token_stride, const void* z, lattice_dtype z_dtype,
+                                      long long z_batch_stride, long long z_token_stride, int z_per_head,
+                                      const void* dy, long long dy_batch_stride, long long dy_token_stride,
+                                      const float* marks, const float* dh_T, void* dx, void* dz, float* dh0,
+                                      const int* lengths, int B, int T, int H, int d, lattice_gate gate,
+                                      lattice_write write, float tau, void* stream) {
+    lattice_status s = check_gated(x_dtype, z_dtype, z_per_head, B, T, H, d, gate, write, tau);
+    if (s != LATTICE_OK) return s;
+    const long long C = (long long)H * d, Cz = z_per_head ? H : C, nm = (T + (long long)kGatedMark - 1) / kGatedMark;
+    const size_t sx_ = type_size(x_dtype), sz_ = type_size(z_dtype);
+    Span sx, sz, sdy;
+    if (!strided_span(x, sx_, B, T, C, x_batch_stride, x_token_stride, &sx) ||
+        !strided_span(z, sz_, B, T, Cz, z_batch_stride, z_token_stride, &sz) ||
+        !strided_span(dy, sx_, B, T, C, dy_batch_stride, dy_token_stride, &sdy))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!dh0 || (T > 0 && (!x || !z || !dy || !marks || !dx || !dz))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(x, sx_) || !aligned(z, sz_) || !aligned(dy, sx_) || !aligned(dx, sx_) || !aligned(dz, sz_) ||
+        !aligned(marks, 16) || !aligned(dh_T, 4) || !aligned(dh0, 4) || !aligned(lengths, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    const size_t nh = (size_t)B * C * 4, nt = (size_t)B * T;
+    const Span ins[] = {sx, sz, sdy, span(marks, T > 0 ? (size_t)B * nm * C * 4 : 0), span(dh_T, dh_T ? nh : 0),
+                        span(lengths, lengths ? (size_t)B * 4 : 0)};
+    const Span outs[] = {span(dx, nt * C * sx_), span(dz, nt * Cz * sz_), span(dh0, nh)};
+    if (clash(ins, 6, outs, 3, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
+    GatedArgs a = {};
+    a.x = x; a.z = z; a.marks = const_cast<float*>(marks); a.lengths = lengths;
+    a.dy = dy; a.dh_T = dh_T; a.dx = dx; a.dz = dz; a.dh0 = dh0;
+    a.xbs = x_batch_stride; a.xts = x_token_stride; a.zbs = z_batch_stride; a.zts = z_token_stride;
+    a.dybs = dy_batch_stride; a.dyts = dy_token_stride;
+    a.B = B; a.T = T; a.C = (int)C; a.d = d; a.nmarks = (int)nm; a.tau = tau;
+    a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
+    a.zwords = gate_words(z, H, a.zbs, a.zts);
+    const bool vec = gated_vec(a, sx_, 16) && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
+                     rows_vec(dy, sx_, B, T, a.dybs, a.dyts, 16) &&
+                     (a.zhead || (rows_vec(z, sz_, B, T, a.zbs, a.zts, 16) && aligned(dz, 16)));
+    return with_x(x_dtype, [&](auto t) {
+        return gated::launch_bwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
+    });
+}
+
+lattice_status lattice_gated_step(const float* h, float* h_out, const void* x, lattice_dtype x_dtype,
+                                  long long x_batch_stride, const void* z, lattice_dtype z_dtype,
+                                  long long z_batch_stride, int z_per_head, void* y, int B, int H, int d,
+                                  lattice_gate gate, lattice_write write, float tau, void* stream) {
+    lattice_status s = check_gated(x_dtype, z_dtype, z_per_head, B, 1, H, d, gate, write, tau);
+    if (s != LATTICE_OK) return s;
+    const long long C = (long long)H * d, Cz = z_per_head ? H : C;
+    const size_t sx_ = type_size(x_dtype), sz_ = type_size(z_dtype);
+    if (!h || !h_out || !x || !z || !y) return LATTICE_ERR_INVALID_ARG;
+    Span sx, sz;
+    if (!strided_span(x, sx_, B, 1, C, x_batch_stride, 0, &sx) || !strided_span(z, sz_, B, 1, Cz, z_batch_stride, 0, &sz))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(h, 4) || !aligned(h_out, 4) || !aligned(x, sx_) || !aligned(z, sz_) || !aligned(y, sx_))
+        return LATTICE_ERR_INVALID_ARG;
+    const size_t nh = (size_t)B * C * 4;
+    const Span ins[] = {sx, sz, span(h, nh)}, outs[] = {span(h_out, nh), span(y, (size_t)B * C * sx_)};
+    if (clash(ins, 3, outs, 2, h, h_out)) return LATTICE_ERR_INVALID_ARG;
+    GatedArgs a = {};
+    a.x = x; a.z = z; a.h0 = h; a.h_out = h_out; a.y = y;
+    a.xbs = x_batch_stride; a.zbs = z_batch_stride;
+    a.B = B; a.T = 1; a.C = (int)C; a.d = d; a.tau = tau;
+    a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
+    const bool vec = gated_vec(a, sx_, kStepVec * sx_) && rows_vec(x, sx_, B, 1, a.xbs, 0, kStepVec * sx_) &&
+                     (a.zhead || rows_vec(z, sz_, B, 1, a.zbs, 0, kStepVec * sz_));
+    return with_x(x_dtype, [&](auto t) {
+        return gated::launch_step<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
+    });
+}
+
 lattice_status lattice_selftest_bounded_wait(unsigned long long limit_ns, void* stream) {
     if (limit_ns < 1 || limit_ns > 1000000000ull) return LATTICE_ERR_INVALID_ARG;
     bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns);
@@ -344,7 +523,9 @@ lattice_status lattice_get_device_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e);
     // every translation unit's copy of the status word (each unit is a module of its own)
     cudaError_t (*const units[])(unsigned int*) = {read_clear_module_status, status_simt_exact,
-                                                   status_simt_chunked, status_step, status_bwd, status_tc};
+                                                   status_simt_chunked, status_step, status_bwd, status_tc,
+                                                   status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
+                                                   status_gated_bwd_f32, status_gated_bwd_bf16, status_gated_bwd_f16};
     unsigned int any = 0;
     for (auto unit : units) {
         unsigned int v = 0;

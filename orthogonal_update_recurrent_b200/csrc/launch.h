@@ -38,11 +38,27 @@ lattice_status launch_tc(lattice_impl impl, const ScanArgs& a, int d, cudaStream
 // clusters of 4 CTAs of the register-chain kernel the current device holds at once
 int reg_cluster_capacity(int d);
 
+// tu_gated_fwd_*.cu, tu_gated_bwd_*.cu: gated linear recurrence, a unit per type of x
+// (ctiles, K set by the launch). form = 3 * gate form + write form (gated.cuh); vec: every
+// row can be read in aligned 16-byte pieces (the step: in aligned vectors of kStepVec elements)
+constexpr int kStepVec = 4;
+namespace gated {
+template <class XT> lattice_status launch_fwd(GatedArgs a, int form, bool vec, cudaStream_t st);
+template <class XT> lattice_status launch_step(const GatedArgs& a, int form, bool vec, cudaStream_t st);
+template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, cudaStream_t st);
+}  // namespace gated
+
 // each unit's device status word (read, and zeroed when set)
 cudaError_t status_simt_exact(unsigned int* v);
 cudaError_t status_simt_chunked(unsigned int* v);
 cudaError_t status_step(unsigned int* v);
 cudaError_t status_bwd(unsigned int* v);
 cudaError_t status_tc(unsigned int* v);
+cudaError_t status_gated_fwd_f32(unsigned int* v);
+cudaError_t status_gated_fwd_bf16(unsigned int* v);
+cudaError_t status_gated_fwd_f16(unsigned int* v);
+cudaError_t status_gated_bwd_f32(unsigned int* v);
+cudaError_t status_gated_bwd_bf16(unsigned int* v);
+cudaError_t status_gated_bwd_f16(unsigned int* v);
 
 }  // namespace lattice

@@ -1,0 +1,276 @@
+"""The gated linear recurrence on the GPU against the token-by-token 64-bit form, at the
+sizes where tiles, runs, clusters, vectors and lengths end."""
+import itertools
+
+import pytest
+
+import gated_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def L():
+    import orthogonal_update_recurrent_b200 as L
+    from orthogonal_update_recurrent_b200 import build
+    build.build()
+    return L
+
+
+def make(B, T, H, d, dtype="f32", zdtype=None, gate="logit", head=False, seed=0, mean=2.0, lengths=None):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    z = n(B, T, H) if head else n(B, T, H, d)
+    z = 1.2 * z + mean
+    if gate == "value":
+        z = 2 * torch.sigmoid(z) - 1 if mean < 1 else torch.sigmoid(z)
+    t = {"x": n(B, T, H, d).to(DT[dtype]), "z": z.to(DT[zdtype or dtype]), "h0": n(B, H, d), "dy": n(B, T, H, d).to(DT[dtype]),
+         "dh_T": n(B, H, d), "lengths": None}
+    if lengths is not None:
+        t["lengths"] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        for b, v in enumerate(lengths):
+            for k in ("x", "z", "dy"):
+                t[k][b, max(v, 0):] = float("nan")
+    return t
+
+
+def both(L, t, gate="logit", write="leaky", tau=1.0, h0=True, dh_T=True):
+    kw = dict(gate=gate, write=write, tau=tau, lengths=t["lengths"])
+    h = t["h0"] if h0 else None
+    k = t["dh_T"] if dh_T else None
+    marks = L.gated_scan_marks(t["x"])
+    y, h_T = L.gated_scan_fwd(t["x"], t["z"], h, marks=marks, **kw)
+    got = L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks, dh_T=k, **kw)
+    got.update(y=y, h_T=h_T)
+    lens = None if t["lengths"] is None else t["lengths"].tolist()
+    ref = R.scan(t["x"], t["z"], h, gate, write, tau, lens, t["dy"], k)
+    for name in ("y", "h_T", "dx", "dz", "dh0"):
+        R.check(got[name], ref, name)
+    assert got["y"].dtype == t["x"].dtype and got["dz"].dtype == t["z"].dtype and got["dx"].dtype == t["x"].dtype
+    return got
+
+
+SHAPES = [(1, 1, 1, 1), (2, 7, 1, 5), (1, 8, 2, 16), (2, 63, 1, 37), (1, 64, 3, 16), (3, 65, 2, 64), (2, 127, 1, 130),
+          (1, 513, 2, 32), (1, 1537, 1, 66), (33, 129, 5, 128)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype,zdtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+def test_shapes_and_types(L, shape, dtype, zdtype):
+    both(L, make(*shape, dtype=dtype, zdtype=zdtype, seed=sum(shape)))
+
+
+@pytest.mark.parametrize("gate,write,tau", list(itertools.product(["value"], ["plain", "leaky", "unit"], [1.0]))
+                         + list(itertools.product(["logit"], ["plain", "leaky", "unit"], [1.0, 0.0625, 2.5])))
+@pytest.mark.parametrize("head", [False, True])
+def test_forms(L, gate, write, tau, head):
+    both(L, make(2, 150, 3, 32, gate=gate, head=head, seed=3), gate, write, tau)
+    both(L, make(2, 150, 3, 32, dtype="bf16", zdtype="f32", gate=gate, head=head, seed=4, mean=0.0), gate, write, tau)
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype,zdtype", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+def test_head_gates(L, d, dtype, zdtype):
+    both(L, make(2, 131, 5, d, dtype=dtype, zdtype=zdtype, head=True, seed=d), write="unit")
+
+
+@pytest.mark.parametrize("lengths", [[0, 0, 0], [0, 1, 200], [64, 63, 65], [200, 128, 7], [-3, 199, 9999]], ids=str)
+@pytest.mark.parametrize("head", [False, True])
+def test_padded_batches(L, lengths, head):
+    got = both(L, make(3, 200, 2, 32, dtype="bf16", zdtype="f32", head=head, seed=9, lengths=lengths), write="unit")
+    for b, v in enumerate(lengths):
+        for k in ("y", "dx", "dz"):
+            assert (got[k][b, max(v, 0):] == 0).all()
+
+
+def test_long_sequence_of_few_channels_spreads_over_a_cluster(L):
+    both(L, make(1, 6000, 1, 24, mean=6.0, seed=5), write="unit")
+    both(L, make(1, 6000, 1, 24, mean=6.0, seed=5, lengths=[4321]), write="leaky", tau=0.25)
+
+
+def test_no_initial_state_and_no_final_cotangent(L):
+    both(L, make(2, 100, 1, 20, seed=6), h0=False, dh_T=False)
+
+
+def test_no_tokens(L):
+    t = make(2, 0, 3, 16)
+    y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"])
+    assert y.shape == (2, 0, 3, 16) and torch.equal(h, t["h0"])
+    g = L.gated_scan_bwd(t["x"], t["z"], t["dy"], L.gated_scan_marks(t["x"]), dh_T=t["dh_T"])
+    assert torch.equal(g["dh0"], t["dh_T"])
+
+
+def test_slices_of_wider_rows(L):
+    B, T, H, d = 2, 90, 2, 32
+    t = make(B, T, H, d, dtype="bf16", seed=7)
+    want = both(L, t)
+    for pad in (0, 1, 8):  # 1: rows that vectors cannot read
+        wide = torch.full((B, T, 3 * H * d + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+        for k, name in enumerate(("x", "z", "dy")):
+            v = wide[:, :, k * H * d + pad:(k + 1) * H * d + pad].unflatten(-1, (H, d))
+            v.copy_(t[name])
+            t[name] = v
+        got = both(L, t)
+        for k in want:
+            assert torch.equal(got[k], want[k]), (pad, k)
+    # time-major storage, and one row shared by the batch
+    t = make(B, T, H, d, seed=8)
+    want = both(L, t)
+    t["x"], t["z"], t["dy"] = (t[k].transpose(0, 1).contiguous().transpose(0, 1) for k in ("x", "z", "dy"))
+    got = both(L, t)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    t["x"] = t["x"][:1].expand(B, T, H, d)
+    both(L, t)
+
+
+def test_misaligned_arrays(L):
+    B, T, H, d = 2, 70, 1, 32
+    t = make(B, T, H, d, dtype="bf16", zdtype="f32", seed=10)
+    want = both(L, t)
+    for k in ("x", "z", "h0", "dy", "dh_T"):
+        flat = torch.empty(t[k].numel() + 1, dtype=t[k].dtype, device="cuda")
+        v = flat[1:].view(t[k].shape)
+        v.copy_(t[k])
+        t[k] = v
+    got = both(L, t)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_in_place_state_and_pieces(L):
+    t = make(2, 300, 2, 32, seed=11)
+    y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"])
+    s = t["h0"].clone()
+    parts = []
+    for lo, hi in ((0, 1), (1, 130), (130, 130), (130, 300)):
+        yp, out = L.gated_scan_fwd(t["x"][:, lo:hi], t["z"][:, lo:hi], s, h_out=s)
+        assert out is s
+        parts.append(yp)
+    ref = R.scan(t["x"], t["z"], t["h0"], "logit", "leaky", 1.0)
+    R.check(torch.cat(parts, 1), ref, "y")
+    R.check(s, ref, "h_T")
+
+
+def test_extreme_gates(L):
+    inf = float("inf")
+    t = make(1, 70, 1, 16, seed=12)
+    t["z"][0, 10] = -inf   # forget everything
+    t["z"][0, 20] = inf    # keep everything
+    t["z"][0, 30] = 200.0
+    t["z"][0, 40] = -200.0
+    for write, tau in itertools.product(("plain", "leaky", "unit"), (1.0, 0.125)):
+        kw = dict(write=write, tau=tau)
+        marks = L.gated_scan_marks(t["x"])
+        y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=marks, **kw)
+        g = L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks, dh_T=t["dh_T"], **kw)
+        for v in (y, h, g["dx"], g["dz"], g["dh0"]):
+            assert torch.isfinite(v).all()
+        ref = R.scan(t["x"], t["z"], t["h0"], "logit", write, tau)
+        R.check(y, ref, "y")
+        other = t["dy"].clone()
+        other[0, 10:] += 1.0
+        g2 = L.gated_scan_bwd(t["x"], t["z"], other, marks, dh_T=3 * t["dh_T"], **kw)
+        assert torch.equal(g["dh0"], g2["dh0"])  # nothing passes a gate of 0
+        assert (g["dz"][0, [10, 20]] == 0).all()
+    t = make(1, 70, 1, 16, seed=12, gate="value")
+    t["z"][0, 10], t["z"][0, 20], t["z"][0, 30] = 0.0, 1.0, -1.0
+    for write in ("plain", "leaky", "unit"):
+        both(L, t, "value", write)
+
+
+def test_not_a_number_stays_in_its_channel_and_after_its_token(L):
+    t = make(2, 200, 1, 32, seed=13)
+    t["x"][1, 100, 0, 3] = float("nan")
+    y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"])
+    bad = torch.isnan(y)
+    assert bad[1, 100:, 0, 3].all() and bad.sum() == 100 and torch.isnan(h).sum() == 1
+
+
+def test_the_same_call_gives_the_same_bits(L):
+    t = make(3, 900, 2, 64, dtype="bf16", seed=14)
+    one, two = both(L, t), both(L, t)
+    assert all(torch.equal(one[k], two[k]) for k in one)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (3, 2, 16), (5, 1, 37), (256, 32, 128)], ids=str)
+@pytest.mark.parametrize("dtype,zdtype,head", [("f32", "f32", False), ("bf16", "bf16", False), ("f16", "f32", True)])
+def test_step(L, shape, dtype, zdtype, head):
+    B, H, d = shape
+    if head and d not in (16, 32, 64, 128):
+        pytest.skip("a gate per head has the library's head widths")
+    for gate, write, tau in (("logit", "leaky", 1.0), ("logit", "unit", 0.25), ("value", "plain", 1.0)):
+        t = make(B, 1, H, d, dtype=dtype, zdtype=zdtype, gate=gate, head=head, seed=15)
+        ref = R.scan(t["x"], t["z"], t["h0"], gate, write, tau)
+        x, z, h = t["x"][:, 0], t["z"][:, 0], t["h0"].clone()
+        out = torch.empty_like(h)
+        y = L.gated_step(h, x, z, gate=gate, write=write, tau=tau, h_out=out)
+        assert torch.equal(h, t["h0"])
+        y2 = L.gated_step(h, x, z, gate=gate, write=write, tau=tau)  # in place
+        assert torch.equal(h, out) and torch.equal(y, y2)
+        R.check(out.unsqueeze(1), {"y": ref["y"], "b_y": ref["b_y"]}, "y")
+        R.check(y.unsqueeze(1), ref, "y")
+        ys, hs = L.gated_scan_fwd(t["x"], t["z"], t["h0"], gate=gate, write=write, tau=tau)
+        assert torch.equal(hs, out) and torch.equal(ys[:, 0], y)  # one token through the scan
+
+
+def test_offsets_beyond_32_bits(L):
+    """One sequence whose rows reach past 2^31 elements."""
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 20 GB")
+    T, wide = 300, 8_000_000  # element offset of the last row: 2.4e9
+    buf = torch.empty((1, T, wide), dtype=torch.bfloat16, device="cuda")
+    t = make(1, T, 1, 64, dtype="bf16", seed=16)
+    want = both(L, t)
+    for k, name in enumerate(("x", "z", "dy")):
+        v = buf[:, :, k * 64:(k + 1) * 64].unflatten(-1, (1, 64))
+        v.copy_(t[name])
+        t[name] = v
+    got = both(L, t)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_streams_and_graphs(L):
+    t = make(2, 300, 2, 64, dtype="bf16", seed=17)
+    want = both(L, t)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    marks = L.gated_scan_marks(t["x"])
+    y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=marks, stream=side)
+    g = L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks, dh_T=t["dh_T"], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want["y"]) and torch.equal(g["dz"], want["dz"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m2 = L.gated_scan_marks(t["x"])
+        y2, h2 = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=m2)
+        g2 = L.gated_scan_bwd(t["x"], t["z"], t["dy"], m2, dh_T=t["dh_T"])
+    t2 = make(2, 300, 2, 64, dtype="bf16", seed=18)
+    for k in ("x", "z", "h0", "dy", "dh_T"):
+        t[k].copy_(t2[k])
+    graph.replay()
+    want = both(L, t2)
+    got = {"y": y2, "h_T": h2, **g2}
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("workload", ["small_train", "mid_layer"])
+def test_full_sizes_on_sampled_channels(L, workload):
+    """The repository's training shapes; every channel is its own recurrence, so the 64-bit
+    form runs on a sample of them."""
+    import lattice_inputs as LI
+    w = LI.WORKLOADS[workload]
+    t = make(w.B, w.T, w.H, w.d, dtype="bf16", seed=19, mean=3.0)
+    kw = dict(write="unit")
+    marks = L.gated_scan_marks(t["x"])
+    y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=marks, **kw)
+    got = L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks, dh_T=t["dh_T"], **kw)
+    got.update(y=y, h_T=h)
+    pick = (slice(w.B - 1, w.B), slice(None), slice(w.H - 1, w.H), slice(w.d - 8, w.d))
+    pick_h = (pick[0], pick[2], pick[3])
+    c = {k: t[k][pick if t[k].dim() == 4 else pick_h].contiguous() for k in ("x", "z", "h0", "dy", "dh_T")}
+    ref = R.scan(c["x"], c["z"], c["h0"], "logit", "unit", 1.0, None, c["dy"], c["dh_T"])
+    for name in ("y", "h_T", "dx", "dz", "dh0"):
+        R.check(got[name][pick if got[name].dim() == 4 else pick_h], ref, name)
