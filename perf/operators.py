@@ -295,9 +295,7 @@ def _own_norm(L, s, c):
     if c["gate"] != "none":
         how["act"] = c["gate"]
     if c["op"] == "norm":
-        if s["residual"] is None:
-            how["out_dtype"] = DTYPES[c["dtype"]]
-        r, n = L.block_norm_fwd(s["y"], **how)
+        r, n = L.block_norm_fwd(s["y"], out_dtype=DTYPES[c["dtype"]], **how)
         return {"r": r} if n is None else {"r": r, "n": n}
     grads = L.block_norm_bwd(s["y"], dr=s["dr"], dn=s["dn"], **how)
     return {k: v for k, v in grads.items() if v is not None}
