@@ -335,6 +335,58 @@ lattice_status lattice_gated_step(const float *h, float *h_out, const void *x,
                                   void *y, int B, int H, int d, lattice_gate gate,
                                   lattice_write write, float tau, void *stream);
 
+/* ---- Norms after and before a block
+ *
+ * What surrounds a recurrence in a layer: the norm of its read-out with the gate on it (the
+ * paper's block has a GeLU gate after the read-out, Appendix C), and after the output
+ * projection the scaled residual and the next block's norm. Per row of D elements:
+ *     u = y / sqrt(mean y^2 + eps)       (u = y with post_norm 0)
+ *     v = scale u w_post act(gate)       (w_post, gate: 1 where NULL)
+ *     r = residual + v                   (r = v without a residual)
+ *     n = r / sqrt(mean r^2 + eps) w_pre (if wanted)
+ * Types: `dtype` is that of gate and n; y, residual and r, and the weights (both) are of it
+ * or fp32. r has the residual's type, or dtype without one. Arithmetic is fp32 and n is
+ * formed from r before its rounding.
+ * Rows: N rows of D contiguous elements, 1 <= D <= 16384, 0 <= N < 2^31. Inputs come in
+ * groups of G rows (N a multiple of G), contiguous within a group, with the given stride
+ * in elements (>= 0) between groups: G = 1 for rows of any stride, G = H for heads
+ * [B*T][H][D] cut out of wider tokens. Outputs are contiguous.
+ * act: applied to the gate; NONE: the gate is not allowed. eps > 0. */
+typedef enum { LATTICE_ACT_NONE = 0, LATTICE_ACT_SIGMOID = 1, LATTICE_ACT_SILU = 2, LATTICE_ACT_GELU = 3 } lattice_act;
+
+/* r_out may be the residual (same buffer, contiguous): the residual stream is then updated
+ * in place. n_out NULL: n is not formed (w_pre must then be NULL). */
+lattice_status lattice_block_norm_fwd(const void *y, lattice_dtype y_dtype, long long y_stride,
+                                      const void *gate, long long gate_stride, const void *residual,
+                                      lattice_dtype residual_dtype, long long residual_stride,
+                                      const void *w_post, const void *w_pre, lattice_dtype w_dtype,
+                                      void *r_out, void *n_out, lattice_dtype dtype, long long N,
+                                      int G, int D, lattice_act act, int post_norm, float scale,
+                                      float eps, void *stream);
+
+/* Bytes of workspace of lattice_block_norm_bwd on the current device (0 for sizes it
+ * rejects). Host function. */
+size_t lattice_block_norm_bwd_workspace_bytes(long long N, int D);
+
+/* Backward pass, recomputing from the forward call's inputs. dr: cotangent of r, in
+ * dr_dtype (fp32 or dtype; with a residual, the residual's type), or NULL (0); dn: cotangent
+ * of n in dtype, or NULL (n was not formed); at least one is given. Writes dy (y's type),
+ * dgate (dtype; required with a gate), dresidual (the residual's type; required with a
+ * residual), all contiguous, and the weights' gradients dw_post, dw_pre [D] fp32, each NULL
+ * where it is not wanted. workspace: lattice_block_norm_bwd_workspace_bytes, 16-byte
+ * aligned, needed if a weight's gradient is wanted. Sums over rows are taken in a fixed
+ * order for given sizes and device. */
+lattice_status lattice_block_norm_bwd(const void *y, lattice_dtype y_dtype, long long y_stride,
+                                      const void *gate, long long gate_stride, const void *residual,
+                                      lattice_dtype residual_dtype, long long residual_stride,
+                                      const void *w_post, const void *w_pre, lattice_dtype w_dtype,
+                                      const void *dr, lattice_dtype dr_dtype, long long dr_stride,
+                                      const void *dn, long long dn_stride, void *dy, void *dgate,
+                                      void *dresidual, float *dw_post, float *dw_pre,
+                                      void *workspace, size_t workspace_bytes, lattice_dtype dtype,
+                                      long long N, int G, int D, lattice_act act, int post_norm,
+                                      float scale, float eps, void *stream);
+
 /* Synchronises `stream`, returns LATTICE_ERR_TIMEOUT if any kernel since the
  * last call gave up a bounded wait (and clears the flag), LATTICE_ERR_CUDA if
  * the stream reports an error, else LATTICE_OK. */

@@ -15,8 +15,9 @@ Tensors (row-major, contiguous, on one CUDA device):
 Decode calls drop the T axis.
 
 Beside the state recurrence: the gated linear recurrence (gated_scan_fwd,
-gated_scan_bwd, gated_step). These also take float16, and rows that are slices of
-wider ones (their last axes contiguous).
+gated_scan_bwd, gated_step) and the norms after and before a block (block_norm_fwd,
+block_norm_bwd). These also take float16, and rows that are slices of wider ones (their
+last axes contiguous).
 """
 from __future__ import annotations
 
@@ -29,7 +30,8 @@ import torch
 
 __all__ = ["LatticeError", "lib", "scan_fwd", "scan_bwd", "scan_bwd_workspace_bytes", "step",
            "readout", "chunk_impl", "device_status", "selftest_bounded_wait", "LIB_PATH",
-           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_marks", "gated_step"]
+           "gated_scan_fwd", "gated_scan_bwd", "gated_scan_marks", "gated_step", "block_norm_fwd",
+           "block_norm_bwd"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblattice.so")
 
@@ -86,7 +88,14 @@ def lib() -> ctypes.CDLL:
         L.lattice_gated_scan_marks_bytes.argtypes = [i, i, i, i]
         L.lattice_gated_scan_marks_bytes.restype = ctypes.c_size_t
         L.lattice_gated_step.argtypes = [fp, fp, vp, i, ll, vp, i, ll, i, vp, i, i, i, i, i, f32, vp]
-        for f in ("lattice_gated_scan_fwd", "lattice_gated_scan_bwd", "lattice_gated_step"):
+        L.lattice_block_norm_fwd.argtypes = [vp, i, ll, vp, ll, vp, i, ll, vp, vp, i, vp, vp, i, ll, i, i, i, i, f32,
+                                             f32, vp]
+        L.lattice_block_norm_bwd.argtypes = [vp, i, ll, vp, ll, vp, i, ll, vp, vp, i, vp, i, ll, vp, ll, vp, vp, vp, fp,
+                                             fp, vp, ctypes.c_size_t, i, ll, i, i, i, i, f32, f32, vp]
+        L.lattice_block_norm_bwd_workspace_bytes.argtypes = [ll, i]
+        L.lattice_block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        for f in ("lattice_gated_scan_fwd", "lattice_gated_scan_bwd", "lattice_gated_step", "lattice_block_norm_fwd",
+                  "lattice_block_norm_bwd"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("lattice_scan_fwd", "lattice_scan_fwd_impl", "lattice_scan_fwd_ex", "lattice_scan_bwd",
                   "lattice_step", "lattice_readout", "lattice_selftest_bounded_wait",
@@ -423,3 +432,163 @@ def gated_step(h: torch.Tensor, x: torch.Tensor, z: torch.Tensor, *, gate: str =
             _DT[z.dtype], zs[0], per_head, y.data_ptr(), B, H, d, _GATE[gate], _WRITE[write], tau, _stream(stream))
     _raise(code, "lattice_gated_step")
     return y
+
+
+# ---------------------------------------------------------------- block norms
+
+_ACT = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3}
+
+
+def _groups(tensors, shape):
+    """(G, strides): rows in groups of G, contiguous within a group, for every tensor of
+    `shape` (None: stride 0), with the stride between groups."""
+    D, lead = shape[-1], shape[:-1]
+    names = [k for k, t in tensors if t is not None]
+    if all(t is None or t.is_contiguous() for _, t in tensors):
+        return 1, [D] * len(tensors)
+    for G, outer in ((1, lead), (lead[-1] if lead else 1, lead[:-1])):
+        strides = []
+        for _, t in tensors:
+            if t is None:
+                strides.append(0)
+                continue
+            st = t.stride()
+            ok = D == 1 or st[-1] == 1
+            if G > 1:
+                ok = ok and st[-2] == D
+            s, width = None, 1  # the outer axes collapse into one, of stride s
+            for n, k in zip(reversed(outer), reversed(st[:len(outer)])):
+                if n != 1:
+                    if s is None:
+                        s = k
+                    ok = ok and k == s * width
+                    width *= n
+            strides.append(G * D if s is None else s)
+            if not ok:
+                break
+        else:
+            return G, strides
+    raise ValueError(f"the rows of {', '.join(names)} must be contiguous, with one stride between rows, or between the "
+                     "groups of rows that the last axis but one makes")
+
+
+def _norm_args(y, w_post, gate, residual, w_pre, act, dtype):
+    if not isinstance(y, torch.Tensor) or not y.is_cuda or y.dim() < 1:
+        raise TypeError("y must be a CUDA tensor [..., D]")
+    shape, dev = y.shape, y.device
+    if dtype is None:
+        dtype = gate.dtype if isinstance(gate, torch.Tensor) else y.dtype
+    if dtype not in _FLOATS:
+        raise TypeError(f"the output dtype must be one of {_FLOATS}, got {dtype}")
+    both = (dtype, torch.float32)
+    for t, name, types in ((y, "y", both), (gate, "gate", (dtype,)), (residual, "residual", both)):
+        if t is not None:
+            _like(t, name, shape, types, dev)
+    w_dtype = torch.float32
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _rows(t, name, shape[-1:], 0, both, dev)
+            w_dtype = t.dtype
+    if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
+        raise TypeError("w_post and w_pre must have the same dtype")
+    if act not in _ACT:
+        raise ValueError(f"act is one of {tuple(_ACT)}")
+    return shape, dev, dtype, w_dtype
+
+
+def _like(t, name, shape, dtypes, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def block_norm_fwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
+                   act: str = "gelu", residual: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                   pre_norm: Optional[bool] = None, post_norm: bool = True, scale: float = 1.0, eps: float = 1e-6,
+                   out_dtype: Optional[torch.dtype] = None, r_out: Optional[torch.Tensor] = None,
+                   n_out: Optional[torch.Tensor] = None, stream=None):
+    """The norm after a block with its gate and residual scale, and the norm before the next:
+    per row of the last axis u = y / sqrt(mean(y^2) + eps) (u = y without post_norm),
+    r = residual + scale * u * w_post * act(gate), n = r / sqrt(mean(r^2) + eps) * w_pre.
+    y [..., D]; gate, residual of y's shape or None; weights [D] or None (1). n is formed with
+    w_pre, or with pre_norm=True. act: "sigmoid", "silu" or "gelu". Dtypes: out_dtype (default:
+    the gate's, else y's) is that of the gate, of n, and of r without a residual; y, the
+    residual, whose dtype r then has, and the weights are of it or float32. Inputs may be
+    slices of wider rows. r_out may be the residual. Returns (r, n), n None if not formed."""
+    shape, dev, dtype, w_dtype = _norm_args(y, w_post, gate, residual, w_pre, act, out_dtype)
+    if pre_norm is None:
+        pre_norm = w_pre is not None or n_out is not None
+    elif not pre_norm and (w_pre is not None or n_out is not None):
+        raise ValueError("w_pre and n_out need pre_norm")
+    r_dtype = dtype if residual is None else residual.dtype
+    _whole(r_out, "r_out", shape, (r_dtype,), dev)
+    _whole(n_out, "n_out", shape, (dtype,), dev)
+    D = shape[-1]
+    N = y.numel() // D if D else 0
+    G, st = _groups((("y", y), ("gate", gate), ("residual", residual)), shape)
+    with _place(dev, stream):
+        if r_out is None:
+            r_out = torch.empty(shape, dtype=r_dtype, device=dev)
+        if n_out is None and pre_norm:
+            n_out = torch.empty(shape, dtype=dtype, device=dev)
+        code = lib().lattice_block_norm_fwd(
+            y.data_ptr(), _DT[y.dtype], st[0], _adr(gate), st[1], _adr(residual), _DT[r_dtype], st[2], _adr(w_post),
+            _adr(w_pre), _DT[w_dtype], r_out.data_ptr(), _adr(n_out), _DT[dtype], N, G, D, _ACT[act], post_norm, scale,
+            eps, _stream(stream))
+    _raise(code, "lattice_block_norm_fwd")
+    return r_out, n_out
+
+
+def block_norm_bwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, dr: Optional[torch.Tensor] = None,
+                   dn: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, act: str = "gelu",
+                   residual: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, post_norm: bool = True,
+                   scale: float = 1.0, eps: float = 1e-6, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward pass of block_norm_fwd from its inputs: gradients of L = sum(dr * r) + sum(dn * n).
+    dr: cotangent of r (with a residual in its dtype, else in the call's or float32) or None
+    (0); dn: cotangent of n or None (n was not formed). The call's dtype is dn's, else the
+    gate's, else dr's. Returns a dict with dy, dgate, dresidual (their input's dtype, None
+    without one) and dw_post, dw_pre (float32, None without the weight). workspace: optional
+    contiguous uint8 tensor for the weights' gradients; allocated when None. The gradient of a
+    learned scale is (dw_post * w_post).sum() / scale."""
+    dtype = next((t.dtype for t in (dn, gate, dr) if isinstance(t, torch.Tensor)), None)
+    if dtype is None:
+        raise ValueError("one of dr and dn is needed")
+    if dn is None and gate is None and dtype == torch.float32:  # r in float32 says nothing about the call's dtype
+        dtype = next((t.dtype for t in (y, residual, w_post) if isinstance(t, torch.Tensor) and t.dtype != dtype), dtype)
+    shape, dev, dtype, w_dtype = _norm_args(y, w_post, gate, residual, w_pre, act, dtype)
+    if w_pre is not None and dn is None:
+        raise ValueError("w_pre needs dn")
+    if dr is not None:
+        _like(dr, "dr", shape, (residual.dtype,) if residual is not None else (dtype, torch.float32), dev)
+    if dn is not None:
+        _like(dn, "dn", shape, (dtype,), dev)
+    D = shape[-1]
+    N = y.numel() // D if D else 0
+    G, st = _groups((("y", y), ("gate", gate), ("residual", residual), ("dr", dr), ("dn", dn)), shape)
+    L = lib()
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
+            raise TypeError("workspace must be a contiguous tensor on the inputs' device")
+    with _place(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        out = {"dy": torch.empty(shape, dtype=y.dtype, device=dev),
+               "dgate": None if gate is None else torch.empty(shape, dtype=dtype, device=dev),
+               "dresidual": None if residual is None else torch.empty(shape, dtype=residual.dtype, device=dev),
+               "dw_post": None if w_post is None else torch.empty(D, **f32),
+               "dw_pre": None if w_pre is None else torch.empty(D, **f32)}
+        if workspace is None and (w_post is not None or w_pre is not None):
+            workspace = torch.empty(L.lattice_block_norm_bwd_workspace_bytes(N, D), dtype=torch.uint8, device=dev)
+        code = L.lattice_block_norm_bwd(
+            y.data_ptr(), _DT[y.dtype], st[0], _adr(gate), st[1], _adr(residual),
+            0 if residual is None else _DT[residual.dtype], st[2], _adr(w_post), _adr(w_pre), _DT[w_dtype], _adr(dr),
+            0 if dr is None else _DT[dr.dtype], st[3], _adr(dn), st[4], out["dy"].data_ptr(), _adr(out["dgate"]),
+            _adr(out["dresidual"]), _adr(out["dw_post"]), _adr(out["dw_pre"]), _adr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _DT[dtype], N, G, D, _ACT[act],
+            post_norm, scale, eps, _stream(stream))
+    _raise(code, "lattice_block_norm_bwd")
+    return out

@@ -116,4 +116,23 @@ struct GatedArgs {
     bool zwords;                   // 16-bit gates per head: every token's are whole 32-bit words
 };
 
+// block_norm.cuh: norms after and before a block
+constexpr int kNormMaxD = 16384;
+
+struct NormArgs {
+    const void* y; const void* gate; const void* residual;  // the last two may be null
+    const void* w_post; const void* w_pre;                  // may be null (=> 1)
+    void* r_out; void* n_out;                               // forward: n_out may be null
+    const void* dr; const void* dn;                         // backward: one may be null (=> 0)
+    void* dy; void* dgate; void* dresidual;                 // backward: the last two may be null
+    float* parts;                                           // backward: weight gradients' sums per CTA, or null
+    long long ys, gs, rs, drs, dns;                         // between groups of G rows, in elements
+    long long N;
+    int G, D, tpr;                                          // tpr: threads per row
+    int act;
+    float scale, eps, inv_d;
+    bool post;
+    bool y32, r32, o32, w32;                                // fp32, else the call's type: y, residual, r (dr), weights
+};
+
 }  // namespace lattice

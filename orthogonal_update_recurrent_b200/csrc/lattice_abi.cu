@@ -176,6 +176,41 @@ lattice_status with_x(lattice_dtype t, F f) {
     return t == LATTICE_F32 ? f(0.f) : t == LATTICE_BF16 ? f(__nv_bfloat16()) : f(__half());
 }
 
+// ---- block norms
+// What both directions check, and the inputs they share, into a.
+lattice_status check_norm(NormArgs& a, const void* y, lattice_dtype y_dtype, long long ys, const void* gate, long long gs,
+                          const void* residual, lattice_dtype r_dtype, long long rs, const void* w_post, const void* w_pre,
+                          lattice_dtype w_dtype, lattice_dtype dtype, long long N, int G, int D, lattice_act act, int post,
+                          float scale, float eps) {
+    if (!type_ok(dtype) || !type_ok(y_dtype) || !type_ok(r_dtype) || !type_ok(w_dtype)) return LATTICE_ERR_INVALID_ARG;
+    if (N < 0 || G < 1 || D < 1 || N % G || ys < 0 || gs < 0 || rs < 0) return LATTICE_ERR_INVALID_ARG;
+    if ((int)act < 0 || (int)act > 3 || (gate && act == LATTICE_ACT_NONE)) return LATTICE_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || !(eps < 3.4e38f) || scale != scale) return LATTICE_ERR_INVALID_ARG;
+    if (D > kNormMaxD || N > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
+    if ((y_dtype != LATTICE_F32 && y_dtype != dtype) || (residual && r_dtype != LATTICE_F32 && r_dtype != dtype) ||
+        ((w_post || w_pre) && w_dtype != LATTICE_F32 && w_dtype != dtype))
+        return LATTICE_ERR_UNSUPPORTED;
+    if (N > 0 && !y) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(y, type_size(y_dtype)) || !aligned(gate, type_size(dtype)) || !aligned(residual, type_size(r_dtype)) ||
+        !aligned(w_post, type_size(w_dtype)) || !aligned(w_pre, type_size(w_dtype)))
+        return LATTICE_ERR_INVALID_ARG;
+    a = NormArgs{};
+    a.y = y; a.gate = gate; a.residual = residual; a.w_post = w_post; a.w_pre = w_pre;
+    a.ys = ys; a.gs = gs; a.rs = rs;
+    a.N = N; a.G = G; a.D = D; a.act = (int)act;
+    a.scale = scale; a.eps = eps; a.inv_d = 1.f / (float)D;
+    a.post = post != 0;
+    a.y32 = y_dtype == LATTICE_F32; a.r32 = r_dtype == LATTICE_F32; a.w32 = w_dtype == LATTICE_F32;
+    return LATTICE_OK;
+}
+// Whether vectors of 8 elements read these rows: 16-byte pieces of a 16-bit type.
+bool norm_rows_vec(const void* p, lattice_dtype t, long long N, int G, long long stride) {
+    return aligned(p, 16) && (N <= G || stride * (long long)type_size(t) % 16 == 0);
+}
+bool group_span(const void* p, lattice_dtype t, long long N, int G, int D, long long stride, Span* s) {
+    return strided_span(p, type_size(t), N / G, 1, (long long)G * D, stride, 0, s) || !p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -511,6 +546,107 @@ lattice_status lattice_gated_step(const float* h, float* h_out, const void* x, l
     });
 }
 
+lattice_status lattice_block_norm_fwd(const void* y, lattice_dtype y_dtype, long long y_stride, const void* gate,
+                                      long long gate_stride, const void* residual, lattice_dtype residual_dtype,
+                                      long long residual_stride, const void* w_post, const void* w_pre,
+                                      lattice_dtype w_dtype, void* r_out, void* n_out, lattice_dtype dtype, long long N,
+                                      int G, int D, lattice_act act, int post_norm, float scale, float eps, void* stream) {
+    if (!residual) residual_dtype = dtype;
+    NormArgs a;
+    lattice_status s = check_norm(a, y, y_dtype, y_stride, gate, gate_stride, residual, residual_dtype, residual_stride, w_post,
+                                  w_pre, w_dtype, dtype, N, G, D, act, post_norm, scale, eps);
+    if (s != LATTICE_OK) return s;
+    if ((N > 0 && !r_out) || (N > 0 && w_pre && !n_out) || !aligned(r_out, type_size(residual_dtype)) || !aligned(n_out, type_size(dtype)))
+        return LATTICE_ERR_INVALID_ARG;
+    if (N == 0) return LATTICE_OK;
+    const size_t n = (size_t)N * D;
+    Span sy, sg = {}, sr = {};
+    if (!group_span(y, y_dtype, N, G, D, y_stride, &sy) || !group_span(gate, dtype, N, G, D, gate_stride, &sg) ||
+        !group_span(residual, residual_dtype, N, G, D, residual_stride, &sr))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!gate) sg = Span{};
+    if (!residual) sr = Span{};
+    const size_t wb = (size_t)D * type_size(w_dtype);
+    const Span ins[] = {sy, sg, sr, span(w_post, w_post ? wb : 0), span(w_pre, w_pre ? wb : 0)};
+    const Span outs[] = {span(r_out, n * type_size(residual_dtype)), span(n_out, n_out ? n * type_size(dtype) : 0)};
+    if (clash(ins, 5, outs, 2, residual, r_out)) return LATTICE_ERR_INVALID_ARG;
+    a.r_out = r_out; a.n_out = n_out;
+    a.o32 = residual_dtype == LATTICE_F32;
+    const bool vec = D % 8 == 0 && norm_rows_vec(y, y_dtype, N, G, y_stride) && norm_rows_vec(gate, dtype, N, G, gate_stride) &&
+                     norm_rows_vec(residual, residual_dtype, N, G, residual_stride) && aligned(w_post, 16) &&
+                     aligned(w_pre, 16) && aligned(r_out, 16) && aligned(n_out, 16);
+    return launch_norm_fwd(a, dtype, vec, static_cast<cudaStream_t>(stream));
+}
+
+size_t lattice_block_norm_bwd_workspace_bytes(long long N, int D) {
+    if (N < 0 || N > 0x7fffffffLL || D < 1 || D > kNormMaxD) return 0;
+    return (size_t)norm_parts(N, D) * 2 * D * 4;
+}
+
+lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long long y_stride, const void* gate,
+                                      long long gate_stride, const void* residual, lattice_dtype residual_dtype,
+                                      long long residual_stride, const void* w_post, const void* w_pre,
+                                      lattice_dtype w_dtype, const void* dr, lattice_dtype dr_dtype, long long dr_stride,
+                                      const void* dn, long long dn_stride, void* dy, void* dgate, void* dresidual,
+                                      float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                      lattice_dtype dtype, long long N, int G, int D, lattice_act act, int post_norm,
+                                      float scale, float eps, void* stream) {
+    if (!residual) residual_dtype = dtype;
+    if (!dr) dr_dtype = residual_dtype;
+    NormArgs a;
+    lattice_status s = check_norm(a, y, y_dtype, y_stride, gate, gate_stride, residual, residual_dtype, residual_stride, w_post,
+                                  w_pre, w_dtype, dtype, N, G, D, act, post_norm, scale, eps);
+    if (s != LATTICE_OK) return s;
+    if (!type_ok(dr_dtype) || dr_stride < 0 || dn_stride < 0) return LATTICE_ERR_INVALID_ARG;
+    if (dr_dtype != LATTICE_F32 && dr_dtype != dtype) return LATTICE_ERR_UNSUPPORTED;
+    if (residual && dr && dr_dtype != residual_dtype) return LATTICE_ERR_UNSUPPORTED;
+    if (N > 0 && ((!dr && !dn) || !dy || (gate && !dgate) || (residual && !dresidual))) return LATTICE_ERR_INVALID_ARG;
+    if ((!gate && dgate) || (!residual && dresidual) || (w_pre && N > 0 && !dn) || (dw_post && !w_post) || (dw_pre && !w_pre))
+        return LATTICE_ERR_INVALID_ARG;
+    const bool dw = dw_post || dw_pre;
+    const size_t need = dw ? lattice_block_norm_bwd_workspace_bytes(N, D) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(dr, type_size(dr_dtype)) || !aligned(dn, type_size(dtype)) || !aligned(dy, type_size(y_dtype)) ||
+        !aligned(dgate, type_size(dtype)) || !aligned(dresidual, type_size(residual_dtype)) || !aligned(dw_post, 4) ||
+        !aligned(dw_pre, 4) || (need && !aligned(workspace, 16)))
+        return LATTICE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        for (float* w : {dw_post, dw_pre}) {
+            cudaError_t e = w ? cudaMemsetAsync(w, 0, (size_t)D * 4, st) : cudaSuccess;
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        return LATTICE_OK;
+    }
+    const size_t n = (size_t)N * D;
+    Span sy, sg = {}, sr = {}, sdr = {}, sdn = {};
+    if (!group_span(y, y_dtype, N, G, D, y_stride, &sy) || !group_span(gate, dtype, N, G, D, gate_stride, &sg) ||
+        !group_span(residual, residual_dtype, N, G, D, residual_stride, &sr) ||
+        !group_span(dr, dr_dtype, N, G, D, dr_stride, &sdr) || !group_span(dn, dtype, N, G, D, dn_stride, &sdn))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!gate) sg = Span{};
+    if (!residual) sr = Span{};
+    if (!dr) sdr = Span{};
+    if (!dn) sdn = Span{};
+    const size_t wb = (size_t)D * type_size(w_dtype);
+    const Span ins[] = {sy, sg, sr, sdr, sdn, span(w_post, w_post ? wb : 0), span(w_pre, w_pre ? wb : 0)};
+    const Span outs[] = {span(dy, n * type_size(y_dtype)), span(dgate, dgate ? n * type_size(dtype) : 0),
+                         span(dresidual, dresidual ? n * type_size(residual_dtype) : 0),
+                         span(dw_post, dw_post ? (size_t)D * 4 : 0), span(dw_pre, dw_pre ? (size_t)D * 4 : 0),
+                         span(workspace, need)};
+    if (clash(ins, 7, outs, 6, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
+    a.dr = dr; a.dn = dn; a.dy = dy; a.dgate = dgate; a.dresidual = dresidual;
+    a.parts = dw ? static_cast<float*>(workspace) : nullptr;
+    a.drs = dr_stride; a.dns = dn_stride;
+    a.o32 = dr_dtype == LATTICE_F32;
+    const bool vec = D % 8 == 0 && norm_rows_vec(y, y_dtype, N, G, y_stride) && norm_rows_vec(gate, dtype, N, G, gate_stride) &&
+                     norm_rows_vec(residual, residual_dtype, N, G, residual_stride) &&
+                     norm_rows_vec(dr, dr_dtype, N, G, dr_stride) && norm_rows_vec(dn, dtype, N, G, dn_stride) &&
+                     aligned(w_post, 16) && aligned(w_pre, 16) && aligned(dy, 16) && aligned(dgate, 16) &&
+                     aligned(dresidual, 16);
+    return launch_norm_bwd(a, dtype, vec, dw_post, dw_pre, st);
+}
+
 lattice_status lattice_selftest_bounded_wait(unsigned long long limit_ns, void* stream) {
     if (limit_ns < 1 || limit_ns > 1000000000ull) return LATTICE_ERR_INVALID_ARG;
     bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns);
@@ -524,7 +660,7 @@ lattice_status lattice_get_device_status(void* stream) {
     // every translation unit's copy of the status word (each unit is a module of its own)
     cudaError_t (*const units[])(unsigned int*) = {read_clear_module_status, status_simt_exact,
                                                    status_simt_chunked, status_step, status_bwd, status_tc,
-                                                   status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
+                                                   status_norm, status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
                                                    status_gated_bwd_f32, status_gated_bwd_bf16, status_gated_bwd_f16};
     unsigned int any = 0;
     for (auto unit : units) {

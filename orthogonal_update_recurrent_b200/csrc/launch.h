@@ -48,12 +48,19 @@ template <class XT> lattice_status launch_step(const GatedArgs& a, int form, boo
 template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, cudaStream_t st);
 }  // namespace gated
 
+// tu_norm.cu: norms after and before a block (tpr set by the launch). vec: rows and weights
+// can be read in aligned vectors of 8 elements
+lattice_status launch_norm_fwd(NormArgs a, lattice_dtype dtype, bool vec, cudaStream_t st);
+lattice_status launch_norm_bwd(NormArgs a, lattice_dtype dtype, bool vec, float* dw_post, float* dw_pre, cudaStream_t st);
+int norm_parts(long long N, int D);  // rows of the backward pass's workspace
+
 // each unit's device status word (read, and zeroed when set)
 cudaError_t status_simt_exact(unsigned int* v);
 cudaError_t status_simt_chunked(unsigned int* v);
 cudaError_t status_step(unsigned int* v);
 cudaError_t status_bwd(unsigned int* v);
 cudaError_t status_tc(unsigned int* v);
+cudaError_t status_norm(unsigned int* v);
 cudaError_t status_gated_fwd_f32(unsigned int* v);
 cudaError_t status_gated_fwd_bf16(unsigned int* v);
 cudaError_t status_gated_fwd_f16(unsigned int* v);
