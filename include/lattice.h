@@ -349,7 +349,7 @@ lattice_status lattice_gated_step(const float *h, float *h_out, const void *x,
  * formed from r before its rounding.
  * Rows: N rows of D contiguous elements, 1 <= D <= 16384, 0 <= N < 2^31. Inputs come in
  * groups of G rows (N a multiple of G), contiguous within a group, with the given stride
- * in elements (>= 0) between groups: G = 1 for rows of any stride, G = H for heads
+ * in elements (0 to 2^31 - 1) between groups: G = 1 for rows of any stride, G = H for heads
  * [B*T][H][D] cut out of wider tokens. Outputs are contiguous.
  * act: applied to the gate; NONE: the gate is not allowed. eps > 0. */
 typedef enum { LATTICE_ACT_NONE = 0, LATTICE_ACT_SIGMOID = 1, LATTICE_ACT_SILU = 2, LATTICE_ACT_GELU = 3 } lattice_act;

@@ -21,7 +21,8 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-warn-spills"]
 LINK_FLAGS = [*ARCH, "-shared", "-cudart", "static"]
 # the C ABI and one unit per kernel family (csrc/launch.h joins them)
-UNITS = ["lattice_abi.cu", "tu_simt_exact.cu", "tu_simt_chunked.cu", "tu_step.cu", "tu_bwd.cu", "tu_tc.cu", "tu_norm.cu",
+UNITS = ["lattice_abi.cu", "tu_simt_exact.cu", "tu_simt_chunked.cu", "tu_step.cu", "tu_bwd.cu", "tu_tc.cu",
+         "tu_norm_f32.cu", "tu_norm_bf16.cu", "tu_norm_f16.cu",
          "tu_gated_fwd_f32.cu", "tu_gated_fwd_bf16.cu", "tu_gated_fwd_f16.cu",
          "tu_gated_bwd_f32.cu", "tu_gated_bwd_bf16.cu", "tu_gated_bwd_f16.cu"]
 OBJDIR = os.path.join(HERE, "_build")

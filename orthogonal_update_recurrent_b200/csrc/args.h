@@ -118,6 +118,7 @@ struct GatedArgs {
 
 // block_norm.cuh: norms after and before a block
 constexpr int kNormMaxD = 16384;
+constexpr long long kNormMaxStride = 0x7fffffff;
 
 struct NormArgs {
     const void* y; const void* gate; const void* residual;  // the last two may be null
@@ -126,13 +127,13 @@ struct NormArgs {
     const void* dr; const void* dn;                         // backward: one may be null (=> 0)
     void* dy; void* dgate; void* dresidual;                 // backward: the last two may be null
     float* parts;                                           // backward: weight gradients' sums per CTA, or null
-    long long ys, gs, rs, drs, dns;                         // between groups of G rows, in elements
+    unsigned ys, gs, rs, drs, dns;                          // between groups of G rows, in elements
     long long N;
-    int G, D, tpr;                                          // tpr: threads per row
+    int G, D, tpr, K;                                       // threads per row and CTA, CTAs per row
     int act;
     float scale, eps, inv_d;
     bool post;
-    bool y32, r32, o32, w32;                                // fp32, else the call's type: y, residual, r (dr), weights
+    bool y32, r32, w32;                                     // fp32, else the call's type: y; residual, r and dr; weights
 };
 
 }  // namespace lattice

@@ -13,10 +13,13 @@
 //   dw_post = sum over rows of dv u act(gate),  dw_pre = sum over rows of dn r rho2
 //
 // HBM bounds both: every input is read once and every output written once, a row's values
-// stay in registers between its reductions, and what is left is to keep enough rows in
-// flight. A row of up to 256 elements takes a part of a warp (8 elements per thread) and its
-// sums are shuffles; a longer one takes a CTA. CTAs stay and take rows by turns, so each
-// thread keeps its columns' weights, and their gradients' sums, in registers.
+// stay in registers between its sums, and what is left is to keep enough bytes in flight.
+// A thread has 8 elements of a row. A row of up to 256 elements takes a part of a warp and
+// its sums are shuffles, one of up to 8192 (backward, with twice the registers: 4096) a
+// CTA, a longer one a cluster of 2 or 4 CTAs.
+// CTAs stay and take rows by turns: each loads its next row before it works on the one it
+// has, and its threads keep their columns' weights, and the sums of the weights' gradients,
+// in shared memory.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,6 +29,8 @@
 #include <type_traits>
 
 #include "args.h"
+#include "f32x2.cuh"
+#include "waits.cuh"
 
 namespace lattice {
 namespace norm {
@@ -108,330 +113,505 @@ __device__ __forceinline__ void store(void* p, bool f32, long long i, const floa
     }
 }
 
-// The gate's activation and, if wanted, its derivative. The normal distribution function of
-// gelu is formula 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 7.5e-8 here),
-// whose exponential the derivative needs too.
+// The gates' activations and, if wanted, their derivatives. The normal distribution function
+// of gelu is formula 7.1.26 of Abramowitz and Stegun's Handbook (absolute error 7.5e-8
+// here), whose exponential the derivative needs too.
 template <bool SLOPE>
-__device__ __forceinline__ void activate(int act, float g, float& f, float& df) {
+__device__ __forceinline__ void activate(int act, F2 g, F2& f, F2& df) {
     if (act == kGelu) {
-        const float x = fabsf(g) * 0.70710678f;
-        const float e = exp2f(-0.72134752f * g * g);  // exp(-g^2/2)
-        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-        float p = 1.061405429f;
-        p = fmaf(p, t, -1.453152027f);
-        p = fmaf(p, t, 1.421413741f);
-        p = fmaf(p, t, -0.284496736f);
-        p = fmaf(p, t, 0.254829592f);
-        const float tail = 0.5f * p * t * e;
-        const float cdf = g >= 0.f ? 1.f - tail : tail;
-        f = g * cdf;
-        if constexpr (SLOPE) df = fmaf(g * 0.39894228f, e, cdf);
+        const F2 x = each(g, [](float v) { return fabsf(v); });
+        const F2 e = each(mul2(mul2(g, g), f2(-0.72134752f)), ex2);  // exp(-g^2/2)
+        const F2 t = each(fma2(x, f2(0.3275911f * 0.70710678f), f2(1.f)), rcp);
+        F2 p = f2(1.061405429f * 0.5f);
+        p = fma2(p, t, f2(-1.453152027f * 0.5f));
+        p = fma2(p, t, f2(1.421413741f * 0.5f));
+        p = fma2(p, t, f2(-0.284496736f * 0.5f));
+        p = fma2(p, t, f2(0.254829592f * 0.5f));
+        const F2 tail = mul2(mul2(p, t), e), head = fma2(tail, f2(-1.f), f2(1.f));
+        float g0, g1, t0, t1, h0, h1;
+        parts(g, g0, g1), parts(tail, t0, t1), parts(head, h0, h1);
+        const F2 cdf = f2(g0 >= 0.f ? h0 : t0, g1 >= 0.f ? h1 : t1);
+        f = mul2(g, cdf);
+        if constexpr (SLOPE) df = fma2(mul2(g, f2(0.39894228f)), e, cdf);
     } else {
-        const float s = __fdividef(1.f, 1.f + __expf(-g));
-        f = act == kSilu ? g * s : s;
-        if constexpr (SLOPE) df = act == kSilu ? s * fmaf(g, 1.f - s, 1.f) : s * (1.f - s);
+        const F2 s = each(each(mul2(g, f2(-1.442695041f)), [](float n) { return 1.f + ex2(n); }), rcp);
+        f = act == kSilu ? mul2(g, s) : s;
+        if constexpr (SLOPE) {
+            const F2 q = fma2(s, f2(-1.f), f2(1.f));
+            df = act == kSilu ? mul2(s, fma2(g, q, f2(1.f))) : mul2(s, q);
+        }
     }
 }
 
-// Sums of M values over the threads of a row: `tpr` lanes of a warp, or the CTA (red: two
-// buffers by turns, so that one barrier per sum is enough).
-template <bool CTA, int M>
-__device__ __forceinline__ void row_sum(float* v, int tpr, float (*red)[32][M], int turn) {
+// A row's threads: tpr lanes of a warp (SUB), or a CTA, or the CTAs of a cluster.
+// Sums over them: shuffles, one barrier per sum in a CTA (buffers by turns), and in a
+// cluster an asynchronous store of the CTA's sum to every CTA, counted on its mbarrier.
+template <bool SUB>
+struct RowSums {
+    float* red;               // [2][256]
+    float4* box;              // [2][4][2]: the CTAs' sums
+    uint32_t bars;
+    volatile uint32_t* abort;
+    int K, rank, tpr, k;      // k: sums so far
+    __device__ __forceinline__ RowSums(const NormArgs& A) : K(SUB ? 1 : A.K), rank(SUB ? 0 : blockIdx.x % A.K), tpr(A.tpr), k(0) {
+        __shared__ float red_[2 * 256];
+        __shared__ float4 box_[2 * 8];
+        __shared__ __align__(8) uint64_t bars_[2];
+        __shared__ uint32_t abort_;
+        red = red_, box = box_, bars = ptx::smem_u32(bars_), abort = &abort_;
+        if (K > 1) {
+            if (threadIdx.x == 0) {
+                ptx::mbar_init(bars, 1);
+                ptx::mbar_init(bars + 8, 1);
+                abort_ = 0u;
+                ptx::fence_mbar_init();
+            }
+            sync_cluster();  // nobody sends before every CTA's mbarriers stand
+        }
+    }
+    static __device__ __forceinline__ void sync_cluster() {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    __device__ __forceinline__ void end() const {  // nobody leaves while something may be on its way to it
+        if (K > 1) sync_cluster();
+    }
+    // Sums of M <= 8 values over the row's threads, in every thread. More than two values:
+    // a lane hands half of them on at each of the first steps (8 values in 9 shuffles
+    // instead of 40) and ends with one value's sum over its warp.
+    template <int M>
+    __device__ __forceinline__ void sum(float* v) {
+        constexpr unsigned ALL = 0xffffffffu;
+        const int lane = threadIdx.x & 31;
+        if constexpr (M <= 2) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        if (CTA || o < tpr)
+            for (int o = 16; o > 0; o >>= 1)
+                if (!SUB || o < tpr)
 #pragma unroll
-            for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
-    if constexpr (CTA) {
-        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-        if ((threadIdx.x & 31) == 0)
+                    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(ALL, v[m], o);
+            if constexpr (SUB) return;
+        } else if (SUB && tpr < 8) {
+            for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
-            for (int m = 0; m < M; ++m) red[turn][warp][m] = v[m];
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(ALL, v[m], o);
+            return;
+        }
+        float own = 0.f;  // M > 2: the lane's value
+        int mine = 0;     // and which
+        if constexpr (M > 2) {
+            float t[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) t[m] = m < M ? v[m] : 0.f;
+            int o = SUB ? tpr >> 1 : 16;
+            const int o1 = o;
+#pragma unroll
+            for (int n = 4; n > 0; n >>= 1, o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int m = 0; m < n; ++m) {
+                    const float keep = up ? t[m + n] : t[m], give = up ? t[m] : t[m + n];
+                    t[m] = keep + __shfl_xor_sync(ALL, give, o);
+                }
+                mine += up ? n : 0;
+            }
+            own = t[0];
+#pragma unroll
+            for (int k_ = 0; k_ < 2; ++k_, o >>= 1)
+                if (o > 0) own += __shfl_xor_sync(ALL, own, o);
+            if constexpr (SUB) {  // value m stands with the lane whose bits below tpr spell it
+                const int base = lane & ~(tpr - 1);
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    v[m] = __shfl_sync(ALL, own, base + (m & 4 ? o1 : 0) + (m & 2 ? o1 >> 1 : 0) + (m & 1 ? o1 >> 2 : 0));
+                return;
+            }
+        }
+        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5, buf = k & 1;
+        float* r = red + buf * 256;  // [warp][8], M <= 2: [m][warp]
+        if constexpr (M <= 2) {
+            if (lane == 0)
+#pragma unroll
+                for (int m = 0; m < M; ++m) r[m * 32 + warp] = v[m];
+        } else if ((lane & 3) == 0) {
+            r[warp * 8 + mine] = own;
+        }
         __syncthreads();
+        if constexpr (M <= 2) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) v[m] = 0.f;
-        for (int w = 0; w < nw; ++w)
+            for (int m = 0; m < M; ++m) v[m] = lane < nw ? r[m * 32 + lane] : 0.f;
 #pragma unroll
-            for (int m = 0; m < M; ++m) v[m] += red[turn][w][m];
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(ALL, v[m], o);
+        } else {
+            own = 0.f;  // lane: value lane % 8 of every fourth warp
+            for (int w = lane >> 3; w < nw; w += 4) own += r[w * 8 + (lane & 7)];
+            own += __shfl_xor_sync(ALL, own, 8);
+            own += __shfl_xor_sync(ALL, own, 16);
+            if (K == 1)
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] = __shfl_sync(ALL, own, m);
+        }
+        if (K > 1) {
+            float4* b = box + buf * 8;  // [rank][2]
+            if constexpr (M <= 2) {
+                if ((int)threadIdx.x < K)
+                    ptx::st_async_v4(ptx::mapa(ptx::smem_u32(b + rank * 2), threadIdx.x),
+                                     make_float4(v[0], M > 1 ? v[M - 1] : 0.f, 0.f, 0.f), ptx::mapa(bars + 8 * buf, threadIdx.x));
+            } else if (warp == 0) {
+                float4 a;
+                const int q = lane & 4;  // lane 0..K-1: values 0-3 to CTA lane; 4 + 0..K-1: values 4-7
+                a.x = __shfl_sync(ALL, own, q), a.y = __shfl_sync(ALL, own, q + 1);
+                a.z = __shfl_sync(ALL, own, q + 2), a.w = __shfl_sync(ALL, own, q + 3);
+                if (lane < 8 && (lane & 3) < K)
+                    ptx::st_async_v4(ptx::mapa(ptx::smem_u32(b + rank * 2 + (lane >> 2)), lane & 3), a,
+                                     ptx::mapa(bars + 8 * buf, lane & 3));
+            }
+            if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bars + 8 * buf, K * (M <= 2 ? 16 : 32));
+            tc_wait(bars + 8 * buf, (k >> 1) & 1, abort);
+#pragma unroll
+            for (int m = 0; m < M; ++m) v[m] = 0.f;
+            for (int q = 0; q < K; ++q) {
+                const float4 a = b[q * 2], d = b[q * 2 + 1];
+                const float t[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += t[m];
+            }
+        }
+        ++k;
+    }
+};
+
+// A thread's columns: 8, next to each other (V = 8) or tpr apart (V = 1).
+template <int V>
+struct Columns {
+    static constexpr int NV = 8 / V;
+    int first, step, D;
+    __device__ __forceinline__ Columns(const NormArgs& A, int rank, int tid)
+        : first(rank * A.tpr * 8 + tid * V), step(A.tpr), D(A.D) {}
+    __device__ __forceinline__ int at(int j) const { return first + j * step; }
+    __device__ __forceinline__ bool has(int j) const { return at(j) < D; }
+};
+template <class XT, int V>
+__device__ __forceinline__ void load8(Raw<XT, V>* r, const void* p, bool f32, long long row, const Columns<V>& c) {
+#pragma unroll
+    for (int j = 0; j < Columns<V>::NV; ++j)
+        if (c.has(j)) r[j] = load<XT, V>(p, f32, row + c.at(j));
+}
+// The 8 values as four pairs.
+template <class XT, int V>
+__device__ __forceinline__ void values8(const Raw<XT, V>* r, bool f32, F2* f) {
+    if (sizeof(XT) == 4 || f32) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            f[v] = f2(__uint_as_float(r[2 * v / V].w[2 * v % V]), __uint_as_float(r[(2 * v + 1) / V].w[(2 * v + 1) % V]));
+    } else if constexpr (sizeof(XT) == 2) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            float a, b, other;
+            if constexpr (V == 8) {
+                unpack(XT(), r[0].w[v], a, b);
+            } else {
+                unpack(XT(), r[2 * v].w[0], a, other);
+                unpack(XT(), r[2 * v + 1].w[0], b, other);
+            }
+            f[v] = f2(a, b);
+        }
     }
 }
-
+template <class XT, int V>
+__device__ __forceinline__ void store8(void* p, bool f32, long long row, const Columns<V>& c, const F2* q) {
+    float f[8];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) parts(q[v], f[2 * v], f[2 * v + 1]);
+#pragma unroll
+    for (int j = 0; j < Columns<V>::NV; ++j)
+        if (c.has(j)) store<XT, V>(p, f32, row + c.at(j), f + j * V);
+}
+template <class XT, int V>
+__device__ __forceinline__ void clear8(Raw<XT, V>* r) {
+#pragma unroll
+    for (int j = 0; j < 8 / V; ++j) r[j] = Raw<XT, V>{};
+}
+__device__ __forceinline__ float both(F2 a) {
+    float x, y;
+    parts(a, x, y);
+    return x + y;
+}
+// Sum of the products of 8 values.
+__device__ __forceinline__ float dot8(const F2* a, const F2* b) {
+    F2 t = mul2(a[0], b[0]);
+#pragma unroll
+    for (int v = 1; v < 4; ++v) t = fma2(a[v], b[v], t);
+    return both(t);
+}
+// 8 floats of the thread's own in shared memory, [2][threads] of 16 bytes
+__device__ __forceinline__ void own_read(const ulonglong2* p, F2* f) {
+    const ulonglong2 a = p[threadIdx.x], b = p[blockDim.x + threadIdx.x];
+    f[0].v = a.x, f[1].v = a.y, f[2].v = b.x, f[3].v = b.y;
+}
+__device__ __forceinline__ void own_write(ulonglong2* p, const F2* f) {
+    p[threadIdx.x] = make_ulonglong2(f[0].v, f[1].v);
+    p[blockDim.x + threadIdx.x] = make_ulonglong2(f[2].v, f[3].v);
+}
+// The columns' weights into the thread's shared memory: w_post with the scale, w_pre. Columns
+// past the row's end have weight 0, and their values stay 0 all the way.
+template <class XT, int V>
+__device__ __forceinline__ void keep_weights(const NormArgs& A, const Columns<V>& c, ulonglong2* wq, ulonglong2* wp) {
+    Raw<XT, V> raw[8 / V] = {};
+    F2 f[4];
+    for (int k = 0; k < 2; ++k) {
+        const void* w = k ? A.w_pre : A.w_post;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) f[v] = f2(1.f);
+        if (w) {
+            load8<XT, V>(raw, w, A.w32, 0, c);
+            values8<XT, V>(raw, A.w32, f);
+        }
+        if (!k)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) f[v] = mul2(f[v], f2(A.scale));
+        own_write(k ? wp : wq, f);
+    }
+}
 // Where row i of a strided array starts: groups of A.G rows, contiguous within a group.
-__device__ __forceinline__ long long row_start(const NormArgs& A, long long stride, unsigned i, unsigned grp) {
-    return (long long)grp * stride + (long long)(i - grp * A.G) * A.D;
-}
+struct RowAt {
+    unsigned grp, off;
+    __device__ __forceinline__ RowAt(const NormArgs& A, unsigned i) : grp(A.G == 1 ? i : i / A.G), off(0) {
+        off = A.G == 1 ? 0u : i - grp * A.G;
+    }
+    __device__ __forceinline__ long long in(const NormArgs& A, unsigned stride) const {
+        return (long long)((unsigned long long)grp * stride + (unsigned long long)off * (unsigned)A.D);
+    }
+};
 
-template <class XT, bool CTA, int V, int NV>
-__global__ void __launch_bounds__(CTA ? 1024 : 256) norm_fwd_kernel(const NormArgs A) {
-    __shared__ float red1[2][32][1], red2[2][32][1];
-    const int tpr = A.tpr, tid = CTA ? threadIdx.x : threadIdx.x % tpr;
-    const int rows = CTA ? 1 : blockDim.x / tpr;  // per CTA and turn
-    const int D = A.D;
-    float wq[NV][V], wp[NV][V];  // the columns' weights
-    bool on[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + tid) * V;
-        on[j] = c < D;
-#pragma unroll
-        for (int v = 0; v < V; ++v) wq[j][v] = A.scale, wp[j][v] = 1.f;
-        if (on[j] && A.w_post) {
-            values<XT, V>(load<XT, V>(A.w_post, A.w32, c), A.w32, wq[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) wq[j][v] *= A.scale;
-        }
-        if (on[j] && A.w_pre) values<XT, V>(load<XT, V>(A.w_pre, A.w32, c), A.w32, wp[j]);
-    }
-    int turn = 0;
-    for (long long first = (long long)blockIdx.x * rows; first < A.N; first += (long long)gridDim.x * rows, turn ^= 1) {
-        const long long i = first + (CTA ? 0 : threadIdx.x / tpr);
-        const bool in = i < A.N;
-        const unsigned grp = A.G == 1 ? (unsigned)i : (unsigned)i / A.G;
-        const long long oy = row_start(A, A.ys, (unsigned)i, grp), og = row_start(A, A.gs, (unsigned)i, grp),
-                        os = row_start(A, A.rs, (unsigned)i, grp), oo = i * D;
-        Raw<XT, V> ry[NV], rg[NV], rr[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * tpr + tid) * V;
-            if (in && on[j]) {
-                ry[j] = load<XT, V>(A.y, A.y32, oy + c);
-                if (A.gate) rg[j] = load<XT, V>(A.gate, false, og + c);
-                if (A.residual) rr[j] = load<XT, V>(A.residual, A.r32, os + c);
-            }
-        }
-        float r[NV][V], s1[1] = {0.f}, s2[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            values<XT, V>(ry[j], A.y32, r[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (!(in && on[j])) r[j][v] = 0.f;
-                s1[0] = fmaf(r[j][v], r[j][v], s1[0]);
-            }
-        }
-        float rho1 = 1.f;
-        if (A.post) {
-            row_sum<CTA, 1>(s1, tpr, red1, turn);
-            rho1 = rsqrtf(fmaf(s1[0], A.inv_d, A.eps));
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!(in && on[j])) continue;
-            float g[V], res[V];
-            if (A.gate) values<XT, V>(rg[j], false, g);
-            if (A.residual) values<XT, V>(rr[j], A.r32, res);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float t = r[j][v] * rho1 * wq[j][v];
-                if (A.gate) {
-                    float f, df;
-                    activate<false>(A.act, g[v], f, df);
-                    t *= f;
-                }
-                r[j][v] = A.residual ? res[v] + t : t;
-                s2[0] = fmaf(r[j][v], r[j][v], s2[0]);
-            }
-            store<XT, V>(A.r_out, A.o32, oo + (j * tpr + tid) * V, r[j]);
-        }
-        if (A.n_out) {
-            row_sum<CTA, 1>(s2, tpr, red2, turn);
-            const float rho2 = rsqrtf(fmaf(s2[0], A.inv_d, A.eps));
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (!(in && on[j])) continue;
-#pragma unroll
-                for (int v = 0; v < V; ++v) r[j][v] = r[j][v] * rho2 * wp[j][v];
-                store<XT, V>(A.n_out, false, oo + (j * tpr + tid) * V, r[j]);
-            }
-        }
-    }
-}
+// Types of a call beside its own XT, and its parts: Y32, R32: y, and residual, r and dr, are
+// fp32; each 0, 1, or -1 where the kernel reads the call's flags (rows without vectors, whose
+// every combination would be a kernel else). PRE: with the norm before the next block.
+template <class XT_, int V_, bool GATE_, int Y32_, int R32_, int PRE_>
+struct Form {
+    using XT = XT_;
+    static constexpr int V = V_;
+    static constexpr bool GATE = GATE_;
+    static __device__ __forceinline__ bool y32(const NormArgs& A) { return Y32_ < 0 ? A.y32 : Y32_ == 1; }
+    static __device__ __forceinline__ bool r32(const NormArgs& A) { return R32_ < 0 ? A.r32 : R32_ == 1; }
+    static __device__ __forceinline__ bool pre(bool runtime) { return PRE_ < 0 ? runtime : PRE_ == 1; }
+};
 
-template <class XT, bool CTA, int V, int NV>
-__global__ void __launch_bounds__(CTA && NV * V > 8 ? 512 : 256) norm_bwd_kernel(const NormArgs A) {
-    __shared__ float red1[2][32][1], red2[2][32][2], red3[2][32][1];
-    const int tpr = A.tpr, tid = CTA ? threadIdx.x : threadIdx.x % tpr;
-    const int rows = CTA ? 1 : blockDim.x / tpr;
-    const int D = A.D;
-    const bool pre = A.dn != nullptr;
-    float wq[NV][V], wp[NV][V], dq[NV][V], dp[NV][V];  // weights (w_post with the scale) and their gradients
-    bool on[NV];
+template <class F, bool SUB>
+__global__ void __launch_bounds__(SUB ? 256 : 1024, SUB ? 4 : 1) norm_fwd_kernel(const NormArgs A) {
+    using XT = typename F::XT;
+    constexpr int V = F::V, NV = 8 / V;
+    constexpr bool GATE = F::GATE;
+    const bool y32 = F::y32(A), r32 = F::r32(A), pre = F::pre(A.n_out != nullptr);
+    extern __shared__ __align__(16) ulonglong2 own[];
+    ulonglong2 *wq = own, *wp = own + 2 * blockDim.x;
+    RowSums<SUB> sums(A);
+    const int tid = SUB ? threadIdx.x % A.tpr : threadIdx.x;
+    const unsigned rows = SUB ? blockDim.x / A.tpr : 1, lane_row = SUB ? threadIdx.x / A.tpr : 0;
+    const Columns<V> c(A, sums.rank, tid);
+    keep_weights<XT, V>(A, c, wq, wp);
+    const unsigned N = (unsigned)A.N, step = gridDim.x / sums.K * rows;
+    Raw<XT, V> ry[NV] = {}, rg[NV] = {}, rr[NV] = {};
+    auto fetch = [&](unsigned i) {
+        if (i >= N) return;
+        const RowAt at(A, i);
+        load8<XT, V>(ry, A.y, y32, at.in(A, A.ys), c);
+        if constexpr (GATE) load8<XT, V>(rg, A.gate, false, at.in(A, A.gs), c);
+        if (A.residual) load8<XT, V>(rr, A.residual, r32, at.in(A, A.rs), c);
+    };
+    unsigned first = blockIdx.x / sums.K * rows;
+    fetch(first + lane_row);
+    for (; first < N; first += step) {  // N + step + rows < 2^32
+        const unsigned i = first + lane_row;
+        const bool in = i < N;
+        F2 y[4], r[4], g[4], w[4];
+        values8<XT, V>(ry, y32, y);
+        if constexpr (GATE) values8<XT, V>(rg, false, g);
+        if (A.residual) {
+            values8<XT, V>(rr, r32, r);
+        } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + tid) * V;
-        on[j] = c < D;
-#pragma unroll
-        for (int v = 0; v < V; ++v) wq[j][v] = A.scale, wp[j][v] = 1.f, dq[j][v] = dp[j][v] = 0.f;
-        if (on[j] && A.w_post) {
-            values<XT, V>(load<XT, V>(A.w_post, A.w32, c), A.w32, wq[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) wq[j][v] *= A.scale;
+            for (int v = 0; v < 4; ++v) r[v] = f2(0.f);
         }
-        if (on[j] && A.w_pre) values<XT, V>(load<XT, V>(A.w_pre, A.w32, c), A.w32, wp[j]);
-    }
-    int turn = 0;
-    for (long long first = (long long)blockIdx.x * rows; first < A.N; first += (long long)gridDim.x * rows, turn ^= 1) {
-        const long long i = first + (CTA ? 0 : threadIdx.x / tpr);
-        const bool in = i < A.N;
-        const unsigned grp = A.G == 1 ? (unsigned)i : (unsigned)i / A.G;
-        const long long oy = row_start(A, A.ys, (unsigned)i, grp), og = row_start(A, A.gs, (unsigned)i, grp),
-                        os = row_start(A, A.rs, (unsigned)i, grp), od = row_start(A, A.drs, (unsigned)i, grp),
-                        on_ = row_start(A, A.dns, (unsigned)i, grp), oo = i * D;
-        Raw<XT, V> ry[NV], rg[NV], rr[NV], rd[NV], rn[NV];
+        fetch(i + step);  // the next row's values are on their way during this row's sums
+        own_read(wq, w);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * tpr + tid) * V;
-            if (in && on[j]) {
-                ry[j] = load<XT, V>(A.y, A.y32, oy + c);
-                if (A.gate) rg[j] = load<XT, V>(A.gate, false, og + c);
-                if (A.residual && pre) rr[j] = load<XT, V>(A.residual, A.r32, os + c);
-                if (pre) rn[j] = load<XT, V>(A.dn, false, on_ + c);
-                if (A.dr) rd[j] = load<XT, V>(A.dr, A.o32, od + c);
+        for (int v = 0; v < 4; ++v)
+            if constexpr (GATE) {
+                F2 f, df;
+                activate<false>(A.act, g[v], f, df);
+                w[v] = mul2(w[v], f);
             }
-        }
-        float y[NV][V], e[NV][V], s1[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            values<XT, V>(ry[j], A.y32, y[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (!(in && on[j])) y[j][v] = 0.f;
-                s1[0] = fmaf(y[j][v], y[j][v], s1[0]);
-            }
-        }
-        float rho1 = 1.f;
+        float s[1], rho = 1.f;
         if (A.post) {
-            row_sum<CTA, 1>(s1, tpr, red1, turn);
-            rho1 = rsqrtf(fmaf(s1[0], A.inv_d, A.eps));
+            s[0] = dot8(y, y);
+            sums.template sum<1>(s);
+            rho = rsqrtf(fmaf(s[0], A.inv_d, A.eps));
         }
-        float f[NV][V], df[NV][V];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float g[V];
-            if (A.gate) values<XT, V>(rg[j], false, g);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                f[j][v] = 1.f, df[j][v] = 0.f;
-                if (A.gate) activate<true>(A.act, g[v], f[j][v], df[j][v]);
-            }
-            if (A.dr) values<XT, V>(rd[j], A.o32, e[j]);
-            else
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[j][v] = 0.f;
-        }
+        for (int v = 0; v < 4; ++v) r[v] = fma2(mul2(y[v], f2(rho)), w[v], r[v]);
+        if (in) store8<XT, V>(A.r_out, r32, (long long)i * A.D, c, r);
         if (pre) {
-            float r[NV][V], dn[NV][V], s2[2] = {0.f, 0.f};
+            s[0] = dot8(r, r);
+            own_read(wp, w);
+            sums.template sum<1>(s);
+            rho = rsqrtf(fmaf(s[0], A.inv_d, A.eps));
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float res[V];
-                if (A.residual) values<XT, V>(rr[j], A.r32, res);
-                values<XT, V>(rn[j], false, dn[j]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float t = y[j][v] * rho1 * wq[j][v] * f[j][v];
-                    r[j][v] = A.residual ? res[v] + t : t;
-                    if (!(in && on[j])) r[j][v] = dn[j][v] = 0.f;
-                    s2[0] = fmaf(r[j][v], r[j][v], s2[0]);
-                    s2[1] = fmaf(r[j][v], dn[j][v] * wp[j][v], s2[1]);
-                }
-            }
-            row_sum<CTA, 2>(s2, tpr, red2, turn);
-            const float rho2 = rsqrtf(fmaf(s2[0], A.inv_d, A.eps));
-            const float k = rho2 * rho2 * rho2 * s2[1] * A.inv_d;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    dp[j][v] = fmaf(dn[j][v], r[j][v] * rho2, dp[j][v]);
-                    e[j][v] += rho2 * wp[j][v] * dn[j][v] - k * r[j][v];
-                }
-        }
-        // e: d residual, then du without rho1
-        float s3[1] = {0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const long long o = oo + (j * tpr + tid) * V;
-            if (!(in && on[j])) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[j][v] = 0.f;
-                continue;
-            }
-            if (A.dresidual) store<XT, V>(A.dresidual, A.r32, o, e[j]);
-            float dg[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float u = y[j][v] * rho1, t = e[j][v] * u;
-                dg[v] = t * wq[j][v] * df[j][v];
-                dq[j][v] = fmaf(t, f[j][v], dq[j][v]);
-                e[j][v] *= wq[j][v] * f[j][v];
-                s3[0] = fmaf(e[j][v], y[j][v], s3[0]);
-            }
-            if (A.dgate) store<XT, V>(A.dgate, false, o, dg);
-        }
-        float k = 0.f;
-        if (A.post) {
-            row_sum<CTA, 1>(s3, tpr, red3, turn);
-            k = rho1 * rho1 * rho1 * s3[0] * A.inv_d;
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!(in && on[j])) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) e[j][v] = e[j][v] * rho1 - k * y[j][v];
-            store<XT, V>(A.dy, A.y32, oo + (j * tpr + tid) * V, e[j]);
+            for (int v = 0; v < 4; ++v) r[v] = mul2(mul2(r[v], f2(rho)), w[v]);
+            if (in) store8<XT, V>(A.n_out, false, (long long)i * A.D, c, r);
         }
     }
+    sums.end();
+}
+
+// With t = scale y w_post act(gate), v = rho1 t, m = w_pre dn and e as above, the sum for dy
+//   sum(du y) = sum(e t) = sum(dr t) + rho2 sum(m t) - k sum(r t), k = rho2^3 mean(m r),
+// is taken apart, so that it needs no exchange of its own after e is known.
+template <class F, bool SUB>
+__global__ void __launch_bounds__(SUB ? 256 : 512, SUB ? 2 : 1) norm_bwd_kernel(const NormArgs A) {
+    using XT = typename F::XT;
+    constexpr int V = F::V, NV = 8 / V;
+    constexpr bool GATE = F::GATE;
+    const bool y32 = F::y32(A), r32 = F::r32(A), pre = F::pre(A.dn != nullptr);
+    extern __shared__ __align__(16) ulonglong2 own[];
+    ulonglong2 *wq = own, *wp = own + 2 * blockDim.x, *dq = own + 4 * blockDim.x, *dp = own + 6 * blockDim.x;
+    RowSums<SUB> sums(A);
+    const int tid = SUB ? threadIdx.x % A.tpr : threadIdx.x;
+    const unsigned rows = SUB ? blockDim.x / A.tpr : 1, lane_row = SUB ? threadIdx.x / A.tpr : 0;
+    const Columns<V> c(A, sums.rank, tid);
+    keep_weights<XT, V>(A, c, wq, wp);
+    {
+        const F2 zero[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+        own_write(dq, zero);
+        own_write(dp, zero);
+    }
+    const unsigned N = (unsigned)A.N, step = gridDim.x / sums.K * rows;
+    Raw<XT, V> ry[NV] = {}, rg[NV] = {}, rr[NV] = {}, rd[NV] = {}, rn[NV] = {};
+    auto fetch = [&](unsigned i) {
+        if (i >= N) {  // rows past the last (a CTA's rows side by side) count as 0
+            if constexpr (SUB) clear8(ry), clear8(rr), clear8(rd), clear8(rn);
+            return;
+        }
+        const RowAt at(A, i);
+        load8<XT, V>(ry, A.y, y32, at.in(A, A.ys), c);
+        if constexpr (GATE) load8<XT, V>(rg, A.gate, false, at.in(A, A.gs), c);
+        if (A.dr) load8<XT, V>(rd, A.dr, r32, at.in(A, A.drs), c);
+        if (pre) {
+            if (A.residual) load8<XT, V>(rr, A.residual, r32, at.in(A, A.rs), c);
+            load8<XT, V>(rn, A.dn, false, at.in(A, A.dns), c);
+        }
+    };
+    unsigned first = blockIdx.x / sums.K * rows;
+    fetch(first + lane_row);
+    for (; first < N; first += step) {
+        const unsigned i = first + lane_row;
+        const bool in = i < N;
+        const long long o = (long long)i * A.D;
+        F2 y[4], e[4], r[4], m[4], f[4], df[4], t[4], w[4], acc[4];
+        values8<XT, V>(ry, y32, y);
+        if constexpr (GATE) values8<XT, V>(rg, false, f);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) e[v] = r[v] = f2(0.f);
+        if (A.dr) values8<XT, V>(rd, r32, e);
+        if (pre) {
+            if (A.residual) values8<XT, V>(rr, r32, r);
+            values8<XT, V>(rn, false, m);
+        }
+        fetch(i + step);
+        float s[5], rho1 = 1.f, k = 0.f;
+        s[0] = dot8(y, y);
+        own_read(wq, w);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            if constexpr (GATE) activate<true>(A.act, f[v], f[v], df[v]);
+            t[v] = mul2(y[v], w[v]);
+            if constexpr (GATE) t[v] = mul2(t[v], f[v]);
+        }
+        if (!pre && A.post) {
+            s[1] = dot8(e, t);
+            sums.template sum<2>(s);
+            k = s[1];
+        } else if (A.post) {
+            sums.template sum<1>(s);
+        }
+        if (A.post) rho1 = rsqrtf(fmaf(s[0], A.inv_d, A.eps));
+        if (pre) {
+            own_read(dp, acc);
+            own_read(wp, w);
+            F2 dnr[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                r[v] = fma2(t[v], f2(rho1), r[v]);
+                dnr[v] = mul2(m[v], r[v]);
+                m[v] = mul2(m[v], w[v]);
+            }
+            s[0] = dot8(r, r), s[1] = dot8(m, r);
+            if (A.post) {
+                s[2] = dot8(e, t), s[3] = dot8(m, t), s[4] = dot8(r, t);
+                sums.template sum<5>(s);
+            } else {
+                sums.template sum<2>(s);
+            }
+            const float rho2 = rsqrtf(fmaf(s[0], A.inv_d, A.eps)), k2 = rho2 * rho2 * rho2 * s[1] * A.inv_d;
+            if (A.post) k = fmaf(rho2, s[3], s[2]) - k2 * s[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                acc[v] = fma2(dnr[v], f2(rho2), acc[v]);
+                e[v] = fma2(r[v], f2(-k2), fma2(m[v], f2(rho2), e[v]));
+            }
+            own_write(dp, acc);
+        }
+        if (A.dresidual && in) store8<XT, V>(A.dresidual, r32, o, c, e);
+        k *= -rho1 * rho1 * rho1 * A.inv_d;
+        own_read(wq, w);
+        own_read(dq, acc);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            e[v] = mul2(e[v], f2(rho1));
+            const F2 u = mul2(e[v], y[v]);
+            acc[v] = GATE ? fma2(u, f[v], acc[v]) : add2(u, acc[v]);
+            if constexpr (GATE) df[v] = mul2(mul2(df[v], u), w[v]);
+            e[v] = mul2(e[v], GATE ? mul2(w[v], f[v]) : w[v]);
+            e[v] = fma2(y[v], f2(k), e[v]);
+        }
+        own_write(dq, acc);
+        if constexpr (GATE)
+            if (in) store8<XT, V>(A.dgate, false, o, c, df);
+        if (in) store8<XT, V>(A.dy, y32, o, c, e);
+    }
+    sums.end();
     // the weights' gradients: the CTA's sums to its row of the workspace, added up by norm_dw_kernel
     if (!A.parts) return;
-    if constexpr (CTA) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = (j * tpr + tid) * V + v;
-                if (c >= D) continue;
-                float* p = A.parts + (long long)blockIdx.x * 2 * D + c;
-                p[0] = dq[j][v];
-                p[D] = dp[j][v];
-            }
-    } else {
-        // rows of the CTA side by side: the first group's threads add them up, one by one
-        __shared__ float side[256 * NV * V];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) side[(j * V + v) * 256 + threadIdx.x] = k ? dp[j][v] : dq[j][v];
-            __syncthreads();
-            if ((int)threadIdx.x < tpr)
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = (j * tpr + tid) * V + v;
-                        float t = 0.f;
-                        for (int q = 0; q < rows; ++q) t += side[(j * V + v) * 256 + q * tpr + tid];
-                        if (c < D) A.parts[(long long)blockIdx.x * 2 * D + k * D + c] = t;
-                    }
+    float* out = A.parts + (long long)(blockIdx.x / sums.K) * 2 * A.D;
+    __syncthreads();
+    if (SUB && (int)threadIdx.x >= A.tpr) return;
+    for (int k = 0; k < 2; ++k) {
+        const ulonglong2* p = k ? dp : dq;
+        F2 t[4];
+        own_read(p, t);
+        for (unsigned q = 1; q < rows; ++q) {  // a CTA's rows side by side, one by one
+            const ulonglong2 a = p[q * A.tpr + threadIdx.x], b = p[blockDim.x + q * A.tpr + threadIdx.x];
+            t[0] = add2(t[0], F2{a.x}), t[1] = add2(t[1], F2{a.y}), t[2] = add2(t[2], F2{b.x}), t[3] = add2(t[3], F2{b.y});
         }
+        store8<float, V>(out, true, k * A.D, c, t);
     }
 }
 
-// dw = scale (w_post) or 1 (w_pre) times the column sums of [parts][2 D]: 32 columns and 8
-// slices of the rows per CTA, slices added up in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* parts, int nparts, int D, float scale, float* dw_post,
+// dw = scale (w_post) or 1 (w_pre) times the column sums of [parts][2 D]: 32 columns and
+// SLICES slices of the rows per CTA, slices added up in order.
+template <int SLICES>
+__global__ void __launch_bounds__(SLICES * 32) norm_dw_kernel(const float* parts, int nparts, int D, float scale, float* dw_post,
                                                       float* dw_pre) {
-    __shared__ float sum[8][32];
+    __shared__ float sum[SLICES][32];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < 2 * D)
-        for (int i = slice; i < nparts; i += 8) t += parts[(long long)i * 2 * D + c];
+#pragma unroll 8
+        for (int i = slice; i < nparts; i += SLICES) t += parts[(long long)i * 2 * D + c];
     sum[slice][lane] = t;
     __syncthreads();
     if (slice || c >= 2 * D) return;
-    for (int s = 1; s < 8; ++s) t += sum[s][lane];
+    for (int s = 1; s < SLICES; ++s) t += sum[s][lane];
     if (c < D) {
         if (dw_post) dw_post[c] = t * scale;
     } else if (dw_pre) {

@@ -186,7 +186,8 @@ lattice_status check_norm(NormArgs& a, const void* y, lattice_dtype y_dtype, lon
     if (N < 0 || G < 1 || D < 1 || N % G || ys < 0 || gs < 0 || rs < 0) return LATTICE_ERR_INVALID_ARG;
     if ((int)act < 0 || (int)act > 3 || (gate && act == LATTICE_ACT_NONE)) return LATTICE_ERR_INVALID_ARG;
     if (!(eps > 0.f) || !(eps < 3.4e38f) || scale != scale) return LATTICE_ERR_INVALID_ARG;
-    if (D > kNormMaxD || N > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
+    if (D > kNormMaxD || N > 0x7fffffffLL || ys > kNormMaxStride || gs > kNormMaxStride || rs > kNormMaxStride)
+        return LATTICE_ERR_UNSUPPORTED;
     if ((y_dtype != LATTICE_F32 && y_dtype != dtype) || (residual && r_dtype != LATTICE_F32 && r_dtype != dtype) ||
         ((w_post || w_pre) && w_dtype != LATTICE_F32 && w_dtype != dtype))
         return LATTICE_ERR_UNSUPPORTED;
@@ -196,7 +197,7 @@ lattice_status check_norm(NormArgs& a, const void* y, lattice_dtype y_dtype, lon
         return LATTICE_ERR_INVALID_ARG;
     a = NormArgs{};
     a.y = y; a.gate = gate; a.residual = residual; a.w_post = w_post; a.w_pre = w_pre;
-    a.ys = ys; a.gs = gs; a.rs = rs;
+    a.ys = (unsigned)ys; a.gs = (unsigned)gs; a.rs = (unsigned)rs;
     a.N = N; a.G = G; a.D = D; a.act = (int)act;
     a.scale = scale; a.eps = eps; a.inv_d = 1.f / (float)D;
     a.post = post != 0;
@@ -571,11 +572,13 @@ lattice_status lattice_block_norm_fwd(const void* y, lattice_dtype y_dtype, long
     const Span outs[] = {span(r_out, n * type_size(residual_dtype)), span(n_out, n_out ? n * type_size(dtype) : 0)};
     if (clash(ins, 5, outs, 2, residual, r_out)) return LATTICE_ERR_INVALID_ARG;
     a.r_out = r_out; a.n_out = n_out;
-    a.o32 = residual_dtype == LATTICE_F32;
+    a.r32 = residual_dtype == LATTICE_F32;
     const bool vec = D % 8 == 0 && norm_rows_vec(y, y_dtype, N, G, y_stride) && norm_rows_vec(gate, dtype, N, G, gate_stride) &&
                      norm_rows_vec(residual, residual_dtype, N, G, residual_stride) && aligned(w_post, 16) &&
                      aligned(w_pre, 16) && aligned(r_out, 16) && aligned(n_out, 16);
-    return launch_norm_fwd(a, dtype, vec, static_cast<cudaStream_t>(stream));
+    return with_x(dtype, [&](auto t) {
+        return norm::launch_norm<decltype(t)>(false, a, vec, static_cast<cudaStream_t>(stream));
+    });
 }
 
 size_t lattice_block_norm_bwd_workspace_bytes(long long N, int D) {
@@ -598,7 +601,8 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
                                   w_pre, w_dtype, dtype, N, G, D, act, post_norm, scale, eps);
     if (s != LATTICE_OK) return s;
     if (!type_ok(dr_dtype) || dr_stride < 0 || dn_stride < 0) return LATTICE_ERR_INVALID_ARG;
-    if (dr_dtype != LATTICE_F32 && dr_dtype != dtype) return LATTICE_ERR_UNSUPPORTED;
+    if ((dr_dtype != LATTICE_F32 && dr_dtype != dtype) || dr_stride > kNormMaxStride || dn_stride > kNormMaxStride)
+        return LATTICE_ERR_UNSUPPORTED;
     if (residual && dr && dr_dtype != residual_dtype) return LATTICE_ERR_UNSUPPORTED;
     if (N > 0 && ((!dr && !dn) || !dy || (gate && !dgate) || (residual && !dresidual))) return LATTICE_ERR_INVALID_ARG;
     if ((!gate && dgate) || (!residual && dresidual) || (w_pre && N > 0 && !dn) || (dw_post && !w_post) || (dw_pre && !w_pre))
@@ -637,14 +641,15 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
     if (clash(ins, 7, outs, 6, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
     a.dr = dr; a.dn = dn; a.dy = dy; a.dgate = dgate; a.dresidual = dresidual;
     a.parts = dw ? static_cast<float*>(workspace) : nullptr;
-    a.drs = dr_stride; a.dns = dn_stride;
-    a.o32 = dr_dtype == LATTICE_F32;
+    a.drs = (unsigned)dr_stride; a.dns = (unsigned)dn_stride;
+    a.r32 = (residual ? residual_dtype : dr_dtype) == LATTICE_F32;
     const bool vec = D % 8 == 0 && norm_rows_vec(y, y_dtype, N, G, y_stride) && norm_rows_vec(gate, dtype, N, G, gate_stride) &&
                      norm_rows_vec(residual, residual_dtype, N, G, residual_stride) &&
                      norm_rows_vec(dr, dr_dtype, N, G, dr_stride) && norm_rows_vec(dn, dtype, N, G, dn_stride) &&
                      aligned(w_post, 16) && aligned(w_pre, 16) && aligned(dy, 16) && aligned(dgate, 16) &&
                      aligned(dresidual, 16);
-    return launch_norm_bwd(a, dtype, vec, dw_post, dw_pre, st);
+    s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, vec, st); });
+    return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, dw_post, dw_pre, st);
 }
 
 lattice_status lattice_selftest_bounded_wait(unsigned long long limit_ns, void* stream) {
@@ -660,7 +665,8 @@ lattice_status lattice_get_device_status(void* stream) {
     // every translation unit's copy of the status word (each unit is a module of its own)
     cudaError_t (*const units[])(unsigned int*) = {read_clear_module_status, status_simt_exact,
                                                    status_simt_chunked, status_step, status_bwd, status_tc,
-                                                   status_norm, status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
+                                                   status_norm_f32, status_norm_bf16,
+                                                   status_norm_f16, status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
                                                    status_gated_bwd_f32, status_gated_bwd_bf16, status_gated_bwd_f16};
     unsigned int any = 0;
     for (auto unit : units) {

@@ -48,11 +48,13 @@ template <class XT> lattice_status launch_step(const GatedArgs& a, int form, boo
 template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, cudaStream_t st);
 }  // namespace gated
 
-// tu_norm.cu: norms after and before a block (tpr set by the launch). vec: rows and weights
-// can be read in aligned vectors of 8 elements
-lattice_status launch_norm_fwd(NormArgs a, lattice_dtype dtype, bool vec, cudaStream_t st);
-lattice_status launch_norm_bwd(NormArgs a, lattice_dtype dtype, bool vec, float* dw_post, float* dw_pre, cudaStream_t st);
+// tu_norm_*.cu: norms after and before a block, a unit per type of the call (tpr, K set by the
+// launch). vec: rows and weights can be read in aligned vectors of 8 elements
+namespace norm {
+template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, bool vec, cudaStream_t st);
+}  // namespace norm
 int norm_parts(long long N, int D);  // rows of the backward pass's workspace
+lattice_status launch_norm_dw(const NormArgs& a, float* dw_post, float* dw_pre, cudaStream_t st);
 
 // each unit's device status word (read, and zeroed when set)
 cudaError_t status_simt_exact(unsigned int* v);
@@ -60,7 +62,9 @@ cudaError_t status_simt_chunked(unsigned int* v);
 cudaError_t status_step(unsigned int* v);
 cudaError_t status_bwd(unsigned int* v);
 cudaError_t status_tc(unsigned int* v);
-cudaError_t status_norm(unsigned int* v);
+cudaError_t status_norm_f32(unsigned int* v);
+cudaError_t status_norm_bf16(unsigned int* v);
+cudaError_t status_norm_f16(unsigned int* v);
 cudaError_t status_gated_fwd_f32(unsigned int* v);
 cudaError_t status_gated_fwd_bf16(unsigned int* v);
 cudaError_t status_gated_fwd_f16(unsigned int* v);
