@@ -21,7 +21,6 @@ last axes contiguous).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -298,7 +297,22 @@ _WRITE = {"plain": 0, "leaky": 1, "unit": 2}
 
 def _rows(t, name: str, shape, lead: int, dtypes, device):
     """Checks a tensor whose first `lead` axes may be strided and whose other axes are
-    contiguous; returns the strides of the first `lead` axes."""
+    contiguous; returns its strides (the first `lead` are the ones that matter)."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == device:
+        strides = t.stride()
+        if t.is_contiguous():
+            return strides
+        want = 1
+        for k in range(len(shape) - 1, lead - 1, -1):
+            if shape[k] != 1 and strides[k] != want:
+                raise ValueError(f"{name} must be contiguous in its last {len(shape) - lead} axes")
+            want *= shape[k]
+        return strides
+    return _like(t, name, shape, dtypes, device)
+
+
+def _like(t, name: str, shape, dtypes, device):
+    """Checks a tensor's place, type and shape."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -307,42 +321,59 @@ def _rows(t, name: str, shape, lead: int, dtypes, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    strides = t.stride()
-    if not t.is_contiguous():
-        want = 1
-        for k in range(len(shape) - 1, lead - 1, -1):
-            if shape[k] != 1 and strides[k] != want:
-                raise ValueError(f"{name} must be contiguous in its last {len(shape) - lead} axes")
-            want *= shape[k]
-    return strides[:lead]
 
 
 def _whole(t, name: str, shape, dtypes, device):
     """Checks a contiguous tensor; None passes."""
-    if t is None:
-        return
-    _rows(t, name, shape, 0, dtypes, device)
+    if t is not None and not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes
+                              and t.device == device and t.is_contiguous()):
+        _rows(t, name, shape, 0, dtypes, device)
 
 
-def _place(device, stream):
-    """Where a call runs: on the tensors' device, its buffers allocated on the stream that
-    the kernels use, so that memory freed after the call is reused in that stream's order."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+# the current stream's handle without a Stream object (a few microseconds less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _enter(device, stream):
+    """(context, stream handle) of a call: on the tensors' device, its buffers allocated on the
+    stream that the kernels use, so that memory freed after the call is reused in that
+    stream's order. The context (or None) is entered; the caller leaves it."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return None, _raw_stream(device.index)
+        ctx = torch.cuda.device(device)
+        ctx.__enter__()
+        return ctx, _raw_stream(device.index)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()
+    return ctx, stream.cuda_stream
+
+
+def _leave(ctx):
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
+
+
+def _new(t, dtype=None):
+    """An empty contiguous tensor like t."""
+    if t.is_contiguous() and (dtype is None or dtype == t.dtype):
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+
+
+_F32_ONLY = (torch.float32,)
+_XZ = {t: (t, torch.float32) for t in (torch.float32, torch.bfloat16, torch.float16)}
 
 
 def _gated_args(x, z, lead: int, lengths, gate: str, write: str):
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 2:
         raise ValueError("x must be a tensor [B, T, H, d] (one token: [B, H, d])")
     shape, device = x.shape, x.device
-    xs = _rows(x, "x", shape, lead, _FLOATS, device)
+    xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
     per_head = isinstance(z, torch.Tensor) and z.dim() == lead + 1
-    zs = _rows(z, "z", shape[:-1] if per_head else shape, lead, (x.dtype, torch.float32), device)
+    zs = _rows(z, "z", shape[:-1] if per_head else shape, lead, _XZ[x.dtype], device)
     if lengths is not None:
         _whole(lengths, "lengths", shape[:1], (torch.int32,), device)
     if gate not in _GATE or write not in _WRITE:
@@ -370,22 +401,26 @@ def gated_scan_fwd(x: torch.Tensor, z: torch.Tensor, h0: Optional[torch.Tensor] 
     fill for gated_scan_bwd. h_out may be h0.
     Returns (y [B,T,H,d] in x's dtype, h_T [B,H,d] float32, the state at each length)."""
     xs, zs, per_head = _gated_args(x, z, 2, lengths, gate, write)
-    B, T, H, d = x.shape
-    dev, f32 = x.device, (torch.float32,)
-    _whole(h0, "h0", (B, H, d), f32, dev)
-    _whole(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), f32, dev)
-    _whole(h_out, "h_out", (B, H, d), f32, dev)
-    _whole(y, "y", x.shape, (x.dtype,), dev)
-    with _place(dev, stream):
+    shape, dev = x.shape, x.device
+    B, T, H, d = shape
+    state = (B, H, d)
+    _whole(h0, "h0", state, _F32_ONLY, dev)
+    _whole(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), _F32_ONLY, dev)
+    _whole(h_out, "h_out", state, _F32_ONLY, dev)
+    _whole(y, "y", shape, (x.dtype,), dev)
+    ctx, st = _enter(dev, stream)
+    try:
         if h_out is None:
-            h_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+            h_out = torch.empty(state, dtype=torch.float32, device=dev) if h0 is None else torch.empty_like(h0)
         if y is None:
-            y = torch.empty((B, T, H, d), dtype=x.dtype, device=dev)
+            y = _new(x)
         code = lib().lattice_gated_scan_fwd(
             x.data_ptr(), _DT[x.dtype], xs[0], xs[1], z.data_ptr(), _DT[z.dtype], zs[0], zs[1], per_head, _adr(h0),
-            h_out.data_ptr(), y.data_ptr(), _adr(marks), _adr(lengths), B, T, H, d, _GATE[gate], _WRITE[write], tau,
-            _stream(stream))
-    _raise(code, "lattice_gated_scan_fwd")
+            h_out.data_ptr(), y.data_ptr(), _adr(marks), _adr(lengths), B, T, H, d, _GATE[gate], _WRITE[write], tau, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_gated_scan_fwd")
     return y, h_out
 
 
@@ -397,20 +432,24 @@ def gated_scan_bwd(x: torch.Tensor, z: torch.Tensor, dy: torch.Tensor, marks: to
     and may be strided as x. Returns a dict with dx (x's dtype), dz (z's dtype and shape) and
     dh0 (float32); gradients of tokens behind a sequence's length are 0."""
     xs, zs, per_head = _gated_args(x, z, 2, lengths, gate, write)
-    B, T, H, d = x.shape
-    dev, f32 = x.device, (torch.float32,)
-    dys = _rows(dy, "dy", x.shape, 2, (x.dtype,), dev)
-    _rows(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), 0, f32, dev)
-    _whole(dh_T, "dh_T", (B, H, d), f32, dev)
-    with _place(dev, stream):
-        out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dz": torch.empty(z.shape, dtype=z.dtype, device=dev),
-               "dh0": torch.empty((B, H, d), dtype=torch.float32, device=dev)}
+    shape, dev = x.shape, x.device
+    B, T, H, d = shape
+    dys = _rows(dy, "dy", shape, 2, (x.dtype,), dev)
+    _rows(marks, "marks", (B, (T + _MARK - 1) // _MARK, H, d), 0, _F32_ONLY, dev)
+    _whole(dh_T, "dh_T", (B, H, d), _F32_ONLY, dev)
+    ctx, st = _enter(dev, stream)
+    try:
+        dx, dz = _new(x), _new(z)
+        dh0 = torch.empty((B, H, d), dtype=torch.float32, device=dev)
         code = lib().lattice_gated_scan_bwd(
             x.data_ptr(), _DT[x.dtype], xs[0], xs[1], z.data_ptr(), _DT[z.dtype], zs[0], zs[1], per_head, dy.data_ptr(),
-            dys[0], dys[1], marks.data_ptr(), _adr(dh_T), out["dx"].data_ptr(), out["dz"].data_ptr(),
-            out["dh0"].data_ptr(), _adr(lengths), B, T, H, d, _GATE[gate], _WRITE[write], tau, _stream(stream))
-    _raise(code, "lattice_gated_scan_bwd")
-    return out
+            dys[0], dys[1], marks.data_ptr(), _adr(dh_T), dx.data_ptr(), dz.data_ptr(), dh0.data_ptr(), _adr(lengths),
+            B, T, H, d, _GATE[gate], _WRITE[write], tau, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_gated_scan_bwd")
+    return {"dx": dx, "dz": dz, "dh0": dh0}
 
 
 def gated_step(h: torch.Tensor, x: torch.Tensor, z: torch.Tensor, *, gate: str = "logit", write: str = "leaky",
@@ -421,16 +460,23 @@ def gated_step(h: torch.Tensor, x: torch.Tensor, z: torch.Tensor, *, gate: str =
     xs, zs, per_head = _gated_args(x, z, 1, None, gate, write)
     shape, dev = x.shape, x.device
     B, H, d = shape
-    _rows(h, "h", shape, 0, (torch.float32,), dev)
-    _whole(h_out, "h_out", shape, (torch.float32,), dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _whole(h_out, "h_out", shape, _F32_ONLY, dev)
+    _rows(h, "h", shape, 0, _F32_ONLY, dev)
     _whole(y, "y", shape, (x.dtype,), dev)
-    with _place(dev, stream):
+    ctx, st = _enter(dev, stream)
+    try:
         if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
+            y = _new(x)
         code = lib().lattice_gated_step(
-            h.data_ptr(), (h if h_out is None else h_out).data_ptr(), x.data_ptr(), _DT[x.dtype], xs[0], z.data_ptr(),
-            _DT[z.dtype], zs[0], per_head, y.data_ptr(), B, H, d, _GATE[gate], _WRITE[write], tau, _stream(stream))
-    _raise(code, "lattice_gated_step")
+            h.data_ptr(), h_out.data_ptr(), x.data_ptr(), _DT[x.dtype], xs[0], z.data_ptr(), _DT[z.dtype], zs[0], per_head,
+            y.data_ptr(), B, H, d, _GATE[gate], _WRITE[write], tau, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_gated_step")
     return y
 
 
@@ -440,12 +486,14 @@ _ACT = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3}
 
 
 def _groups(tensors, shape):
-    """(G, strides): rows in groups of G, contiguous within a group, for every tensor of
-    `shape` (None: stride 0), with the stride between groups."""
+    """(G, strides): rows in groups of G, contiguous within a group, for every (name, tensor)
+    of `shape` (None: stride 0), with the stride between groups."""
     D, lead = shape[-1], shape[:-1]
-    names = [k for k, t in tensors if t is not None]
-    if all(t is None or t.is_contiguous() for _, t in tensors):
-        return 1, [D] * len(tensors)
+    for _, t in tensors:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
+        return 1, (D,) * len(tensors)
     for G, outer in ((1, lead), (lead[-1] if lead else 1, lead[:-1])):
         strides = []
         for _, t in tensors:
@@ -468,8 +516,9 @@ def _groups(tensors, shape):
                 break
         else:
             return G, strides
-    raise ValueError(f"the rows of {', '.join(names)} must be contiguous, with one stride between rows, or between the "
-                     "groups of rows that the last axis but one makes")
+    names = ", ".join(k for k, t in tensors if t is not None)
+    raise ValueError(f"the rows of {names} must be contiguous, with one stride between rows, or between the groups of rows "
+                     "that the last axis but one makes")
 
 
 def _norm_args(y, w_post, gate, residual, w_pre, act, dtype):
@@ -478,33 +527,27 @@ def _norm_args(y, w_post, gate, residual, w_pre, act, dtype):
     shape, dev = y.shape, y.device
     if dtype is None:
         dtype = gate.dtype if isinstance(gate, torch.Tensor) else y.dtype
-    if dtype not in _FLOATS:
+    both = _XZ.get(dtype)
+    if both is None:
         raise TypeError(f"the output dtype must be one of {_FLOATS}, got {dtype}")
-    both = (dtype, torch.float32)
-    for t, name, types in ((y, "y", both), (gate, "gate", (dtype,)), (residual, "residual", both)):
-        if t is not None:
-            _like(t, name, shape, types, dev)
+    if y.dtype not in both:
+        _like(y, "y", shape, both, dev)
+    if gate is not None:
+        _like(gate, "gate", shape, (dtype,), dev)
+    if residual is not None:
+        _like(residual, "residual", shape, both, dev)
     w_dtype = torch.float32
-    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if t is not None:
-            _rows(t, name, shape[-1:], 0, both, dev)
-            w_dtype = t.dtype
-    if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
-        raise TypeError("w_post and w_pre must have the same dtype")
+    if w_post is not None:
+        _whole(w_post, "w_post", shape[-1:], both, dev)
+        w_dtype = w_post.dtype
+    if w_pre is not None:
+        _whole(w_pre, "w_pre", shape[-1:], both, dev)
+        if w_post is not None and w_dtype != w_pre.dtype:
+            raise TypeError("w_post and w_pre must have the same dtype")
+        w_dtype = w_pre.dtype
     if act not in _ACT:
         raise ValueError(f"act is one of {tuple(_ACT)}")
     return shape, dev, dtype, w_dtype
-
-
-def _like(t, name, shape, dtypes, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def block_norm_fwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
@@ -530,17 +573,21 @@ def block_norm_fwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, ga
     _whole(n_out, "n_out", shape, (dtype,), dev)
     D = shape[-1]
     N = y.numel() // D if D else 0
-    G, st = _groups((("y", y), ("gate", gate), ("residual", residual)), shape)
-    with _place(dev, stream):
+    G, gs = _groups((("y", y), ("gate", gate), ("residual", residual)), shape)
+    ctx, st = _enter(dev, stream)
+    try:
         if r_out is None:
-            r_out = torch.empty(shape, dtype=r_dtype, device=dev)
+            r_out = _new(y if residual is None else residual, r_dtype)
         if n_out is None and pre_norm:
-            n_out = torch.empty(shape, dtype=dtype, device=dev)
+            n_out = _new(y, dtype)
         code = lib().lattice_block_norm_fwd(
-            y.data_ptr(), _DT[y.dtype], st[0], _adr(gate), st[1], _adr(residual), _DT[r_dtype], st[2], _adr(w_post),
+            y.data_ptr(), _DT[y.dtype], gs[0], _adr(gate), gs[1], _adr(residual), _DT[r_dtype], gs[2], _adr(w_post),
             _adr(w_pre), _DT[w_dtype], r_out.data_ptr(), _adr(n_out), _DT[dtype], N, G, D, _ACT[act], post_norm, scale,
-            eps, _stream(stream))
-    _raise(code, "lattice_block_norm_fwd")
+            eps, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_block_norm_fwd")
     return r_out, n_out
 
 
@@ -569,26 +616,30 @@ def block_norm_bwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, dr
         _like(dn, "dn", shape, (dtype,), dev)
     D = shape[-1]
     N = y.numel() // D if D else 0
-    G, st = _groups((("y", y), ("gate", gate), ("residual", residual), ("dr", dr), ("dn", dn)), shape)
-    L = lib()
+    G, gs = _groups((("y", y), ("gate", gate), ("residual", residual), ("dr", dr), ("dn", dn)), shape)
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
             raise TypeError("workspace must be a contiguous tensor on the inputs' device")
-    with _place(dev, stream):
-        f32 = dict(dtype=torch.float32, device=dev)
-        out = {"dy": torch.empty(shape, dtype=y.dtype, device=dev),
-               "dgate": None if gate is None else torch.empty(shape, dtype=dtype, device=dev),
-               "dresidual": None if residual is None else torch.empty(shape, dtype=residual.dtype, device=dev),
-               "dw_post": None if w_post is None else torch.empty(D, **f32),
-               "dw_pre": None if w_pre is None else torch.empty(D, **f32)}
-        if workspace is None and (w_post is not None or w_pre is not None):
-            workspace = torch.empty(L.lattice_block_norm_bwd_workspace_bytes(N, D), dtype=torch.uint8, device=dev)
+    L = lib()
+    ctx, st = _enter(dev, stream)
+    try:
+        dy = _new(y)
+        dgate = None if gate is None else _new(gate)
+        dresidual = None if residual is None else _new(residual)
+        dw_post = None if w_post is None else _new(w_post, torch.float32)
+        dw_pre = None if w_pre is None else _new(w_pre, torch.float32)
+        bytes_ = 0
+        if w_post is not None or w_pre is not None:
+            if workspace is None:
+                workspace = torch.empty(L.lattice_block_norm_bwd_workspace_bytes(N, D), dtype=torch.uint8, device=dev)
+            bytes_ = workspace.numel() * workspace.element_size()
         code = L.lattice_block_norm_bwd(
-            y.data_ptr(), _DT[y.dtype], st[0], _adr(gate), st[1], _adr(residual),
-            0 if residual is None else _DT[residual.dtype], st[2], _adr(w_post), _adr(w_pre), _DT[w_dtype], _adr(dr),
-            0 if dr is None else _DT[dr.dtype], st[3], _adr(dn), st[4], out["dy"].data_ptr(), _adr(out["dgate"]),
-            _adr(out["dresidual"]), _adr(out["dw_post"]), _adr(out["dw_pre"]), _adr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _DT[dtype], N, G, D, _ACT[act],
-            post_norm, scale, eps, _stream(stream))
-    _raise(code, "lattice_block_norm_bwd")
-    return out
+            y.data_ptr(), _DT[y.dtype], gs[0], _adr(gate), gs[1], _adr(residual),
+            0 if residual is None else _DT[residual.dtype], gs[2], _adr(w_post), _adr(w_pre), _DT[w_dtype], _adr(dr),
+            0 if dr is None else _DT[dr.dtype], gs[3], _adr(dn), gs[4], dy.data_ptr(), _adr(dgate), _adr(dresidual),
+            _adr(dw_post), _adr(dw_pre), _adr(workspace), bytes_, _DT[dtype], N, G, D, _ACT[act], post_norm, scale, eps, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_block_norm_bwd")
+    return {"dy": dy, "dgate": dgate, "dresidual": dresidual, "dw_post": dw_post, "dw_pre": dw_pre}
