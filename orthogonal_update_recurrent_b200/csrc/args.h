@@ -99,6 +99,8 @@ constexpr int kGatedMaxK = 8;   // CTAs of a cluster at most
 
 constexpr int kGatedMaxSize = 1 << 30;  // channels, and tokens: tile indices stay within int
 
+constexpr int kGatedPoly = 10;  // coefficients
+
 struct GatedArgs {
     const void* x; const void* z;  // z: fp32 (z32) or x's type, per channel or per head (zhead)
     const float* h0;               // may be null (=> 0)
@@ -112,6 +114,8 @@ struct GatedArgs {
     int B, T, C, d;                // C = H*d channels
     int ctiles, K, nmarks;         // channel tiles, CTAs per cluster, marks per sequence
     float tau;
+    int squares;                   // tau != 1: poly stands for tau / 2^squares <= 1
+    unsigned long long poly[kGatedPoly];  // (1 - (1 + t)^-tau)/t on [0, 1], each coefficient twice
     bool z32, zhead;
     bool zwords;                   // 16-bit gates per head: every token's are whole 32-bit words
 };

@@ -88,21 +88,6 @@ __device__ __forceinline__ void store_vec(T* p, const float* f, int n) {
 
 constexpr float kLog2e = 1.442695041f;
 
-// log(1 + t), 0 <= t <= 1: t times the polynomial that meets log(1 + t)/t at the ten
-// Chebyshev nodes of [0, 1] (relative error 5e-9 before rounding).
-__device__ __forceinline__ F2 log1p_unit(F2 t) {
-    F2 p = f2(-0.0031760570f);
-    p = fma2(p, t, f2(0.0195425265f));
-    p = fma2(p, t, f2(-0.0563736111f));
-    p = fma2(p, t, f2(0.1054362357f));
-    p = fma2(p, t, f2(-0.1526966691f));
-    p = fma2(p, t, f2(0.1966327429f));
-    p = fma2(p, t, f2(-0.2495161593f));
-    p = fma2(p, t, f2(0.3332971036f));
-    p = fma2(p, t, f2(-0.4999989271f));
-    p = fma2(p, t, f2(1.f));
-    return mul2(p, t);
-}
 // exp(w) - 1 for -0.25 <= w <= 0 by the power series.
 constexpr float kSmall = -0.25f;
 __device__ __forceinline__ F2 expm1_small(F2 w) {
@@ -117,9 +102,11 @@ __device__ __forceinline__ F2 expm1_small(F2 w) {
 // The gates a and q = 1 - a of two channels. Errors of a gate near 1 are multiplied by the
 // retention time, so its last bit must not be biased, as an approximate reciprocal's may
 // be: with t = exp(-z), r = 1/(1 + t) gets one Newton step, a = r (2 - (1 + t) r), and 1 - a is
-// t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126.
+// t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126. With
+// tau, `fast` says that the run has no z < 0 and tau <= 1, which leaves out what those need
+// (long context SEEPOLY us; by log(1 + t) and exp, for every z, 307 us).
 template <int GATE>
-__device__ __forceinline__ void gates_of(F2 z, float tau, F2& a, F2& q) {
+__device__ __forceinline__ void gates_of(F2 z, const GatedArgs& A, bool fast, F2& a, F2& q) {
     if constexpr (GATE == kValue) {
         a = z;
         q = fma2(z, f2(-1.f), f2(1.f));
@@ -131,16 +118,31 @@ __device__ __forceinline__ void gates_of(F2 z, float tau, F2& a, F2& q) {
         q = mul2(t, a);
         a = add2(a, f2(-1.17549435e-38f));  // 2^-126 at z = -inf becomes the 0 it stands for
     } else {
-        // log a = -tau (log(1 + exp(-|z|)) + max(-z, 0))
+        // With t = exp(-|z|) <= 1, q0 = 1 - (1 + t)^-tau is t times a polynomial for tau <= 1; a
+        // larger tau halves it often enough and squares 1 - q0 as often. z < 0 has the factor
+        // exp(tau z) besides. Every element's result depends on its own z alone.
         const F2 t = each(z, [](float v) { return ex2(-fabsf(v) * kLog2e); });
-        const F2 w = mul2(f2(-tau), add2(log1p_unit(t), each(z, [](float v) { return fmaxf(-v, 0.f); })));
-        const F2 e = each(mul2(w, f2(kLog2e)), ex2), m = expm1_small(w);
+        F2 p = {A.poly[kGatedPoly - 1]};
+#pragma unroll
+        for (int k = kGatedPoly - 2; k >= 0; --k) p = fma2(p, t, F2{A.poly[k]});
+        q = mul2(p, t);
+        a = fma2(q, f2(-1.f), f2(1.f));
+        if (fast) return;
+        for (int k = 0; k < A.squares; ++k) {
+            q = mul2(q, fma2(q, f2(-1.f), f2(2.f)));
+            a = mul2(a, a);
+        }
+        const F2 x = mul2(f2(A.tau), each(z, [](float v) { return fminf(v, 0.f); }));
+        const F2 e = each(mul2(x, f2(kLog2e)), ex2), m = expm1_small(x), e1 = add2(e, f2(-1.f));
+        float x0, x1, m0, m1, e10, e11;
+        parts(x, x0, x1), parts(m, m0, m1), parts(e1, e10, e11);
+        const F2 em = f2(x0 > kSmall ? m0 : e10, x1 > kSmall ? m1 : e11);
+        q = fma2(mul2(a, f2(-1.f)), em, q);
         // near 1: 1 - (1 - a), one rounding
-        const F2 a1 = add2(m, f2(1.f)), q1 = mul2(m, f2(-1.f)), q2 = fma2(e, f2(-1.f), f2(1.f));
-        float w0, w1, e0, e1, a10, a11, q10, q11, q20, q21;
-        parts(w, w0, w1), parts(e, e0, e1), parts(a1, a10, a11), parts(q1, q10, q11), parts(q2, q20, q21);
-        a = f2(w0 > kSmall ? a10 : e0, w1 > kSmall ? a11 : e1);
-        q = f2(w0 > kSmall ? q10 : q20, w1 > kSmall ? q11 : q21);
+        const F2 near = fma2(q, f2(-1.f), f2(1.f)), far = mul2(a, e);
+        float q0, q1, n0, n1, f0, f1;
+        parts(q, q0, q1), parts(near, n0, n1), parts(far, f0, f1);
+        a = f2(q0 < 0.5f ? n0 : f0, q1 < 0.5f ? n1 : f1);
     }
 }
 // da/dz
@@ -331,6 +333,19 @@ __device__ __forceinline__ void load_state(const float* p, int n, F2* f) {  // p
 #pragma unroll
         for (int v = 0; v < N; ++v) f[v] = f2(t.v[2 * v], t.v[2 * v + 1]);
     }
+}
+// Whether no lane's z of a run is negative.
+template <class ZT, int N, int R>
+__device__ __forceinline__ bool none_negative(const ZT* z, int row) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        constexpr int W = N * 2 * sizeof(ZT) / 4;
+        const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(z + r * row);
+#pragma unroll
+        for (int v = 0; v < W; ++v) bits |= w.v[v];
+    }
+    return !__any_sync(0xffffffffu, (bits & (sizeof(ZT) == 2 ? 0x80008000u : 0x80000000u)) != 0);
 }
 template <class XT>
 __device__ __forceinline__ float load_gate(const void* z, long long off, bool z32) {
@@ -526,10 +541,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
             hg.read(A, reinterpret_cast<const uint32_t*>(zw), t0, len, neutral_z<GATE>(), lane);
             hg.keep(gates, lane, [&](F2 hz, F2* out) {
                 F2 hq;
-                gates_of<GATE>(hz, A.tau, out[0], hq);
+                gates_of<GATE>(hz, A, false, out[0], hq);
                 out[1] = writes_of<GATE, WRITE>(out[0], hq);
             });
         }
+        bool fast = false;
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ZT, N, R>(zs, Lay::ROW);
         // P: products of the run's gates, H: the run's states from h = 0, after each token
         F2 P[R][NG], H[R][N];
 #pragma unroll
@@ -548,7 +565,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 const int k = HEAD ? 0 : v;
                 if constexpr (!HEAD) {
                     F2 q;
-                    gates_of<GATE>(zf[v], A.tau, a[v], q);
+                    gates_of<GATE>(zf[v], A, fast, a[v], q);
                     w[v] = writes_of<GATE, WRITE>(a[v], q);
                 }
                 const F2 u = WRITE == kPlain ? xf[v] : mul2(w[k], xf[v]);
@@ -756,12 +773,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
             hg.read(A, reinterpret_cast<const uint32_t*>(zw), t0, len, neutral_z<GATE>(), lane);
             hg.keep(gates, lane, [&](F2 hz, F2* out) {
                 F2 hq;
-                gates_of<GATE>(hz, A.tau, out[0], hq);
+                gates_of<GATE>(hz, A, false, out[0], hq);
                 out[1] = writes_of<GATE, WRITE>(out[0], hq);
                 out[2] = WRITE == kUnit ? unit_slopes(out[0], out[1]) : f2(0.f);
                 out[3] = f2(0.f);
             });
         }
+        bool fast = false;
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ZT, N, R>(zw + lane * V, Lay::ROW);
         // Of each token: a, then the product of the run's gates behind it; s (per head it stays
         // in shared memory); dz / g, per head without da/dz; the run's own adjoint, from 0.
         F2 a[R][NG], s[HEAD ? 1 : R][NG], k[R][N], gl[R][N], h[N];
@@ -783,7 +802,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 const int i = HEAD ? 0 : v;
                 F2 q;
                 if constexpr (!HEAD) {
-                    gates_of<GATE>(zf[v], A.tau, a[r][i], q);
+                    gates_of<GATE>(zf[v], A, fast, a[r][i], q);
                     s[r][i] = writes_of<GATE, WRITE>(a[r][i], q);
                     if constexpr (WRITE == kUnit) hs = unit_slopes(a[r][i], s[r][i]);
                 }
@@ -918,7 +937,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 float v = (t.x + t.y) + (t.z + t.w);
                 if constexpr (GATE != kValue) {
                     F2 ga, gq;
-                    gates_of<GATE>(hz, A.tau, ga, gq);
+                    gates_of<GATE>(hz, A, false, ga, gq);
                     float lo, hi;
                     parts(slopes_of<GATE>(hz, A.tau, ga, gq), lo, hi);
                     v *= m ? hi : lo;
@@ -973,7 +992,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedArgs A) {
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
         F2 a, q;
-        gates_of<GATE>(f2(zf[v], zf[v + 1]), A.tau, a, q);
+        gates_of<GATE>(f2(zf[v], zf[v + 1]), A, false, a, q);
         const F2 u = mul2(writes_of<GATE, WRITE>(a, q), f2(to_f(xr.v[v]), to_f(xr.v[v + 1])));
         parts(fma2(a, f2(h.v[v], h.v[v + 1]), u), h.v[v], h.v[v + 1]);
     }

@@ -5,8 +5,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <string.h>
 
 #include <mutex>
 
@@ -150,6 +152,40 @@ lattice_status check_gated(lattice_dtype x_dtype, lattice_dtype z_dtype, int z_p
     if ((long long)H * d > kGatedMaxSize || T > kGatedMaxSize) return LATTICE_ERR_UNSUPPORTED;
     if (z_per_head && !d_supported(d)) return LATTICE_ERR_UNSUPPORTED;
     return LATTICE_OK;
+}
+
+// The polynomial in t that meets (1 - (1 + t)^-tau)/t at the Chebyshev nodes of [0, 1], for
+// tau <= 1, where its error is a few 1e-9 of its value; larger tau are halved first.
+void gated_poly(GatedArgs& a) {
+    constexpr int n = kGatedPoly;
+    double tau = a.tau;
+    for (a.squares = 0; tau > 1; ++a.squares) tau /= 2;
+    const double pi = 3.14159265358979323846;
+    double f[n], cheb[n], c[n] = {}, prev[n] = {}, cur[n] = {};
+    for (int k = 0; k < n; ++k) {
+        const double t = 0.5 + 0.5 * cos(pi * (k + 0.5) / n);
+        f[k] = -expm1(-tau * log1p(t)) / t;
+    }
+    for (int j = 0; j < n; ++j) {
+        double s = 0;
+        for (int k = 0; k < n; ++k) s += f[k] * cos(pi * j * (k + 0.5) / n);
+        cheb[j] = s * (j ? 2.0 : 1.0) / n;
+    }
+    // T_0 = 1, T_1 = x, T_{j+1} = 2 x T_j - T_{j-1} with x = 2 t - 1, in powers of t
+    prev[0] = 1, cur[0] = -1, cur[1] = 2;
+    for (int j = 0; j < n; ++j) {
+        for (int k = 0; k < n; ++k) c[k] += cheb[j] * (j ? cur[k] : prev[k]);
+        if (j == 0) continue;
+        double next[n];
+        for (int k = 0; k < n; ++k) next[k] = (k ? 4 * cur[k - 1] : 0) - 2 * cur[k] - prev[k];
+        for (int k = 0; k < n; ++k) prev[k] = cur[k], cur[k] = next[k];
+    }
+    for (int k = 0; k < n; ++k) {
+        const float v = (float)c[k];
+        uint32_t bits;
+        memcpy(&bits, &v, 4);
+        a.poly[k] = (unsigned long long)bits << 32 | bits;
+    }
 }
 
 int gated_form(lattice_gate gate, lattice_write write, float tau) {
@@ -465,6 +501,7 @@ lattice_status lattice_gated_scan_fwd(const void* x, lattice_dtype x_dtype, long
     a.B = B; a.T = T; a.C = (int)C; a.d = d; a.nmarks = (int)nm; a.tau = tau;
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
     a.zwords = gate_words(z, H, a.zbs, a.zts);
+    if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
     const bool vec = gated_vec(a, type_size(x_dtype), 16) && rows_vec(x, type_size(x_dtype), B, T, a.xbs, a.xts, 16) &&
                      (a.zhead || rows_vec(z, type_size(z_dtype), B, T, a.zbs, a.zts, 16));
     return with_x(x_dtype, [&](auto t) {
@@ -510,6 +547,7 @@ lattice_status lattice_gated_scan_bwd(const void* x, lattice_dtype x_dtype, long
     a.B = B; a.T = T; a.C = (int)C; a.d = d; a.nmarks = (int)nm; a.tau = tau;
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
     a.zwords = gate_words(z, H, a.zbs, a.zts);
+    if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
     const bool vec = gated_vec(a, sx_, 16) && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
                      rows_vec(dy, sx_, B, T, a.dybs, a.dyts, 16) &&
                      (a.zhead || (rows_vec(z, sz_, B, T, a.zbs, a.zts, 16) && aligned(dz, 16)));
@@ -540,6 +578,7 @@ lattice_status lattice_gated_step(const float* h, float* h_out, const void* x, l
     a.xbs = x_batch_stride; a.zbs = z_batch_stride;
     a.B = B; a.T = 1; a.C = (int)C; a.d = d; a.tau = tau;
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
+    if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
     const bool vec = gated_vec(a, sx_, kStepVec * sx_) && rows_vec(x, sx_, B, 1, a.xbs, 0, kStepVec * sx_) &&
                      (a.zhead || rows_vec(z, sz_, B, 1, a.zbs, 0, kStepVec * sz_));
     return with_x(x_dtype, [&](auto t) {
