@@ -117,6 +117,7 @@ struct GatedArgs {
     int squares;                   // tau != 1: poly stands for tau / 2^squares <= 1
     unsigned long long poly[kGatedPoly];  // (1 - (1 + t)^-tau)/t on [0, 1], each coefficient twice
     bool z32, zhead;
+    bool wide;                     // rows can be read in 16-byte pieces
     bool zwords;                   // 16-bit gates per head: every token's are whole 32-bit words
 };
 

@@ -221,46 +221,79 @@ __device__ __forceinline__ int row_length(const GatedArgs& A, int b) {
 }
 
 // Copies a run's R rows of 32 V channels (n of them exist from the tile's first on) into a
-// stage of the warp's, and moves on to the warp's next run: 16 bytes per cp.async, with
-// each lane's place worked out once, or element by element.
+// stage of the warp's, and moves on to the warp's next run. VEC: asynchronously, 16 bytes at
+// a time where rows allow it (wide), else a lane's V channels; otherwise element by element.
 template <bool VEC, class T, int V, int R>
 struct Stager {
     static constexpr int ROW = 32 * V, PER = 16 / sizeof(T), CH = ROW / PER, STEP = 32 / CH;  // chunks per row
     static_assert(CH <= 32 && R % STEP == 0, "whole warps of chunks");
-    const T* p;            // the next run's first row, VEC: the lane's first chunk in it
-    long long ts, move;    // VEC: STEP rows; one row
-    uint32_t at;           // VEC: the chunk's place in a stage
-    int n;
-    __device__ __forceinline__ Stager(const T* base, long long token_stride, int channels, long long first, long long ahead, int lane) {
-        ts = VEC ? STEP * token_stride : token_stride;
+    const T* p;            // the next run's first row, VEC: the lane's first piece in it
+    long long ts, move;    // wide: STEP rows; one row
+    uint32_t at;           // VEC: the lane's place in a stage
+    int n;                 // VEC: whether the lane copies
+    bool wide;
+    __device__ __forceinline__ Stager(const T* base, long long token_stride, int channels, bool wide_, long long first,
+                                      long long ahead, int lane)
+        : wide(wide_) {
+        ts = VEC && wide ? STEP * token_stride : token_stride;
         move = ahead * token_stride;
         p = base + first * token_stride;
         n = channels;
         at = 0;
         if constexpr (VEC) {
-            p += (lane / CH) * token_stride + lane % CH * PER;
-            at = (uint32_t)(((lane / CH) * ROW + lane % CH * PER) * sizeof(T));
-            n = lane % CH * PER < channels ? R : 0;  // rows to copy
+            const int row = wide ? lane / CH : 0, e = wide ? lane % CH * PER : lane * V;
+            p += row * token_stride + e;
+            at = (uint32_t)((row * ROW + e) * sizeof(T));
+            n = e < channels;
         }
     }
+    template <int BYTES>
+    static __device__ __forceinline__ void piece(uint32_t dst, const T* src) {
+        if constexpr (BYTES == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+    }
     __device__ __forceinline__ void copy(T* stage, int rows, int lane) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(stage) + at;
+        const T* q = p;
         if constexpr (VEC) {
-            if (n) {
-                const uint32_t d = (uint32_t)__cvta_generic_to_shared(stage) + at;
-                const T* q = p;
+            if (!n) return;
+            if (wide) {
 #pragma unroll
                 for (int k = 0; k < R / STEP; ++k) {
-                    if (rows >= R || k * STEP + lane / CH < rows)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + k * STEP * ROW * (int)sizeof(T)), "l"(q)
-                                     : "memory");
+                    if (rows >= R || k * STEP + lane / CH < rows) piece<16>(d + k * STEP * ROW * (int)sizeof(T), q);
+                    q += ts;
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (r < rows) piece<V * sizeof(T)>(d + r * ROW * (int)sizeof(T), q);
                     q += ts;
                 }
             }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (r < rows && k * 32 + lane < n) piece<4>(d + (r * ROW + k * 32 + lane) * 4, q + k * 32 + lane);
+                q += ts;
+            }
         } else {
+            T t[R][V];  // all loads before the first store
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (r < rows && k * 32 + lane < n) t[r][k] = q[k * 32 + lane];
+                q += ts;
+            }
+#pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    if (r < rows && k * 32 + lane < n) stage[r * ROW + k * 32 + lane] = p[r * ts + k * 32 + lane];
+                    if (r < rows && k * 32 + lane < n) stage[r * ROW + k * 32 + lane] = t[r][k];
         }
     }
 };
@@ -500,8 +533,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = rank * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, ts, K * L, lane);
-    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, HEAD ? 0 : ts, K * L, lane);
+    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, A.wide, ts, K * L, lane);
+    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, K * L, lane);
     HeadGates<XT, V, R, 2> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts < len) {
@@ -720,8 +753,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = ((iters - 1) * K + rank) * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, ts, -K * L, lane), sd(dy, A.dyts, A.C - c0, ts, -K * L, lane);
-    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, HEAD ? 0 : ts, -K * L, lane);
+    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, A.wide, ts, -K * L, lane), sd(dy, A.dyts, A.C - c0, A.wide, ts, -K * L, lane);
+    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, -K * L, lane);
     HeadGates<XT, V, R, 4> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts >= 0) {

@@ -21,8 +21,8 @@ lattice_status bwd_of(GatedArgs a, cudaStream_t st) {
 // whose stages are twice as large.
 template <class XT, int FORM, int ZM, bool VEC>
 lattice_status bwd(const GatedArgs& a, cudaStream_t st) {
-    if constexpr (ZM == kZHead) return bwd_of<XT, FORM, ZM, VEC, 4, sizeof(XT) == 2 ? 8 : 4, 2, 1>(a, st);
-    else return bwd_of<XT, FORM, ZM, VEC, 2, 4, 2, 2>(a, st);
+    if constexpr (ZM == kZHead) return bwd_of<XT, FORM, ZM, VEC, kGatedHeadVec, sizeof(XT) == 2 ? 8 : 4, 2, 1>(a, st);
+    else return bwd_of<XT, FORM, ZM, VEC, kGatedBwdVec, 4, 2, 2>(a, st);
 }
 
 template <class XT>

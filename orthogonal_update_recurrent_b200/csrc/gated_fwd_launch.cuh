@@ -11,7 +11,7 @@ namespace gated {
 // elements). fp32 rows are twice as wide, so runs of 8 keep the stages as large.
 template <class XT, int FORM, int ZM, bool VEC>
 lattice_status fwd(GatedArgs a, cudaStream_t st) {
-    constexpr int V = 2, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
+    constexpr int V = kGatedFwdVec, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
     a.K = cluster_ctas(a, NW * R, MINB);
     return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32,

@@ -193,10 +193,10 @@ int gated_form(lattice_gate gate, lattice_write write, float tau) {
 }
 
 // Whether the contiguous arrays of a gated call, whichever it has, and the channels suit
-// vectors of `bytes` bytes.
-bool gated_vec(const GatedArgs& a, size_t size, size_t bytes) {
-    return (size_t)a.C * size % bytes == 0 && aligned(a.y, bytes) && aligned(a.dx, bytes) && aligned(a.h0, 16) &&
-           aligned(a.h_out, 16) && aligned(a.dh_T, 16) && aligned(a.dh0, 16) && aligned(a.marks, 16);
+// vectors of v elements of x's size, and of fp32.
+bool gated_vec(const GatedArgs& a, size_t size, size_t v) {
+    return a.C % v == 0 && aligned(a.y, v * size) && aligned(a.dx, v * size) && aligned(a.h0, 4 * v) &&
+           aligned(a.h_out, 4 * v) && aligned(a.dh_T, 4 * v) && aligned(a.dh0, 4 * v);
 }
 // Whether the rows at p do.
 bool rows_vec(const void* p, size_t size, int B, int T, long long bs, long long ts, size_t bytes) {
@@ -502,8 +502,11 @@ lattice_status lattice_gated_scan_fwd(const void* x, lattice_dtype x_dtype, long
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
     a.zwords = gate_words(z, H, a.zbs, a.zts);
     if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
-    const bool vec = gated_vec(a, type_size(x_dtype), 16) && rows_vec(x, type_size(x_dtype), B, T, a.xbs, a.xts, 16) &&
-                     (a.zhead || rows_vec(z, type_size(z_dtype), B, T, a.zbs, a.zts, 16));
+    const size_t sx_ = type_size(x_dtype), sz_ = type_size(z_dtype), v = kGatedFwdVec;
+    const bool vec = gated_vec(a, sx_, v) && rows_vec(x, sx_, B, T, a.xbs, a.xts, v * sx_) &&
+                     (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, v * sz_));
+    a.wide = vec && C % (16 / sx_) == 0 && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
+             (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, 16));
     return with_x(x_dtype, [&](auto t) {
         return gated::launch_fwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
     });
@@ -548,9 +551,12 @@ lattice_status lattice_gated_scan_bwd(const void* x, lattice_dtype x_dtype, long
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
     a.zwords = gate_words(z, H, a.zbs, a.zts);
     if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
-    const bool vec = gated_vec(a, sx_, 16) && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
-                     rows_vec(dy, sx_, B, T, a.dybs, a.dyts, 16) &&
-                     (a.zhead || (rows_vec(z, sz_, B, T, a.zbs, a.zts, 16) && aligned(dz, 16)));
+    const size_t v = a.zhead ? kGatedHeadVec : kGatedBwdVec;
+    const bool vec = gated_vec(a, sx_, v) && rows_vec(x, sx_, B, T, a.xbs, a.xts, v * sx_) &&
+                     rows_vec(dy, sx_, B, T, a.dybs, a.dyts, v * sx_) &&
+                     (a.zhead || (rows_vec(z, sz_, B, T, a.zbs, a.zts, v * sz_) && aligned(dz, v * sz_)));
+    a.wide = vec && C % (16 / sx_) == 0 && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
+             rows_vec(dy, sx_, B, T, a.dybs, a.dyts, 16) && (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, 16));
     return with_x(x_dtype, [&](auto t) {
         return gated::launch_bwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
     });
@@ -579,7 +585,7 @@ lattice_status lattice_gated_step(const float* h, float* h_out, const void* x, l
     a.B = B; a.T = 1; a.C = (int)C; a.d = d; a.tau = tau;
     a.z32 = z_dtype == LATTICE_F32; a.zhead = z_per_head != 0;
     if (gate == LATTICE_GATE_LOGIT && tau != 1.f) gated_poly(a);
-    const bool vec = gated_vec(a, sx_, kStepVec * sx_) && rows_vec(x, sx_, B, 1, a.xbs, 0, kStepVec * sx_) &&
+    const bool vec = gated_vec(a, sx_, kStepVec) && rows_vec(x, sx_, B, 1, a.xbs, 0, kStepVec * sx_) &&
                      (a.zhead || rows_vec(z, sz_, B, 1, a.zbs, 0, kStepVec * sz_));
     return with_x(x_dtype, [&](auto t) {
         return gated::launch_step<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));

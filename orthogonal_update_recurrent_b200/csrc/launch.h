@@ -40,8 +40,8 @@ int reg_cluster_capacity(int d);
 
 // tu_gated_fwd_*.cu, tu_gated_bwd_*.cu: gated linear recurrence, a unit per type of x
 // (ctiles, K set by the launch). form = 3 * gate form + write form (gated.cuh); vec: every
-// row can be read in aligned 16-byte pieces (the step: in aligned vectors of kStepVec elements)
-constexpr int kStepVec = 4;
+// row can be read in aligned vectors of the elements that a lane has
+constexpr int kGatedFwdVec = 2, kGatedBwdVec = 2, kGatedHeadVec = 4, kStepVec = 4;
 namespace gated {
 template <class XT> lattice_status launch_fwd(GatedArgs a, int form, bool vec, cudaStream_t st);
 template <class XT> lattice_status launch_step(const GatedArgs& a, int form, bool vec, cudaStream_t st);
