@@ -13,9 +13,8 @@ template <class XT, int FORM, int ZM, bool VEC>
 lattice_status fwd(GatedArgs a, cudaStream_t st) {
     constexpr int V = kGatedFwdVec, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
-    a.K = cluster_ctas(a, NW * R, MINB);
-    return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32,
-                  FwdLayout<XT, ZM, V, R, NW, NST>::bytes(a.K), st);
+    return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
+                  [](int K) { return FwdLayout<XT, ZM, V, R, NW, NST>::bytes(K); }, st);
 }
 
 template <class XT, int FORM, int ZM, bool VEC>

@@ -1,5 +1,6 @@
 // gated_launch.cuh -- what the launches of the gated recurrence's two directions share.
 #pragma once
+#include <atomic>
 #include <type_traits>
 
 #include "gated.cuh"
@@ -8,39 +9,57 @@
 namespace lattice {
 namespace gated {
 
-// CTAs per cluster: the most, by doubling, with which the grid is still resident at once
-// (`resident` CTAs per SM) and every CTA has a tile of the sequence. Measured (bf16, logit
-// gates): small training shape, 32 tiles of channels, 8 CTAs 11.5 us against 24.9 us on one;
-// long context, 32 tiles, 185 against 675 us; mid-size layer, 256 tiles, 72 us on one CTA
-// against 86 us on two.
-inline int cluster_ctas(const GatedArgs& a, int tile, int resident) {
-    const long long base = (long long)a.B * a.ctiles, most = (long long)resident * sm_count();
-    int K = 1;
-    while (K < kGatedMaxK && base * 2 * K <= most && (long long)K * tile < a.T) K *= 2;
-    return K;
-}
+// Launches `base` clusters of K CTAs, a.B * a.ctiles of them: the largest K with which all are
+// resident at once (up to `resident` CTAs per SM) and every CTA has a tile of the sequence.
+// Clusters lie within a GPC, which may hold fewer of a size than its SMs would, so the device
+// is asked (once per kernel, size and device). Measured (bf16, logit gates): small training
+// shape, 32 tiles of channels, 8 CTAs 11.8 us against 26.9 us on one; 50 tiles of 8192
+// tokens, 5 CTAs 43 us, 4 50 us, 6 (not all resident) 58 us; mid-size layer, 256 tiles,
+// 72 us on one CTA against 86 us on two.
+constexpr int kMaxDevices = 16;
 
-template <class Kernel>
-lattice_status launch(Kernel k, const GatedArgs& a, int threads, int smem, cudaStream_t st) {
-    const long long ctas = (long long)a.B * a.ctiles * a.K;
-    if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
+template <class Kernel, class Bytes>
+lattice_status launch(Kernel k, GatedArgs a, int threads, int tile, int resident, Bytes bytes, cudaStream_t st) {
+    static std::atomic<int> held[kMaxDevices][kGatedMaxK + 1];  // clusters of a size that the device holds, plus 1
+    const long long base = (long long)a.B * a.ctiles;
+    long long K = (long long)resident * sm_count() / base;
+    if (K > kGatedMaxK) K = kGatedMaxK;
+    if (K > ((long long)a.T + tile - 1) / tile) K = ((long long)a.T + tile - 1) / tile;
+    if (K < 1) K = 1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.K;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.K > 1 ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
+    for (;; --K) {
+        a.K = (int)K;
+        const int smem = bytes(a.K);
+        if (smem > 40 * 1024) {
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        cfg.dynamicSmemBytes = smem;
+        attr[0].val.clusterDim.x = (unsigned)K;
+        cfg.numAttrs = K > 1 ? 1 : 0;
+        if (base * K > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
+        cfg.gridDim = dim3((unsigned)(base * K));
+        if (K == 1) break;
+        int n = dev < kMaxDevices ? held[dev][K].load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+            if (e != cudaSuccess) return cuda_fail(e);
+            ++n;
+            if (dev < kMaxDevices) held[dev][K].store(n, std::memory_order_relaxed);
+        }
+        if (n - 1 >= base) break;
+    }
+    e = cudaLaunchKernelEx(&cfg, k, a);
     return e == cudaSuccess ? LATTICE_OK : cuda_fail(e);
 }
 
