@@ -327,11 +327,6 @@ __device__ __forceinline__ void store8(void* p, bool f32, long long row, const C
     for (int j = 0; j < Columns<V>::NV; ++j)
         if (c.has(j)) store<XT, V>(p, f32, row + c.at(j), f + j * V);
 }
-template <class XT, int V>
-__device__ __forceinline__ void clear8(Raw<XT, V>* r) {
-#pragma unroll
-    for (int j = 0; j < 8 / V; ++j) r[j] = Raw<XT, V>{};
-}
 __device__ __forceinline__ float both(F2 a) {
     float x, y;
     parts(a, x, y);
@@ -384,25 +379,30 @@ struct RowAt {
     }
 };
 
-// Types of a call beside its own XT, and its parts: Y32, R32: y, and residual, r and dr, are
-// fp32; each 0, 1, or -1 where the kernel reads the call's flags (rows without vectors, whose
-// every combination would be a kernel else). PRE: with the norm before the next block.
-template <class XT_, int V_, bool GATE_, int Y32_, int R32_, int PRE_>
+// Types of a call beside its own XT, and its parts. Y32; R32: y; residual, r and dr are fp32.
+// PRE: with the norm before the next block (-1: the call says). As run-time flags, types alone
+// cost the backward pass 20 of 71 instructions per element.
+template <class XT_, int V_, bool GATE_, bool Y32_, bool R32_, int PRE_>
 struct Form {
     using XT = XT_;
     static constexpr int V = V_;
     static constexpr bool GATE = GATE_;
-    static __device__ __forceinline__ bool y32(const NormArgs& A) { return Y32_ < 0 ? A.y32 : Y32_ == 1; }
-    static __device__ __forceinline__ bool r32(const NormArgs& A) { return R32_ < 0 ? A.r32 : R32_ == 1; }
+    static constexpr bool Y32 = Y32_, R32 = R32_;
     static __device__ __forceinline__ bool pre(bool runtime) { return PRE_ < 0 ? runtime : PRE_ == 1; }
 };
 
+// Threads of a CTA at most: 64 registers each forward (80 where rows are read element by
+// element), 128 backward.
+constexpr int kFwdThreads = 1024, kFwdOddThreads = 768, kBwdThreads = 512;
+
 template <class F, bool SUB>
-__global__ void __launch_bounds__(SUB ? 256 : 1024, SUB ? 4 : 1) norm_fwd_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(SUB ? 256 : F::V == 8 ? kFwdThreads : kFwdOddThreads, SUB ? (F::V == 8 ? 4 : 2) : 1)
+norm_fwd_kernel(const NormArgs A) {
     using XT = typename F::XT;
     constexpr int V = F::V, NV = 8 / V;
     constexpr bool GATE = F::GATE;
-    const bool y32 = F::y32(A), r32 = F::r32(A), pre = F::pre(A.n_out != nullptr);
+    constexpr bool y32 = F::Y32, r32 = F::R32;
+    const bool pre = F::pre(A.n_out != nullptr);
     extern __shared__ __align__(16) ulonglong2 own[];
     ulonglong2 *wq = own, *wp = own + 2 * blockDim.x;
     RowSums<SUB> sums(A);
@@ -468,11 +468,12 @@ __global__ void __launch_bounds__(SUB ? 256 : 1024, SUB ? 4 : 1) norm_fwd_kernel
 //   sum(du y) = sum(e t) = sum(dr t) + rho2 sum(m t) - k sum(r t), k = rho2^3 mean(m r),
 // is taken apart, so that it needs no exchange of its own after e is known.
 template <class F, bool SUB>
-__global__ void __launch_bounds__(SUB ? 256 : 512, SUB ? 2 : 1) norm_bwd_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd_kernel(const NormArgs A) {
     using XT = typename F::XT;
     constexpr int V = F::V, NV = 8 / V;
     constexpr bool GATE = F::GATE;
-    const bool y32 = F::y32(A), r32 = F::r32(A), pre = F::pre(A.dn != nullptr);
+    constexpr bool y32 = F::Y32, r32 = F::R32;
+    const bool pre = F::pre(A.dn != nullptr);
     extern __shared__ __align__(16) ulonglong2 own[];
     ulonglong2 *wq = own, *wp = own + 2 * blockDim.x, *dq = own + 4 * blockDim.x, *dp = own + 6 * blockDim.x;
     RowSums<SUB> sums(A);
@@ -488,10 +489,7 @@ __global__ void __launch_bounds__(SUB ? 256 : 512, SUB ? 2 : 1) norm_bwd_kernel(
     const unsigned N = (unsigned)A.N, step = gridDim.x / sums.K * rows;
     Raw<XT, V> ry[NV] = {}, rg[NV] = {}, rr[NV] = {}, rd[NV] = {}, rn[NV] = {};
     auto fetch = [&](unsigned i) {
-        if (i >= N) {  // rows past the last (a CTA's rows side by side) count as 0
-            if constexpr (SUB) clear8(ry), clear8(rr), clear8(rd), clear8(rn);
-            return;
-        }
+        if (i >= N) return;
         const RowAt at(A, i);
         load8<XT, V>(ry, A.y, y32, at.in(A, A.ys), c);
         if constexpr (GATE) load8<XT, V>(rg, A.gate, false, at.in(A, A.gs), c);
@@ -517,7 +515,11 @@ __global__ void __launch_bounds__(SUB ? 256 : 512, SUB ? 2 : 1) norm_bwd_kernel(
             if (A.residual) values8<XT, V>(rr, r32, r);
             values8<XT, V>(rn, false, m);
         }
-        fetch(i + step);
+        if (SUB && first + rows > N && !in) {  // the last turn's rows past the end count as 0
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] = e[v] = r[v] = m[v] = f[v] = f2(0.f);
+        }
+        fetch(i + step);  // the next row's values are on their way during this row's sums
         float s[5], rho1 = 1.f, k = 0.f;
         s[0] = dot8(y, y);
         own_read(wq, w);

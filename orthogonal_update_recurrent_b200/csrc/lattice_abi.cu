@@ -622,7 +622,7 @@ lattice_status lattice_block_norm_fwd(const void* y, lattice_dtype y_dtype, long
                      norm_rows_vec(residual, residual_dtype, N, G, residual_stride) && aligned(w_post, 16) &&
                      aligned(w_pre, 16) && aligned(r_out, 16) && aligned(n_out, 16);
     return with_x(dtype, [&](auto t) {
-        return norm::launch_norm<decltype(t)>(false, a, vec, static_cast<cudaStream_t>(stream));
+        return norm::launch_norm<decltype(t)>(false, a, vec, nullptr, static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -693,8 +693,9 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
                      norm_rows_vec(dr, dr_dtype, N, G, dr_stride) && norm_rows_vec(dn, dtype, N, G, dn_stride) &&
                      aligned(w_post, 16) && aligned(w_pre, 16) && aligned(dy, 16) && aligned(dgate, 16) &&
                      aligned(dresidual, 16);
-    s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, vec, st); });
-    return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, dw_post, dw_pre, st);
+    int groups = 0;
+    s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, vec, &groups, st); });
+    return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, groups, dw_post, dw_pre, st);
 }
 
 lattice_status lattice_selftest_bounded_wait(unsigned long long limit_ns, void* stream) {

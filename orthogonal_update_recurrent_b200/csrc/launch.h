@@ -49,12 +49,13 @@ template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, c
 }  // namespace gated
 
 // tu_norm_*.cu: norms after and before a block, a unit per type of the call (tpr, K set by the
-// launch). vec: rows and weights can be read in aligned vectors of 8 elements
+// launch). vec: rows and weights can be read in aligned vectors of 8 elements; groups
+// (or null): how many rows of weight gradients the backward pass leaves in the workspace
 namespace norm {
-template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, bool vec, cudaStream_t st);
+template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st);
 }  // namespace norm
-int norm_parts(long long N, int D);  // rows of the backward pass's workspace
-lattice_status launch_norm_dw(const NormArgs& a, float* dw_post, float* dw_pre, cudaStream_t st);
+int norm_parts(long long N, int D);  // at most so many
+lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st);
 
 // each unit's device status word (read, and zeroed when set)
 cudaError_t status_simt_exact(unsigned int* v);

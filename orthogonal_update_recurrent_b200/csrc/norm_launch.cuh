@@ -1,22 +1,23 @@
 // norm_launch.cuh -- launches of the block norms' kernels (block_norm.cuh), instantiated per
 // type of the call in tu_norm_*.cu.
 #pragma once
+#include <atomic>
+
 #include "block_norm.cuh"
 #include "launch.h"
 
 namespace lattice {
 namespace norm {
 
-// 64 and 128 registers per thread: threads of a CTA at most, and resident on an SM.
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;
-inline int most_threads(bool bwd) { return bwd ? kBwdThreads : kFwdThreads; }
+inline int most_threads(bool bwd, bool vec) { return bwd ? kBwdThreads : vec ? kFwdThreads : kFwdOddThreads; }
 
 // 8 elements per thread: a row's CTAs (1, 2 or 4) and its threads in each, a power of two
 // within a warp and whole warps above.
 struct Split {
     int K, tpr, threads, rows;  // threads of a CTA, rows that it takes at once
-    Split(int D, bool bwd) : K(1) {
-        while (K * most_threads(bwd) * 8 < D) K *= 2;
+    int most, resident;
+    Split(int D, bool bwd, bool vec) : K(1), most(most_threads(bwd, vec)), resident(bwd ? kBwdThreads : kFwdThreads) {
+        while (K * most * 8 < D) K *= 2;
         const int need = (D + 8 * K - 1) / (8 * K);
         tpr = 1;
         if (need > 32) tpr = (need + 31) / 32 * 32;
@@ -25,23 +26,29 @@ struct Split {
         threads = tpr > 32 ? tpr : 256;
         rows = threads / tpr;
     }
-    // groups of K CTAs that take N rows: as many as are resident at once, or fewer
-    long long groups(long long N, bool bwd) const {
-        const long long turns = (N + rows - 1) / rows, most = (long long)sm_count() * (most_threads(bwd) / threads) / K;
-        return turns < most ? turns : most;
+    // groups of K CTAs that take N rows: at most what `resident` threads per SM are
+    long long groups(long long N) const {
+        const long long turns = (N + rows - 1) / rows, at_once = (long long)sm_count() * (resident / threads) / K;
+        return turns < at_once ? turns : at_once;
     }
 };
 
+// The grid is what the device holds at once, or fewer: it is asked once per kernel, CTA size and
+// device. (Clusters lie within a GPC, which may hold fewer than its SMs would: 4096 rows of
+// 16384, backward: 543 us with a cluster of 4 for every 4 SMs, 316 us with as many as are held.)
+constexpr int kMaxDevices = 16;
+
 template <class Kernel>
-lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int bytes_per_thread, cudaStream_t st) {
-    const Split split(a.D, bwd);
+lattice_status launch(Kernel k, const NormArgs& a, bool bwd, bool vec, int bytes_per_thread, int* groups, cudaStream_t st) {
+    const Split split(a.D, bwd, vec);
     const int threads = split.threads, smem = threads * bytes_per_thread;
+    cudaError_t e;
     if (smem > 40 * 1024) {  // 48 KB with the static arrays
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(split.groups(a.N, bwd) * split.K));
+    cfg.gridDim = dim3((unsigned)a.K);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -52,39 +59,59 @@ lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int bytes_per_threa
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.K > 1 ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
+    static std::atomic<int> held[kMaxDevices][33][3];  // by warps of a CTA, and K: 1, 2, 4
+    int dev = 0, c = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::atomic<int>* slot = dev < kMaxDevices ? &held[dev][threads / 32][a.K / 2] : nullptr;
+    if (slot) c = slot->load(std::memory_order_relaxed);
+    if (c == 0) {
+        e = a.K > 1 ? cudaOccupancyMaxActiveClusters(&c, k, &cfg)
+                    : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c, k, threads, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (a.K == 1) c *= sm_count();
+        if (c < 1) return LATTICE_ERR_UNSUPPORTED;
+        if (slot) slot->store(c, std::memory_order_relaxed);
+    }
+    long long n = split.groups(a.N);
+    if (n > c) n = c;
+    cfg.gridDim = dim3((unsigned)(n * a.K));
+    if (groups) *groups = (int)n;
+    e = cudaLaunchKernelEx(&cfg, k, a);
     return e == cudaSuccess ? LATTICE_OK : cuda_fail(e);
 }
 
 template <class F, bool SUB>
-lattice_status run(bool bwd, const NormArgs& a, cudaStream_t st) {
-    return bwd ? launch(norm_bwd_kernel<F, SUB>, a, true, 128, st) : launch(norm_fwd_kernel<F, SUB>, a, false, 64, st);
+lattice_status run(bool bwd, const NormArgs& a, int* groups, cudaStream_t st) {
+    return bwd ? launch(norm_bwd_kernel<F, SUB>, a, true, F::V == 8, 128, groups, st)
+               : launch(norm_fwd_kernel<F, SUB>, a, false, F::V == 8, 64, groups, st);
 }
 
 template <class T, bool SUB, bool GATE, int Y32, int R32>
-lattice_status run_vec(bool bwd, const NormArgs& a, cudaStream_t st) {
-    return (bwd ? a.dn : a.n_out) ? run<Form<T, 8, GATE, Y32, R32, 1>, SUB>(bwd, a, st)
-                                  : run<Form<T, 8, GATE, Y32, R32, 0>, SUB>(bwd, a, st);
+lattice_status run_typed(bool bwd, const NormArgs& a, bool vec, int* groups, cudaStream_t st) {
+    if (!vec) return run<Form<T, 1, GATE, Y32, R32, -1>, SUB>(bwd, a, groups, st);
+    return (bwd ? a.dn : a.n_out) ? run<Form<T, 8, GATE, Y32, R32, 1>, SUB>(bwd, a, groups, st)
+                                  : run<Form<T, 8, GATE, Y32, R32, 0>, SUB>(bwd, a, groups, st);
 }
 
 template <class T, bool SUB, bool GATE>
-lattice_status run_types(bool bwd, const NormArgs& a, bool vec, cudaStream_t st) {
-    if (!vec) return run<Form<T, 1, GATE, -1, -1, -1>, SUB>(bwd, a, st);
+lattice_status run_types(bool bwd, const NormArgs& a, bool vec, int* groups, cudaStream_t st) {
     if constexpr (sizeof(T) == 2) {
-        if (a.y32) return a.r32 ? run_vec<T, SUB, GATE, 1, 1>(bwd, a, st) : run_vec<T, SUB, GATE, 1, 0>(bwd, a, st);
-        return a.r32 ? run_vec<T, SUB, GATE, 0, 1>(bwd, a, st) : run_vec<T, SUB, GATE, 0, 0>(bwd, a, st);
+        if (a.y32)
+            return a.r32 ? run_typed<T, SUB, GATE, 1, 1>(bwd, a, vec, groups, st) : run_typed<T, SUB, GATE, 1, 0>(bwd, a, vec, groups, st);
+        return a.r32 ? run_typed<T, SUB, GATE, 0, 1>(bwd, a, vec, groups, st) : run_typed<T, SUB, GATE, 0, 0>(bwd, a, vec, groups, st);
     } else {
-        return run_vec<T, SUB, GATE, 1, 1>(bwd, a, st);
+        return run_typed<T, SUB, GATE, 1, 1>(bwd, a, vec, groups, st);
     }
 }
 
 template <class T>
-lattice_status launch_norm(bool bwd, NormArgs a, bool vec, cudaStream_t st) {
-    const Split split(a.D, bwd);
+lattice_status launch_norm(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st) {
+    const Split split(a.D, bwd, vec);
     a.tpr = split.tpr;
     a.K = split.K;
-    if (a.tpr <= 32) return a.gate ? run_types<T, true, true>(bwd, a, vec, st) : run_types<T, true, false>(bwd, a, vec, st);
-    return a.gate ? run_types<T, false, true>(bwd, a, vec, st) : run_types<T, false, false>(bwd, a, vec, st);
+    if (a.tpr <= 32) return a.gate ? run_types<T, true, true>(bwd, a, vec, groups, st) : run_types<T, true, false>(bwd, a, vec, groups, st);
+    return a.gate ? run_types<T, false, true>(bwd, a, vec, groups, st) : run_types<T, false, false>(bwd, a, vec, groups, st);
 }
 
 }  // namespace norm

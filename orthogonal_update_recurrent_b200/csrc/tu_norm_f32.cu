@@ -4,12 +4,12 @@
 
 namespace lattice {
 
-template lattice_status norm::launch_norm<float>(bool bwd, NormArgs a, bool vec, cudaStream_t st);
+template lattice_status norm::launch_norm<float>(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st);
 
-int norm_parts(long long N, int D) { return (int)norm::Split(D, true).groups(N, true); }
+int norm_parts(long long N, int D) { return (int)norm::Split(D, true, true).groups(N); }
 
-lattice_status launch_norm_dw(const NormArgs& a, float* dw_post, float* dw_pre, cudaStream_t st) {
-    norm::norm_dw_kernel<32><<<(unsigned)((2 * a.D + 31) / 32), 1024, 0, st>>>(a.parts, norm_parts(a.N, a.D), a.D, a.scale,
+lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st) {
+    norm::norm_dw_kernel<32><<<(unsigned)((2 * a.D + 31) / 32), 1024, 0, st>>>(a.parts, groups, a.D, a.scale,
                                                                              dw_post, dw_pre);
     return launch_status();
 }
