@@ -12,8 +12,9 @@ events on the launching stream.
 
 The same JSON line also reports, under "extra", the small training shape and the
 mid-size layer (each with its own roofline record), the exact recurrence, the
-chunk-form variants, the backward pass and the decode step (1000 consecutive
-steps of B=256, H=32, m=d=128).
+chunk-form variants, the backward pass, the gated recurrence and the block norms on
+the mid-size layer, and the decode step (1000 consecutive steps of B=256, H=32,
+m=d=128).
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 
@@ -74,6 +75,13 @@ def bwd_alg_bytes(w: LI.Workload) -> int:
     qb = 2 if w.q_dtype == "bf16" else 4
     per_tok = (w.d * xb + w.m * qb + 4 * w.m + 4 + 4 * w.d) + (4 * w.d + 8 * w.m + 4)
     return w.B * w.T * w.H * per_tok + 3 * 4 * w.B * w.H * w.m * w.d
+
+
+def gated_alg_bytes(w: LI.Workload, bwd: bool) -> int:
+    """Algorithmic HBM bytes of the gated recurrence, bf16 x and gate per channel: forward
+    x, z and y; backward x, z, dy, dx and dz; the fp32 states at either end."""
+    n = w.B * w.T * w.H * w.d
+    return 2 * n * (5 if bwd else 3) + 4 * w.B * w.H * w.d
 
 
 def chunk_mma_flops(w: LI.Workload, C: int, B=None, T=None, H=None) -> int:
@@ -308,6 +316,53 @@ def time_bwd(torch, L, t, chunk, steps, warmup, flush=None):
     torch.cuda.synchronize()
     L.device_status()
     return [e0.elapsed_time(e1) for e0, e1 in ev]
+
+
+def time_calls(torch, f, steps, warmup, flush=None):
+    """Milliseconds of each call of f, by events on the current stream."""
+    for _ in range(warmup):
+        f()
+    times = []
+    for _ in range(steps):
+        if flush is not None:
+            flush.zero_()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return times
+
+
+def layer_ops(torch, L, w: LI.Workload, device, flush, pk) -> dict:
+    """The gated recurrence and the block norms on a workload's shape (bf16, logit gates):
+    what a layer of this size runs beside the state scan. Bytes count every input read
+    once and every output written once."""
+    gen = torch.Generator(device=device)
+    gen.manual_seed(w.seed)
+    n = lambda *s, dt=torch.bfloat16: torch.randn(s, generator=gen, device=device).to(dt)  # noqa: E731
+    x, z, dy = n(w.B, w.T, w.H, w.d), n(w.B, w.T, w.H, w.d) + 3, n(w.B, w.T, w.H, w.d)
+    y, marks = torch.empty_like(x), L.gated_scan_marks(x)
+    els = x.numel()
+    out = {}
+
+    def add(name, f, nbytes, kernel):
+        ms = statistics.mean(time_calls(torch, f, 10, 3, flush))
+        out[name] = {"ms": ms, "kernel": kernel, "alg_bytes": nbytes, "gbps": nbytes / ms / 1e6,
+                     "hbm_frac": nbytes / ms / 1e6 / pk["hbm_gbs"]}
+    add("gated_scan_fwd", lambda: L.gated_scan_fwd(x, z, y=y, marks=marks), gated_alg_bytes(w, False), "gated_fwd_kernel")
+    add("gated_scan_bwd", lambda: L.gated_scan_bwd(x, z, dy, marks), gated_alg_bytes(w, True), "gated_bwd_kernel")
+    del z, marks
+    ro, res = y.float(), n(w.B, w.T, w.H * w.d, dt=torch.float32)
+    wd, wD = torch.ones(w.d, device=device), torch.ones(w.H * w.d, device=device)
+    u = x.flatten(-2)
+    add("readout_norm_gate", lambda: L.block_norm_fwd(ro, wd, gate=x, out_dtype=x.dtype), els * 8, "norm_fwd_kernel")
+    add("readout_norm_gate_bwd", lambda: L.block_norm_bwd(ro, wd, gate=x, dr=dy), els * 14, "norm_bwd_kernel")
+    add("residual_norms", lambda: L.block_norm_fwd(u, wD, residual=res, w_pre=wD), els * 12, "norm_fwd_kernel")
+    add("residual_norms_bwd", lambda: L.block_norm_bwd(u, wD, residual=res, w_pre=wD, dr=res, dn=u), els * 18,
+        "norm_bwd_kernel")
+    return out
 
 
 def time_scan_e2e(torch, L, inp, chunk, steps, warmup, device):
@@ -746,6 +801,9 @@ def main():
                 extra[name] = ent
                 del tn
                 torch.cuda.empty_cache()
+            # the gated recurrence and the norms around a block, on the mid-size layer
+            extra["layer_ops_mid_layer"] = layer_ops(torch, L, LI.WORKLOADS["mid_layer"], device, flush, pk)
+            torch.cuda.empty_cache()
             # chunk-form variants and the backward pass on the small training shape
             ws = LI.WORKLOADS["small_train"]
             ts = _dev_inputs(torch, LI.make_inputs(ws), device)

@@ -11,6 +11,14 @@ import norm_ref
 H = 1e-5
 
 
+def test_bench_byte_models():
+    import bench
+    import lattice_inputs as LI
+    w = LI.WORKLOADS["mid_layer"]  # 8 * 4096 * 16 * 128 elements, 16 * 128 channels of 8 sequences
+    assert bench.gated_alg_bytes(w, False) == 67108864 * 6 + 8 * 2048 * 4
+    assert bench.gated_alg_bytes(w, True) == 67108864 * 10 + 8 * 2048 * 4
+
+
 def differences(loss, t):
     out = torch.zeros_like(t)
     flat, grad = t.view(-1), out.view(-1)
