@@ -360,7 +360,9 @@ def layer_ops(torch, L, w: LI.Workload, device, flush, pk) -> dict:
     add("readout_norm_gate", lambda: L.block_norm_fwd(ro, wd, gate=x, out_dtype=x.dtype), els * 8, "norm_fwd_kernel")
     add("readout_norm_gate_bwd", lambda: L.block_norm_bwd(ro, wd, gate=x, dr=dy), els * 14, "norm_bwd_kernel")
     add("residual_norms", lambda: L.block_norm_fwd(u, wD, residual=res, w_pre=wD), els * 12, "norm_fwd_kernel")
-    add("residual_norms_bwd", lambda: L.block_norm_bwd(u, wD, residual=res, w_pre=wD, dr=res, dn=u), els * 18,
+    del ro
+    dr, dn = n(w.B, w.T, w.H * w.d, dt=torch.float32), dy.flatten(-2)
+    add("residual_norms_bwd", lambda: L.block_norm_bwd(u, wD, residual=res, w_pre=wD, dr=dr, dn=dn), els * 18,
         "norm_bwd_kernel")
     return out
 
