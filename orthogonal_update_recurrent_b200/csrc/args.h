@@ -95,7 +95,7 @@ inline size_t chunk_bwd_ws_floats(int B, int T, int H, int m, int D, int chunk) 
 
 // gated.cuh: gated linear recurrence
 constexpr int kGatedMark = 16;  // tokens between the states the forward pass leaves for the backward pass
-constexpr int kGatedMaxK = 8;   // CTAs of a cluster at most
+constexpr int kGatedMaxK = 16;  // CTAs of a cluster at most
 
 constexpr int kGatedMaxSize = 1 << 30;  // channels, and tokens: tile indices stay within int
 

@@ -104,7 +104,7 @@ __device__ __forceinline__ F2 expm1_small(F2 w) {
 // be: with t = exp(-z), r = 1/(1 + t) gets one Newton step, a = r (2 - (1 + t) r), and 1 - a is
 // t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126. With
 // tau, `fast` says that the run has no z < 0 and tau <= 1, which leaves out what those need
-// (long context SEEPOLY us; by log(1 + t) and exp, for every z, 307 us).
+// (long context 259 us; by log(1 + t) and exp, for every z, 307 us).
 template <int GATE>
 __device__ __forceinline__ void gates_of(F2 z, const GatedArgs& A, bool fast, F2& a, F2& q) {
     if constexpr (GATE == kValue) {

@@ -9,6 +9,7 @@ namespace gated {
 template <class XT, int FORM, int ZM, bool VEC, int V, int NW, int NST, int MINB>
 lattice_status bwd_of(GatedArgs a, cudaStream_t st) {
     constexpr int R = kGatedMark;
+    static_assert(BwdLayout<XT, ZM, V, R, NW, NST>::bytes(kGatedMaxK) <= kMaxShared, "every cluster size fits");
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
     return launch(gated_bwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
                   [](int K) { return BwdLayout<XT, ZM, V, R, NW, NST>::bytes(K); }, st);

@@ -7,11 +7,12 @@ namespace lattice {
 namespace gated {
 
 // Two channels per lane; runs of 16 tokens on 8 warps, two CTAs per SM (mid-size layer, bf16:
-// 72 us; runs of 8 on three CTAs 86 us: a run's exchange is then spread over half the
+// 78 us; runs of 8 on three CTAs 86 us: a run's exchange is then spread over half the
 // elements). fp32 rows are twice as wide, so runs of 8 keep the stages as large.
 template <class XT, int FORM, int ZM, bool VEC>
 lattice_status fwd(GatedArgs a, cudaStream_t st) {
     constexpr int V = kGatedFwdVec, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
+    static_assert(FwdLayout<XT, ZM, V, R, NW, NST>::bytes(kGatedMaxK) <= kMaxShared, "every cluster size fits");
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
     return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
                   [](int K) { return FwdLayout<XT, ZM, V, R, NW, NST>::bytes(K); }, st);

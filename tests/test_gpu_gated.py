@@ -92,6 +92,12 @@ def test_long_sequence_of_few_channels_spreads_over_a_cluster(L):
     both(L, make(1, 6000, 1, 24, mean=6.0, seed=5, lengths=[4321]), write="leaky", tau=0.25)
 
 
+@pytest.mark.parametrize("dtype,zdtype,d,head", [("bf16", "bf16", 37, False), ("f16", "f32", 64, False),
+                                                 ("bf16", "bf16", 64, True), ("f32", "f32", 64, True)])
+def test_long_sequences_in_clusters_above_the_portable_size(L, dtype, zdtype, d, head):
+    both(L, make(2, 4700, 1, d, dtype=dtype, zdtype=zdtype, head=head, mean=5.0, seed=11, lengths=[4700, 2063]), write="unit")
+
+
 def test_no_initial_state_and_no_final_cotangent(L):
     both(L, make(2, 100, 1, 20, seed=6), h0=False, dh_T=False)
 
