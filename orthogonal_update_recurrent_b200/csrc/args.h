@@ -122,6 +122,7 @@ struct GatedArgs {
 };
 
 // block_norm.cuh: norms after and before a block
+constexpr int kNormOdd = 0, kNormVec = 1, kNormShift = 2;  // how rows are read
 constexpr int kNormMaxD = 16384;
 constexpr long long kNormMaxStride = 0x7fffffff;
 

@@ -281,21 +281,58 @@ struct RowSums {
     }
 };
 
-// A thread's columns: 8, next to each other (V = 8) or tpr apart (V = 1).
-template <int V>
+// How a thread reads its 8 columns of a row: one by one, tpr apart; as a vector; or as a vector
+// that starts up to 7 columns before the row does. The last is for widths that are no
+// multiple of 8: row i starts m = i D mod 8 elements past a multiple of 16 bytes, and the grid's
+// step is a multiple of 8 rows (of 8/gcd(D, 8)), so that m, and with it a thread's columns, are
+// the same in all its rows. Only a row's two outer vectors, the edges, have columns of other
+// rows: they are put to 0 after the load and left out of the store (bf16, one by one and
+// so: 16384 rows of 2055, both norms, forward 106 and 66 us, backward 262 and 223 us; 8192 rows of
+// 6055 with a gate, 117 and 86 us, 442 and 209 us).
+constexpr int kOdd = kNormOdd, kVec = kNormVec, kShift = kNormShift;
+
+template <int MODE>
 struct Columns {
-    static constexpr int NV = 8 / V;
+    static constexpr int V = MODE == kOdd ? 1 : 8, NV = 8 / V;
     int first, step, D;
-    __device__ __forceinline__ Columns(const NormArgs& A, int rank, int tid)
-        : first(rank * A.tpr * 8 + tid * V), step(A.tpr), D(A.D) {}
+    __device__ __forceinline__ Columns(const NormArgs& A, int rank, int tid, unsigned row)
+        : first(rank * A.tpr * 8 + tid * V - (MODE == kShift ? (int)(row * (unsigned)A.D & 7u) : 0)), step(A.tpr), D(A.D) {}
     __device__ __forceinline__ int at(int j) const { return first + j * step; }
     __device__ __forceinline__ bool has(int j) const { return at(j) < D; }
+    __device__ __forceinline__ bool edge() const { return MODE == kShift && (first < 0 || first + 8 > D); }
+    __device__ __forceinline__ bool mine(int v) const { return (unsigned)(first + v) < (unsigned)D; }  // the vector's v-th
 };
-template <class XT, int V>
-__device__ __forceinline__ void load8(Raw<XT, V>* r, const void* p, bool f32, long long row, const Columns<V>& c) {
+// `inside`: the row's outer vectors lie within the array, too
+template <class XT, int MODE>
+__device__ __forceinline__ void load8(Raw<XT, Columns<MODE>::V>* r, const void* p, bool f32, long long row,
+                                      const Columns<MODE>& c, bool inside = true) {
+    constexpr int V = Columns<MODE>::V;
+    if (MODE == kShift && !inside && c.edge()) {
 #pragma unroll
-    for (int j = 0; j < Columns<V>::NV; ++j)
+        for (int v = 0; v < 8; ++v) {
+            if (!c.mine(v)) continue;
+            const Raw<XT, 1> e = load<XT, 1>(p, f32, row + c.first + v);
+            if (sizeof(XT) == 4 || f32) r[0].w[v % V] = e.w[0];
+            else r[0].w[v / 2 % V] = v & 1 ? (r[0].w[v / 2 % V] & 0xffffu) | e.w[0] << 16 : e.w[0];
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < Columns<MODE>::NV; ++j)
         if (c.has(j)) r[j] = load<XT, V>(p, f32, row + c.at(j));
+}
+// Puts the columns of other rows to 0.
+template <class XT, int MODE>
+__device__ __forceinline__ void trim8(Raw<XT, Columns<MODE>::V>* r, bool f32, const Columns<MODE>& c) {
+    if constexpr (MODE == kShift) {
+        if (!c.edge()) return;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            if (c.mine(v)) continue;
+            if (sizeof(XT) == 4 || f32) r[0].w[v] = 0u;
+            else r[0].w[v / 2] &= v & 1 ? 0xffffu : 0xffff0000u;
+        }
+    }
 }
 // The 8 values as four pairs.
 template <class XT, int V>
@@ -318,13 +355,20 @@ __device__ __forceinline__ void values8(const Raw<XT, V>* r, bool f32, F2* f) {
         }
     }
 }
-template <class XT, int V>
-__device__ __forceinline__ void store8(void* p, bool f32, long long row, const Columns<V>& c, const F2* q) {
+template <class XT, int MODE>
+__device__ __forceinline__ void store8(void* p, bool f32, long long row, const Columns<MODE>& c, const F2* q) {
+    constexpr int V = Columns<MODE>::V;
     float f[8];
 #pragma unroll
     for (int v = 0; v < 4; ++v) parts(q[v], f[2 * v], f[2 * v + 1]);
+    if (c.edge()) {
 #pragma unroll
-    for (int j = 0; j < Columns<V>::NV; ++j)
+        for (int v = 0; v < 8; ++v)
+            if (c.mine(v)) store<XT, 1>(p, f32, row + c.first + v, f + v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < Columns<MODE>::NV; ++j)
         if (c.has(j)) store<XT, V>(p, f32, row + c.at(j), f + j * V);
 }
 __device__ __forceinline__ float both(F2 a) {
@@ -350,8 +394,9 @@ __device__ __forceinline__ void own_write(ulonglong2* p, const F2* f) {
 }
 // The columns' weights into the thread's shared memory: w_post with the scale, w_pre. Columns
 // past the row's end have weight 0, and their values stay 0 all the way.
-template <class XT, int V>
-__device__ __forceinline__ void keep_weights(const NormArgs& A, const Columns<V>& c, ulonglong2* wq, ulonglong2* wp) {
+template <class XT, int MODE>
+__device__ __forceinline__ void keep_weights(const NormArgs& A, const Columns<MODE>& c, ulonglong2* wq, ulonglong2* wp) {
+    constexpr int V = Columns<MODE>::V;
     Raw<XT, V> raw[8 / V] = {};
     F2 f[4];
     for (int k = 0; k < 2; ++k) {
@@ -359,8 +404,19 @@ __device__ __forceinline__ void keep_weights(const NormArgs& A, const Columns<V>
 #pragma unroll
         for (int v = 0; v < 4; ++v) f[v] = f2(1.f);
         if (w) {
-            load8<XT, V>(raw, w, A.w32, 0, c);
-            values8<XT, V>(raw, A.w32, f);
+            if constexpr (MODE == kShift) {
+                float t[8];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    t[v] = 0.f;
+                    if (c.mine(v)) values<XT, 1>(load<XT, 1>(w, A.w32, c.first + v), A.w32, t + v);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) f[v] = f2(t[2 * v], t[2 * v + 1]);
+            } else {
+                load8<XT, MODE>(raw, w, A.w32, 0, c);
+                values8<XT, V>(raw, A.w32, f);
+            }
         }
         if (!k)
 #pragma unroll
@@ -382,10 +438,10 @@ struct RowAt {
 // Types of a call beside its own XT, and its parts. Y32; R32: y; residual, r and dr are fp32.
 // PRE: with the norm before the next block (-1: the call says). As run-time flags, types alone
 // cost the backward pass 20 of 71 instructions per element.
-template <class XT_, int V_, bool GATE_, bool Y32_, bool R32_, int PRE_>
+template <class XT_, int MODE_, bool GATE_, bool Y32_, bool R32_, int PRE_>
 struct Form {
     using XT = XT_;
-    static constexpr int V = V_;
+    static constexpr int MODE = MODE_, V = MODE == kOdd ? 1 : 8;
     static constexpr bool GATE = GATE_;
     static constexpr bool Y32 = Y32_, R32 = R32_;
     static __device__ __forceinline__ bool pre(bool runtime) { return PRE_ < 0 ? runtime : PRE_ == 1; }
@@ -399,7 +455,7 @@ template <class F, bool SUB>
 __global__ void __launch_bounds__(SUB ? 256 : F::V == 8 ? kFwdThreads : kFwdOddThreads, SUB ? (F::V == 8 ? 4 : 2) : 1)
 norm_fwd_kernel(const NormArgs A) {
     using XT = typename F::XT;
-    constexpr int V = F::V, NV = 8 / V;
+    constexpr int MODE = F::MODE, V = F::V, NV = 8 / V;
     constexpr bool GATE = F::GATE;
     constexpr bool y32 = F::Y32, r32 = F::R32;
     const bool pre = F::pre(A.n_out != nullptr);
@@ -408,26 +464,33 @@ norm_fwd_kernel(const NormArgs A) {
     RowSums<SUB> sums(A);
     const int tid = SUB ? threadIdx.x % A.tpr : threadIdx.x;
     const unsigned rows = SUB ? blockDim.x / A.tpr : 1, lane_row = SUB ? threadIdx.x / A.tpr : 0;
-    const Columns<V> c(A, sums.rank, tid);
-    keep_weights<XT, V>(A, c, wq, wp);
+    const unsigned row0 = blockIdx.x / sums.K * rows;
+    const Columns<MODE> c(A, sums.rank, tid, row0 + lane_row);
+    keep_weights<XT, MODE>(A, c, wq, wp);
     const unsigned N = (unsigned)A.N, step = gridDim.x / sums.K * rows;
     Raw<XT, V> ry[NV] = {}, rg[NV] = {}, rr[NV] = {};
     auto fetch = [&](unsigned i) {
         if (i >= N) return;
         const RowAt at(A, i);
-        load8<XT, V>(ry, A.y, y32, at.in(A, A.ys), c);
-        if constexpr (GATE) load8<XT, V>(rg, A.gate, false, at.in(A, A.gs), c);
-        if (A.residual) load8<XT, V>(rr, A.residual, r32, at.in(A, A.rs), c);
+        const bool inside = i + 8 < N;  // the rows behind it hold a vector's columns past its end
+        load8<XT, MODE>(ry, A.y, y32, at.in(A, A.ys), c, inside);
+        if constexpr (GATE) load8<XT, MODE>(rg, A.gate, false, at.in(A, A.gs), c, inside);
+        if (A.residual) load8<XT, MODE>(rr, A.residual, r32, at.in(A, A.rs), c, inside);
     };
-    unsigned first = blockIdx.x / sums.K * rows;
+    unsigned first = row0;
     fetch(first + lane_row);
     for (; first < N; first += step) {  // N + step + rows < 2^32
         const unsigned i = first + lane_row;
         const bool in = i < N;
         F2 y[4], r[4], g[4], w[4];
+        trim8<XT, MODE>(ry, y32, c);
         values8<XT, V>(ry, y32, y);
-        if constexpr (GATE) values8<XT, V>(rg, false, g);
+        if constexpr (GATE) {
+            trim8<XT, MODE>(rg, false, c);
+            values8<XT, V>(rg, false, g);
+        }
         if (A.residual) {
+            trim8<XT, MODE>(rr, r32, c);
             values8<XT, V>(rr, r32, r);
         } else {
 #pragma unroll
@@ -450,7 +513,7 @@ norm_fwd_kernel(const NormArgs A) {
         }
 #pragma unroll
         for (int v = 0; v < 4; ++v) r[v] = fma2(mul2(y[v], f2(rho)), w[v], r[v]);
-        if (in) store8<XT, V>(A.r_out, r32, (long long)i * A.D, c, r);
+        if (in) store8<XT, MODE>(A.r_out, r32, (long long)i * A.D, c, r);
         if (pre) {
             s[0] = dot8(r, r);
             own_read(wp, w);
@@ -458,7 +521,7 @@ norm_fwd_kernel(const NormArgs A) {
             rho = rsqrtf(fmaf(s[0], A.inv_d, A.eps));
 #pragma unroll
             for (int v = 0; v < 4; ++v) r[v] = mul2(mul2(r[v], f2(rho)), w[v]);
-            if (in) store8<XT, V>(A.n_out, false, (long long)i * A.D, c, r);
+            if (in) store8<XT, MODE>(A.n_out, false, (long long)i * A.D, c, r);
         }
     }
     sums.end();
@@ -470,7 +533,7 @@ norm_fwd_kernel(const NormArgs A) {
 template <class F, bool SUB>
 __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd_kernel(const NormArgs A) {
     using XT = typename F::XT;
-    constexpr int V = F::V, NV = 8 / V;
+    constexpr int MODE = F::MODE, V = F::V, NV = 8 / V;
     constexpr bool GATE = F::GATE;
     constexpr bool y32 = F::Y32, r32 = F::R32;
     const bool pre = F::pre(A.dn != nullptr);
@@ -479,8 +542,9 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
     RowSums<SUB> sums(A);
     const int tid = SUB ? threadIdx.x % A.tpr : threadIdx.x;
     const unsigned rows = SUB ? blockDim.x / A.tpr : 1, lane_row = SUB ? threadIdx.x / A.tpr : 0;
-    const Columns<V> c(A, sums.rank, tid);
-    keep_weights<XT, V>(A, c, wq, wp);
+    const unsigned row0 = blockIdx.x / sums.K * rows;
+    const Columns<MODE> c(A, sums.rank, tid, row0 + lane_row);
+    keep_weights<XT, MODE>(A, c, wq, wp);
     {
         const F2 zero[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
         own_write(dq, zero);
@@ -491,28 +555,40 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
     auto fetch = [&](unsigned i) {
         if (i >= N) return;
         const RowAt at(A, i);
-        load8<XT, V>(ry, A.y, y32, at.in(A, A.ys), c);
-        if constexpr (GATE) load8<XT, V>(rg, A.gate, false, at.in(A, A.gs), c);
-        if (A.dr) load8<XT, V>(rd, A.dr, r32, at.in(A, A.drs), c);
+        const bool inside = i + 8 < N;  // the rows behind it hold a vector's columns past its end
+        load8<XT, MODE>(ry, A.y, y32, at.in(A, A.ys), c, inside);
+        if constexpr (GATE) load8<XT, MODE>(rg, A.gate, false, at.in(A, A.gs), c, inside);
+        if (A.dr) load8<XT, MODE>(rd, A.dr, r32, at.in(A, A.drs), c, inside);
         if (pre) {
-            if (A.residual) load8<XT, V>(rr, A.residual, r32, at.in(A, A.rs), c);
-            load8<XT, V>(rn, A.dn, false, at.in(A, A.dns), c);
+            if (A.residual) load8<XT, MODE>(rr, A.residual, r32, at.in(A, A.rs), c, inside);
+            load8<XT, MODE>(rn, A.dn, false, at.in(A, A.dns), c, inside);
         }
     };
-    unsigned first = blockIdx.x / sums.K * rows;
+    unsigned first = row0;
     fetch(first + lane_row);
     for (; first < N; first += step) {
         const unsigned i = first + lane_row;
         const bool in = i < N;
         const long long o = (long long)i * A.D;
         F2 y[4], e[4], r[4], m[4], f[4], df[4], t[4], w[4], acc[4];
+        trim8<XT, MODE>(ry, y32, c);
         values8<XT, V>(ry, y32, y);
-        if constexpr (GATE) values8<XT, V>(rg, false, f);
+        if constexpr (GATE) {
+            trim8<XT, MODE>(rg, false, c);
+            values8<XT, V>(rg, false, f);
+        }
 #pragma unroll
         for (int v = 0; v < 4; ++v) e[v] = r[v] = f2(0.f);
-        if (A.dr) values8<XT, V>(rd, r32, e);
+        if (A.dr) {
+            trim8<XT, MODE>(rd, r32, c);
+            values8<XT, V>(rd, r32, e);
+        }
         if (pre) {
-            if (A.residual) values8<XT, V>(rr, r32, r);
+            if (A.residual) {
+                trim8<XT, MODE>(rr, r32, c);
+                values8<XT, V>(rr, r32, r);
+            }
+            trim8<XT, MODE>(rn, false, c);
             values8<XT, V>(rn, false, m);
         }
         if (SUB && first + rows > N && !in) {  // the last turn's rows past the end count as 0
@@ -563,7 +639,7 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
             }
             own_write(dp, acc);
         }
-        if (A.dresidual && in) store8<XT, V>(A.dresidual, r32, o, c, e);
+        if (A.dresidual && in) store8<XT, MODE>(A.dresidual, r32, o, c, e);
         k *= -rho1 * rho1 * rho1 * A.inv_d;
         own_read(wq, w);
         own_read(dq, acc);
@@ -578,14 +654,34 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
         }
         own_write(dq, acc);
         if constexpr (GATE)
-            if (in) store8<XT, V>(A.dgate, false, o, c, df);
-        if (in) store8<XT, V>(A.dy, y32, o, c, e);
+            if (in) store8<XT, MODE>(A.dgate, false, o, c, df);
+        if (in) store8<XT, MODE>(A.dy, y32, o, c, e);
     }
     sums.end();
     // the weights' gradients: the CTA's sums to its row of the workspace, added up by norm_dw_kernel
     if (!A.parts) return;
     float* out = A.parts + (long long)(blockIdx.x / sums.K) * 2 * A.D;
     __syncthreads();
+    if constexpr (MODE == kShift) {
+        for (int k = 0; k < 2; ++k) {
+            const float* p = reinterpret_cast<const float*>(k ? dp : dq);
+            if constexpr (SUB) {  // a column is another thread's in each of the rows
+                for (int q = threadIdx.x; q < A.D; q += blockDim.x) {
+                    float t = 0.f;
+                    for (unsigned i = 0; i < rows; ++i) {
+                        const unsigned j = q + ((row0 + i) * (unsigned)A.D & 7u), v = j & 7u;
+                        t += p[((v >> 2) * blockDim.x + i * A.tpr + (j >> 3)) * 4 + (v & 3u)];
+                    }
+                    out[k * A.D + q] = t;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    if (c.mine(v)) out[k * A.D + c.first + v] = p[((v >> 2) * blockDim.x + threadIdx.x) * 4 + (v & 3)];
+            }
+        }
+        return;
+    }
     if (SUB && (int)threadIdx.x >= A.tpr) return;
     for (int k = 0; k < 2; ++k) {
         const ulonglong2* p = k ? dp : dq;
@@ -595,7 +691,7 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
             const ulonglong2 a = p[q * A.tpr + threadIdx.x], b = p[blockDim.x + q * A.tpr + threadIdx.x];
             t[0] = add2(t[0], F2{a.x}), t[1] = add2(t[1], F2{a.y}), t[2] = add2(t[2], F2{b.x}), t[3] = add2(t[3], F2{b.y});
         }
-        store8<float, V>(out, true, k * A.D, c, t);
+        store8<float, MODE>(out, true, k * A.D, c, t);
     }
 }
 

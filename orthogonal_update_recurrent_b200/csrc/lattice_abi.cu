@@ -244,6 +244,12 @@ lattice_status check_norm(NormArgs& a, const void* y, lattice_dtype y_dtype, lon
 bool norm_rows_vec(const void* p, lattice_dtype t, long long N, int G, long long stride) {
     return aligned(p, 16) && (N <= G || stride * (long long)type_size(t) % 16 == 0);
 }
+// Whether row i starts i D mod 8 elements past a 16-byte boundary, with every row behind the one
+// before it: then vectors may start before their row does (null: no such rows).
+bool norm_rows_shift(const void* p, lattice_dtype t, long long N, int G, int D, long long stride) {
+    const long long more = stride - (long long)G * D;
+    return !p || (aligned(p, 16) && (N <= G || (more >= 0 && more * (long long)type_size(t) % 16 == 0)));
+}
 bool group_span(const void* p, lattice_dtype t, long long N, int G, int D, long long stride, Span* s) {
     return strided_span(p, type_size(t), N / G, 1, (long long)G * D, stride, 0, s) || !p;
 }
@@ -621,8 +627,13 @@ lattice_status lattice_block_norm_fwd(const void* y, lattice_dtype y_dtype, long
     const bool vec = D % 8 == 0 && norm_rows_vec(y, y_dtype, N, G, y_stride) && norm_rows_vec(gate, dtype, N, G, gate_stride) &&
                      norm_rows_vec(residual, residual_dtype, N, G, residual_stride) && aligned(w_post, 16) &&
                      aligned(w_pre, 16) && aligned(r_out, 16) && aligned(n_out, 16);
+    const bool shift = D % 8 != 0 && D + 7 <= kNormMaxD && norm_rows_shift(y, y_dtype, N, G, D, y_stride) &&
+                       norm_rows_shift(gate, dtype, N, G, D, gate_stride) &&
+                       norm_rows_shift(residual, residual_dtype, N, G, D, residual_stride) && aligned(r_out, 16) &&
+                       aligned(n_out, 16);
+    const int mode = vec ? kNormVec : shift ? kNormShift : kNormOdd;
     return with_x(dtype, [&](auto t) {
-        return norm::launch_norm<decltype(t)>(false, a, vec, nullptr, static_cast<cudaStream_t>(stream));
+        return norm::launch_norm<decltype(t)>(false, a, mode, nullptr, static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -693,8 +704,14 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
                      norm_rows_vec(dr, dr_dtype, N, G, dr_stride) && norm_rows_vec(dn, dtype, N, G, dn_stride) &&
                      aligned(w_post, 16) && aligned(w_pre, 16) && aligned(dy, 16) && aligned(dgate, 16) &&
                      aligned(dresidual, 16);
+    const bool shift = D % 8 != 0 && D + 7 <= kNormMaxD && norm_rows_shift(y, y_dtype, N, G, D, y_stride) &&
+                       norm_rows_shift(gate, dtype, N, G, D, gate_stride) &&
+                       norm_rows_shift(residual, residual_dtype, N, G, D, residual_stride) &&
+                       norm_rows_shift(dr, dr_dtype, N, G, D, dr_stride) && norm_rows_shift(dn, dtype, N, G, D, dn_stride) &&
+                       aligned(dy, 16) && aligned(dgate, 16) && aligned(dresidual, 16);
+    const int mode = vec ? kNormVec : shift ? kNormShift : kNormOdd;
     int groups = 0;
-    s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, vec, &groups, st); });
+    s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, mode, &groups, st); });
     return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, groups, dw_post, dw_pre, st);
 }
 

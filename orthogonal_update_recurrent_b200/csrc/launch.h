@@ -49,10 +49,11 @@ template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, c
 }  // namespace gated
 
 // tu_norm_*.cu: norms after and before a block, a unit per type of the call (tpr, K set by the
-// launch). vec: rows and weights can be read in aligned vectors of 8 elements; groups
+// launch). mode: rows and weights can be read in aligned vectors of 8 elements (kNormVec), rows in
+// vectors that start where a vector does (kNormShift), or one by one (kNormOdd); groups
 // (or null): how many rows of weight gradients the backward pass leaves in the workspace
 namespace norm {
-template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st);
+template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
 }  // namespace norm
 int norm_parts(long long N, int D);  // at most so many
 lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st);

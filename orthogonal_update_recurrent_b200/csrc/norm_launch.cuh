@@ -9,16 +9,19 @@
 namespace lattice {
 namespace norm {
 
-inline int most_threads(bool bwd, bool vec) { return bwd ? kBwdThreads : vec ? kFwdThreads : kFwdOddThreads; }
+inline int most_threads(bool bwd, int mode) { return bwd ? kBwdThreads : mode != kOdd ? kFwdThreads : kFwdOddThreads; }
+// Rows after which they start at the same place among 8 elements again.
+inline int period(int D) { return D % 8 == 0 ? 1 : D % 4 == 0 ? 2 : D % 2 == 0 ? 4 : 8; }
 
 // 8 elements per thread: a row's CTAs (1, 2 or 4) and its threads in each, a power of two
-// within a warp and whole warps above.
+// within a warp and whole warps above. Shifted vectors (kShift) start up to `shift` early.
 struct Split {
     int K, tpr, threads, rows;  // threads of a CTA, rows that it takes at once
     int most, resident;
-    Split(int D, bool bwd, bool vec) : K(1), most(most_threads(bwd, vec)), resident(bwd ? kBwdThreads : kFwdThreads) {
-        while (K * most * 8 < D) K *= 2;
-        const int need = (D + 8 * K - 1) / (8 * K);
+    Split(int D, bool bwd, int mode) : K(1), most(most_threads(bwd, mode)), resident(bwd ? kBwdThreads : kFwdThreads) {
+        const int shift = mode == kShift ? 8 - 8 / period(D) : 0;
+        while (K * most * 8 < D + shift) K *= 2;
+        const int need = (D + shift + 8 * K - 1) / (8 * K);
         tpr = 1;
         if (need > 32) tpr = (need + 31) / 32 * 32;
         else
@@ -31,6 +34,12 @@ struct Split {
         const long long turns = (N + rows - 1) / rows, at_once = (long long)sm_count() * (resident / threads) / K;
         return turns < at_once ? turns : at_once;
     }
+    // n of them, rounded so that those with several turns step by whole periods
+    long long whole_periods(long long n, long long N, int D) const {
+        const long long turns = (N + rows - 1) / rows, p = period(D);
+        if (n >= turns || rows % p == 0) return n;
+        return n >= p ? n / p * p : p < turns ? p : turns;
+    }
 };
 
 // The grid is what the device holds at once, or fewer: it is asked once per kernel, CTA size and
@@ -39,8 +48,8 @@ struct Split {
 constexpr int kMaxDevices = 16;
 
 template <class Kernel>
-lattice_status launch(Kernel k, const NormArgs& a, bool bwd, bool vec, int bytes_per_thread, int* groups, cudaStream_t st) {
-    const Split split(a.D, bwd, vec);
+lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int mode, int bytes_per_thread, int* groups, cudaStream_t st) {
+    const Split split(a.D, bwd, mode);
     const int threads = split.threads, smem = threads * bytes_per_thread;
     cudaError_t e;
     if (smem > 40 * 1024) {  // 48 KB with the static arrays
@@ -75,6 +84,7 @@ lattice_status launch(Kernel k, const NormArgs& a, bool bwd, bool vec, int bytes
     }
     long long n = split.groups(a.N);
     if (n > c) n = c;
+    if (mode == kShift) n = split.whole_periods(n, a.N, a.D);
     cfg.gridDim = dim3((unsigned)(n * a.K));
     if (groups) *groups = (int)n;
     e = cudaLaunchKernelEx(&cfg, k, a);
@@ -83,35 +93,39 @@ lattice_status launch(Kernel k, const NormArgs& a, bool bwd, bool vec, int bytes
 
 template <class F, bool SUB>
 lattice_status run(bool bwd, const NormArgs& a, int* groups, cudaStream_t st) {
-    return bwd ? launch(norm_bwd_kernel<F, SUB>, a, true, F::V == 8, 128, groups, st)
-               : launch(norm_fwd_kernel<F, SUB>, a, false, F::V == 8, 64, groups, st);
+    return bwd ? launch(norm_bwd_kernel<F, SUB>, a, true, F::MODE, 128, groups, st)
+               : launch(norm_fwd_kernel<F, SUB>, a, false, F::MODE, 64, groups, st);
 }
 
 template <class T, bool SUB, bool GATE, int Y32, int R32>
-lattice_status run_typed(bool bwd, const NormArgs& a, bool vec, int* groups, cudaStream_t st) {
-    if (!vec) return run<Form<T, 1, GATE, Y32, R32, -1>, SUB>(bwd, a, groups, st);
-    return (bwd ? a.dn : a.n_out) ? run<Form<T, 8, GATE, Y32, R32, 1>, SUB>(bwd, a, groups, st)
-                                  : run<Form<T, 8, GATE, Y32, R32, 0>, SUB>(bwd, a, groups, st);
+lattice_status run_typed(bool bwd, const NormArgs& a, int mode, int* groups, cudaStream_t st) {
+    const bool pre = bwd ? a.dn != nullptr : a.n_out != nullptr;
+    if (mode == kOdd) return run<Form<T, kOdd, GATE, Y32, R32, -1>, SUB>(bwd, a, groups, st);
+    if (mode == kShift)
+        return pre ? run<Form<T, kShift, GATE, Y32, R32, 1>, SUB>(bwd, a, groups, st)
+                   : run<Form<T, kShift, GATE, Y32, R32, 0>, SUB>(bwd, a, groups, st);
+    return pre ? run<Form<T, kVec, GATE, Y32, R32, 1>, SUB>(bwd, a, groups, st)
+               : run<Form<T, kVec, GATE, Y32, R32, 0>, SUB>(bwd, a, groups, st);
 }
 
 template <class T, bool SUB, bool GATE>
-lattice_status run_types(bool bwd, const NormArgs& a, bool vec, int* groups, cudaStream_t st) {
+lattice_status run_types(bool bwd, const NormArgs& a, int mode, int* groups, cudaStream_t st) {
     if constexpr (sizeof(T) == 2) {
         if (a.y32)
-            return a.r32 ? run_typed<T, SUB, GATE, 1, 1>(bwd, a, vec, groups, st) : run_typed<T, SUB, GATE, 1, 0>(bwd, a, vec, groups, st);
-        return a.r32 ? run_typed<T, SUB, GATE, 0, 1>(bwd, a, vec, groups, st) : run_typed<T, SUB, GATE, 0, 0>(bwd, a, vec, groups, st);
+            return a.r32 ? run_typed<T, SUB, GATE, 1, 1>(bwd, a, mode, groups, st) : run_typed<T, SUB, GATE, 1, 0>(bwd, a, mode, groups, st);
+        return a.r32 ? run_typed<T, SUB, GATE, 0, 1>(bwd, a, mode, groups, st) : run_typed<T, SUB, GATE, 0, 0>(bwd, a, mode, groups, st);
     } else {
-        return run_typed<T, SUB, GATE, 1, 1>(bwd, a, vec, groups, st);
+        return run_typed<T, SUB, GATE, 1, 1>(bwd, a, mode, groups, st);
     }
 }
 
 template <class T>
-lattice_status launch_norm(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st) {
-    const Split split(a.D, bwd, vec);
+lattice_status launch_norm(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st) {
+    const Split split(a.D, bwd, mode);
     a.tpr = split.tpr;
     a.K = split.K;
-    if (a.tpr <= 32) return a.gate ? run_types<T, true, true>(bwd, a, vec, groups, st) : run_types<T, true, false>(bwd, a, vec, groups, st);
-    return a.gate ? run_types<T, false, true>(bwd, a, vec, groups, st) : run_types<T, false, false>(bwd, a, vec, groups, st);
+    if (a.tpr <= 32) return a.gate ? run_types<T, true, true>(bwd, a, mode, groups, st) : run_types<T, true, false>(bwd, a, mode, groups, st);
+    return a.gate ? run_types<T, false, true>(bwd, a, mode, groups, st) : run_types<T, false, false>(bwd, a, mode, groups, st);
 }
 
 }  // namespace norm

@@ -4,7 +4,7 @@
 
 namespace lattice {
 
-template lattice_status norm::launch_norm<__half>(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st);
+template lattice_status norm::launch_norm<__half>(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
 
 cudaError_t status_norm_f16(unsigned int* v) { return read_clear_module_status(v); }
 

@@ -4,9 +4,15 @@
 
 namespace lattice {
 
-template lattice_status norm::launch_norm<float>(bool bwd, NormArgs a, bool vec, int* groups, cudaStream_t st);
+template lattice_status norm::launch_norm<float>(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
 
-int norm_parts(long long N, int D) { return (int)norm::Split(D, true, true).groups(N); }
+int norm_parts(long long N, int D) {
+    const norm::Split vec(D, true, norm::kVec), shift(D, true, norm::kShift);
+    long long n = vec.groups(N), m = shift.groups(N);
+    if (D % 8 != 0 && D + 7 <= kNormMaxD) m = shift.whole_periods(m, N, D);
+    else m = n;
+    return (int)(m > n ? m : n);
+}
 
 lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st) {
     norm::norm_dw_kernel<32><<<(unsigned)((2 * a.D + 31) / 32), 1024, 0, st>>>(a.parts, groups, a.D, a.scale,

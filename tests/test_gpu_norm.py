@@ -131,6 +131,67 @@ def test_groups_of_wider_rows(L):
         both(L, t)
 
 
+@pytest.mark.parametrize("N,D", [(9, 1), (3000, 3), (5000, 12), (4, 50), (2600, 129), (700, 250), (5, 255), (1500, 257),
+                                 (600, 2055), (301, 4090), (450, 4095), (200, 4097), (90, 8187), (75, 16377), (75, 16378)])
+@pytest.mark.parametrize("dtype,ydtype,rdtype", [("bf16", "bf16", "f32"), ("f32", "f32", "f32"), ("f16", "f32", "f16")])
+def test_widths_that_are_no_multiple_of_a_vector(L, N, D, dtype, ydtype, rdtype):
+    both(L, make((N, D), dtype, ydtype, rdtype, seed=N + D))
+    both(L, make((N, D), dtype, ydtype, rdtype, gate=False, residual=False, seed=N + D + 1), pre=False)
+
+
+@pytest.mark.parametrize("more", [8, 16, 4, 3])
+def test_groups_of_odd_rows(L, more):
+    """Rows that start where those of whole arrays would (8, 16; 4 in fp32), and elsewhere."""
+    G, D, groups = 5, 77, 130
+    t = make((groups, G, D), "bf16", "f32", "f32", seed=21)
+    want = both(L, t)
+    for k in ("y", "gate", "residual", "dr", "dn"):
+        w = torch.full((groups, G * D + more), float("nan"), dtype=t[k].dtype, device="cuda")
+        w[:, :G * D] = t[k].flatten(1)
+        t[k] = w[:, :G * D].view(groups, G, D)
+    got = both(L, t)
+    if more % 8 == 0:
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("D", [5, 300, 999, 5000, 9001])
+def test_rows_that_start_anywhere(L, D):
+    N = 23
+    t = make((N, D), "bf16", "f32", "f32", seed=D)
+    for k in ("y", "gate", "residual", "dr", "dn"):
+        w = torch.full((N * D + 1,), float("nan"), dtype=t[k].dtype, device="cuda")
+        w[1:] = t[k].flatten()
+        t[k] = w[1:].view(N, D)
+    both(L, t)
+
+
+def test_odd_rows_keep_to_themselves(L):
+    """What stands around a row is neither read into it nor written."""
+    for N, D in ((40, 37), (700, 259), (20, 5003)):
+        t = make((N, D), "bf16", "f32", "f32", seed=22)
+        kw = dict(act="gelu", scale=0.5)
+        want, n = L.block_norm_fwd(t["y"], t["w_post"], gate=t["gate"], residual=t["residual"], w_pre=t["w_pre"], **kw)
+        for i in (0, N // 2, N - 1):
+            bad = {k: t[k].clone() for k in ("y", "gate", "residual", "dr", "dn")}
+            for k in bad:
+                bad[k][i] = float("nan")
+            r, m = L.block_norm_fwd(bad["y"], t["w_post"], gate=bad["gate"], residual=bad["residual"], w_pre=t["w_pre"], **kw)
+            keep = [j for j in range(N) if j != i]
+            assert torch.equal(r[keep], want[keep]) and torch.equal(m[keep], n[keep])
+            one = L.block_norm_bwd(t["y"], t["w_post"], gate=t["gate"], residual=t["residual"], w_pre=t["w_pre"], dr=t["dr"],
+                                   dn=t["dn"], **kw)
+            two = L.block_norm_bwd(bad["y"], t["w_post"], gate=bad["gate"], residual=bad["residual"], w_pre=t["w_pre"],
+                                   dr=bad["dr"], dn=bad["dn"], **kw)
+            for k in ("dy", "dgate", "dresidual"):
+                assert torch.equal(two[k][keep], one[k][keep]) and two[k][i].isnan().any()
+        room = torch.full((N * D + 32,), 7.0, device="cuda")
+        out = room[16:16 + N * D].view(N, D)
+        out.copy_(t["residual"])
+        r, m = L.block_norm_fwd(t["y"], t["w_post"], gate=t["gate"], residual=out, w_pre=t["w_pre"], r_out=out, **kw)
+        assert torch.equal(r, want) and torch.equal(m, n)
+        assert (room[:16] == 7).all() and (room[16 + N * D:] == 7).all()
+
+
 def test_residual_in_place(L):
     t = make((7, 256), "bf16", rdtype="f32", seed=12)
     want, n = L.block_norm_fwd(t["y"], t["w_post"], residual=t["residual"], w_pre=t["w_pre"])
