@@ -220,31 +220,46 @@ __device__ __forceinline__ int row_length(const GatedArgs& A, int b) {
     return n < 0 ? 0 : n > A.T ? A.T : n;
 }
 
+// How rows stand in a stage: next to each other, or, where they may start anywhere (VEC
+// false), with room for a row's start within its first 16 bytes.
+template <bool VEC, class T, int V>
+struct RowOf {
+    static constexpr int N = 32 * V, STRIDE = N + (VEC ? 0 : 16 / (int)sizeof(T));
+};
 // Copies a run's R rows of 32 V channels (n of them exist from the tile's first on) into a
-// stage of the warp's, and moves on to the warp's next run. VEC: asynchronously, 16 bytes at
-// a time where rows allow it (wide), else a lane's V channels; otherwise element by element.
+// stage of the warp's, and moves on to the warp's next run. VEC: 16 bytes at a time where rows
+// allow it (wide), else a lane's V channels. Otherwise the 16-byte pieces that a row's bytes lie in,
+// the last one as far as the row goes, so that an element stands as far behind a multiple of 16
+// as it does in memory (2047 bf16 channels, 8 sequences of 4096: forward 331 us
+// and backward 498 us with elements loaded one by one, 141 and 336 us so).
 template <bool VEC, class T, int V, int R>
 struct Stager {
     static constexpr int ROW = 32 * V, PER = 16 / sizeof(T), CH = ROW / PER, STEP = 32 / CH;  // chunks per row
+    static constexpr int STRIDE = RowOf<VEC, T, V>::STRIDE;
     static_assert(CH <= 32 && R % STEP == 0, "whole warps of chunks");
     const T* p;            // the next run's first row, VEC: the lane's first piece in it
     long long ts, move;    // wide: STEP rows; one row
     uint32_t at;           // VEC: the lane's place in a stage
-    int n;                 // VEC: whether the lane copies
+    int n;                 // VEC: whether the lane copies; else a row's bytes
     bool wide;
-    __device__ __forceinline__ Stager(const T* base, long long token_stride, int channels, bool wide_, long long first,
-                                      long long ahead, int lane)
-        : wide(wide_) {
+    uintptr_t lowest;      // the array's first byte: nothing before it is read
+    uintptr_t back;        // VEC false: from p, at the lane's first row, to the run's
+    __device__ __forceinline__ Stager(const void* array, const T* base, long long token_stride, int channels, bool wide_,
+                                      long long first, long long ahead, int lane)
+        : wide(wide_), lowest(reinterpret_cast<uintptr_t>(array)) {
         ts = VEC && wide ? STEP * token_stride : token_stride;
         move = ahead * token_stride;
         p = base + first * token_stride;
-        n = channels;
+        n = (channels < ROW ? channels : ROW) * (int)sizeof(T);
         at = 0;
         if constexpr (VEC) {
             const int row = wide ? lane / CH : 0, e = wide ? lane % CH * PER : lane * V;
             p += row * token_stride + e;
             at = (uint32_t)((row * ROW + e) * sizeof(T));
             n = e < channels;
+        } else {
+            p += lane / CH * token_stride;
+            back = (uintptr_t)(lane / CH * token_stride * (long long)sizeof(T));
         }
     }
     template <int BYTES>
@@ -272,29 +287,40 @@ struct Stager {
                     q += ts;
                 }
             }
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (r < rows && k * 32 + lane < n) piece<4>(d + (r * ROW + k * 32 + lane) * 4, q + k * 32 + lane);
-                q += ts;
-            }
         } else {
-            T t[R][V];  // all loads before the first store
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (r < rows && k * 32 + lane < n) t[r][k] = q[k * 32 + lane];
-                q += ts;
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (r < rows && k * 32 + lane < n) stage[r * ROW + k * 32 + lane] = t[r][k];
+            for (int k = 0; k < R / STEP; ++k) part(stage, d, q + (long long)(k * STEP) * ts, k * STEP + lane / CH, lane % CH, rows);
+            static_assert(R <= 32, "a lane per row");
+            if (lane < R) part(stage, d, reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(p) - back) + lane * ts, lane, CH, rows);
         }
+    }
+    // Piece k of a row that starts at q
+    __device__ __forceinline__ void part(T* stage, uint32_t d, const T* q, int row, int k, int rows) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q), src = (a & ~(uintptr_t)15) + 16 * k;
+        const int left = n - 16 * k + (int)(a & 15);  // bytes of the row, from src on
+        if (row >= rows || left <= 0) return;
+        if (src >= lowest) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + (uint32_t)(row * STRIDE * (int)sizeof(T) + 16 * k)),
+                         "l"(src), "r"(left < 16 ? left : 16)
+                         : "memory");
+        } else {  // the array starts within these 16 bytes
+            T* e = stage + row * STRIDE;
+            for (int v = 0; v < PER; ++v) {
+                const uintptr_t s = src + v * sizeof(T);
+                if (s >= a && s < a + n) e[v] = *reinterpret_cast<const T*>(s);
+            }
+        }
+    }
+};
+// Where a run's rows start in their stages, behind a multiple of 16 bytes.
+template <bool VEC, class T>
+struct RowStart {
+    uint32_t at, step;
+    __device__ __forceinline__ RowStart(const T* base, long long token_stride)
+        : at((uint32_t)reinterpret_cast<uintptr_t>(base)), step((uint32_t)(token_stride * sizeof(T))) {}
+    __device__ __forceinline__ const T* row(const T* stage, int stride, int t0, int r) const {
+        if constexpr (VEC) return stage + r * stride;
+        else return stage + r * stride + ((at + (uint32_t)(t0 + r) * step & 15u) / sizeof(T));
     }
 };
 // Rows behind the sequence's end are made neutral in the stage: a gate of 1 that writes 0.
@@ -302,9 +328,9 @@ template <int GATE>
 __device__ __forceinline__ float neutral_z() {
     return GATE == kValue ? 1.f : __int_as_float(0x7f800000);
 }
-template <class T, int V, int R>
+template <class T, int STRIDE, int R>
 __device__ __forceinline__ void fill_rows(T* stage, int first, float value, int lane) {
-    for (int i = (first > 0 ? first : 0) * 32 * V + lane; i < R * 32 * V; i += 32) stage[i] = from_f<T>(value);
+    for (int i = (first > 0 ? first : 0) * STRIDE + lane; i < R * STRIDE; i += 32) stage[i] = from_f<T>(value);
 }
 __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -339,6 +365,16 @@ __device__ __forceinline__ void read_pairs(const T* p, F2* f) {
         }
     }
 }
+// A row's, wherever it starts
+template <bool VEC, class T, int N>
+__device__ __forceinline__ void read_row(const T* p, F2* f) {
+    if constexpr (VEC) {
+        read_pairs<T, N>(p, f);
+    } else {
+#pragma unroll
+        for (int v = 0; v < N; ++v) f[v] = f2(to_f(p[2 * v]), to_f(p[2 * v + 1]));
+    }
+}
 // The same for fp32 shared memory, and back
 template <int N>
 __device__ __forceinline__ void write_pairs(float* p, const F2* f) {
@@ -357,6 +393,33 @@ __device__ __forceinline__ void store_pairs(T* p, const F2* f, int n) {
     for (int v = 0; v < N; ++v) parts(f[v], t[2 * v], t[2 * v + 1]);
     store_vec<VEC, T, 2 * N>(p, t, n);
 }
+// A row of a result by the whole warp, n of the lane's channels (lanes without any call too). Two
+// 16-bit channels per lane that start on an odd element are stored as the words that they
+// share with the lane before.
+template <bool VEC, class T, int N>
+__device__ __forceinline__ void store_row(T* p, const F2* f, int n, int lane) {
+    if constexpr (VEC || sizeof(T) == 4 || N != 1) {
+        if (n > 0) store_pairs<VEC, T, N>(p, f, n);
+    } else {
+        Vec<T, 2> own;
+        float a, b;
+        parts(f[0], a, b);
+        own.v[0] = from_f<T>(a), own.v[1] = from_f<T>(b);
+        if ((reinterpret_cast<uintptr_t>(p) & 2u) == 0) {  // the same in all lanes
+            if (n >= 2) *reinterpret_cast<Vec<T, 2>*>(p) = own;
+            else if (n == 1) p[0] = own.v[0];
+        } else {
+            uint32_t w;
+            memcpy(&w, &own, 4);
+            const uint32_t before = __shfl_up_sync(0xffffffffu, w, 1);
+            if (n >= 1) {
+                if (lane == 0) p[0] = own.v[0];
+                else *reinterpret_cast<uint32_t*>(p - 1) = before >> 16 | w << 16;
+                if (n >= 2 && (lane == 31 || n == 2)) p[1] = own.v[1];
+            }
+        }
+    }
+}
 template <bool VEC, int N>
 __device__ __forceinline__ void load_state(const float* p, int n, F2* f) {  // p may be null: 0
 #pragma unroll
@@ -368,17 +431,26 @@ __device__ __forceinline__ void load_state(const float* p, int n, F2* f) {  // p
     }
 }
 // Whether no lane's z of a run is negative.
-template <class ZT, int N, int R>
-__device__ __forceinline__ bool none_negative(const ZT* z, int row) {
+template <bool VEC, class ZT, int N, int R>
+__device__ __forceinline__ bool none_negative(const RowStart<VEC, ZT>& at, const ZT* z, int stride, int t0) {
     uint32_t bits = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        constexpr int W = N * 2 * sizeof(ZT) / 4;
-        const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(z + r * row);
+        const ZT* p = at.row(z, stride, t0, r);
+        if constexpr (VEC) {
+            constexpr int W = N * 2 * sizeof(ZT) / 4;
+            const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(p);
 #pragma unroll
-        for (int v = 0; v < W; ++v) bits |= w.v[v];
+            for (int v = 0; v < W; ++v) bits |= w.v[v];
+        } else {
+#pragma unroll
+            for (int v = 0; v < 2 * N; ++v) {
+                if constexpr (sizeof(ZT) == 4) bits |= reinterpret_cast<const uint32_t*>(p)[v];
+                else bits |= reinterpret_cast<const uint16_t*>(p)[v];
+            }
+        }
     }
-    return !__any_sync(0xffffffffu, (bits & (sizeof(ZT) == 2 ? 0x80008000u : 0x80000000u)) != 0);
+    return !__any_sync(0xffffffffu, (bits & (sizeof(ZT) == 4 ? 0x80000000u : 0x80008000u)) != 0);
 }
 template <class XT>
 __device__ __forceinline__ float load_gate(const void* z, long long off, bool z32) {
@@ -487,12 +559,12 @@ struct HeadGates {
 };
 
 // ---- forward
-template <class XT, int ZM, int V, int R, int NW, int NST>
+template <class XT, int ZM, bool VEC, int V, int R, int NW, int NST>
 struct FwdLayout {
     using ZT = typename std::conditional<ZM == kZ32, float, XT>::type;
-    static constexpr int ROW = 32 * V, RUN = R * ROW;
+    static constexpr int XROW = RowOf<VEC, XT, V>::STRIDE, ZROW = RowOf<VEC, ZT, V>::STRIDE;
     static constexpr int HO = ZM == kZHead ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, H)
-    static constexpr int X = RUN * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : RUN * sizeof(ZT);
+    static constexpr int X = R * XROW * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : R * ZROW * sizeof(ZT);
     static constexpr int STAGE = X + Z;                      // bytes of a warp's stage
     static constexpr int HG = NW * NST * STAGE;              // a warp's gates per head
     static constexpr int SW = HG + (ZM == kZHead ? NW * HeadGates<XT, V, R, 2>::BYTES : 0);  // [2][NW][32][PAIR]
@@ -505,7 +577,7 @@ struct FwdLayout {
 // holds the same gate twice.
 template <class XT, int ZM, int FORM, bool VEC, int V, int R, int NW, int NST, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArgs A) {
-    using Lay = FwdLayout<XT, ZM, V, R, NW, NST>;
+    using Lay = FwdLayout<XT, ZM, VEC, V, R, NW, NST>;
     using ZT = typename Lay::ZT;
     constexpr int GATE = FORM / 3, WRITE = FORM % 3, L = NW * R, PAIR = Lay::PAIR, HO = Lay::HO, N = V / 2;
     constexpr bool HEAD = ZM == kZHead;
@@ -533,8 +605,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = rank * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, A.wide, ts, K * L, lane);
-    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, K * L, lane);
+    Stager<VEC, XT, V, R> sx(A.x, x, A.xts, A.C - c0, A.wide, ts, K * L, lane);
+    Stager<VEC, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, K * L, lane);
+    const RowStart<VEC, XT> x_at(x, A.xts);
+    const RowStart<VEC, ZT> z_at(z, A.zts);
     HeadGates<XT, V, R, 2> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts < len) {
@@ -566,8 +640,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
         slot = slot == NST - 1 ? 0 : slot + 1;
         const bool full = t0 + R <= len;
         if (!full) {
-            fill_rows<XT, V, R>(xw, len - t0, 0.f, lane);
-            if constexpr (!HEAD) fill_rows<ZT, V, R>(zw, len - t0, neutral_z<GATE>(), lane);
+            fill_rows<XT, Lay::XROW, R>(xw, len - t0, 0.f, lane);
+            if constexpr (!HEAD) fill_rows<ZT, Lay::ZROW, R>(zw, len - t0, neutral_z<GATE>(), lane);
             __syncwarp();
         }
         if constexpr (HEAD) {
@@ -579,19 +653,19 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
             });
         }
         bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ZT, N, R>(zs, Lay::ROW);
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<VEC, ZT, N, R>(z_at, zs, Lay::ZROW, t0);
         // P: products of the run's gates, H: the run's states from h = 0, after each token
         F2 P[R][NG], H[R][N];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 xf[N], zf[N], a[N], w[N];
-            read_pairs<XT, N>(xs + r * Lay::ROW, xf);
+            read_row<VEC, XT, N>(x_at.row(xs, Lay::XROW, t0, r), xf);
             if constexpr (HEAD) {
                 F2 t[2];
                 hg.template get<2>(gates, r, t);
                 a[0] = t[0], w[0] = t[1];
             } else {
-                read_pairs<ZT, N>(zs + r * Lay::ROW, zf);
+                read_row<VEC, ZT, N>(z_at.row(zs, Lay::ZROW, t0, r), zf);
             }
 #pragma unroll
             for (int v = 0; v < N; ++v) {
@@ -660,8 +734,8 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
             for (int v = 0; v < N; ++v) h[v] = fma2(P[R - 1][HEAD ? 0 : v], hin[v], H[R - 1][v]);
             write_pairs<N>(sc + ((buf ^ 1) * 32 + lane) * V, h);
         }
-        if (on) {
-            if (A.marks) {
+        if (on || !VEC) {  // a row's store may be the whole warp's
+            if (on && A.marks) {
 #pragma unroll
                 for (int r = 0; r < R; r += kGatedMark) {
                     F2 f[N];
@@ -677,7 +751,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                     F2 f[N];
 #pragma unroll
                     for (int v = 0; v < N; ++v) f[v] = fma2(P[r][HEAD ? 0 : v], hin[v], H[r][v]);
-                    store_pairs<VEC, XT, N>(yt + (long long)r * A.C, f, n);
+                    store_row<VEC, XT, N>(yt + (long long)r * A.C, f, n, lane);
                 };
                 if (full) {
 #pragma unroll
@@ -704,12 +778,12 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
 // dh_0 = a_1 g_1. Tiles run from the sequence's end to its start; a run's
 // states are rebuilt from the mark that the forward pass left at its start, and the
 // adjoint enters from behind, by the runs' pairs (P, G).
-template <class XT, int ZM, int V, int R, int NW, int NST>
+template <class XT, int ZM, bool VEC, int V, int R, int NW, int NST>
 struct BwdLayout {
     using ZT = typename std::conditional<ZM == kZ32, float, XT>::type;
-    static constexpr int ROW = 32 * V, RUN = R * ROW;
+    static constexpr int XROW = RowOf<VEC, XT, V>::STRIDE, ZROW = RowOf<VEC, ZT, V>::STRIDE;
     static constexpr int HO = ZM == kZHead ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, G)
-    static constexpr int X = RUN * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : RUN * sizeof(ZT);
+    static constexpr int X = R * XROW * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : R * ZROW * sizeof(ZT);
     static constexpr int M = 2 * X + Z;           // the mark's place in a stage
     static constexpr int STAGE = M + 32 * V * 4;
     static constexpr int HG = NW * NST * STAGE;             // a warp's gates per head
@@ -721,7 +795,7 @@ struct BwdLayout {
 
 template <class XT, int ZM, int FORM, bool VEC, int V, int R, int NW, int NST, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArgs A) {
-    using Lay = BwdLayout<XT, ZM, V, R, NW, NST>;
+    using Lay = BwdLayout<XT, ZM, VEC, V, R, NW, NST>;
     using ZT = typename Lay::ZT;
     constexpr int GATE = FORM / 3, WRITE = FORM % 3, L = NW * R, PAIR = Lay::PAIR, HO = Lay::HO, N = V / 2;
     constexpr bool HEAD = ZM == kZHead;
@@ -753,8 +827,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = ((iters - 1) * K + rank) * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(x, A.xts, A.C - c0, A.wide, ts, -K * L, lane), sd(dy, A.dyts, A.C - c0, A.wide, ts, -K * L, lane);
-    Stager<VEC, ZT, V, R> sz(z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, -K * L, lane);
+    Stager<VEC, XT, V, R> sx(A.x, x, A.xts, A.C - c0, A.wide, ts, -K * L, lane), sd(A.dy, dy, A.dyts, A.C - c0, A.wide, ts, -K * L, lane);
+    Stager<VEC, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, -K * L, lane);
+    const RowStart<VEC, XT> x_at(x, A.xts), dy_at(dy, A.dyts);
+    const RowStart<VEC, ZT> z_at(z, A.zts);
     HeadGates<XT, V, R, 4> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts >= 0) {
@@ -771,7 +847,11 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                                      : "memory");
                     } else {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) to[v] = v < n ? m[v] : 0.f;
+                        for (int v = 0; v < V; ++v)
+                            if (v < n)
+                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to + v)),
+                                             "l"(m + v)
+                                             : "memory");
                     }
                 }
                 if constexpr (HEAD) hg.stage(A, reinterpret_cast<uint32_t*>(s + 2 * Lay::X), ts, len, lane);
@@ -797,9 +877,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
         slot = slot == NST - 1 ? 0 : slot + 1;
         const bool full = t0 + R <= len;
         if (!full) {
-            fill_rows<XT, V, R>(xw, len - t0, 0.f, lane);
-            fill_rows<XT, V, R>(dw, len - t0, 0.f, lane);
-            if constexpr (!HEAD) fill_rows<ZT, V, R>(zw, len - t0, neutral_z<GATE>(), lane);
+            fill_rows<XT, Lay::XROW, R>(xw, len - t0, 0.f, lane);
+            fill_rows<XT, Lay::XROW, R>(dw, len - t0, 0.f, lane);
+            if constexpr (!HEAD) fill_rows<ZT, Lay::ZROW, R>(zw, len - t0, neutral_z<GATE>(), lane);
             __syncwarp();
         }
         if constexpr (HEAD) {  // gate, write scale, its slope (unit write)
@@ -813,7 +893,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
             });
         }
         bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ZT, N, R>(zw + lane * V, Lay::ROW);
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<VEC, ZT, N, R>(z_at, zw + lane * V, Lay::ZROW, t0);
         // Of each token: a, then the product of the run's gates behind it; s (per head it stays
         // in shared memory); dz / g, per head without da/dz; the run's own adjoint, from 0.
         F2 a[R][NG], s[HEAD ? 1 : R][NG], k[R][N], gl[R][N], h[N];
@@ -821,14 +901,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 xf[N], zf[N], hs = f2(0.f);
-            read_pairs<XT, N>(xw + r * Lay::ROW + lane * V, xf);
+            read_row<VEC, XT, N>(x_at.row(xw + lane * V, Lay::XROW, t0, r), xf);
             if constexpr (HEAD) {
                 F2 t[WRITE == kUnit ? 4 : 2];
                 hg.template get<WRITE == kUnit ? 4 : 2>(gates, r, t);
                 a[r][0] = t[0], s[0][0] = t[1];
                 if constexpr (WRITE == kUnit) hs = t[2];
             } else {
-                read_pairs<ZT, N>(zw + r * Lay::ROW + lane * V, zf);
+                read_row<VEC, ZT, N>(z_at.row(zw + lane * V, Lay::ZROW, t0, r), zf);
             }
 #pragma unroll
             for (int v = 0; v < N; ++v) {
@@ -850,7 +930,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
         F2 P[NG], G[N];
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) {
-            read_pairs<XT, N>(dw + r * Lay::ROW + lane * V, gl[r]);
+            read_row<VEC, XT, N>(dy_at.row(dw + lane * V, Lay::XROW, t0, r), gl[r]);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 if (r < R - 1) gl[r][v] = add2(gl[r][v], G[v]);
@@ -938,7 +1018,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 dxf[v] = WRITE == kPlain ? g_ : mul2(HEAD ? t[1] : s[HEAD ? 0 : r][i], g_);
                 dzf[v] = mul2(k[r][v], g_);
             }
-            if (in) store_pairs<VEC, XT, N>(dxt + (long long)r * A.C, dxf, n);
+            if (in) store_row<VEC, XT, N>(dxt + (long long)r * A.C, dxf, n, lane);
             if constexpr (HEAD) {
                 F2 sum = dzf[0];
 #pragma unroll
@@ -947,15 +1027,15 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 parts(sum, lo, hi);
                 sums[r * 36 + lane] = on ? lo + hi : 0.f;
             } else if (in) {
-                store_pairs<VEC, ZT, N>(dzt + (long long)r * nz, dzf, n);
+                store_row<VEC, ZT, N>(dzt + (long long)r * nz, dzf, n, lane);
             }
         };
-        if (full && on) {
+        if (full && (on || !VEC)) {
 #pragma unroll
             for (int r = 0; r < R; ++r) put(r, true);
         } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) put(r, on && t0 + r < len);
+            for (int r = 0; r < R; ++r) put(r, (on || !VEC) && t0 + r < len);
         }
         if constexpr (HEAD) {  // a head's d channels are those of d/V lanes; the gate's lane adds them up
             __syncwarp();

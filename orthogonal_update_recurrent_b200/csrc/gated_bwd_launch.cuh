@@ -9,10 +9,10 @@ namespace gated {
 template <class XT, int FORM, int ZM, bool VEC, int V, int NW, int NST, int MINB>
 lattice_status bwd_of(GatedArgs a, cudaStream_t st) {
     constexpr int R = kGatedMark;
-    static_assert(BwdLayout<XT, ZM, V, R, NW, NST>::bytes(kGatedMaxK) <= kMaxShared, "every cluster size fits");
+    static_assert(BwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(8) <= kMaxShared, "clusters of 8 fit");
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
     return launch(gated_bwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
-                  [](int K) { return BwdLayout<XT, ZM, V, R, NW, NST>::bytes(K); }, st);
+                  [](int K) { return BwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(K); }, st);
 }
 
 // Gates per channel: two channels per lane, 4 warps, two CTAs per SM. Gates per head: four

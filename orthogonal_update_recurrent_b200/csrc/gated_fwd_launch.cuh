@@ -12,10 +12,10 @@ namespace gated {
 template <class XT, int FORM, int ZM, bool VEC>
 lattice_status fwd(GatedArgs a, cudaStream_t st) {
     constexpr int V = kGatedFwdVec, NW = 8, R = sizeof(XT) == 2 ? 16 : 8, NST = ZM == kZHead ? 3 : 2, MINB = R == 16 ? 2 : 3;
-    static_assert(FwdLayout<XT, ZM, V, R, NW, NST>::bytes(kGatedMaxK) <= kMaxShared, "every cluster size fits");
+    static_assert(FwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(8) <= kMaxShared, "clusters of 8 fit");
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
     return launch(gated_fwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
-                  [](int K) { return FwdLayout<XT, ZM, V, R, NW, NST>::bytes(K); }, st);
+                  [](int K) { return FwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(K); }, st);
 }
 
 template <class XT, int FORM, int ZM, bool VEC>

@@ -28,6 +28,7 @@ lattice_status launch(Kernel k, GatedArgs a, int threads, int tile, int resident
     if (K > kGatedMaxK) K = kGatedMaxK;
     if (K > ((long long)a.T + tile - 1) / tile) K = ((long long)a.T + tile - 1) / tile;
     if (K < 1) K = 1;
+    while (bytes((int)K) > kMaxShared) --K;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);

@@ -98,6 +98,39 @@ def test_long_sequences_in_clusters_above_the_portable_size(L, dtype, zdtype, d,
     both(L, make(2, 4700, 1, d, dtype=dtype, zdtype=zdtype, head=head, mean=5.0, seed=11, lengths=[4700, 2063]), write="unit")
 
 
+@pytest.mark.parametrize("dtype,zdtype", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("B,T,H,d", [(2, 700, 1, 63), (1, 333, 1, 65), (2, 130, 13, 5), (3, 260, 3, 43), (5, 40, 1, 1)])
+def test_odd_channels(L, B, T, H, d, dtype, zdtype):
+    both(L, make(B, T, H, d, dtype=dtype, zdtype=zdtype, seed=T + d, mean=1.0), write="unit", tau=0.25)
+    lengths = [T - 1 - 17 * b for b in range(B)]
+    both(L, make(B, T, H, d, dtype=dtype, zdtype=zdtype, seed=T, lengths=lengths))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,head", [(32, False), (33, False), (64, True), (7, False)])
+def test_arrays_that_start_anywhere(L, d, head, dtype):
+    """What stands around the rows is neither read into them nor written."""
+    B, T, H = 2, 150, 1
+    t = make(B, T, H, d, dtype=dtype, head=head, seed=31)
+    want = both(L, t)
+    for k in ("x", "z", "dy"):
+        wide = torch.full((B * T * t[k][0, 0].numel() + 9,), float("nan"), dtype=t[k].dtype, device="cuda")
+        for off in (1, 3):
+            wide[:] = float("nan")
+            part = wide[off:off + t[k].numel()].view(t[k].shape)
+            part.copy_(t[k])
+            moved = dict(t)
+            moved[k] = part
+            got = both(L, moved)
+            # a head's dz is a sum of products, of which the kernel for such rows may round one less
+            assert all(torch.equal(got[n], want[n]) for n in want if n != "dz" or not head)
+    for off in (0, 1, 2, 5):
+        room = torch.full((t["x"].numel() + 16,), 7.0, dtype=t["x"].dtype, device="cuda")
+        y = room[off:off + t["x"].numel()].view(t["x"].shape)
+        L.gated_scan_fwd(t["x"], t["z"], t["h0"], y=y, write="leaky")
+        assert torch.equal(y, want["y"]) and (room[:off] == 7).all() and (room[off + y.numel():] == 7).all()
+
+
 def test_no_initial_state_and_no_final_cotangent(L):
     both(L, make(2, 100, 1, 20, seed=6), h0=False, dh_T=False)
 
