@@ -220,83 +220,83 @@ __device__ __forceinline__ int row_length(const GatedArgs& A, int b) {
     return n < 0 ? 0 : n > A.T ? A.T : n;
 }
 
-// How rows stand in a stage: next to each other, or, where they may start anywhere (VEC
-// false), with room for a row's start within its first 16 bytes.
-template <bool VEC, class T, int V>
+// How rows start: at any element (kAny), at a multiple of a lane's V channels (kPairs), or of 16
+// bytes (kWide). Shifted rows stand in a stage as far behind a multiple of 16 bytes as in memory,
+// and have room for it.
+constexpr int kAny = 0, kPairs = 1, kWide = 2;
+template <int ROWS, class T>
+constexpr bool kShifted = ROWS == kAny || (ROWS == kPairs && sizeof(T) == 4);
+template <int ROWS, class T, int V>
 struct RowOf {
-    static constexpr int N = 32 * V, STRIDE = N + (VEC ? 0 : 16 / (int)sizeof(T));
+    static constexpr int N = 32 * V, STRIDE = N + (kShifted<ROWS, T> ? 16 / (int)sizeof(T) : 0);
 };
 // Copies a run's R rows of 32 V channels (n of them exist from the tile's first on) into a
-// stage of the warp's, and moves on to the warp's next run. VEC: 16 bytes at a time where rows
-// allow it (wide), else a lane's V channels. Otherwise the 16-byte pieces that a row's bytes lie in,
-// the last one as far as the row goes, so that an element stands as far behind a multiple of 16
-// as it does in memory (2047 bf16 channels, 8 sequences of 4096: forward 331 us
-// and backward 498 us with elements loaded one by one, 141 and 336 us so).
-template <bool VEC, class T, int V, int R>
+// stage of the warp's, and moves on to the warp's next run. kWide: 16 bytes at a time. 16-bit
+// kPairs: a lane's V channels. Shifted rows: the 16-byte pieces that a row's bytes lie in, the
+// last one as far as the row goes. 8 sequences of 4096 tokens, forward and backward: 2047
+// channels in bf16 331 and 498 us with elements loaded one by one, 140 and 332 us with shifted
+// pieces; 2046 channels in bf16 102 and 190 us by lanes, 111 and 212 us with shifted
+// pieces, in fp32 220 and 375 us by lanes, 160 and 296 us with shifted pieces.
+template <int ROWS, class T, int V, int R>
 struct Stager {
     static constexpr int ROW = 32 * V, PER = 16 / sizeof(T), CH = ROW / PER, STEP = 32 / CH;  // chunks per row
-    static constexpr int STRIDE = RowOf<VEC, T, V>::STRIDE;
-    static_assert(CH <= 32 && R % STEP == 0, "whole warps of chunks");
-    const T* p;            // the next run's first row, VEC: the lane's first piece in it
-    long long ts, move;    // wide: STEP rows; one row
-    uint32_t at;           // VEC: the lane's place in a stage
-    int n;                 // VEC: whether the lane copies; else a row's bytes
-    bool wide;
+    static constexpr int STRIDE = RowOf<ROWS, T, V>::STRIDE;
+    static_assert(CH <= 32 && R % STEP == 0 && R <= 32, "whole warps of chunks, a lane per row");
+    const T* p;            // of the next run: the lane's first row, or its first piece there
+    long long ts, move;    // STEP rows, by lanes: one; from run to run
+    uintptr_t back;        // bytes from the run's first row to the lane's
     uintptr_t lowest;      // the array's first byte: nothing before it is read
-    uintptr_t back;        // VEC false: from p, at the lane's first row, to the run's
-    __device__ __forceinline__ Stager(const void* array, const T* base, long long token_stride, int channels, bool wide_,
-                                      long long first, long long ahead, int lane)
-        : wide(wide_), lowest(reinterpret_cast<uintptr_t>(array)) {
-        ts = VEC && wide ? STEP * token_stride : token_stride;
-        move = ahead * token_stride;
-        p = base + first * token_stride;
+    long long row;         // bytes from row to row
+    int n;                 // shifted: a row's bytes; else whether the lane copies
+    __device__ __forceinline__ Stager(const void* array, const T* base, long long token_stride, int channels, long long first,
+                                      long long ahead, int lane)
+        : ts(STEP * token_stride), move(ahead * token_stride), lowest(reinterpret_cast<uintptr_t>(array)),
+          row(token_stride * (long long)sizeof(T)) {
+        p = base + (first + lane / CH) * token_stride;
+        back = (uintptr_t)(lane / CH * row);
         n = (channels < ROW ? channels : ROW) * (int)sizeof(T);
-        at = 0;
-        if constexpr (VEC) {
-            const int row = wide ? lane / CH : 0, e = wide ? lane % CH * PER : lane * V;
-            p += row * token_stride + e;
-            at = (uint32_t)((row * ROW + e) * sizeof(T));
-            n = e < channels;
-        } else {
-            p += lane / CH * token_stride;
-            back = (uintptr_t)(lane / CH * token_stride * (long long)sizeof(T));
+        if constexpr (ROWS == kWide) {
+            p += lane % CH * PER;
+            n = lane % CH * PER < channels;
+        } else if constexpr (!kShifted<ROWS, T>) {
+            p = base + first * token_stride + lane * V;
+            ts = token_stride;
+            n = lane * V < channels;
         }
     }
-    template <int BYTES>
-    static __device__ __forceinline__ void piece(uint32_t dst, const T* src) {
-        if constexpr (BYTES == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-    }
     __device__ __forceinline__ void copy(T* stage, int rows, int lane) {
-        const uint32_t d = (uint32_t)__cvta_generic_to_shared(stage) + at;
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(stage);
         const T* q = p;
-        if constexpr (VEC) {
+        if constexpr (ROWS == kWide) {
             if (!n) return;
-            if (wide) {
 #pragma unroll
-                for (int k = 0; k < R / STEP; ++k) {
-                    if (rows >= R || k * STEP + lane / CH < rows) piece<16>(d + k * STEP * ROW * (int)sizeof(T), q);
-                    q += ts;
-                }
-            } else {
+            for (int k = 0; k < R / STEP; ++k) {
+                if (rows >= R || k * STEP + lane / CH < rows)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + (k * 32 + lane) * 16), "l"(q) : "memory");
+                q += ts;
+            }
+        } else if constexpr (!kShifted<ROWS, T>) {
+            if (!n) return;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r < rows) piece<V * sizeof(T)>(d + r * ROW * (int)sizeof(T), q);
-                    q += ts;
-                }
+            for (int r = 0; r < R; ++r) {
+                if (r < rows)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d + (r * ROW + lane * V) * (int)sizeof(T)), "l"(q),
+                                 "n"(V * sizeof(T))
+                                 : "memory");
+                q += ts;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < R / STEP; ++k) part(stage, d, q + (long long)(k * STEP) * ts, k * STEP + lane / CH, lane % CH, rows);
-            static_assert(R <= 32, "a lane per row");
-            if (lane < R) part(stage, d, reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(p) - back) + lane * ts, lane, CH, rows);
+            for (int k = 0; k < R / STEP; ++k) {
+                part(stage, d, reinterpret_cast<uintptr_t>(q), k * STEP + lane / CH, lane % CH, rows);
+                q += ts;
+            }
+            if (lane < R) part(stage, d, reinterpret_cast<uintptr_t>(p) - back + lane * row, lane, CH, rows);
         }
     }
-    // Piece k of a row that starts at q
-    __device__ __forceinline__ void part(T* stage, uint32_t d, const T* q, int row, int k, int rows) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(q), src = (a & ~(uintptr_t)15) + 16 * k;
+    // Piece k of the row at a
+    __device__ __forceinline__ void part(T* stage, uint32_t d, uintptr_t a, int row, int k, int rows) const {
+        const uintptr_t src = (a & ~(uintptr_t)15) + 16 * k;
         const int left = n - 16 * k + (int)(a & 15);  // bytes of the row, from src on
         if (row >= rows || left <= 0) return;
         if (src >= lowest) {
@@ -313,13 +313,13 @@ struct Stager {
     }
 };
 // Where a run's rows start in their stages, behind a multiple of 16 bytes.
-template <bool VEC, class T>
+template <int ROWS, class T>
 struct RowStart {
     uint32_t at, step;
     __device__ __forceinline__ RowStart(const T* base, long long token_stride)
         : at((uint32_t)reinterpret_cast<uintptr_t>(base)), step((uint32_t)(token_stride * sizeof(T))) {}
     __device__ __forceinline__ const T* row(const T* stage, int stride, int t0, int r) const {
-        if constexpr (VEC) return stage + r * stride;
+        if constexpr (!kShifted<ROWS, T>) return stage + r * stride;
         else return stage + r * stride + ((at + (uint32_t)(t0 + r) * step & 15u) / sizeof(T));
     }
 };
@@ -366,10 +366,13 @@ __device__ __forceinline__ void read_pairs(const T* p, F2* f) {
     }
 }
 // A row's, wherever it starts
-template <bool VEC, class T, int N>
+template <int ROWS, class T, int N>
 __device__ __forceinline__ void read_row(const T* p, F2* f) {
-    if constexpr (VEC) {
+    if constexpr (!kShifted<ROWS, T> || (ROWS == kPairs && N == 1)) {
         read_pairs<T, N>(p, f);
+    } else if constexpr (ROWS == kPairs) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) read_pairs<T, 1>(p + 2 * v, f + v);
     } else {
 #pragma unroll
         for (int v = 0; v < N; ++v) f[v] = f2(to_f(p[2 * v]), to_f(p[2 * v + 1]));
@@ -431,23 +434,23 @@ __device__ __forceinline__ void load_state(const float* p, int n, F2* f) {  // p
     }
 }
 // Whether no lane's z of a run is negative.
-template <bool VEC, class ZT, int N, int R>
-__device__ __forceinline__ bool none_negative(const RowStart<VEC, ZT>& at, const ZT* z, int stride, int t0) {
+template <int ROWS, class ZT, int N, int R>
+__device__ __forceinline__ bool none_negative(const RowStart<ROWS, ZT>& at, const ZT* z, int stride, int t0) {
     uint32_t bits = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const ZT* p = at.row(z, stride, t0, r);
-        if constexpr (VEC) {
-            constexpr int W = N * 2 * sizeof(ZT) / 4;
+        constexpr int W = N * 2 * sizeof(ZT) / 4;
+        if constexpr (!kShifted<ROWS, ZT>) {
             const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(p);
 #pragma unroll
             for (int v = 0; v < W; ++v) bits |= w.v[v];
+        } else if constexpr (sizeof(ZT) == 4) {
+#pragma unroll
+            for (int v = 0; v < W; ++v) bits |= reinterpret_cast<const uint32_t*>(p)[v];
         } else {
 #pragma unroll
-            for (int v = 0; v < 2 * N; ++v) {
-                if constexpr (sizeof(ZT) == 4) bits |= reinterpret_cast<const uint32_t*>(p)[v];
-                else bits |= reinterpret_cast<const uint16_t*>(p)[v];
-            }
+            for (int v = 0; v < 2 * N; ++v) bits |= reinterpret_cast<const uint16_t*>(p)[v];
         }
     }
     return !__any_sync(0xffffffffu, (bits & (sizeof(ZT) == 4 ? 0x80000000u : 0x80008000u)) != 0);
@@ -559,10 +562,10 @@ struct HeadGates {
 };
 
 // ---- forward
-template <class XT, int ZM, bool VEC, int V, int R, int NW, int NST>
+template <class XT, int ZM, int ROWS, int V, int R, int NW, int NST>
 struct FwdLayout {
     using ZT = typename std::conditional<ZM == kZ32, float, XT>::type;
-    static constexpr int XROW = RowOf<VEC, XT, V>::STRIDE, ZROW = RowOf<VEC, ZT, V>::STRIDE;
+    static constexpr int XROW = RowOf<ROWS, XT, V>::STRIDE, ZROW = RowOf<ROWS, ZT, V>::STRIDE;
     static constexpr int HO = ZM == kZHead ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, H)
     static constexpr int X = R * XROW * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : R * ZROW * sizeof(ZT);
     static constexpr int STAGE = X + Z;                      // bytes of a warp's stage
@@ -575,12 +578,12 @@ struct FwdLayout {
 
 // A lane has N = V/2 pairs of channels; with one gate per head, its first pair of gates
 // holds the same gate twice.
-template <class XT, int ZM, int FORM, bool VEC, int V, int R, int NW, int NST, int MINB>
+template <class XT, int ZM, int FORM, int ROWS, int V, int R, int NW, int NST, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArgs A) {
-    using Lay = FwdLayout<XT, ZM, VEC, V, R, NW, NST>;
+    using Lay = FwdLayout<XT, ZM, ROWS, V, R, NW, NST>;
     using ZT = typename Lay::ZT;
     constexpr int GATE = FORM / 3, WRITE = FORM % 3, L = NW * R, PAIR = Lay::PAIR, HO = Lay::HO, N = V / 2;
-    constexpr bool HEAD = ZM == kZHead;
+    constexpr bool HEAD = ZM == kZHead, VEC = ROWS != kAny;
     constexpr int NG = HEAD ? 1 : N;
     static_assert(kGatedMark % R == 0 || R % kGatedMark == 0, "runs and marks fall together");
     extern __shared__ __align__(16) unsigned char smem[];
@@ -605,10 +608,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = rank * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(A.x, x, A.xts, A.C - c0, A.wide, ts, K * L, lane);
-    Stager<VEC, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, K * L, lane);
-    const RowStart<VEC, XT> x_at(x, A.xts);
-    const RowStart<VEC, ZT> z_at(z, A.zts);
+    Stager<ROWS, XT, V, R> sx(A.x, x, A.xts, A.C - c0, ts, K * L, lane);
+    Stager<ROWS, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, HEAD ? 0 : ts, K * L, lane);
+    const RowStart<ROWS, XT> x_at(x, A.xts);
+    const RowStart<ROWS, ZT> z_at(z, A.zts);
     HeadGates<XT, V, R, 2> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts < len) {
@@ -653,19 +656,19 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
             });
         }
         bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<VEC, ZT, N, R>(z_at, zs, Lay::ZROW, t0);
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ROWS, ZT, N, R>(z_at, zs, Lay::ZROW, t0);
         // P: products of the run's gates, H: the run's states from h = 0, after each token
         F2 P[R][NG], H[R][N];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 xf[N], zf[N], a[N], w[N];
-            read_row<VEC, XT, N>(x_at.row(xs, Lay::XROW, t0, r), xf);
+            read_row<ROWS, XT, N>(x_at.row(xs, Lay::XROW, t0, r), xf);
             if constexpr (HEAD) {
                 F2 t[2];
                 hg.template get<2>(gates, r, t);
                 a[0] = t[0], w[0] = t[1];
             } else {
-                read_row<VEC, ZT, N>(z_at.row(zs, Lay::ZROW, t0, r), zf);
+                read_row<ROWS, ZT, N>(z_at.row(zs, Lay::ZROW, t0, r), zf);
             }
 #pragma unroll
             for (int v = 0; v < N; ++v) {
@@ -778,10 +781,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
 // dh_0 = a_1 g_1. Tiles run from the sequence's end to its start; a run's
 // states are rebuilt from the mark that the forward pass left at its start, and the
 // adjoint enters from behind, by the runs' pairs (P, G).
-template <class XT, int ZM, bool VEC, int V, int R, int NW, int NST>
+template <class XT, int ZM, int ROWS, int V, int R, int NW, int NST>
 struct BwdLayout {
     using ZT = typename std::conditional<ZM == kZ32, float, XT>::type;
-    static constexpr int XROW = RowOf<VEC, XT, V>::STRIDE, ZROW = RowOf<VEC, ZT, V>::STRIDE;
+    static constexpr int XROW = RowOf<ROWS, XT, V>::STRIDE, ZROW = RowOf<ROWS, ZT, V>::STRIDE;
     static constexpr int HO = ZM == kZHead ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, G)
     static constexpr int X = R * XROW * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : R * ZROW * sizeof(ZT);
     static constexpr int M = 2 * X + Z;           // the mark's place in a stage
@@ -793,12 +796,12 @@ struct BwdLayout {
     static constexpr int bytes(int K) { return SC + 2 * 32 * 4 * (K > 1 ? K * PAIR : V); }
 };
 
-template <class XT, int ZM, int FORM, bool VEC, int V, int R, int NW, int NST, int MINB>
+template <class XT, int ZM, int FORM, int ROWS, int V, int R, int NW, int NST, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArgs A) {
-    using Lay = BwdLayout<XT, ZM, VEC, V, R, NW, NST>;
+    using Lay = BwdLayout<XT, ZM, ROWS, V, R, NW, NST>;
     using ZT = typename Lay::ZT;
     constexpr int GATE = FORM / 3, WRITE = FORM % 3, L = NW * R, PAIR = Lay::PAIR, HO = Lay::HO, N = V / 2;
-    constexpr bool HEAD = ZM == kZHead;
+    constexpr bool HEAD = ZM == kZHead, VEC = ROWS != kAny;
     constexpr int NG = HEAD ? 1 : N;
     static_assert(R == kGatedMark, "a run starts at a mark");
     extern __shared__ __align__(16) unsigned char smem[];
@@ -827,10 +830,10 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 K * 32 * PAIR * 4, K > 1);
     unsigned char* mine = smem + warp * NST * Lay::STAGE;
     int ts = ((iters - 1) * K + rank) * L + warp * R;  // the run that is staged next
-    Stager<VEC, XT, V, R> sx(A.x, x, A.xts, A.C - c0, A.wide, ts, -K * L, lane), sd(A.dy, dy, A.dyts, A.C - c0, A.wide, ts, -K * L, lane);
-    Stager<VEC, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, A.wide, HEAD ? 0 : ts, -K * L, lane);
-    const RowStart<VEC, XT> x_at(x, A.xts), dy_at(dy, A.dyts);
-    const RowStart<VEC, ZT> z_at(z, A.zts);
+    Stager<ROWS, XT, V, R> sx(A.x, x, A.xts, A.C - c0, ts, -K * L, lane), sd(A.dy, dy, A.dyts, A.C - c0, ts, -K * L, lane);
+    Stager<ROWS, ZT, V, R> sz(A.z, z, A.zts, A.C - c0, HEAD ? 0 : ts, -K * L, lane);
+    const RowStart<ROWS, XT> x_at(x, A.xts), dy_at(dy, A.dyts);
+    const RowStart<ROWS, ZT> z_at(z, A.zts);
     HeadGates<XT, V, R, 4> hg(A, b, c0, lane);
     auto stage = [&](int slot) {
         if (ts >= 0) {
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
             });
         }
         bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<VEC, ZT, N, R>(z_at, zw + lane * V, Lay::ZROW, t0);
+        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ROWS, ZT, N, R>(z_at, zw + lane * V, Lay::ZROW, t0);
         // Of each token: a, then the product of the run's gates behind it; s (per head it stays
         // in shared memory); dz / g, per head without da/dz; the run's own adjoint, from 0.
         F2 a[R][NG], s[HEAD ? 1 : R][NG], k[R][N], gl[R][N], h[N];
@@ -901,14 +904,14 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 xf[N], zf[N], hs = f2(0.f);
-            read_row<VEC, XT, N>(x_at.row(xw + lane * V, Lay::XROW, t0, r), xf);
+            read_row<ROWS, XT, N>(x_at.row(xw + lane * V, Lay::XROW, t0, r), xf);
             if constexpr (HEAD) {
                 F2 t[WRITE == kUnit ? 4 : 2];
                 hg.template get<WRITE == kUnit ? 4 : 2>(gates, r, t);
                 a[r][0] = t[0], s[0][0] = t[1];
                 if constexpr (WRITE == kUnit) hs = t[2];
             } else {
-                read_row<VEC, ZT, N>(z_at.row(zw + lane * V, Lay::ZROW, t0, r), zf);
+                read_row<ROWS, ZT, N>(z_at.row(zw + lane * V, Lay::ZROW, t0, r), zf);
             }
 #pragma unroll
             for (int v = 0; v < N; ++v) {
@@ -930,7 +933,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
         F2 P[NG], G[N];
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) {
-            read_row<VEC, XT, N>(dy_at.row(dw + lane * V, Lay::XROW, t0, r), gl[r]);
+            read_row<ROWS, XT, N>(dy_at.row(dw + lane * V, Lay::XROW, t0, r), gl[r]);
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 if (r < R - 1) gl[r][v] = add2(gl[r][v], G[v]);

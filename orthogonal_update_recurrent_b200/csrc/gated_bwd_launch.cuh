@@ -6,29 +6,29 @@
 namespace lattice {
 namespace gated {
 
-template <class XT, int FORM, int ZM, bool VEC, int V, int NW, int NST, int MINB>
+template <class XT, int FORM, int ZM, int ROWS, int V, int NW, int NST, int MINB>
 lattice_status bwd_of(GatedArgs a, cudaStream_t st) {
     constexpr int R = kGatedMark;
-    static_assert(BwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(8) <= kMaxShared, "clusters of 8 fit");
+    static_assert(BwdLayout<XT, ZM, ROWS, V, R, NW, NST>::bytes(8) <= kMaxShared, "clusters of 8 fit");
     a.ctiles = (a.C + 32 * V - 1) / (32 * V);
-    return launch(gated_bwd_kernel<XT, ZM, FORM, VEC, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
-                  [](int K) { return BwdLayout<XT, ZM, VEC, V, R, NW, NST>::bytes(K); }, st);
+    return launch(gated_bwd_kernel<XT, ZM, FORM, ROWS, V, R, NW, NST, MINB>, a, NW * 32, NW * R, MINB,
+                  [](int K) { return BwdLayout<XT, ZM, ROWS, V, R, NW, NST>::bytes(K); }, st);
 }
 
 // Gates per channel: two channels per lane, 4 warps, two CTAs per SM. Gates per head: four
 // channels per lane, so that a warp's 128 channels hold whole heads (d <= 128) and a head's
 // gradient is summed within it; 8 warps (mid-size layer 90 us, 4 warps 106 us), 4 for fp32,
 // whose stages are twice as large.
-template <class XT, int FORM, int ZM, bool VEC>
+template <class XT, int FORM, int ZM, int ROWS>
 lattice_status bwd(const GatedArgs& a, cudaStream_t st) {
-    if constexpr (ZM == kZHead) return bwd_of<XT, FORM, ZM, VEC, kGatedHeadVec, sizeof(XT) == 2 ? 8 : 4, 2, 1>(a, st);
-    else return bwd_of<XT, FORM, ZM, VEC, kGatedBwdVec, 4, 2, 2>(a, st);
+    if constexpr (ZM == kZHead) return bwd_of<XT, FORM, ZM, ROWS, kGatedHeadVec, sizeof(XT) == 2 ? 8 : 4, 2, 1>(a, st);
+    else return bwd_of<XT, FORM, ZM, ROWS, kGatedBwdVec, 4, 2, 2>(a, st);
 }
 
 template <class XT>
 lattice_status launch_bwd(GatedArgs a, int form, bool vec, cudaStream_t st) {
     return with_form(form, [&](auto f) {
-        return with_gates<XT>(a, vec, [&](auto zm, auto v) {
+        return with_gates<XT>(a, vec ? a.wide ? kWide : kPairs : kAny, [&](auto zm, auto v) {
             return bwd<XT, decltype(f)::value, decltype(zm)::value, decltype(v)::value>(a, st);
         });
     });

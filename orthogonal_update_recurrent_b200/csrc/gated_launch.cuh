@@ -90,14 +90,17 @@ lattice_status with_form(int form, F f) {
     return LATTICE_ERR_INVALID_ARG;
 }
 
-// Calls f with where the gates come from and whether rows are vectors.
+// Calls f with where the gates come from and how rows start.
 template <class XT, class F>
-lattice_status with_gates(const GatedArgs& a, bool vec, F f) {
-    if (a.zhead) return vec ? f(Int<kZHead>(), std::true_type()) : f(Int<kZHead>(), std::false_type());
+lattice_status with_gates(const GatedArgs& a, int rows, F f) {
+    auto g = [&](auto zm) {
+        return rows == kWide ? f(zm, Int<kWide>()) : rows == kPairs ? f(zm, Int<kPairs>()) : f(zm, Int<kAny>());
+    };
+    if (a.zhead) return g(Int<kZHead>());
     if constexpr (sizeof(XT) == 2) {
-        if (a.z32) return vec ? f(Int<kZ32>(), std::true_type()) : f(Int<kZ32>(), std::false_type());
+        if (a.z32) return g(Int<kZ32>());
     }
-    return vec ? f(Int<kZSame>(), std::true_type()) : f(Int<kZSame>(), std::false_type());
+    return g(Int<kZSame>());
 }
 
 // Calls f with a value of x's type.
