@@ -566,7 +566,7 @@ template <class XT, int ZM, int ROWS, int V, int R, int NW, int NST>
 struct FwdLayout {
     using ZT = typename std::conditional<ZM == kZ32, float, XT>::type;
     static constexpr int XROW = RowOf<ROWS, XT, V>::STRIDE, ZROW = RowOf<ROWS, ZT, V>::STRIDE;
-    static constexpr int HO = ZM == kZHead ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, H)
+    static constexpr int HO = ZM == kZHead && V > 2 ? 4 : V, PAIR = (HO + V + 3) / 4 * 4;  // floats of a lane's (P, H)
     static constexpr int X = R * XROW * sizeof(XT), Z = ZM == kZHead ? V * R * 8 : R * ZROW * sizeof(ZT);
     static constexpr int STAGE = X + Z;                      // bytes of a warp's stage
     static constexpr int HG = NW * NST * STAGE;              // a warp's gates per head
