@@ -103,7 +103,7 @@ __device__ __forceinline__ F2 expm1_small(F2 w) {
 // retention time, so its last bit must not be biased, as an approximate reciprocal's may
 // be: with t = exp(-z), r = 1/(1 + t) gets one Newton step, a = r (2 - (1 + t) r), and 1 - a is
 // t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126. With
-// tau, `fast` says that the run has no z < 0 and tau <= 1, which leaves out what those need
+// tau, `fast` says that the warp's gates of the token have no z < 0 and tau <= 1, which leaves out what those need
 // (long context 259 us; by log(1 + t) and exp, for every z, 307 us).
 template <int GATE>
 __device__ __forceinline__ void gates_of(F2 z, const GatedArgs& A, bool fast, F2& a, F2& q) {
@@ -433,27 +433,34 @@ __device__ __forceinline__ void load_state(const float* p, int n, F2* f) {  // p
         for (int v = 0; v < N; ++v) f[v] = f2(t.v[2 * v], t.v[2 * v + 1]);
     }
 }
-// Whether no lane's z of a run is negative.
-template <int ROWS, class ZT, int N, int R>
-__device__ __forceinline__ bool none_negative(const RowStart<ROWS, ZT>& at, const ZT* z, int stride, int t0) {
+// The sign bits of a lane's z of a row, at any place of the words.
+template <int ROWS, class ZT, int N>
+__device__ __forceinline__ uint32_t signs(const ZT* p) {
+    constexpr int W = N * 2 * sizeof(ZT) / 4;
     uint32_t bits = 0;
+    if constexpr (!kShifted<ROWS, ZT>) {
+        const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(p);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const ZT* p = at.row(z, stride, t0, r);
-        constexpr int W = N * 2 * sizeof(ZT) / 4;
-        if constexpr (!kShifted<ROWS, ZT>) {
-            const Vec<uint32_t, W> w = *reinterpret_cast<const Vec<uint32_t, W>*>(p);
+        for (int v = 0; v < W; ++v) bits |= w.v[v];
+    } else if constexpr (sizeof(ZT) == 4) {
 #pragma unroll
-            for (int v = 0; v < W; ++v) bits |= w.v[v];
-        } else if constexpr (sizeof(ZT) == 4) {
+        for (int v = 0; v < W; ++v) bits |= reinterpret_cast<const uint32_t*>(p)[v];
+    } else {
 #pragma unroll
-            for (int v = 0; v < W; ++v) bits |= reinterpret_cast<const uint32_t*>(p)[v];
-        } else {
-#pragma unroll
-            for (int v = 0; v < 2 * N; ++v) bits |= reinterpret_cast<const uint16_t*>(p)[v];
-        }
+        for (int v = 0; v < 2 * N; ++v) bits |= reinterpret_cast<const uint16_t*>(p)[v];
     }
-    return !__any_sync(0xffffffffu, (bits & (sizeof(ZT) == 4 ? 0x80000000u : 0x80008000u)) != 0);
+    return bits & (sizeof(ZT) == 4 ? 0x80000000u : 0x80008000u);
+}
+// The rows of a run, as bits, in which some lane's z is negative; mostly none.
+template <int ROWS, class ZT, int N, int R>
+__device__ __forceinline__ uint32_t negative_rows(const RowStart<ROWS, ZT>& at, const ZT* z, int stride, int t0) {
+    uint32_t all = 0, rows = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) all |= signs<ROWS, ZT, N>(at.row(z, stride, t0, r));
+    if (!__any_sync(0xffffffffu, all != 0)) return 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) rows |= signs<ROWS, ZT, N>(at.row(z, stride, t0, r)) ? 1u << r : 0u;
+    return __reduce_or_sync(0xffffffffu, rows);
 }
 template <class XT>
 __device__ __forceinline__ float load_gate(const void* z, long long off, bool z32) {
@@ -655,8 +662,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 out[1] = writes_of<GATE, WRITE>(out[0], hq);
             });
         }
-        bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ROWS, ZT, N, R>(z_at, zs, Lay::ZROW, t0);
+        uint32_t slow = ~0u;  // rows of which some gate needs more
+        if constexpr (!HEAD && GATE == kLogitTau)
+            if (A.squares == 0) slow = negative_rows<ROWS, ZT, N, R>(z_at, zs, Lay::ZROW, t0);
         // P: products of the run's gates, H: the run's states from h = 0, after each token
         F2 P[R][NG], H[R][N];
 #pragma unroll
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_fwd_kernel(const GatedArg
                 const int k = HEAD ? 0 : v;
                 if constexpr (!HEAD) {
                     F2 q;
-                    gates_of<GATE>(zf[v], A, fast, a[v], q);
+                    gates_of<GATE>(zf[v], A, !(slow >> r & 1u), a[v], q);
                     w[v] = writes_of<GATE, WRITE>(a[v], q);
                 }
                 const F2 u = WRITE == kPlain ? xf[v] : mul2(w[k], xf[v]);
@@ -895,8 +903,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 out[3] = f2(0.f);
             });
         }
-        bool fast = false;
-        if constexpr (!HEAD && GATE == kLogitTau) fast = A.squares == 0 && none_negative<ROWS, ZT, N, R>(z_at, zw + lane * V, Lay::ZROW, t0);
+        uint32_t slow = ~0u;  // rows of which some gate needs more
+        if constexpr (!HEAD && GATE == kLogitTau)
+            if (A.squares == 0) slow = negative_rows<ROWS, ZT, N, R>(z_at, zw + lane * V, Lay::ZROW, t0);
         // Of each token: a, then the product of the run's gates behind it; s (per head it stays
         // in shared memory); dz / g, per head without da/dz; the run's own adjoint, from 0.
         F2 a[R][NG], s[HEAD ? 1 : R][NG], k[R][N], gl[R][N], h[N];
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
                 const int i = HEAD ? 0 : v;
                 F2 q;
                 if constexpr (!HEAD) {
-                    gates_of<GATE>(zf[v], A, fast, a[r][i], q);
+                    gates_of<GATE>(zf[v], A, !(slow >> r & 1u), a[r][i], q);
                     s[r][i] = writes_of<GATE, WRITE>(a[r][i], q);
                     if constexpr (WRITE == kUnit) hs = unit_slopes(a[r][i], s[r][i]);
                 }
