@@ -104,7 +104,7 @@ __device__ __forceinline__ F2 expm1_small(F2 w) {
 // be: with t = exp(-z), r = 1/(1 + t) gets one Newton step, a = r (2 - (1 + t) r), and 1 - a is
 // t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126. With
 // tau, `fast` says that the warp's gates of the token have no z < 0 and tau <= 1, which leaves out what those need
-// (long context 259 us; by log(1 + t) and exp, for every z, 307 us).
+// (long context 264 us, 317 us without `fast`; by log(1 + t) and exp, for every z, 307 us).
 template <int GATE>
 __device__ __forceinline__ void gates_of(F2 z, const GatedArgs& A, bool fast, F2& a, F2& q) {
     if constexpr (GATE == kValue) {
@@ -473,7 +473,7 @@ __device__ __forceinline__ float load_gate(const void* z, long long off, bool z3
 // each token needs in the warp's shared memory, every value twice, ready for packed
 // arithmetic. The raw gates are staged with the rows: a register that a load is still to
 // fill cannot be moved on, which kept them one iteration ahead and made the load's latency
-// the iteration's length (head gates of the mid-size layer 84 us, staged 61 us).
+// the iteration's length (head gates of the mid-size layer 84 us, staged 61 us, 54 us since).
 template <class XT, int V, int R, int W>
 struct HeadGates {
     static constexpr int PER = V * R / 16;           // gates per lane: at most 32 V / 16 heads
@@ -1014,9 +1014,9 @@ __global__ void __launch_bounds__(NW * 32, MINB) gated_bwd_kernel(const GatedArg
             for (int v = 0; v < N; ++v) g[v] = fma2(P[HEAD ? 0 : v], gin[v], G[v]);
             write_pairs<N>(sc + ((buf ^ 1) * 32 + lane) * V, g);
         }
-        // per head: the lanes' shares of dz, [R][36], where x stood
+        // per head: the lanes' shares of dz, [R][36], where x and dy stood
         float* sums = reinterpret_cast<float*>(xw);
-        static_assert(!HEAD || R * 36 * 4 <= Lay::X, "x's stage holds the shares");
+        static_assert(!HEAD || R * 36 * 4 <= 2 * Lay::X, "the stages hold the shares");
         if constexpr (HEAD) __syncwarp();
         XT* dxt = dx + (long long)t0 * A.C;
         ZT* dzt = static_cast<ZT*>(A.dz) + dzoff + (long long)t0 * nz;

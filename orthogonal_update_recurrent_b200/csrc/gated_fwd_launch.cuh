@@ -7,7 +7,7 @@ namespace lattice {
 namespace gated {
 
 // Two channels per lane; runs of 16 tokens on 8 warps, two CTAs per SM (mid-size layer, bf16:
-// 78 us; runs of 8 on three CTAs 86 us: a run's exchange is then spread over half the
+// 78 us, 74 us since; runs of 8 on three CTAs 86 us: a run's exchange is then spread over half the
 // elements). fp32 rows are twice as wide, so runs of 8 keep the stages as large.
 template <class XT, int FORM, int ZM, int ROWS>
 lattice_status fwd(GatedArgs a, cudaStream_t st) {

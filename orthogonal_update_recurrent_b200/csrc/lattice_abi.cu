@@ -155,7 +155,7 @@ lattice_status check_gated(lattice_dtype x_dtype, lattice_dtype z_dtype, int z_p
 }
 
 // The polynomial in t that meets (1 - (1 + t)^-tau)/t at the Chebyshev nodes of [0, 1], for
-// tau <= 1, where its error is a few 1e-9 of its value; larger tau are halved first.
+// tau <= 1, where its error is at most 5e-8 of its value; larger tau are halved first.
 void gated_poly(GatedArgs& a) {
     constexpr int n = kGatedPoly;
     double tau = a.tau;
