@@ -283,8 +283,8 @@ lattice_status lattice_readout(const float *S, const void *q, lattice_dtype q_dt
  * Layouts: x [B][T][H][d]; z [B][T][H][d], or [B][T][H] with z_per_head != 0 (then d in
  * {16, 32, 64, 128}); h0, h_out [B][H][d] fp32, row-major; y [B][T][H][d] in x's type. x,
  * z and dy may be slices of wider rows: their batch and token strides are given in
- * elements (>= 0), a token's own H*d (or H) elements are contiguous. Every output is
- * contiguous. x: fp32, bf16 or fp16; z: fp32 or x's type. Arithmetic and state are fp32
+ * elements (>= 0), a token's own H*d (or H) elements are contiguous; the bytes between
+ * rows must be readable, whatever they hold. Every output is contiguous. x: fp32, bf16 or fp16; z: fp32 or x's type. Arithmetic and state are fp32
  * whatever the types; y and the gradients are rounded once.
  * Sizes: B, H, d >= 1, T >= 0; H*d and T up to 2^30.
  * lengths (int32 [B], device, or NULL for T each) gives every sequence its own length,
@@ -350,7 +350,8 @@ lattice_status lattice_gated_step(const float *h, float *h_out, const void *x,
  * Rows: N rows of D contiguous elements, 1 <= D <= 16384, 0 <= N < 2^31. Inputs come in
  * groups of G rows (N a multiple of G), contiguous within a group, with the given stride
  * in elements (0 to 2^31 - 1) between groups: G = 1 for rows of any stride, G = H for heads
- * [B*T][H][D] cut out of wider tokens. Outputs are contiguous.
+ * [B*T][H][D] cut out of wider tokens; what is between groups must be readable, whatever it
+ * holds. Outputs are contiguous.
  * act: applied to the gate; NONE: the gate is not allowed. eps > 0. */
 typedef enum { LATTICE_ACT_NONE = 0, LATTICE_ACT_SIGMOID = 1, LATTICE_ACT_SILU = 2, LATTICE_ACT_GELU = 3 } lattice_act;
 

@@ -131,6 +131,30 @@ def test_arrays_that_start_anywhere(L, d, head, dtype):
         assert torch.equal(y, want["y"]) and (room[:off] == 7).all() and (room[off + y.numel():] == 7).all()
 
 
+def test_large_clusters_on_two_streams_at_once(L):
+    """Clusters of many CTAs, launched side by side: each call's results are its own."""
+    ts = [make(1, 5000, 1, d, dtype="bf16", mean=4.0, seed=40 + d) for d in (40, 64)]
+    want = []
+    for t in ts:
+        marks = L.gated_scan_marks(t["x"])
+        y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=marks)
+        want.append((y, h, L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ts]
+    got = [[], []]
+    for _ in range(10):
+        for k, (t, s) in enumerate(zip(ts, streams)):
+            with torch.cuda.stream(s):
+                marks = L.gated_scan_marks(t["x"])
+                y, h = L.gated_scan_fwd(t["x"], t["z"], t["h0"], marks=marks)
+                got[k].append((y, h, L.gated_scan_bwd(t["x"], t["z"], t["dy"], marks)))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for y, h, g in got[k]:
+            assert torch.equal(y, want[k][0]) and torch.equal(h, want[k][1])
+            assert all(torch.equal(g[n], want[k][2][n]) for n in g)
+
+
 def test_no_initial_state_and_no_final_cotangent(L):
     both(L, make(2, 100, 1, 20, seed=6), h0=False, dh_T=False)
 
