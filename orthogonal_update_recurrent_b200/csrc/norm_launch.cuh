@@ -47,9 +47,13 @@ struct Split {
 // 16384, backward: 543 us with a cluster of 4 for every 4 SMs, 316 us with as many as are held.)
 constexpr int kMaxDevices = 16;
 
-template <class Kernel>
-lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int mode, int bytes_per_thread, int* groups, cudaStream_t st) {
-    const Split split(a.D, bwd, mode);
+template <class F, bool SUB, bool BWD>  // names the kernel: all of them have one type
+lattice_status launch(const NormArgs& a, int* groups, cudaStream_t st) {
+    constexpr int mode = F::MODE, bytes_per_thread = BWD ? 128 : 64;
+    void (*k)(NormArgs);
+    if constexpr (BWD) k = norm_bwd_kernel<F, SUB>;
+    else k = norm_fwd_kernel<F, SUB>;
+    const Split split(a.D, BWD, mode);
     const int threads = split.threads, smem = threads * bytes_per_thread;
     cudaError_t e;
     if (smem > 40 * 1024) {  // 48 KB with the static arrays
@@ -68,7 +72,7 @@ lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int mode, int bytes
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.K > 1 ? 1 : 0;
-    static std::atomic<int> held[kMaxDevices][33][3];  // by warps of a CTA, and K: 1, 2, 4
+    static std::atomic<int> held[kMaxDevices][33][3];  // of this kernel, by warps of a CTA, and K: 1, 2, 4
     int dev = 0, c = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -93,8 +97,7 @@ lattice_status launch(Kernel k, const NormArgs& a, bool bwd, int mode, int bytes
 
 template <class F, bool SUB>
 lattice_status run(bool bwd, const NormArgs& a, int* groups, cudaStream_t st) {
-    return bwd ? launch(norm_bwd_kernel<F, SUB>, a, true, F::MODE, 128, groups, st)
-               : launch(norm_fwd_kernel<F, SUB>, a, false, F::MODE, 64, groups, st);
+    return bwd ? launch<F, SUB, true>(a, groups, st) : launch<F, SUB, false>(a, groups, st);
 }
 
 template <class T, bool SUB, bool GATE, int Y32, int R32>
