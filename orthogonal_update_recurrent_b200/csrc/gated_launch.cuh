@@ -28,7 +28,9 @@ lattice_status launch(Kernel k, GatedArgs a, int threads, int tile, int resident
     if (K > kGatedMaxK) K = kGatedMaxK;
     if (K > ((long long)a.T + tile - 1) / tile) K = ((long long)a.T + tile - 1) / tile;
     if (K < 1) K = 1;
-    while (bytes((int)K) > kMaxShared) --K;
+    int most = kGatedMaxK;  // the largest K whose shared memory a CTA may have
+    while (bytes(most) > kMaxShared) --most;
+    if (K > most) K = most;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -44,7 +46,7 @@ lattice_status launch(Kernel k, GatedArgs a, int threads, int tile, int resident
         a.K = (int)K;
         const int smem = bytes(a.K);
         if (smem > 40 * 1024) {
-            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = allow_shared(k, bytes(most));
             if (e != cudaSuccess) return cuda_fail(e);
         }
         if (K > 8) {  // above the portable size

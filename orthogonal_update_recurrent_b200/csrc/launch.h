@@ -14,6 +14,13 @@ namespace lattice {
 lattice_status cuda_fail(cudaError_t e);
 lattice_status launch_status();
 int sm_count();
+// Lets a kernel be launched with up to `most` bytes of dynamic shared memory. The limit belongs to
+// the kernel on its device, whoever calls: it is set to the most that any of the kernel's launches
+// takes, so that a launch never meets the smaller limit of another host thread's call.
+template <class... A>
+cudaError_t allow_shared(void (*kernel)(A...), size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
 // CTAs per sequence for the CUDA-core kernels (a cluster when > 1)
 int cluster_split(int B, int H, int m);
 

@@ -4,6 +4,8 @@ import ctypes
 import os
 import subprocess
 import sys
+import threading
+import time
 
 import pytest
 
@@ -69,3 +71,77 @@ def test_a_norm_kernels_grid_is_its_own(L):
                           check=True, capture_output=True, text=True, timeout=300).stdout for before in (False, True)]
     assert got[0] == got[1]
     assert got[0].count("(") == 2
+
+
+def recorded(L, f):
+    """The library call that f makes, as (function, arguments), and what f returned."""
+    library, calls = L.lib(), []
+
+    class Recorder:
+        def __getattr__(self, name):
+            fn = getattr(library, name)
+
+            def call(*args):
+                calls.append((fn, args))
+                return fn(*args)
+            return call if name.startswith("lattice_") and not name.endswith("bytes") else fn
+    L.lib, real = lambda: Recorder(), L.lib
+    try:
+        out = f()
+    finally:
+        L.lib = real
+    assert len(calls) == 1
+    return calls[0], out
+
+
+def at_once(L, fs, seconds=2.0):
+    """Repeats the library calls of fs, each on a host thread of its own, and counts those that fail."""
+    calls = [recorded(L, f) for f in fs]
+    torch.cuda.synchronize()
+    failed, start = [0] * len(fs), threading.Barrier(len(fs))
+
+    def repeat(k):
+        fn, args = calls[k][0]
+        start.wait()
+        end = time.monotonic() + seconds
+        while time.monotonic() < end:
+            for _ in range(100):
+                failed[k] += fn(*args) != 0
+    switch = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        threads = [threading.Thread(target=repeat, args=(k,)) for k in range(len(fs))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(switch)
+    torch.cuda.synchronize()
+    return failed
+
+
+def normal(*shape, dtype=torch.float32, seed=0):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("head", [False, True])
+def test_gated_calls_of_two_host_threads(L, dtype, head):
+    """Shapes of one kernel that take clusters of different sizes, and so of different shared memory."""
+    sets = []
+    for B, T, H in ((1, 5000, 1), (64, 2, 16), (1, 900, 1)):
+        x, dy = normal(B, T, H, 64, dtype=dtype), normal(B, T, H, 64, dtype=dtype, seed=1)
+        z = normal(B, T, H, dtype=dtype) if head else normal(B, T, H, 64, dtype=dtype, seed=2)
+        marks = L.gated_scan_marks(x)
+        y, h = L.gated_scan_fwd(x, z, marks=marks)
+        sets.append((x, z, dy, marks, y, h, L.gated_scan_bwd(x, z, dy, marks)))
+    assert at_once(L, [lambda s=s: L.gated_scan_fwd(s[0], s[1], y=s[4], h_out=s[5]) for s in sets]) == [0, 0, 0]
+    assert at_once(L, [lambda s=s: L.gated_scan_bwd(*s[:4]) for s in sets]) == [0, 0, 0]
+    for x, z, dy, marks, y, h, g in sets:
+        again, state = L.gated_scan_fwd(x, z)
+        assert torch.equal(again, y) and torch.equal(state, h)
+        grads = L.gated_scan_bwd(x, z, dy, marks)
+        assert all(torch.equal(grads[k], g[k]) for k in g)
