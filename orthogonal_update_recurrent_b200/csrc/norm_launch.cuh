@@ -57,7 +57,7 @@ lattice_status launch(const NormArgs& a, int* groups, cudaStream_t st) {
     const int threads = split.threads, smem = threads * bytes_per_thread;
     cudaError_t e;
     if (smem > 40 * 1024) {  // 48 KB with the static arrays
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = allow_shared(k, (size_t)split.most * bytes_per_thread);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     cudaLaunchConfig_t cfg = {};

@@ -145,3 +145,20 @@ def test_gated_calls_of_two_host_threads(L, dtype, head):
         assert torch.equal(again, y) and torch.equal(state, h)
         grads = L.gated_scan_bwd(x, z, dy, marks)
         assert all(torch.equal(grads[k], g[k]) for k in g)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_calls_of_two_host_threads(L, dtype):
+    """Widths of one kernel that take different shared memory."""
+    for back, widths in ((False, (8192, 6000)), (True, (4096, 2888)), (True, (8192, 6000))):
+        sets = []
+        for D in widths:
+            y, w = normal(8, D, dtype=dtype), normal(D, seed=1)
+            out = L.block_norm_fwd(y, w)[0]
+            sets.append((y, out, L.block_norm_bwd(y, dr=y)["dy"], w))
+        if back:
+            assert at_once(L, [lambda s=s: L.block_norm_bwd(s[0], dr=s[0]) for s in sets]) == [0, 0]
+        else:
+            assert at_once(L, [lambda s=s: L.block_norm_fwd(s[0], s[3], r_out=s[1]) for s in sets]) == [0, 0]
+        for y, out, dy, w in sets:
+            assert torch.equal(L.block_norm_fwd(y, w)[0], out) and torch.equal(L.block_norm_bwd(y, dr=y)["dy"], dy)
