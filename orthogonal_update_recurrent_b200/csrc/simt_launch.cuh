@@ -33,7 +33,7 @@ template <int D, int RQ, bool CH, bool DEC, bool LIN1>
 lattice_status launch_scan_simt_t(const ScanArgs& a, int nw, cudaStream_t st) {
     size_t smem = scan_smem_bytes<D>(a.m, nw, DEC);
     auto k = scan_simt_kernel<D, RQ, CH, DEC, LIN1>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(k, scan_smem_bytes<D>(64 * RQ, 16, DEC));  // every m it serves
     if (e != cudaSuccess) return cuda_fail(e);
     k<<<a.B * a.H, nw * 32, smem, st>>>(a);
     return launch_status();
@@ -44,7 +44,7 @@ template <int D, bool CH, bool DEC, bool LIN1>
 lattice_status launch_scan_simt_split(const ScanArgs& a, cudaStream_t st) {
     const size_t smem = scan_smem_bytes<D>(a.m, 8, DEC, true, CH);
     auto k = scan_simt_kernel<D, 1, CH, DEC, LIN1, true>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(k, scan_smem_bytes<D>(4 * 32, 8, DEC, true, CH));  // 32 slots per CTA at most
     if (e != cudaSuccess) return cuda_fail(e);
     ScanArgs arg = a;
     void* args[] = {&arg};

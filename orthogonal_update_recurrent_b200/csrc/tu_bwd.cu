@@ -12,7 +12,7 @@ lattice_status launch_bwd_t(const BwdArgs& a, cudaStream_t st) {
     constexpr int nt = bwd_threads(SPLIT);
     const size_t smem = bwd_smem_bytes(D, a.spc, nt / 32, SPLIT);
     auto k = scan_bwd_kernel<D, RQ, CH, SPLIT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(k, bwd_smem_bytes(D, SPLIT ? 32 : 64 * RQ, nt / 32, SPLIT));  // every m it serves
     if (e != cudaSuccess) return cuda_fail(e);
     if (a.G == 1) {
         k<<<a.B * a.H, nt, smem, st>>>(a);

@@ -162,3 +162,25 @@ def test_norm_calls_of_two_host_threads(L, dtype):
             assert at_once(L, [lambda s=s: L.block_norm_fwd(s[0], s[3], r_out=s[1]) for s in sets]) == [0, 0]
         for y, out, dy, w in sets:
             assert torch.equal(L.block_norm_fwd(y, w)[0], out) and torch.equal(L.block_norm_bwd(y, dr=y)["dy"], dy)
+
+
+@pytest.mark.parametrize("B,H,ms,chunk", [(200, 1, (16, 64), 1), (200, 1, (16, 64), 8), (200, 1, (68, 128), 1), (1, 2, (40, 100), 1),
+                                          (1, 2, (40, 100), 16)])
+@pytest.mark.parametrize("mode", ["sim", "dec"])
+def test_state_recurrence_calls_of_two_host_threads(L, B, H, ms, chunk, mode):
+    """Slot counts of one kernel, on one CTA per sequence and in clusters: CUDA-core scan, and the
+    token-by-token backward pass."""
+    T, d, sets = 16, 64, []
+    for m in ms:
+        ins = (normal(B, T, H, d), torch.sigmoid(normal(B, T, H, m, seed=1)), normal(B, T, H, m, seed=2),
+               torch.sigmoid(normal(B, T, H, seed=3)), torch.nn.functional.normalize(normal(B, H, m, d, seed=4), dim=-1))
+        kw = dict(chunk=chunk, mode=mode)
+        sets.append((ins, kw, L.scan_fwd(*ins, **kw)))
+    assert at_once(L, [lambda s=s: L.scan_fwd(*s[0], **s[1]) for s in sets], 1.0) == [0, 0]
+    if mode == "sim" and chunk == 1:
+        dy = normal(B, T, H, d, seed=5)
+        room = [torch.empty(L.scan_bwd_workspace_bytes(B, T, H, m, d), dtype=torch.uint8, device="cuda") for m in ms]
+        assert at_once(L, [lambda s=s, w=w: L.scan_bwd(*s[0], dy, workspace=w) for s, w in zip(sets, room)], 1.0) == [0, 0]
+    for ins, kw, (y, S) in sets:
+        again, state = L.scan_fwd(*ins, **kw)
+        assert torch.equal(again, y) and torch.equal(state, S)
