@@ -346,7 +346,7 @@ lattice_status lattice_gated_step(const float *h, float *h_out, const void *x,
  *     n = r / sqrt(mean r^2 + eps) w_pre (if wanted)
  * Types: `dtype` is that of gate and n; y, residual and r, and the weights (both) are of it
  * or fp32. r has the residual's type, or dtype without one. Arithmetic is fp32 and n is
- * formed from r before its rounding.
+ * formed from r before its rounding; the sum of a row's squares must be within fp32's range.
  * Rows: N rows of D contiguous elements, 1 <= D <= 16384, 0 <= N < 2^31. Inputs come in
  * groups of G rows (N a multiple of G), contiguous within a group, with the given stride
  * in elements (0 to 2^31 - 1) between groups: G = 1 for rows of any stride, G = H for heads

@@ -630,7 +630,8 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
             } else {
                 sums.template sum<2>(s);
             }
-            const float rho2 = rsqrtf(fmaf(s[0], A.inv_d, A.eps)), k2 = rho2 * rho2 * rho2 * s[1] * A.inv_d;
+            // from the sum on: rho^3 alone leaves fp32's range for rows of 1e13 and an eps of 1e-26
+            const float rho2 = rsqrtf(fmaf(s[0], A.inv_d, A.eps)), k2 = s[1] * A.inv_d * rho2 * rho2 * rho2;
             if (A.post) k = fmaf(rho2, s[3], s[2]) - k2 * s[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
             own_write(dp, acc);
         }
         if (A.dresidual && in) store8<XT, MODE>(A.dresidual, r32, o, c, e);
-        k *= -rho1 * rho1 * rho1 * A.inv_d;
+        k *= -rho1 * A.inv_d * rho1;  // and once more with y
         own_read(wq, w);
         own_read(dq, acc);
 #pragma unroll
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
             acc[v] = GATE ? fma2(u, f[v], acc[v]) : add2(u, acc[v]);
             if constexpr (GATE) df[v] = mul2(mul2(df[v], u), w[v]);
             e[v] = mul2(e[v], GATE ? mul2(w[v], f[v]) : w[v]);
-            e[v] = fma2(y[v], f2(k), e[v]);
+            e[v] = fma2(mul2(y[v], f2(rho1)), f2(k), e[v]);
         }
         own_write(dq, acc);
         if constexpr (GATE)

@@ -107,6 +107,36 @@ def test_rows_of_nothing(L):
     both(L, t)
 
 
+@pytest.mark.parametrize("N,D", [(5, 64), (7, 63), (3, 200), (3, 2048), (2, 9000)])
+def test_rows_of_nothing_with_a_tiny_epsilon(L, N, D):
+    """1/sqrt(eps) to the third power is past fp32's range here, for zero rows, and in the threads
+    of a CTA that have no row, too."""
+    for post in (True, False):
+        t = make((N, D), "f32", seed=D)
+        both(L, t, post=post, eps=1e-30)
+        t["y"][1], t["residual"][1] = 0, 0
+        both(L, t, post=post, eps=1e-30)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,D", [(5, 64), (3, 2048), (4, 1001), (2, 9000)])
+@pytest.mark.parametrize("size", [1e13, 1e15, 1e17])
+def test_rows_of_large_values(L, N, D, dtype, size):
+    """Their inverse root mean square to the third power is below fp32's range; their gradients are not.
+    A row's sum of squares has to be within it, too: 9000 values of deviation 2e17 have 3.6e38, past
+    the 3.4e38 that fp32 holds, and are not supported."""
+    if D * (2 * size) ** 2 > 3.4e38:
+        pytest.skip("the sum of squares is past fp32's range")
+    for post, residual in ((True, True), (False, True), (True, False)):
+        t = make((N, D), dtype, seed=D, residual=residual)
+        t["y"] *= size
+        if residual:
+            t["residual"] *= size
+            t["dr"] /= size
+        both(L, t, post=post)
+        both(L, t, post=post, pre=False)
+
+
 def test_groups_of_wider_rows(L):
     B, T, H, d = 2, 6, 3, 32
     t = make((B, T, H, d), "bf16", seed=9)
