@@ -10,6 +10,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "launch.h"
@@ -206,6 +207,13 @@ bool rows_vec(const void* p, size_t size, int B, int T, long long bs, long long 
 bool gate_words(const void* z, int H, long long bs, long long ts) {
     return aligned(z, 4) && H % 2 == 0 && bs % 2 == 0 && ts % 2 == 0;
 }
+
+// The layer operators' units, by type of x or of the call, that a call has launched or captured
+// kernels of. Only these can have set their status word, and reading one takes 12 us.
+enum LayerUnit { kGatedFwdUnit, kGatedBwdUnit, kNormUnit };
+std::atomic<bool> g_unit_used[3][3];
+void use_unit(LayerUnit u, lattice_dtype t) { g_unit_used[u][t].store(true, std::memory_order_relaxed); }
+bool unit_used(LayerUnit u, lattice_dtype t) { return g_unit_used[u][t].load(std::memory_order_relaxed); }
 
 template <class F>
 lattice_status with_x(lattice_dtype t, F f) {
@@ -513,6 +521,7 @@ lattice_status lattice_gated_scan_fwd(const void* x, lattice_dtype x_dtype, long
                      (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, v * sz_));
     a.wide = vec && C % (16 / sx_) == 0 && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
              (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, 16));
+    use_unit(kGatedFwdUnit, x_dtype);
     return with_x(x_dtype, [&](auto t) {
         return gated::launch_fwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
     });
@@ -563,6 +572,7 @@ lattice_status lattice_gated_scan_bwd(const void* x, lattice_dtype x_dtype, long
                      (a.zhead || (rows_vec(z, sz_, B, T, a.zbs, a.zts, v * sz_) && aligned(dz, v * sz_)));
     a.wide = vec && C % (16 / sx_) == 0 && rows_vec(x, sx_, B, T, a.xbs, a.xts, 16) &&
              rows_vec(dy, sx_, B, T, a.dybs, a.dyts, 16) && (a.zhead || rows_vec(z, sz_, B, T, a.zbs, a.zts, 16));
+    use_unit(kGatedBwdUnit, x_dtype);
     return with_x(x_dtype, [&](auto t) {
         return gated::launch_bwd<decltype(t)>(a, gated_form(gate, write, tau), vec, static_cast<cudaStream_t>(stream));
     });
@@ -632,6 +642,7 @@ lattice_status lattice_block_norm_fwd(const void* y, lattice_dtype y_dtype, long
                        norm_rows_shift(residual, residual_dtype, N, G, D, residual_stride) && aligned(r_out, 16) &&
                        aligned(n_out, 16);
     const int mode = vec ? kNormVec : shift ? kNormShift : kNormOdd;
+    use_unit(kNormUnit, dtype);
     return with_x(dtype, [&](auto t) {
         return norm::launch_norm<decltype(t)>(false, a, mode, nullptr, static_cast<cudaStream_t>(stream));
     });
@@ -711,6 +722,7 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
                        aligned(dy, 16) && aligned(dgate, 16) && aligned(dresidual, 16);
     const int mode = vec ? kNormVec : shift ? kNormShift : kNormOdd;
     int groups = 0;
+    use_unit(kNormUnit, dtype);
     s = with_x(dtype, [&](auto t) { return norm::launch_norm<decltype(t)>(true, a, mode, &groups, st); });
     return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, groups, dw_post, dw_pre, st);
 }
@@ -725,16 +737,31 @@ lattice_status lattice_get_device_status(void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e);
-    // every translation unit's copy of the status word (each unit is a module of its own)
-    cudaError_t (*const units[])(unsigned int*) = {read_clear_module_status, status_simt_exact,
-                                                   status_simt_chunked, status_step, status_bwd, status_tc,
-                                                   status_norm_f32, status_norm_bf16,
-                                                   status_norm_f16, status_gated_fwd_f32, status_gated_fwd_bf16, status_gated_fwd_f16,
-                                                   status_gated_bwd_f32, status_gated_bwd_bf16, status_gated_bwd_f16};
+    // every translation unit's copy of the status word (each unit is a module of its own), the layer
+    // operators' where they have been used (their one-token form has no waits)
+    const struct {
+        cudaError_t (*read)(unsigned int*);
+        bool used;
+    } units[] = {{read_clear_module_status, true},
+                 {status_simt_exact, true},
+                 {status_simt_chunked, true},
+                 {status_step, true},
+                 {status_bwd, true},
+                 {status_tc, true},
+                 {status_norm_f32, unit_used(kNormUnit, LATTICE_F32)},
+                 {status_norm_bf16, unit_used(kNormUnit, LATTICE_BF16)},
+                 {status_norm_f16, unit_used(kNormUnit, LATTICE_F16)},
+                 {status_gated_fwd_f32, unit_used(kGatedFwdUnit, LATTICE_F32)},
+                 {status_gated_fwd_bf16, unit_used(kGatedFwdUnit, LATTICE_BF16)},
+                 {status_gated_fwd_f16, unit_used(kGatedFwdUnit, LATTICE_F16)},
+                 {status_gated_bwd_f32, unit_used(kGatedBwdUnit, LATTICE_F32)},
+                 {status_gated_bwd_bf16, unit_used(kGatedBwdUnit, LATTICE_BF16)},
+                 {status_gated_bwd_f16, unit_used(kGatedBwdUnit, LATTICE_F16)}};
     unsigned int any = 0;
-    for (auto unit : units) {
+    for (const auto& unit : units) {
+        if (!unit.used) continue;
         unsigned int v = 0;
-        e = unit(&v);
+        e = unit.read(&v);
         if (e != cudaSuccess) return cuda_fail(e);
         any |= v;
     }

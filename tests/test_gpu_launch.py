@@ -184,3 +184,40 @@ def test_state_recurrence_calls_of_two_host_threads(L, B, H, ms, chunk, mode):
     for ins, kw, (y, S) in sets:
         again, state = L.scan_fwd(*ins, **kw)
         assert torch.equal(again, y) and torch.equal(state, S)
+
+
+def status_times():
+    """Microseconds of a status check before any layer operator's call, and after calls of all
+    types and directions, in a process of its own."""
+    import orthogonal_update_recurrent_b200 as L
+
+    def each(n=200):
+        best = float("inf")
+        for _ in range(5):
+            start = time.perf_counter()
+            for _ in range(n):
+                L.device_status()
+            best = min(best, (time.perf_counter() - start) / n)
+        return best * 1e6
+    x = normal(1, 40, 1, 16)
+    torch.cuda.synchronize()
+    L.device_status()
+    before = each()
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        v = x.to(dtype)
+        marks = L.gated_scan_marks(v)
+        L.gated_scan_fwd(v, v, marks=marks)
+        L.gated_scan_bwd(v, v, v, marks)
+        L.block_norm_fwd(v)
+        L.block_norm_bwd(v, dr=v)
+    return before, each()
+
+
+def test_a_status_check_reads_what_can_have_failed(L):
+    """Units of the layer operators that nothing was launched of are not read: there are 6 other
+    units, and 9 of these, at about 12 us each."""
+    code = (f"import sys; sys.path[:0] = [{ROOT!r}, {os.path.join(ROOT, 'tests')!r}]\n"
+            "import test_gpu_launch as t\nprint(*t.status_times())")
+    out = subprocess.run([sys.executable, "-c", code], check=True, capture_output=True, text=True, timeout=300).stdout
+    before, after = map(float, out.split())
+    assert before < 0.7 * after, (before, after)
