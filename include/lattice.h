@@ -47,7 +47,7 @@
  *
  * Errors: arguments are checked on the host before anything is launched; a
  * failed check launches nothing and returns the code. LATTICE_ERR_CUDA means a
- * launch or attribute call failed (call cudaGetLastError for the detail).
+ * launch or attribute call failed (lattice_last_cuda_error has the detail).
  * Device-side waits are bounded: a kernel that gives up sets the status word
  * and returns; lattice_get_device_status() reports it as LATTICE_ERR_TIMEOUT.
  *

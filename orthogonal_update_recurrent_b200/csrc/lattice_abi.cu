@@ -51,6 +51,7 @@ int sm_count() {
 }
 
 lattice_status cuda_fail(cudaError_t e) {
+    cudaGetLastError();  // reported here, and not again by the next call's launch_status
     snprintf(g_last_error, sizeof(g_last_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
     return LATTICE_ERR_CUDA;
 }

@@ -221,3 +221,32 @@ def test_a_status_check_reads_what_can_have_failed(L):
     out = subprocess.run([sys.executable, "-c", code], check=True, capture_output=True, text=True, timeout=300).stdout
     before, after = map(float, out.split())
     assert before < 0.7 * after, (before, after)
+
+
+def calls_after_a_failed_one():
+    """A status check inside a capture is refused by CUDA. What the next calls return."""
+    import orthogonal_update_recurrent_b200 as L
+    h, x = torch.zeros(2, 2, 64, device="cuda"), torch.ones(2, 2, 64, device="cuda")
+    S = torch.ones(2, 2, 16, 64, device="cuda")
+    q = torch.ones(2, 2, 16, device="cuda")
+    out = [L.gated_step(h, x, x), L.readout(S, q)]
+    torch.cuda.synchronize()
+    for f in (lambda: L.gated_step(h.zero_(), x, x), lambda: L.readout(S, q)):
+        code = 0
+        try:
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                try:
+                    L.device_status()
+                except L.LatticeError as e:
+                    code = e.code
+        except RuntimeError:  # the capture was given up
+            pass
+        assert code == L.ERR_CUDA
+        assert torch.equal(f(), out.pop(0))
+
+
+def test_an_error_is_reported_once(L):
+    code = (f"import sys; sys.path[:0] = [{ROOT!r}, {os.path.join(ROOT, 'tests')!r}]\n"
+            "import test_gpu_launch as t\nt.calls_after_a_failed_one()")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
