@@ -187,3 +187,20 @@ def test_refusals_of_the_binding(L):
         L.block_norm_bwd(r, w_pre=torch.ones(64, device="cuda"), dr=r)
     with pytest.raises(L.LatticeError):
         L.block_norm_fwd(torch.zeros(1, 16385, device="cuda"))
+
+
+def test_sizes_past_a_c_int_are_refused(L):
+    """They would reach the library as their lower 32 bits: 3 tokens, 64 columns."""
+    x = torch.zeros(1, 1, 1, 1, device="cuda").bfloat16()
+    many = x.expand(1, (1 << 32) + 3, 1, 1)
+    with pytest.raises(L.LatticeError) as e:
+        L.gated_scan_fwd(many, many)
+    assert e.value.code == L.ERR_UNSUPPORTED
+    with pytest.raises(L.LatticeError) as e:
+        L.gated_scan_bwd(many, many, many, torch.zeros(1, 1, 1, 1, device="cuda"))
+    assert e.value.code == L.ERR_UNSUPPORTED
+    wide = torch.empty(1, (1 << 32) + 64, dtype=torch.bfloat16, device="cuda")
+    for f in (lambda: L.block_norm_fwd(wide), lambda: L.block_norm_bwd(wide, dr=wide)):
+        with pytest.raises(L.LatticeError) as e:
+            f()
+        assert e.value.code == L.ERR_UNSUPPORTED
