@@ -204,3 +204,37 @@ def test_sizes_past_a_c_int_are_refused(L):
         with pytest.raises(L.LatticeError) as e:
             f()
         assert e.value.code == L.ERR_UNSUPPORTED
+
+
+def test_the_documented_calls(L):
+    """The example of the project's front page, as it stands there, on a batch of three: its calls run,
+    and the token that it decodes goes on from the sequence's state."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        example, = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    b, t, heads, width, slots = 3, 130, 2, 64, 64
+    names = {"x": n(b, t, heads, width).bfloat16(), "c": torch.sigmoid(n(b, t, heads, slots)),
+             "q": n(b, t, heads, slots).bfloat16(), "mu": torch.sigmoid(n(b, t, heads)),
+             "S0": torch.nn.functional.normalize(n(b, heads, slots, width), dim=-1), "dS_T": n(b, heads, slots, width),
+             "x_t": n(b, heads, width).bfloat16(), "c_t": torch.sigmoid(n(b, heads, slots)),
+             "q_t": n(b, heads, slots).bfloat16(), "mu_t": torch.sigmoid(n(b, heads)),
+             "z": (n(b, t, heads, width) + 2).bfloat16(), "h0": n(b, heads, width), "dh": n(b, heads, width),
+             "z_t": (n(b, heads, width) + 2).bfloat16(), "w_head": n(width), "gate": n(b, t, heads, width).bfloat16(),
+             "p": n(b, t, heads * width).bfloat16(), "w_post": n(heads * width), "w_pre": n(heads * width),
+             "r0": n(b, t, heads * width), "dr": n(b, t, heads * width), "dn": n(b, t, heads * width).bfloat16()}
+    names["dy"] = n(b, t, heads, width)
+    for line in example.splitlines():
+        if line.startswith("g = lattice.gated_scan_bwd"):  # here dy has x's type
+            names["dy"] = names["dy"].bfloat16()
+        exec(line, names)
+    both = torch.cat([names["x"], names["x_t"].unsqueeze(1)], 1), torch.cat([names["z"], names["z_t"].unsqueeze(1)], 1)
+    ref = gated_ref.scan(*both, names["h0"], "logit", "unit", 0.125)
+    gated_ref.check(names["h"], ref, "h_T")
+    gated_ref.check(names["y_t"].unsqueeze(1), {"y": ref["y"][:, -1:], "b_y": ref["b_y"][:, -1:]}, "y")
+    assert set(names["g"]) == {"dy", "dgate", "dresidual", "dw_post", "dw_pre"}
+    L.device_status()
