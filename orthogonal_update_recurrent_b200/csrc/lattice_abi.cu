@@ -157,7 +157,9 @@ lattice_status check_gated(lattice_dtype x_dtype, lattice_dtype z_dtype, int z_p
 }
 
 // The polynomial in t that meets (1 - (1 + t)^-tau)/t at the Chebyshev nodes of [0, 1], for
-// tau <= 1, where its error is at most 5e-8 of its value; larger tau are halved first.
+// tau <= 1; larger tau are halved first. It is off by at most 5e-8 of its value (tau = 1). With
+// its coefficients rounded to fp32, of which they are up to 14 times the value together, and summed
+// in fp32, 1 - a is off by up to 4e-7 of itself (1.2e-7 to 4e-7 over tau from 0.001 to 1).
 void gated_poly(GatedArgs& a) {
     constexpr int n = kGatedPoly;
     double tau = a.tau;

@@ -1,6 +1,7 @@
 """The gated linear recurrence on the GPU against the token-by-token 64-bit form, at the
 sizes where tiles, runs, clusters, vectors and lengths end."""
 import itertools
+import math
 
 import pytest
 
@@ -242,6 +243,32 @@ def test_extreme_gates(L):
     t["z"][0, 10], t["z"][0, 20], t["z"][0, 30] = 0.0, 1.0, -1.0
     for write in ("plain", "leaky", "unit"):
         both(L, t, "value", write)
+
+
+@pytest.mark.parametrize("tau", [0.001, 0.0625, 0.125, 0.3, 0.5, 0.75, 0.999, 1.0, 1.5, 2.5, 10.0])
+def test_gates_alone(L, tau):
+    """a, 1 - a and sqrt(1 - a^2) as one step from h = 1, x = 0, or from h = 0, x = 1, gives them.
+    With e = 2^-24: exp(-|z|) is off by 2 + 1.5 |z| (its argument's rounding); the polynomial's
+    coefficients and its sum by 14 each, with alternating terms of up to 14 times the value; each
+    halving of tau is a squaring, which leaves 1 - a's relative error as it is and adds 2, and
+    doubles a's. z < 0 has the factor exp(tau z): 2 + 1.5 tau |z|, its 1 - exp() within 12. In all
+    1 - a is off by 45 + 2 s + 3 (1 + tau) |z| of itself, a by that of 1 - a and one rounding where a > 1/2,
+    else by 2^s times that of itself. tau = 1 has no polynomial: a = r (2 - (1 + t) r) rounds 1 + t, the
+    bracket and the product, 3 in place of that one rounding (r's own error enters squared)."""
+    z = torch.cat([torch.linspace(-30, 30, 4001), torch.tensor([0.0, -0.0, 1e-20, -1e-20, 87.0, 100.0, -100.0, -1000.0, 1000.0]),
+                   torch.logspace(-9, 1.5, 2000), -torch.logspace(-9, 1.5, 2000)]).cuda().view(1, 1, -1)
+    one, zero = torch.ones_like(z), torch.zeros_like(z)
+    out = [torch.empty_like(z) for _ in range(3)]
+    for (h, x, write), o in zip(((one, zero, "plain"), (zero, one, "leaky"), (zero, one, "unit")), out):
+        L.gated_step(h, x, z, gate="logit", write=write, tau=tau, h_out=o)
+    w = tau * torch.nn.functional.logsigmoid(z.double())
+    a, q = w.exp(), -torch.expm1(w)
+    s = max(0, math.ceil(math.log2(tau)))
+    off = (45 + 2 * s + 3 * (1 + tau) * z.double().abs()) * R.E
+    assert ((out[1].double() - q).abs() <= off * q + 1e-37).all()
+    assert ((out[0].double() - a).abs() <= torch.where(q < 0.5, off * q + (3 if tau == 1 else 1) * R.E * a, 2 ** s * off * a) + 1e-37).all()
+    unit = (q * (1 + a)).sqrt()  # half the relative error of each factor, a root of 2 e and two products
+    assert ((out[2].double() - unit).abs() <= (2 ** s * off + 4 * R.E) * unit + 1e-18).all()
 
 
 def test_not_a_number_stays_in_its_channel_and_after_its_token(L):
