@@ -79,6 +79,22 @@ def test_head_gates(L, d, dtype, zdtype):
     both(L, make(2, 131, 5, d, dtype=dtype, zdtype=zdtype, head=True, seed=d), write="unit")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("H,d", [(2, 16), (4, 16), (10, 16), (2, 32), (6, 32), (2, 64), (4, 64), (12, 64), (2, 128), (16, 128)])
+def test_head_gates_in_16_bits(L, H, d, dtype):
+    """An even number of heads: a token's gates are whole words, which are copied as such. Gates
+    that start on an odd element, or rows an odd number of elements apart, are copied one by one."""
+    both(L, make(2, 131, H, d, dtype=dtype, head=True, seed=H + d), write="unit")
+    t = make(3, 77, H, d, dtype=dtype, head=True, seed=H, lengths=[77, 0, 34])
+    want = both(L, t, tau=0.25)
+    for pad, first in ((0, 1), (1, 0), (2, 1), (4, 2), (6, 0)):  # wider rows, in words or not
+        wide = torch.full((3, 77, H + pad + first), float("nan"), dtype=DT[dtype], device="cuda")
+        moved = dict(t, z=wide[:, :, first:first + H])
+        moved["z"].copy_(t["z"])
+        got = both(L, moved, tau=0.25)
+        assert all(torch.equal(got[k], want[k]) for k in want), (pad, first)
+
+
 @pytest.mark.parametrize("lengths", [[0, 0, 0], [0, 1, 200], [64, 63, 65], [200, 128, 7], [-3, 199, 9999]], ids=str)
 @pytest.mark.parametrize("head", [False, True])
 def test_padded_batches(L, lengths, head):

@@ -245,6 +245,29 @@ def test_the_same_call_gives_the_same_bits(L):
         assert all(torch.equal(one[k], two[k]) for k in one)
 
 
+@pytest.mark.parametrize("N,D", [(1, 1), (300, 64), (3000, 100), (90, 2056), (40, 8187), (75, 16384)])
+def test_a_callers_workspace(L, N, D):
+    """Of the stated size, whatever it holds: the same bits as with the library's own. Nothing
+    behind it is written, and a smaller one is refused."""
+    t = make((N, D), "bf16", "f32", "f32", seed=N)
+    kw = dict(gate=t["gate"], residual=t["residual"], w_pre=t["w_pre"], dr=t["dr"], dn=t["dn"])
+    want = L.block_norm_bwd(t["y"], t["w_post"], **kw)
+    need = L.lib().lattice_block_norm_bwd_workspace_bytes(N, D)
+    room = torch.full((need // 4 + 4,), float("nan"), device="cuda")
+    room[need // 4:] = 7.0
+    for _ in range(2):
+        got = L.block_norm_bwd(t["y"], t["w_post"], workspace=room[:need // 4], **kw)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        assert (room[need // 4:] == 7).all()
+    with pytest.raises(L.LatticeError) as e:
+        L.block_norm_bwd(t["y"], t["w_post"], workspace=room[:need // 4 - 1], **kw)
+    assert e.value.code == L.ERR_INVALID_ARG
+    with pytest.raises(L.LatticeError):  # over an input
+        L.block_norm_bwd(t["y"], t["w_post"], workspace=t["residual"] if t["residual"].numel() * 4 >= need else t["w_post"], **kw)
+    small = L.block_norm_bwd(t["y"], gate=t["gate"], residual=t["residual"], dr=t["dr"])  # no weights: none is needed
+    assert small["dw_post"] is None and small["dw_pre"] is None
+
+
 def test_streams_and_graphs(L):
     t = make((300, 1024), "bf16", seed=15)
     kw = dict(gate=t["gate"], residual=t["residual"], w_pre=t["w_pre"])
