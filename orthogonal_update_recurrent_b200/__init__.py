@@ -367,9 +367,12 @@ _F32_ONLY = (torch.float32,)
 _XZ = {t: (t, torch.float32) for t in (torch.float32, torch.bfloat16, torch.float16)}
 
 
+_INT_MAX = 0x7fffffff
+
+
 def _fits(what: str, *sizes):
     """Refuses sizes that are no C int: ctypes would cut them off."""
-    if max(sizes) > 0x7fffffff:
+    if max(sizes) > _INT_MAX:
         raise LatticeError(ERR_UNSUPPORTED, what)
 
 
@@ -377,7 +380,8 @@ def _gated_args(x, z, lead: int, lengths, gate: str, write: str):
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 2:
         raise ValueError("x must be a tensor [B, T, H, d] (one token: [B, H, d])")
     shape, device = x.shape, x.device
-    _fits("the gated recurrence's sizes", *shape)
+    if x.numel() > _INT_MAX:
+        _fits("the gated recurrence's sizes", *shape)
     xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
     per_head = isinstance(z, torch.Tensor) and z.dim() == lead + 1
     zs = _rows(z, "z", shape[:-1] if per_head else shape, lead, _XZ[x.dtype], device)
@@ -532,7 +536,8 @@ def _norm_args(y, w_post, gate, residual, w_pre, act, dtype):
     if not isinstance(y, torch.Tensor) or not y.is_cuda or y.dim() < 1:
         raise TypeError("y must be a CUDA tensor [..., D]")
     shape, dev = y.shape, y.device
-    _fits("the norm's sizes", *shape[-2:])
+    if y.numel() > _INT_MAX:
+        _fits("the norm's sizes", *shape[-2:])
     if dtype is None:
         dtype = gate.dtype if isinstance(gate, torch.Tensor) else y.dtype
     both = _XZ.get(dtype)
