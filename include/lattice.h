@@ -40,10 +40,14 @@
  * Decode calls drop the T axis.
  *
  * Ownership and execution: every pointer is caller-owned DEVICE memory. The
- * library allocates nothing and keeps no state besides one device status
- * word (and the static scratch array of lattice_scan_bwd_noalloc, described
- * there). Every call is asynchronous on `stream` (a cudaStream_t passed as
- * void*, NULL = the legacy default stream) and returns after the launch.
+ * library allocates nothing and keeps no state that a result depends on besides
+ * the device status word (and the static scratch array of
+ * lattice_scan_bwd_noalloc, described there). On the host it keeps how many CTAs
+ * of a kernel a device holds at once, and which units' status words can be set;
+ * a kernel's limit of shared memory is set to the most that its launches take.
+ * Every call is asynchronous on `stream` (a cudaStream_t passed as void*,
+ * NULL = the legacy default stream) and returns after the launch. Several host
+ * threads may call at once, on buffers that no two calls in flight write.
  *
  * Errors: arguments are checked on the host before anything is launched; a
  * failed check launches nothing and returns the code. LATTICE_ERR_CUDA means a
@@ -284,8 +288,9 @@ lattice_status lattice_readout(const float *S, const void *q, lattice_dtype q_dt
  * {16, 32, 64, 128}); h0, h_out [B][H][d] fp32, row-major; y [B][T][H][d] in x's type. x,
  * z and dy may be slices of wider rows: their batch and token strides are given in
  * elements (>= 0), a token's own H*d (or H) elements are contiguous; the bytes between
- * rows must be readable, whatever they hold. Every output is contiguous. x: fp32, bf16 or fp16; z: fp32 or x's type. Arithmetic and state are fp32
- * whatever the types; y and the gradients are rounded once.
+ * rows must be readable, whatever they hold. Every output is contiguous. x: fp32, bf16 or
+ * fp16; z: fp32 or x's type. Arithmetic and state are fp32 whatever the types; y and the
+ * gradients are rounded once.
  * Sizes: B, H, d >= 1, T >= 0; H*d and T up to 2^30.
  * lengths (int32 [B], device, or NULL for T each) gives every sequence its own length,
  * taken into 0..T. Tokens behind it are not read: their y and gradients are written as

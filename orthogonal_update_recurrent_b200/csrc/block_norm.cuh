@@ -15,8 +15,8 @@
 // HBM bounds both: every input is read once and every output written once, a row's values
 // stay in registers between its sums, and what is left is to keep enough bytes in flight.
 // A thread has 8 elements of a row. A row of up to 256 elements takes a part of a warp and
-// its sums are shuffles, one of up to 8192 (backward, with twice the registers: 4096) a
-// CTA, a longer one a cluster of 2 or 4 CTAs.
+// its sums are shuffles, one of up to 8192 (read one by one: 6144; backward, with twice the
+// registers: 4096) a CTA, a longer one a cluster of 2 or 4 CTAs.
 // CTAs stay and take rows by turns: each loads its next row before it works on the one it
 // has, and its threads keep their columns' weights, and the sums of the weights' gradients,
 // in shared memory.

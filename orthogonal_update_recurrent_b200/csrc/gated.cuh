@@ -104,7 +104,8 @@ __device__ __forceinline__ F2 expm1_small(F2 w) {
 // be: with t = exp(-z), r = 1/(1 + t) gets one Newton step, a = r (2 - (1 + t) r), and 1 - a is
 // t a, which keeps its relative accuracy however near 1 a is. exp(-z) stops at 2^126. With
 // tau, `fast` says that the warp's gates of the token have no z < 0 and tau <= 1, which leaves out what those need
-// (long context 264 us, 317 us without `fast`; by log(1 + t) and exp, for every z, 307 us).
+// (65536 tokens of 2048 channels, tau 1/8, unit write: 264 us, 317 us without `fast`; by log(1 + t)
+// and exp, for every z, 307 us).
 template <int GATE>
 __device__ __forceinline__ void gates_of(F2 z, const GatedArgs& A, bool fast, F2& a, F2& q) {
     if constexpr (GATE == kValue) {
@@ -175,8 +176,8 @@ __device__ __forceinline__ void cluster_sync_all() {
 // The exchange of a cluster's pairs: every CTA sends its own to all K, into one of two
 // buffers by turns, as asynchronous stores that count their bytes on the receiver's
 // mbarrier, so that neither side fences its other memory traffic (a cluster barrier's
-// release waited for the rows' stores: the long context took 203 us with one,
-// 185 us so). A buffer is sent to again only after its sender has everyone's pairs of the
+// release waited for the rows' stores: 65536 tokens of 2048 channels, tau 1, took 203 us with
+// one, 185 us so). A buffer is sent to again only after its sender has everyone's pairs of the
 // iteration between, and a CTA sends those after its warps have read the buffer.
 struct Exchange {
     uint32_t bars;  // two mbarriers
@@ -236,7 +237,9 @@ struct RowOf {
 // last one as far as the row goes. 8 sequences of 4096 tokens, forward and backward: 2047
 // channels in bf16 331 and 498 us with elements loaded one by one, 140 and 332 us with shifted
 // pieces; 2046 channels in bf16 102 and 190 us by lanes, 111 and 212 us with shifted
-// pieces, in fp32 220 and 375 us by lanes, 160 and 296 us with shifted pieces.
+// pieces, in fp32 220 and 375 us by lanes, 160 and 296 us with shifted pieces. Where few
+// channels leave the device idle it can be the other way: 37 channels in bf16, one sequence of
+// 32768 tokens, backward, 156 us one by one, 201 us with shifted pieces.
 template <int ROWS, class T, int V, int R>
 struct Stager {
     static constexpr int ROW = 32 * V, PER = 16 / sizeof(T), CH = ROW / PER, STEP = 32 / CH;  // chunks per row

@@ -16,7 +16,8 @@ namespace gated {
 // shape, 32 tiles of channels, 8 CTAs 11.8 us against 26.9 us on one; 50 tiles of 8192
 // tokens, 5 CTAs 43 us, 4 50 us, 6 (not all resident) 58 us; mid-size layer, 256 tiles,
 // 78 us on one CTA against 86 us on two (74 us since). More than 8 CTAs, where the device allows them, serve few
-// channels over long sequences: 256 channels of 20000 tokens, 16 CTAs 49 us, 8 86 us.
+// channels over long sequences: 256 channels of 20000 tokens, tau 1/16 and unit write, 16 CTAs
+// 49 us, 8 86 us (16 41 us since).
 constexpr int kMaxDevices = 16;
 constexpr int kMaxShared = 227 * 1024;  // bytes of shared memory a CTA may have
 
