@@ -1,4 +1,6 @@
 // tu_step.cu -- launches of the decode step and read-out kernels (step.cuh).
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "step.cuh"
@@ -23,18 +25,17 @@ template <int D, int RQ, bool DEC>
 lattice_status launch_step_pf(const StepArgs& a, int nw, int nheads, cudaStream_t st) {
     const StepPfLayout L(a.m, D, a.x_bf16);
     auto k = step_pf_kernel<D, RQ, DEC>;
-    static int cache[kStepMaxDevices][2][kMaxM + 1];  // CTAs resident on the device; 0 = unknown
+    static std::atomic<int> cache[kStepMaxDevices][2][kMaxM + 1];  // CTAs resident on the device; 0 = unknown
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    int* slot = dev < kStepMaxDevices ? &cache[dev][a.x_bf16 ? 1 : 0][a.m] : nullptr;
-    int resident = slot ? *slot : 0;
+    std::atomic<int>* slot = dev < kStepMaxDevices ? &cache[dev][a.x_bf16 ? 1 : 0][a.m] : nullptr;
+    int resident = slot ? slot->load() : 0;
     if (resident == 0) {
         // the largest buffer this instantiation can take (every m it serves, fp32 x), so
         // that a later launch with a larger m never meets a smaller limit
         const int m_max = 64 * RQ < kMaxM ? 64 * RQ : kMaxM;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)StepPfLayout(m_max, D, false).bytes);
+        e = allow_shared(k, StepPfLayout(m_max, D, false).bytes);
         if (e != cudaSuccess) return cuda_fail(e);
         int per_sm = 0, sms = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, nw * 32, L.bytes);
@@ -43,7 +44,7 @@ lattice_status launch_step_pf(const StepArgs& a, int nw, int nheads, cudaStream_
         if (e != cudaSuccess) return cuda_fail(e);
         if (per_sm < 1) return LATTICE_ERR_UNSUPPORTED;
         resident = per_sm * sms;
-        if (slot) *slot = resident;
+        if (slot) slot->store(resident);
     }
     k<<<dim3(nheads < resident ? nheads : resident), dim3(nw * 32), L.bytes, st>>>(a);
     return launch_status();

@@ -1,6 +1,8 @@
 // tu_tc.cu -- launches of the tensor-core chunked scans: one CTA per sequence
 // (chunk_tc.cuh), the cluster kernel (chunk_split.cuh) and the register-chain cluster
 // kernel (chunk_reg.cuh).
+#include <atomic>
+
 #include "chunk_reg.cuh"
 #include "launch.h"
 
@@ -31,16 +33,18 @@ lattice_status launch_tc(lattice_impl impl, const ScanArgs& a, int d, cudaStream
 // Clusters of 4 CTAs of the register-chain kernel the current device holds at once
 // (queried once per device; without a device, the SMs / 4 of a 148-SM B200).
 int reg_cluster_capacity(int d) {
-    static int cache[64][2] = {};
+    static std::atomic<int> cache[64][2];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return sm_count() / 4;
     }
-    int& c = cache[dev][d == 128 ? 1 : 0];
+    std::atomic<int>& known = cache[dev][d == 128 ? 1 : 0];
+    int c = known.load();
     if (c == 0) {
         c = chunk_reg_max_clusters(d, 16);
         if (c <= 0) c = -1;
+        known.store(c);
     }
     return c > 0 ? c : sm_count() / 4;
 }

@@ -250,3 +250,16 @@ def test_an_error_is_reported_once(L):
             "import test_gpu_launch as t\nt.calls_after_a_failed_one()")
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("mode", ["sim", "dec"])
+def test_decode_calls_of_two_host_threads(L, mode):
+    """Slot counts of one kernel, as many heads as make the decode step persistent."""
+    sets = []
+    for m in (8, 16, 32):
+        S, x, c, q, mu = (normal(200, 1, m, 64), normal(200, 1, 64), torch.sigmoid(normal(200, 1, m)), normal(200, 1, m),
+                          torch.sigmoid(normal(200, 1)))
+        sets.append((torch.nn.functional.normalize(S, dim=-1), x, c, q, mu))
+    assert at_once(L, [lambda s=s: L.step(*s, mode=mode) for s in sets], 1.0) == [0, 0, 0]
+    for S, x, c, q, mu in sets:
+        assert torch.isfinite(S).all()
