@@ -76,7 +76,8 @@ typedef enum {
     LATTICE_ERR_TIMEOUT = 4      /* a bounded device-side wait gave up        */
 } lattice_status;
 
-/* F16 is accepted by the gated recurrence and the block norms only. */
+/* F16 is accepted by the layer operators only: the gated recurrence, the norms, the short
+ * convolution and the selective scan. */
 typedef enum { LATTICE_F32 = 0, LATTICE_BF16 = 1, LATTICE_F16 = 2 } lattice_dtype;
 
 /* Objective (§3.1.1, eq. OSR): what each token writes into the slots.
@@ -392,6 +393,157 @@ lattice_status lattice_block_norm_bwd(const void *y, lattice_dtype y_dtype, long
                                       void *workspace, size_t workspace_bytes, lattice_dtype dtype,
                                       long long N, int G, int D, lattice_act act, int post_norm,
                                       float scale, float eps, void *stream);
+
+/* ---- Short causal convolution
+ *
+ * The convolution of few taps that stands before a recurrence (the paper's block has one on keys and
+ * queries, Appendix C), every channel by itself, over the tokens of a sequence:
+ *     v_t = bias + sum_k w[k] x_{t-K+1+k},  y_t = act(v_t),  k = 0..K-1.
+ * The K-1 inputs before the first token are the state's rows, oldest first, or 0 without one.
+ *
+ * Layouts: x [B][T][C], w [C][K], bias [C] (or NULL: 0), state [B][K-1][C], row-major; y in x's type
+ * and layout. x and dy may be slices of wider rows: batch and token strides in elements (>= 0), a
+ * token's C elements contiguous. Outputs are contiguous. x: fp32, bf16 or fp16; w and bias, one type
+ * for both, fp32 or x's; the state has x's type. Arithmetic is fp32, results are rounded once.
+ * Sizes: B, C >= 1, T >= 0, 1 <= K <= 8; C and T up to 2^30. act: NONE or SILU.
+ * lengths (int32 [B], device, or NULL for T each), taken into 0..T: tokens behind a sequence's
+ * length are not read, their y and gradients are written as zero, and the state left is that at the
+ * sequence's own end. Sums have a fixed order for given sizes and device. */
+
+/* Whole sequences. state_out (or NULL): the last K-1 inputs before each sequence's end, for the next
+ * call; it may be the state itself. Other outputs must not overlap inputs or each other. */
+lattice_status lattice_short_conv_fwd(const void *x, lattice_dtype x_dtype, long long x_batch_stride,
+                                      long long x_token_stride, const void *w, const void *bias,
+                                      lattice_dtype w_dtype, const void *state, void *state_out, void *y,
+                                      const int *lengths, int B, int T, int C, int K, lattice_act act,
+                                      void *stream);
+
+/* Bytes of workspace of lattice_short_conv_bwd on the current device (0 for sizes it rejects). Host
+ * function. */
+size_t lattice_short_conv_bwd_workspace_bytes(int B, int T, int C, int K);
+
+/* Backward pass for L = sum dy . y + sum dstate_out . state_out, from the forward call's inputs; dy
+ * in x's type, dstate_out [B][K-1][C] in x's type or NULL (0). Writes dx and dstate (x's type; dstate
+ * only with a state, or NULL), dw [C][K] and dbias [C] (fp32, each NULL where it is not wanted).
+ * workspace: lattice_short_conv_bwd_workspace_bytes, 16-byte aligned, needed for dw or dbias. */
+lattice_status lattice_short_conv_bwd(const void *x, lattice_dtype x_dtype, long long x_batch_stride,
+                                      long long x_token_stride, const void *w, const void *bias,
+                                      lattice_dtype w_dtype, const void *state, const void *dy,
+                                      long long dy_batch_stride, long long dy_token_stride,
+                                      const void *dstate_out, void *dx, float *dw, float *dbias,
+                                      void *dstate, void *workspace, size_t workspace_bytes,
+                                      const int *lengths, int B, int T, int C, int K, lattice_act act,
+                                      void *stream);
+
+/* One token: y from the state and x [B][C]; state_out is the state without its oldest row and with x
+ * as its last (state_out == state: in place). */
+lattice_status lattice_short_conv_step(const void *state, void *state_out, const void *x,
+                                       lattice_dtype x_dtype, long long x_batch_stride, const void *w,
+                                       const void *bias, lattice_dtype w_dtype, void *y, int B, int C,
+                                       int K, lattice_act act, void *stream);
+
+/* ---- Selective state space scan
+ *
+ * The gated linear recurrence with N states per channel, whose decay, write and read are chosen by
+ * the token. Per (batch, channel e, state n), for t = 1..len_b, with
+ * dt_t = softplus(dt_raw + dt_bias[e]) (or dt_raw + dt_bias[e] with softplus 0):
+ *     h_t[n] = exp(dt_t A[e][n]) h_{t-1}[n] + dt_t x_t b_t[n]
+ *     y_t = (sum_n c_t[n] h_t[n] + skip[e] x_t) silu(z_t)          (no last factor without z)
+ * b and c belong to a group of E/G neighbouring channels. dt_t A <= 0 is expected: growing states
+ * may overflow, also where the whole sequence's would not.
+ *
+ * Layouts: x, z, dt [B][T][E]; b, c [B][T][G][N]; A [E][N], skip, dt_bias [E], h0, h_out [B][E][N]
+ * fp32, row-major. x, z, dt, b, c and dy may be slices of wider rows: batch and token strides in
+ * elements (>= 0), a token's own E (or G*N) elements contiguous. x, z, b, c, y and dy have one type
+ * (fp32, bf16 or fp16), dt it or fp32. Arithmetic and states are fp32 whatever the types; y and the
+ * gradients are rounded once. Outputs are contiguous.
+ * Sizes: B, E, N, G >= 1, E a multiple of G, N <= 128, T >= 0; E and T up to 2^30.
+ * lengths: as for the gated recurrence: tokens behind a sequence's length are not read, their y and
+ * gradients are zero, and h_out is the state at the sequence's own end.
+ * workspace: lattice_selective_scan_workspace_bytes on the current device (which may be 0), 16-byte
+ * aligned. Results do not depend on the run: every sum has a fixed order for given sizes and device. */
+
+/* Whole sequences. h0 NULL: 0; h_out NULL or h0 (in place); z, skip, dt_bias, lengths may be NULL; y
+ * may be NULL when marks is given. marks (or NULL): device memory of
+ * lattice_selective_scan_marks_bytes, 16-byte aligned, for the backward pass: filled with the state
+ * before every 8th token up to each sequence's end. */
+lattice_status lattice_selective_scan_fwd(const void *x, lattice_dtype x_dtype, long long x_batch_stride,
+                                          long long x_token_stride, const void *dt, lattice_dtype dt_dtype,
+                                          long long dt_batch_stride, long long dt_token_stride,
+                                          const float *A, const void *b, long long b_batch_stride,
+                                          long long b_token_stride, const void *c, long long c_batch_stride,
+                                          long long c_token_stride, const float *skip, const void *z,
+                                          long long z_batch_stride, long long z_token_stride,
+                                          const float *dt_bias, int softplus, const float *h0, float *h_out,
+                                          void *y, float *marks, const int *lengths, void *workspace,
+                                          size_t workspace_bytes, int B, int T, int E, int N, int G,
+                                          void *stream);
+
+/* Bytes of marks, and of workspace for one direction, for these sizes (0 also for sizes the scan
+ * rejects). Host functions. */
+size_t lattice_selective_scan_marks_bytes(int B, int T, int E, int N);
+size_t lattice_selective_scan_workspace_bytes(int B, int T, int E, int N, int G, int backward);
+
+/* Backward pass for L = sum_t dy_t . y_t + dh_T . h_len. The inputs are those of the forward call
+ * that filled marks (which carries h0); dh_T [B][E][N] fp32 or NULL (0). Writes dx, dz (z only), db,
+ * dc (x's type), ddt (dt's type: the gradient of dt_raw), dA [E][N], dskip, ddt_bias [E] (each of
+ * these two NULL where it is not wanted) and dh0 [B][E][N] (fp32), all contiguous and in full. */
+lattice_status lattice_selective_scan_bwd(const void *x, lattice_dtype x_dtype, long long x_batch_stride,
+                                          long long x_token_stride, const void *dt, lattice_dtype dt_dtype,
+                                          long long dt_batch_stride, long long dt_token_stride,
+                                          const float *A, const void *b, long long b_batch_stride,
+                                          long long b_token_stride, const void *c, long long c_batch_stride,
+                                          long long c_token_stride, const float *skip, const void *z,
+                                          long long z_batch_stride, long long z_token_stride,
+                                          const float *dt_bias, int softplus, const void *dy,
+                                          long long dy_batch_stride, long long dy_token_stride,
+                                          const float *marks, const float *dh_T, void *dx, void *ddt,
+                                          float *dA, void *db, void *dc, float *dskip, void *dz,
+                                          float *ddt_bias, float *dh0, const int *lengths, void *workspace,
+                                          size_t workspace_bytes, int B, int T, int E, int N, int G,
+                                          void *stream);
+
+/* One token: h_out from h (h_out == h: in place) and y [B][E]; x, z, dt [B][E], b, c [B][G][N], with
+ * batch strides as above. */
+lattice_status lattice_selective_step(const float *h, float *h_out, const void *x, lattice_dtype x_dtype,
+                                      long long x_batch_stride, const void *dt, lattice_dtype dt_dtype,
+                                      long long dt_batch_stride, const float *A, const void *b,
+                                      long long b_batch_stride, const void *c, long long c_batch_stride,
+                                      const float *skip, const void *z, long long z_batch_stride,
+                                      const float *dt_bias, int softplus, void *y, int B, int E, int N,
+                                      int G, void *stream);
+
+/* ---- Layer norm
+ *
+ * The norm before a block whose rows are also centred, with the residual that they are added to:
+ *     r = residual + x              (rounded to the residual's type; r = x without a residual)
+ *     n = (r - mean r) / sqrt(mean (r - mean r)^2 + eps) w + b
+ * n is formed from r as it is kept. w, b [D] or NULL (1, 0), one type for both. Types, rows, strides,
+ * sizes and eps are those of the block norms: `dtype` is n's; x, the residual and r (the residual's
+ * type) and the weights are of it or fp32. */
+
+/* r_out is given exactly with a residual, which it may be (same buffer, contiguous). */
+lattice_status lattice_layer_norm_fwd(const void *x, lattice_dtype x_dtype, long long x_stride,
+                                      const void *residual, lattice_dtype residual_dtype,
+                                      long long residual_stride, const void *w, const void *b,
+                                      lattice_dtype w_dtype, void *r_out, void *n_out, lattice_dtype dtype,
+                                      long long N, int G, int D, float eps, void *stream);
+
+/* Bytes of workspace of lattice_layer_norm_bwd on the current device (0 for sizes it rejects). Host
+ * function. */
+size_t lattice_layer_norm_bwd_workspace_bytes(long long N, int D);
+
+/* Backward pass from the normed rows r (the forward call's r_out, or x without a residual): dn is n's
+ * cotangent, dr that of r from elsewhere (r's type, or NULL: 0). Writes dr_out, the gradient of r and
+ * so of the residual and of x, in r's type; dx (or NULL), the same in x's type; and dw, db [D] fp32
+ * (each NULL where it is not wanted; dw only with w). workspace: lattice_layer_norm_bwd_workspace_bytes,
+ * 16-byte aligned, needed for dw or db. Sums over rows have a fixed order for given sizes and device. */
+lattice_status lattice_layer_norm_bwd(const void *r, lattice_dtype r_dtype, long long r_stride,
+                                      const void *dn, long long dn_stride, const void *dr,
+                                      long long dr_stride, const void *w, lattice_dtype w_dtype,
+                                      void *dr_out, void *dx, lattice_dtype x_dtype, float *dw, float *db,
+                                      void *workspace, size_t workspace_bytes, lattice_dtype dtype,
+                                      long long N, int G, int D, float eps, void *stream);
 
 /* Synchronises `stream`, returns LATTICE_ERR_TIMEOUT if any kernel since the
  * last call gave up a bounded wait (and clears the flag), LATTICE_ERR_CUDA if

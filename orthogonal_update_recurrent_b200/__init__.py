@@ -15,9 +15,11 @@ Tensors (row-major, contiguous, on one CUDA device):
 Decode calls drop the T axis.
 
 Beside the state recurrence: the gated linear recurrence (gated_scan_fwd,
-gated_scan_bwd, gated_step) and the norms after and before a block (block_norm_fwd,
-block_norm_bwd). These also take float16, and rows that are slices of wider ones (their
-last axes contiguous).
+gated_scan_bwd, gated_step), the norms after and before a block (block_norm_fwd,
+block_norm_bwd), the layer norm (layer_norm_fwd, layer_norm_bwd), the short causal convolution
+(short_conv_fwd, short_conv_bwd, short_conv_step) and the selective state space scan
+(selective_scan_fwd, selective_scan_bwd, selective_step). These also take float16, and rows
+that are slices of wider ones (their last axes contiguous).
 """
 from __future__ import annotations
 
@@ -30,7 +32,8 @@ import torch
 __all__ = ["LatticeError", "lib", "scan_fwd", "scan_bwd", "scan_bwd_workspace_bytes", "step",
            "readout", "chunk_impl", "device_status", "selftest_bounded_wait", "LIB_PATH",
            "gated_scan_fwd", "gated_scan_bwd", "gated_scan_marks", "gated_step", "block_norm_fwd",
-           "block_norm_bwd"]
+           "block_norm_bwd", "layer_norm_fwd", "layer_norm_bwd", "short_conv_fwd", "short_conv_bwd", "short_conv_step",
+           "selective_scan_fwd", "selective_scan_bwd", "selective_scan_marks", "selective_step"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblattice.so")
 
@@ -93,6 +96,25 @@ def lib() -> ctypes.CDLL:
                                              fp, vp, ctypes.c_size_t, i, ll, i, i, i, i, f32, f32, vp]
         L.lattice_block_norm_bwd_workspace_bytes.argtypes = [ll, i]
         L.lattice_block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        sz = ctypes.c_size_t
+        L.lattice_short_conv_fwd.argtypes = [vp, i, ll, ll, vp, vp, i, vp, vp, vp, vp, i, i, i, i, i, vp]
+        L.lattice_short_conv_bwd.argtypes = [vp, i, ll, ll, vp, vp, i, vp, vp, ll, ll, vp, vp, fp, fp, vp, vp, sz, vp,
+                                             i, i, i, i, i, vp]
+        L.lattice_short_conv_step.argtypes = [vp, vp, vp, i, ll, vp, vp, i, vp, i, i, i, i, vp]
+        scan = [vp, i, ll, ll, vp, i, ll, ll, fp, vp, ll, ll, vp, ll, ll, fp, vp, ll, ll, fp, i]
+        L.lattice_selective_scan_fwd.argtypes = scan + [fp, fp, vp, fp, vp, vp, sz, i, i, i, i, i, vp]
+        L.lattice_selective_scan_bwd.argtypes = scan + [vp, ll, ll, fp, fp, vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, vp, sz,
+                                                        i, i, i, i, i, vp]
+        L.lattice_selective_step.argtypes = [fp, fp, vp, i, ll, vp, i, ll, fp, vp, ll, vp, ll, fp, vp, ll, fp, i, vp,
+                                             i, i, i, i, vp]
+        L.lattice_layer_norm_fwd.argtypes = [vp, i, ll, vp, i, ll, vp, vp, i, vp, vp, i, ll, i, i, f32, vp]
+        L.lattice_layer_norm_bwd.argtypes = [vp, i, ll, vp, ll, vp, ll, vp, i, vp, vp, i, fp, fp, vp, sz, i, ll, i, i, f32, vp]
+        for f, a in (("lattice_short_conv_bwd_workspace_bytes", [i] * 4), ("lattice_selective_scan_marks_bytes", [i] * 4),
+                     ("lattice_selective_scan_workspace_bytes", [i] * 6), ("lattice_layer_norm_bwd_workspace_bytes", [ll, i])):
+            getattr(L, f).argtypes, getattr(L, f).restype = a, sz
+        for f in ("lattice_short_conv_fwd", "lattice_short_conv_bwd", "lattice_short_conv_step", "lattice_selective_scan_fwd",
+                  "lattice_selective_scan_bwd", "lattice_selective_step", "lattice_layer_norm_fwd", "lattice_layer_norm_bwd"):
+            getattr(L, f).restype = i
         for f in ("lattice_gated_scan_fwd", "lattice_gated_scan_bwd", "lattice_gated_step", "lattice_block_norm_fwd",
                   "lattice_block_norm_bwd"):
             getattr(L, f).restype = ctypes.c_int
@@ -656,3 +678,366 @@ def block_norm_bwd(y: torch.Tensor, w_post: Optional[torch.Tensor] = None, *, dr
     if code:
         _raise(code, "lattice_block_norm_bwd")
     return {"dy": dy, "dgate": dgate, "dresidual": dresidual, "dw_post": dw_post, "dw_pre": dw_pre}
+
+
+# ---------------------------------------------------------------- layer norm
+
+def layer_norm_fwd(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torch.Tensor] = None, *,
+                   residual: Optional[torch.Tensor] = None, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
+                   r_out: Optional[torch.Tensor] = None, n_out: Optional[torch.Tensor] = None, stream=None):
+    """The layer norm before a block, with the residual that a block's output is added to: per row of the
+    last axis r = residual + x (r = x without a residual), n = (r - mean(r)) / sqrt(var(r) + eps) * w + b, with
+    r as it is kept, in the residual's dtype. x [..., D]; w, b [D], of one dtype, or None (1, 0).
+    out_dtype (default: x's) is n's; x, the residual and the weights are of it or float32. Inputs may be
+    slices of wider rows. r_out may be the residual. Returns (r, n); r is x without a residual."""
+    shape, dev, dtype, w_dtype = _norm_args(x, w, None, residual, None, "none", out_dtype)
+    if b is not None:
+        _whole(b, "b", shape[-1:], _XZ[dtype], dev)
+        if w is not None and b.dtype != w_dtype:
+            raise TypeError("w and b must have the same dtype")
+        w_dtype = b.dtype
+    if residual is None:
+        if r_out is not None:
+            raise ValueError("r_out needs a residual")
+    else:
+        _whole(r_out, "r_out", shape, (residual.dtype,), dev)
+    _whole(n_out, "n_out", shape, (dtype,), dev)
+    D = shape[-1]
+    N = x.numel() // D if D else 0
+    G, gs = _groups((("x", x), ("residual", residual)), shape)
+    ctx, st = _enter(dev, stream)
+    try:
+        if residual is not None and r_out is None:
+            r_out = _new(residual)
+        if n_out is None:
+            n_out = _new(x, dtype)
+        code = lib().lattice_layer_norm_fwd(
+            x.data_ptr(), _DT[x.dtype], gs[0], _adr(residual), 0 if residual is None else _DT[residual.dtype], gs[1], _adr(w),
+            _adr(b), _DT[w_dtype], _adr(r_out), n_out.data_ptr(), _DT[dtype], N, G, D, eps, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_layer_norm_fwd")
+    return x if residual is None else r_out, n_out
+
+
+def layer_norm_bwd(r: torch.Tensor, dn: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torch.Tensor] = None, *,
+                   dr: Optional[torch.Tensor] = None, eps: float = 1e-5, x_dtype: Optional[torch.dtype] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward pass of layer_norm_fwd from the rows r that it returned: gradients of L = sum(dn * n) + sum(dr * r).
+    dn: n's cotangent, in the call's dtype; dr: r's from elsewhere, in r's dtype, or None (0). Returns a dict
+    with dr, the gradient of the residual and of x in r's dtype; dx, the same in x_dtype (default: r's; then it
+    is dr itself); dw, db (float32, None without the weight: b's values are not used). workspace: optional contiguous
+    uint8 tensor for the weights' gradients; allocated when None."""
+    if not isinstance(dn, torch.Tensor):
+        raise TypeError("dn must be a CUDA tensor")
+    shape, dev, dtype, w_dtype = _norm_args(r, w, None, None, None, "none", dn.dtype)
+    _like(dn, "dn", shape, (dtype,), dev)
+    if dr is not None:
+        _like(dr, "dr", shape, (r.dtype,), dev)
+    if b is not None:
+        _whole(b, "b", shape[-1:], _XZ[dtype], dev)
+    if x_dtype is None:
+        x_dtype = r.dtype
+    elif x_dtype not in _XZ[dtype]:
+        raise TypeError(f"x_dtype must be one of {_XZ[dtype]}, got {x_dtype}")
+    D = shape[-1]
+    N = r.numel() // D if D else 0
+    G, gs = _groups((("r", r), ("dn", dn), ("dr", dr)), shape)
+    _scratch(workspace, dev)
+    L = lib()
+    ctx, st = _enter(dev, stream)
+    try:
+        dr_out = _new(r)
+        dx = None if x_dtype == r.dtype else _new(r, x_dtype)
+        dw = None if w is None else _new(w, torch.float32)
+        db = None if b is None else _new(b, torch.float32)
+        bytes_ = 0
+        if w is not None or b is not None:
+            if workspace is None:
+                workspace = torch.empty(L.lattice_layer_norm_bwd_workspace_bytes(N, D), dtype=torch.uint8, device=dev)
+            bytes_ = workspace.numel() * workspace.element_size()
+        code = L.lattice_layer_norm_bwd(
+            r.data_ptr(), _DT[r.dtype], gs[0], dn.data_ptr(), gs[1], _adr(dr), gs[2], _adr(w), _DT[w_dtype], dr_out.data_ptr(),
+            _adr(dx), _DT[x_dtype], _adr(dw), _adr(db), _adr(workspace), bytes_, _DT[dtype], N, G, D, eps, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_layer_norm_bwd")
+    return {"dr": dr_out, "dx": dr_out if dx is None else dx, "dw": dw, "db": db}
+
+
+def _scratch(workspace, device):
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != device:
+            raise TypeError("workspace must be a contiguous tensor on the inputs' device")
+
+
+# ---------------------------------------------------------------- short convolution
+
+_CONV_ACT = {"none": 0, "silu": 2}
+
+
+def _conv_args(x, w, bias, act: str, lead: int, lengths):
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
+        raise ValueError("x must be a tensor [B, T, C] (one token: [B, C])")
+    shape, device = x.shape, x.device
+    if x.numel() > _INT_MAX:
+        _fits("the convolution's sizes", *shape)
+    xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor [C, K]")
+    K = w.shape[1]
+    _rows(w, "w", torch.Size((shape[-1], K)), 0, _XZ[x.dtype], device)
+    if bias is not None:
+        _whole(bias, "bias", shape[-1:], (w.dtype,), device)
+    if lengths is not None:
+        _whole(lengths, "lengths", shape[:1], (torch.int32,), device)
+    if act not in _CONV_ACT:
+        raise ValueError(f"act is one of {tuple(_CONV_ACT)}")
+    return xs, K
+
+
+def short_conv_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: str = "silu",
+                   state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                   state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Short causal convolution of every channel: y_t = act(bias + sum_k w[:, k] * x_{t-K+1+k}).
+    x [B,T,C], may be a slice of wider rows; w [C,K], K up to 8; bias [C] of w's dtype or None (0); w has
+    x's dtype or float32. state [B,K-1,C] in x's dtype: the inputs before the first token, oldest first,
+    or None (0). act "silu" or "none". lengths int32 [B] or None (T): tokens behind a sequence's length are
+    not read and their y is 0. state_out may be the state.
+    Returns (y [B,T,C] in x's dtype, the state [B,K-1,C] at each sequence's end)."""
+    xs, K = _conv_args(x, w, bias, act, 2, lengths)
+    dev, (B, T, C) = x.device, x.shape
+    _whole(state, "state", (B, K - 1, C), (x.dtype,), dev)
+    _whole(state_out, "state_out", (B, K - 1, C), (x.dtype,), dev)
+    _whole(y, "y", x.shape, (x.dtype,), dev)
+    ctx, st = _enter(dev, stream)
+    try:
+        if state_out is None:
+            state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
+        if y is None:
+            y = _new(x)
+        code = lib().lattice_short_conv_fwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], w.data_ptr(), _adr(bias), _DT[w.dtype], _adr(state), state_out.data_ptr(),
+            y.data_ptr(), _adr(lengths), B, T, C, K, _CONV_ACT[act], st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_short_conv_fwd")
+    return y, state_out
+
+
+def short_conv_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: str = "silu",
+                   state: Optional[torch.Tensor] = None, dstate_out: Optional[torch.Tensor] = None,
+                   lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward pass of short_conv_fwd from its inputs: gradients of L = sum(dy * y) + sum(dstate_out * state_out).
+    dy has x's dtype and may be strided as x; dstate_out [B,K-1,C] in x's dtype or None (0). Returns a dict
+    with dx, dstate (x's dtype; dstate None without a state), dw [C,K] and dbias [C] (float32; dbias None
+    without a bias). workspace: optional contiguous uint8 tensor for the weights' gradients; allocated when None."""
+    xs, K = _conv_args(x, w, bias, act, 2, lengths)
+    dev, (B, T, C) = x.device, x.shape
+    dys = _rows(dy, "dy", x.shape, 2, (x.dtype,), dev)
+    _whole(state, "state", (B, K - 1, C), (x.dtype,), dev)
+    _whole(dstate_out, "dstate_out", (B, K - 1, C), (x.dtype,), dev)
+    _scratch(workspace, dev)
+    L = lib()
+    ctx, st = _enter(dev, stream)
+    try:
+        dx = _new(x)
+        dw = _new(w, torch.float32)
+        dbias = None if bias is None else _new(bias, torch.float32)
+        dstate = None if state is None else torch.empty_like(state)
+        if workspace is None:
+            workspace = torch.empty(L.lattice_short_conv_bwd_workspace_bytes(B, T, C, K), dtype=torch.uint8, device=dev)
+        code = L.lattice_short_conv_bwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], w.data_ptr(), _adr(bias), _DT[w.dtype], _adr(state), dy.data_ptr(), dys[0],
+            dys[1], _adr(dstate_out), dx.data_ptr(), dw.data_ptr(), _adr(dbias), _adr(dstate), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _adr(lengths), B, T, C, K, _CONV_ACT[act], st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_short_conv_bwd")
+    return {"dx": dx, "dw": dw, "dbias": dbias, "dstate": dstate}
+
+
+def short_conv_step(state: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                    act: str = "silu", state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """One token of the short convolution: state [B,K-1,C] and x [B,C] of one dtype. The state is updated in
+    place (its rows move up, x becomes the last), or written to state_out. Returns y [B,C]."""
+    xs, K = _conv_args(x, w, bias, act, 1, None)
+    dev, (B, C) = x.device, x.shape
+    _rows(state, "state", torch.Size((B, K - 1, C)), 0, (x.dtype,), dev)
+    _whole(state_out, "state_out", (B, K - 1, C), (x.dtype,), dev)
+    _whole(y, "y", x.shape, (x.dtype,), dev)
+    if state_out is None:
+        state_out = state
+    ctx, st = _enter(dev, stream)
+    try:
+        if y is None:
+            y = _new(x)
+        code = lib().lattice_short_conv_step(
+            state.data_ptr(), state_out.data_ptr(), x.data_ptr(), _DT[x.dtype], xs[0], w.data_ptr(), _adr(bias), _DT[w.dtype],
+            y.data_ptr(), B, C, K, _CONV_ACT[act], st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_short_conv_step")
+    return y
+
+
+# ---------------------------------------------------------------- selective scan
+
+_SEL_MARK = 8  # tokens between the states kept for the backward pass
+_NO_STRIDES = (0, 0)
+
+
+def _sel_args(x, dt, A, b, c, skip, z, dt_bias, lead: int, lengths):
+    """(strides of x, dt, b, c and z; N; G)"""
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
+        raise ValueError("x must be a tensor [B, T, E] (one token: [B, E])")
+    shape, device = x.shape, x.device
+    if x.numel() > _INT_MAX:
+        _fits("the selective scan's sizes", *shape)
+    xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
+    same = (x.dtype,)
+    ds = _rows(dt, "dt", shape, lead, _XZ[x.dtype], device)
+    zs = _NO_STRIDES if z is None else _rows(z, "z", shape, lead, same, device)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [E, N]")
+    E, N = shape[-1], A.shape[1]
+    _rows(A, "A", torch.Size((E, N)), 0, _F32_ONLY, device)
+    if not isinstance(b, torch.Tensor) or b.dim() not in (lead + 1, lead + 2):
+        raise ValueError("b must be a tensor [B, T, N] or [B, T, G, N] (one token: without T)")
+    G = b.shape[lead] if b.dim() == lead + 2 else 1
+    rows = shape[:lead] + ((G, N) if b.dim() == lead + 2 else (N,))
+    bs = _rows(b, "b", rows, lead, same, device)
+    cs = _rows(c, "c", rows, lead, same, device)
+    _whole(skip, "skip", shape[-1:], _F32_ONLY, device)
+    _whole(dt_bias, "dt_bias", shape[-1:], _F32_ONLY, device)
+    if lengths is not None:
+        _whole(lengths, "lengths", shape[:1], (torch.int32,), device)
+    if G < 1 or E % G:
+        raise ValueError(f"{E} channels do not make {G} groups")
+    return xs, ds, bs, cs, zs, N, G
+
+
+def selective_scan_marks(x: torch.Tensor, N: int) -> torch.Tensor:
+    """An empty buffer for the states that selective_scan_fwd leaves for selective_scan_bwd: the state before
+    every 8th token, [B, ceil(T/8), E, N] float32."""
+    B, T, E = x.shape
+    return torch.empty((B, (T + _SEL_MARK - 1) // _SEL_MARK, E, N), dtype=torch.float32, device=x.device)
+
+
+def selective_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
+                       skip: Optional[torch.Tensor] = None, *, z: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, h0: Optional[torch.Tensor] = None,
+                       lengths: Optional[torch.Tensor] = None, marks: Optional[torch.Tensor] = None,
+                       h_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Selective state space scan over whole sequences: with d_t = softplus(dt_t + dt_bias),
+    h_t = exp(d_t A) h_{t-1} + d_t x_t b_t and y_t = (c_t . h_t + skip x_t) silu(z_t).
+    x, z (or None: no gate) [B,T,E]; dt [B,T,E], of x's dtype or float32 (softplus=False: d_t = dt_t + dt_bias);
+    A [E,N] float32, N up to 128, with d_t A <= 0; b, c [B,T,N], or [B,T,G,N] for G groups of E/G neighbouring
+    channels; skip, dt_bias [E] float32 or None (0); h0 [B,E,N] float32 or None (0). x, z, dt, b and c may be
+    slices of wider rows. lengths int32 [B] or None (T): tokens behind a sequence's length are not read and
+    their y is 0. marks: a buffer of selective_scan_marks to fill for selective_scan_bwd. h_out may be h0. workspace:
+    optional contiguous uint8 tensor; allocated when None and needed.
+    Returns (y [B,T,E] in x's dtype, h_T [B,E,N] float32, the state at each length)."""
+    xs, ds, bs, cs, zs, N, G = _sel_args(x, dt, A, b, c, skip, z, dt_bias, 2, lengths)
+    dev, (B, T, E) = x.device, x.shape
+    state = (B, E, N)
+    _whole(h0, "h0", state, _F32_ONLY, dev)
+    _whole(marks, "marks", (B, (T + _SEL_MARK - 1) // _SEL_MARK, E, N), _F32_ONLY, dev)
+    _whole(h_out, "h_out", state, _F32_ONLY, dev)
+    _whole(y, "y", x.shape, (x.dtype,), dev)
+    _scratch(workspace, dev)
+    L = lib()
+    ctx, st = _enter(dev, stream)
+    try:
+        if h_out is None:
+            h_out = torch.empty(state, dtype=torch.float32, device=dev)
+        if y is None:
+            y = _new(x)
+        workspace, bytes_ = _sel_space(L, workspace, B, T, E, N, G, 0, dev)
+        code = L.lattice_selective_scan_fwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], dt.data_ptr(), _DT[dt.dtype], ds[0], ds[1], A.data_ptr(), b.data_ptr(), bs[0],
+            bs[1], c.data_ptr(), cs[0], cs[1], _adr(skip), _adr(z), zs[0], zs[1], _adr(dt_bias), softplus, _adr(h0),
+            h_out.data_ptr(), y.data_ptr(), _adr(marks), _adr(lengths), _adr(workspace), bytes_, B, T, E, N, G, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_selective_scan_fwd")
+    return y, h_out
+
+
+def _sel_space(L, workspace, B, T, E, N, G, backward, dev):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    need = L.lattice_selective_scan_workspace_bytes(B, T, E, N, G, backward)
+    return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+
+
+def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, b: torch.Tensor, c: torch.Tensor, dy: torch.Tensor,
+                       marks: torch.Tensor, skip: Optional[torch.Tensor] = None, *, z: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, dh_T: Optional[torch.Tensor] = None,
+                       lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Backward pass of selective_scan_fwd: gradients of L = sum(dy * y) + sum(dh_T * h_T). The inputs and the filled
+    marks are those of the forward call; dy has x's dtype and may be strided as x; dh_T [B,E,N] float32 or None (0).
+    Returns a dict with dx, dz, db, dc (x's dtype), ddt (dt's dtype), dA, dskip, ddt_bias and dh0 (float32); dz, dskip
+    and ddt_bias are None without their input. Gradients of tokens behind a sequence's length are 0."""
+    xs, ds, bs, cs, zs, N, G = _sel_args(x, dt, A, b, c, skip, z, dt_bias, 2, lengths)
+    dev, (B, T, E) = x.device, x.shape
+    dys = _rows(dy, "dy", x.shape, 2, (x.dtype,), dev)
+    _rows(marks, "marks", torch.Size((B, (T + _SEL_MARK - 1) // _SEL_MARK, E, N)), 0, _F32_ONLY, dev)
+    _whole(dh_T, "dh_T", (B, E, N), _F32_ONLY, dev)
+    _scratch(workspace, dev)
+    L = lib()
+    ctx, st = _enter(dev, stream)
+    try:
+        g = {"dx": _new(x), "ddt": _new(dt), "dA": torch.empty_like(A), "db": _new(b), "dc": _new(c),
+             "dskip": None if skip is None else torch.empty_like(skip), "dz": None if z is None else _new(z),
+             "ddt_bias": None if dt_bias is None else torch.empty_like(dt_bias),
+             "dh0": torch.empty((B, E, N), dtype=torch.float32, device=dev)}
+        workspace, bytes_ = _sel_space(L, workspace, B, T, E, N, G, 1, dev)
+        code = L.lattice_selective_scan_bwd(
+            x.data_ptr(), _DT[x.dtype], xs[0], xs[1], dt.data_ptr(), _DT[dt.dtype], ds[0], ds[1], A.data_ptr(), b.data_ptr(), bs[0],
+            bs[1], c.data_ptr(), cs[0], cs[1], _adr(skip), _adr(z), zs[0], zs[1], _adr(dt_bias), softplus, dy.data_ptr(), dys[0],
+            dys[1], marks.data_ptr(), _adr(dh_T), *(_adr(t) for t in g.values()), _adr(lengths), _adr(workspace), bytes_,
+            B, T, E, N, G, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_selective_scan_bwd")
+    return g
+
+
+def selective_step(h: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
+                   skip: Optional[torch.Tensor] = None, *, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, softplus: bool = True, h_out: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the selective scan: h [B,E,N] float32; x, dt, z [B,E]; b, c [B,N] or [B,G,N]. The state is updated
+    in place, or written to h_out. Returns y [B,E] in x's dtype."""
+    xs, ds, bs, cs, zs, N, G = _sel_args(x, dt, A, b, c, skip, z, dt_bias, 1, None)
+    dev, (B, E) = x.device, x.shape
+    state = torch.Size((B, E, N))
+    _rows(h, "h", state, 0, _F32_ONLY, dev)
+    _whole(h_out, "h_out", state, _F32_ONLY, dev)
+    _whole(y, "y", x.shape, (x.dtype,), dev)
+    if h_out is None:
+        h_out = h
+    ctx, st = _enter(dev, stream)
+    try:
+        if y is None:
+            y = _new(x)
+        code = lib().lattice_selective_step(
+            h.data_ptr(), h_out.data_ptr(), x.data_ptr(), _DT[x.dtype], xs[0], dt.data_ptr(), _DT[dt.dtype], ds[0], A.data_ptr(),
+            b.data_ptr(), bs[0], c.data_ptr(), cs[0], _adr(skip), _adr(z), zs[0], _adr(dt_bias), softplus, y.data_ptr(), B, E, N,
+            G, st)
+    finally:
+        _leave(ctx)
+    if code:
+        _raise(code, "lattice_selective_step")
+    return y

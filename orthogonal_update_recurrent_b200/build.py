@@ -24,7 +24,10 @@ LINK_FLAGS = [*ARCH, "-shared", "-cudart", "static"]
 UNITS = ["lattice_abi.cu", "tu_simt_exact.cu", "tu_simt_chunked.cu", "tu_step.cu", "tu_bwd.cu", "tu_tc.cu",
          "tu_norm_f32.cu", "tu_norm_bf16.cu", "tu_norm_f16.cu",
          "tu_gated_fwd_f32.cu", "tu_gated_fwd_bf16.cu", "tu_gated_fwd_f16.cu",
-         "tu_gated_bwd_f32.cu", "tu_gated_bwd_bf16.cu", "tu_gated_bwd_f16.cu"]
+         "tu_gated_bwd_f32.cu", "tu_gated_bwd_bf16.cu", "tu_gated_bwd_f16.cu",
+         "tu_lnorm_f32.cu", "tu_lnorm_bf16.cu", "tu_lnorm_f16.cu",
+         "conv_f32.cu", "conv_bf16.cu", "conv_f16.cu",
+         "sel_fwd_f32.cu", "sel_fwd_bf16.cu", "sel_fwd_f16.cu", "sel_bwd_f32.cu", "sel_bwd_bf16.cu", "sel_bwd_f16.cu"]
 OBJDIR = os.path.join(HERE, "_build")
 
 

@@ -142,4 +142,53 @@ struct NormArgs {
     bool y32, r32, w32;                                     // fp32, else the call's type: y; residual, r and dr; weights
 };
 
+// short_conv.cuh: short causal convolution
+constexpr int kConvMaxK = 8;
+constexpr int kConvVecBytes = 16, kConvBwdVec = 4;  // forward: bytes, backward: channels per thread
+constexpr int kConvRun = 32, kConvBwdRun = 64, kConvMaxRuns = 1024;
+constexpr int kConvMaxSize = 1 << 30;  // channels, and tokens
+constexpr int kConvFwd = 0, kConvBwd = 1, kConvStep = 2;
+
+struct ConvArgs {
+    const void *x, *w, *bias, *state;   // w [C][K]; bias, state [B][K-1][C] may be null
+    const void *dy, *dstate_out;        // backward: dstate_out may be null
+    void *y, *state_out;                // forward: state_out may be null
+    void *dx, *dstate;                  // backward: dstate may be null
+    float *parts, *dw, *dbias;          // backward: parts null where neither is wanted
+    const int* lengths;                 // may be null (=> T)
+    long long xbs, xts, ybs, yts;       // batch and token strides of x and dy, in elements
+    int B, T, C, K, run, runs;          // tokens of a thread's run, runs per sequence
+    bool w32, silu;                     // weights and bias fp32, else x's type
+};
+
+// selective.cuh: selective state space scan
+constexpr int kSelTile = 16;     // tokens that a CTA stages at once
+constexpr int kSelMark = 8;      // tokens between the states that the forward pass leaves for the backward pass
+constexpr int kSelThreads = 256;
+constexpr int kSelMaxN = 128;
+constexpr int kSelMaxSize = 1 << 30;  // channels, and tokens
+
+struct SelArgs {
+    const void *x, *dt, *z, *b, *c;                // z may be null
+    const float *A, *skip, *dt_bias, *h0;          // the last three may be null
+    float* h_out; void* y; float* marks;           // forward: h_out, marks may be null
+    const int* lengths;                            // may be null (=> T)
+    const void* dy; const float* dh_T;             // backward: dh_T may be null (=> 0)
+    void *dx, *ddt, *dz; float* dh0;               // backward: dz null without z
+    void *db, *dc; float *dA, *dskip, *ddt_bias;
+    float *seg_state, *seg_sum;                    // [B][nseg][E][N], [B][nseg][E]: null where nseg is 1
+    float *parts_A, *parts_ch, *parts_bc;          // backward: sums per CTA
+    long long xbs, xts, dbs, dts, zbs, zts, bbs, bts, cbs, cts, ybs, yts;  // batch and token strides; y: dy's
+    int B, T, E, N, G, Eg;                         // Eg = E/G channels per group of b and c
+    int tiles, nseg, seg, nmarks;                  // channel tiles per group; segments of the time axis, their tokens
+    bool dt32, softplus, vec, vec_n;               // vec: pairs of channels, vec_n: four states in one access
+};
+
+// Lanes that share a channel's states, 4 states each (2 in the forward pass where that fills the device better).
+LATTICE_HD inline int sel_padded(int N) {
+    int np = 8;
+    while (np < N) np *= 2;
+    return np;
+}
+
 }  // namespace lattice

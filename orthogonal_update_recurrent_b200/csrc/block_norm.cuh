@@ -527,6 +527,47 @@ norm_fwd_kernel(const NormArgs A) {
     sums.end();
 }
 
+// The weights' gradients: the CTA's sums (dq, dp: 8 floats of each thread's own columns) to its row of the
+// workspace, added up by norm_dw_kernel.
+template <class XT, int MODE, bool SUB>
+__device__ __forceinline__ void write_parts(const NormArgs& A, const Columns<MODE>& c, const ulonglong2* dq, const ulonglong2* dp,
+                                            unsigned rows, unsigned row0, int K) {
+    if (!A.parts) return;
+    float* out = A.parts + (long long)(blockIdx.x / K) * 2 * A.D;
+    __syncthreads();
+    if constexpr (MODE == kShift) {
+        for (int k = 0; k < 2; ++k) {
+            const float* p = reinterpret_cast<const float*>(k ? dp : dq);
+            if constexpr (SUB) {  // a column is another thread's in each of the rows
+                for (int q = threadIdx.x; q < A.D; q += blockDim.x) {
+                    float t = 0.f;
+                    for (unsigned i = 0; i < rows; ++i) {
+                        const unsigned j = q + ((row0 + i) * (unsigned)A.D & 7u), v = j & 7u;
+                        t += p[((v >> 2) * blockDim.x + i * A.tpr + (j >> 3)) * 4 + (v & 3u)];
+                    }
+                    out[k * A.D + q] = t;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    if (c.mine(v)) out[k * A.D + c.first + v] = p[((v >> 2) * blockDim.x + threadIdx.x) * 4 + (v & 3)];
+            }
+        }
+        return;
+    }
+    if (SUB && (int)threadIdx.x >= A.tpr) return;
+    for (int k = 0; k < 2; ++k) {
+        const ulonglong2* p = k ? dp : dq;
+        F2 t[4];
+        own_read(p, t);
+        for (unsigned q = 1; q < rows; ++q) {  // a CTA's rows side by side, one by one
+            const ulonglong2 a = p[q * A.tpr + threadIdx.x], b = p[blockDim.x + q * A.tpr + threadIdx.x];
+            t[0] = add2(t[0], F2{a.x}), t[1] = add2(t[1], F2{a.y}), t[2] = add2(t[2], F2{b.x}), t[3] = add2(t[3], F2{b.y});
+        }
+        store8<float, MODE>(out, true, k * A.D, c, t);
+    }
+}
+
 // With t = scale y w_post act(gate), v = rho1 t, m = w_pre dn and e as above, the sum for dy
 //   sum(du y) = sum(e t) = sum(dr t) + rho2 sum(m t) - k sum(r t), k = rho2^3 mean(m r),
 // is taken apart, so that it needs no exchange of its own after e is known.
@@ -659,41 +700,7 @@ __global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) norm_bwd
         if (in) store8<XT, MODE>(A.dy, y32, o, c, e);
     }
     sums.end();
-    // the weights' gradients: the CTA's sums to its row of the workspace, added up by norm_dw_kernel
-    if (!A.parts) return;
-    float* out = A.parts + (long long)(blockIdx.x / sums.K) * 2 * A.D;
-    __syncthreads();
-    if constexpr (MODE == kShift) {
-        for (int k = 0; k < 2; ++k) {
-            const float* p = reinterpret_cast<const float*>(k ? dp : dq);
-            if constexpr (SUB) {  // a column is another thread's in each of the rows
-                for (int q = threadIdx.x; q < A.D; q += blockDim.x) {
-                    float t = 0.f;
-                    for (unsigned i = 0; i < rows; ++i) {
-                        const unsigned j = q + ((row0 + i) * (unsigned)A.D & 7u), v = j & 7u;
-                        t += p[((v >> 2) * blockDim.x + i * A.tpr + (j >> 3)) * 4 + (v & 3u)];
-                    }
-                    out[k * A.D + q] = t;
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    if (c.mine(v)) out[k * A.D + c.first + v] = p[((v >> 2) * blockDim.x + threadIdx.x) * 4 + (v & 3)];
-            }
-        }
-        return;
-    }
-    if (SUB && (int)threadIdx.x >= A.tpr) return;
-    for (int k = 0; k < 2; ++k) {
-        const ulonglong2* p = k ? dp : dq;
-        F2 t[4];
-        own_read(p, t);
-        for (unsigned q = 1; q < rows; ++q) {  // a CTA's rows side by side, one by one
-            const ulonglong2 a = p[q * A.tpr + threadIdx.x], b = p[blockDim.x + q * A.tpr + threadIdx.x];
-            t[0] = add2(t[0], F2{a.x}), t[1] = add2(t[1], F2{a.y}), t[2] = add2(t[2], F2{b.x}), t[3] = add2(t[3], F2{b.y});
-        }
-        store8<float, MODE>(out, true, k * A.D, c, t);
-    }
+    write_parts<XT, MODE, SUB>(A, c, dq, dp, rows, row0, sums.K);
 }
 
 // dw = scale (w_post) or 1 (w_pre) times the column sums of [parts][2 D]: 32 columns and

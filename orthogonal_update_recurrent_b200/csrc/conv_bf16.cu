@@ -1,0 +1,8 @@
+// conv_bf16.cu -- the short convolution's kernels for x of this type.
+#include "conv_launch.cuh"
+
+namespace lattice {
+
+template lattice_status conv::launch<__nv_bfloat16>(const ConvArgs& a, int what, bool vec, cudaStream_t st);
+
+}  // namespace lattice

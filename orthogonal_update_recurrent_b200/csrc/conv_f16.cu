@@ -1,0 +1,8 @@
+// conv_f16.cu -- the short convolution's kernels for x of this type.
+#include "conv_launch.cuh"
+
+namespace lattice {
+
+template lattice_status conv::launch<__half>(const ConvArgs& a, int what, bool vec, cudaStream_t st);
+
+}  // namespace lattice

@@ -213,8 +213,8 @@ bool gate_words(const void* z, int H, long long bs, long long ts) {
 
 // The layer operators' units, by type of x or of the call, that a call has launched or captured
 // kernels of. Only these can have set their status word, and reading one takes 12 us.
-enum LayerUnit { kGatedFwdUnit, kGatedBwdUnit, kNormUnit };
-std::atomic<bool> g_unit_used[3][3];
+enum LayerUnit { kGatedFwdUnit, kGatedBwdUnit, kNormUnit, kLayerNormUnit };
+std::atomic<bool> g_unit_used[4][3];
 void use_unit(LayerUnit u, lattice_dtype t) { g_unit_used[u][t].store(true, std::memory_order_relaxed); }
 bool unit_used(LayerUnit u, lattice_dtype t) { return g_unit_used[u][t].load(std::memory_order_relaxed); }
 
@@ -263,6 +263,127 @@ bool norm_rows_shift(const void* p, lattice_dtype t, long long N, int G, int D, 
 }
 bool group_span(const void* p, lattice_dtype t, long long N, int G, int D, long long stride, Span* s) {
     return strided_span(p, type_size(t), N / G, 1, (long long)G * D, stride, 0, s) || !p;
+}
+
+// ---- short convolution
+lattice_status check_conv(lattice_dtype x_dtype, lattice_dtype w_dtype, int B, int T, int C, int K, lattice_act act) {
+    if (B < 1 || T < 0 || C < 1 || K < 1 || !type_ok(x_dtype) || !type_ok(w_dtype)) return LATTICE_ERR_INVALID_ARG;
+    if ((int)act < 0 || (int)act > 3) return LATTICE_ERR_INVALID_ARG;
+    if (act != LATTICE_ACT_NONE && act != LATTICE_ACT_SILU) return LATTICE_ERR_UNSUPPORTED;
+    if (w_dtype != LATTICE_F32 && w_dtype != x_dtype) return LATTICE_ERR_UNSUPPORTED;
+    if (K > kConvMaxK || C > kConvMaxSize || T > kConvMaxSize) return LATTICE_ERR_UNSUPPORTED;
+    return LATTICE_OK;
+}
+// Tokens of a thread's run: kConvRun, fewer (whole eights) where the device would not be filled, more where the
+// backward pass would leave more than kConvMaxRuns rows of weight gradients per sequence.
+int conv_run(long long B, int T, int C, bool bwd, bool vec) {
+    const long long per = vec ? bwd ? kConvBwdVec : 8 : 1, lanes = B * ((C + per - 1) / per), want = (long long)sm_count() * 1024;
+    long long run = bwd ? kConvBwdRun : kConvRun;
+    while (run > 8 && lanes * ((T + run - 1) / run) < want) run /= 2;
+    while (bwd && run < (1 << 29) && (T + run - 1) / run > kConvMaxRuns) run *= 2;
+    return (int)run;
+}
+size_t conv_workspace(int B, int T, int C, int K) {  // either width of a thread's channels
+    const int a = conv_run(B, T, C, true, true), b = conv_run(B, T, C, true, false), run = a < b ? a : b;
+    return (size_t)B * (((size_t)T + run - 1) / run) * (K + 1) * C * 4;
+}
+void conv_args(ConvArgs& a, const void* x, lattice_dtype x_dtype, long long xbs, long long xts, const void* w, const void* bias,
+               lattice_dtype w_dtype, const void* state, const int* lengths, int B, int T, int C, int K, lattice_act act) {
+    a = ConvArgs{};
+    a.x = x; a.w = w; a.bias = bias; a.state = state; a.lengths = lengths;
+    a.xbs = xbs; a.xts = xts;
+    a.B = B; a.T = T; a.C = C; a.K = K; a.w32 = w_dtype == LATTICE_F32; a.silu = act == LATTICE_ACT_SILU;
+}
+
+// ---- selective scan
+struct SelPlan {
+    int S, tiles, nseg, seg;
+};
+long long sel_tiles(int Eg, int lanes) { return ((long long)Eg + kSelThreads / lanes - 1) / (kSelThreads / lanes); }
+// How the work is spread. A CTA has 256/L channels with N padded to L S states, and a whole sequence, which fills
+// the device from one CTA per SM on. With fewer: two states per lane instead of four (twice the CTAs, of half the work per
+// token), or the time axis in segments, whose states take a pass of their own and so twice the exponentials
+// (backward: half as many again). The cheapest of these, by the work on the fullest SM.
+SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
+    const int np = sel_padded(N), Eg = E / G;
+    const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4);
+    SelPlan p = {4, (int)sel_tiles(Eg, np / 4), 1, T > 0 ? T : 1};
+    auto rounds = [&](long long ctas) { return (double)((ctas + sm - 1) / sm); };
+    double best = rounds(base);
+    if (!bwd && np <= 32) {
+        const long long tiles = sel_tiles(Eg, np / 2);
+        const double cost = 0.55 * rounds((long long)B * G * tiles);
+        if (cost < best) best = cost, p.S = 2, p.tiles = (int)tiles;
+    }
+    long long n = 2 * sm / base, most = T / (8 * kSelTile);
+    if (n > most) n = most;
+    if (n > 1 && (bwd ? 1.6 : 2.1) * rounds(base * n) / n < best) {
+        const long long tiles = ((long long)T + kSelTile - 1) / kSelTile, per = (tiles + n - 1) / n;
+        p = {4, (int)sel_tiles(Eg, np / 4), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
+    }
+    return p;
+}
+// Floats of the workspace's parts, each a multiple of 4: the segments' states and sums, and backward the CTAs' sums
+struct SelSpace {
+    size_t state, sum, A, ch, bc;
+    size_t bytes() const { return 4 * (state + sum + A + ch + bc); }
+};
+SelSpace sel_space(const SelPlan& p, int B, int T, int E, int N, int G, bool bwd) {
+    auto four = [](size_t n) { return (n + 3) / 4 * 4; };
+    const size_t rows = (size_t)B * p.nseg;
+    SelSpace s = {};
+    if (p.nseg > 1) s.state = four(rows * E * N), s.sum = four(rows * E);
+    if (bwd) s.A = four(rows * E * N), s.ch = four(rows * 2 * E), s.bc = four((size_t)G * p.tiles * B * T * 2 * N);
+    return s;
+}
+lattice_status check_selective(lattice_dtype x_dtype, lattice_dtype dt_dtype, int B, int T, int E, int N, int G) {
+    if (B < 1 || T < 0 || E < 1 || N < 1 || G < 1 || E % G || !type_ok(x_dtype) || !type_ok(dt_dtype)) return LATTICE_ERR_INVALID_ARG;
+    if (dt_dtype != LATTICE_F32 && dt_dtype != x_dtype) return LATTICE_ERR_UNSUPPORTED;
+    if (N > kSelMaxN || E > kSelMaxSize || T > kSelMaxSize) return LATTICE_ERR_UNSUPPORTED;
+    return LATTICE_OK;
+}
+// What the calls share: their inputs, checked, into a, and their spans.
+struct SelInputs {
+    Span s[10];
+    int n;
+};
+lattice_status sel_inputs(SelArgs& a, SelInputs& in, const void* x, lattice_dtype x_dtype, long long xbs, long long xts, const void* dt,
+                          lattice_dtype dt_dtype, long long dbs, long long dts, const float* A, const void* b, long long bbs,
+                          long long bts, const void* c, long long cbs, long long cts, const float* skip, const void* z,
+                          long long zbs, long long zts, const float* dt_bias, int softplus, const int* lengths, int B, int T, int E,
+                          int N, int G) {
+    const size_t sx = type_size(x_dtype), sd = type_size(dt_dtype);
+    if (!A || (T > 0 && (!x || !dt || !b || !c))) return LATTICE_ERR_INVALID_ARG;
+    Span s[5] = {};
+    if (!strided_span(x, sx, B, T, E, xbs, xts, s) || !strided_span(dt, sd, B, T, E, dbs, dts, s + 1) ||
+        !strided_span(b, sx, B, T, (long long)G * N, bbs, bts, s + 2) || !strided_span(c, sx, B, T, (long long)G * N, cbs, cts, s + 3) ||
+        (z && !strided_span(z, sx, B, T, E, zbs, zts, s + 4)))
+        return LATTICE_ERR_INVALID_ARG;
+    for (const void* p : {x, b, c, z})
+        if (!aligned(p, sx)) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(dt, sd) || !aligned(A, 4) || !aligned(skip, 4) || !aligned(dt_bias, 4) || !aligned(lengths, 4)) return LATTICE_ERR_INVALID_ARG;
+    in.n = 0;
+    for (const Span& v : s) in.s[in.n++] = v;
+    in.s[in.n++] = span(A, (size_t)E * N * 4);
+    in.s[in.n++] = span(skip, skip ? (size_t)E * 4 : 0);
+    in.s[in.n++] = span(dt_bias, dt_bias ? (size_t)E * 4 : 0);
+    in.s[in.n++] = span(lengths, lengths ? (size_t)B * 4 : 0);
+    a = SelArgs{};
+    a.x = x; a.dt = dt; a.z = z; a.b = b; a.c = c; a.A = A; a.skip = skip; a.dt_bias = dt_bias; a.lengths = lengths;
+    a.xbs = xbs; a.xts = xts; a.dbs = dbs; a.dts = dts; a.zbs = zbs; a.zts = zts; a.bbs = bbs; a.bts = bts; a.cbs = cbs; a.cts = cts;
+    a.B = B; a.T = T; a.E = E; a.N = N; a.G = G; a.Eg = E / G;
+    a.nmarks = (int)((T + (long long)kSelMark - 1) / kSelMark);
+    a.dt32 = dt_dtype == LATTICE_F32; a.softplus = softplus != 0;
+    a.vec = a.Eg % 2 == 0 && rows_vec(x, sx, B, T, xbs, xts, 2 * sx) && rows_vec(dt, sd, B, T, dbs, dts, 2 * sd) &&
+            (!z || rows_vec(z, sx, B, T, zbs, zts, 2 * sx));
+    a.vec_n = N % 4 == 0 && aligned(A, 16);
+    return LATTICE_OK;
+}
+void sel_place(SelArgs& a, const SelPlan& p, const SelSpace& s, void* workspace) {
+    a.tiles = p.tiles; a.nseg = p.nseg; a.seg = p.seg;
+    float* w = static_cast<float*>(workspace);
+    if (p.nseg > 1) a.seg_state = w, a.seg_sum = w + s.state;
+    if (s.A) a.parts_A = w + s.state + s.sum, a.parts_ch = a.parts_A + s.A, a.parts_bc = a.parts_ch + s.ch;
 }
 
 }  // namespace
@@ -730,6 +851,297 @@ lattice_status lattice_block_norm_bwd(const void* y, lattice_dtype y_dtype, long
     return s != LATTICE_OK || !dw ? s : launch_norm_dw(a, groups, dw_post, dw_pre, st);
 }
 
+lattice_status lattice_short_conv_fwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride, long long x_token_stride,
+                                      const void* w, const void* bias, lattice_dtype w_dtype, const void* state, void* state_out,
+                                      void* y, const int* lengths, int B, int T, int C, int K, lattice_act act, void* stream) {
+    lattice_status s = check_conv(x_dtype, w_dtype, B, T, C, K, act);
+    if (s != LATTICE_OK) return s;
+    const size_t sx = type_size(x_dtype), sw = type_size(w_dtype), sb = (size_t)B * (K - 1) * C * sx;
+    Span xs;
+    if (!strided_span(x, sx, B, T, C, x_batch_stride, x_token_stride, &xs)) return LATTICE_ERR_INVALID_ARG;
+    if (!w || (T > 0 && (!x || !y))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(x, sx) || !aligned(y, sx) || !aligned(state, sx) || !aligned(state_out, sx) || !aligned(w, sw) || !aligned(bias, sw) ||
+        !aligned(lengths, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    const Span ins[] = {xs, span(w, (size_t)C * K * sw), span(bias, bias ? (size_t)C * sw : 0), span(state, state ? sb : 0),
+                        span(lengths, lengths ? (size_t)B * 4 : 0)};
+    const Span outs[] = {span(y, (size_t)B * T * C * sx), span(state_out, state_out ? sb : 0)};
+    if (clash(ins, 5, outs, 2, state, state_out)) return LATTICE_ERR_INVALID_ARG;
+    ConvArgs a;
+    conv_args(a, x, x_dtype, x_batch_stride, x_token_stride, w, bias, w_dtype, state, lengths, B, T, C, K, act);
+    a.y = y;
+    a.state_out = K > 1 ? state_out : nullptr;
+    const bool vec = C % (kConvVecBytes / sx) == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, kConvVecBytes) && aligned(y, kConvVecBytes) &&
+                     aligned(state, kConvVecBytes) && aligned(state_out, kConvVecBytes);
+    a.run = conv_run(B, T, C, false, vec);
+    a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvFwd, vec, static_cast<cudaStream_t>(stream)); });
+}
+
+size_t lattice_short_conv_bwd_workspace_bytes(int B, int T, int C, int K) {
+    if (check_conv(LATTICE_F32, LATTICE_F32, B, T, C, K, LATTICE_ACT_NONE) != LATTICE_OK) return 0;
+    return conv_workspace(B, T > 0 ? T : 1, C, K);
+}
+
+lattice_status lattice_short_conv_bwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride, long long x_token_stride,
+                                      const void* w, const void* bias, lattice_dtype w_dtype, const void* state, const void* dy,
+                                      long long dy_batch_stride, long long dy_token_stride, const void* dstate_out, void* dx,
+                                      float* dw, float* dbias, void* dstate, void* workspace, size_t workspace_bytes,
+                                      const int* lengths, int B, int T, int C, int K, lattice_act act, void* stream) {
+    lattice_status s = check_conv(x_dtype, w_dtype, B, T, C, K, act);
+    if (s != LATTICE_OK) return s;
+    const size_t sx = type_size(x_dtype), sw = type_size(w_dtype), sb = (size_t)B * (K - 1) * C * sx;
+    Span xs, ys;
+    if (!strided_span(x, sx, B, T, C, x_batch_stride, x_token_stride, &xs) ||
+        !strided_span(dy, sx, B, T, C, dy_batch_stride, dy_token_stride, &ys))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!w || (T > 0 && (!x || !dy || !dx)) || (dbias && !bias) || (dstate && !state)) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(x, sx) || !aligned(dy, sx) || !aligned(dx, sx) || !aligned(state, sx) || !aligned(dstate, sx) ||
+        !aligned(dstate_out, sx) || !aligned(w, sw) || !aligned(bias, sw) || !aligned(dw, 4) || !aligned(dbias, 4) || !aligned(lengths, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    const bool sums = dw || dbias;
+    const size_t need = sums ? lattice_short_conv_bwd_workspace_bytes(B, T, C, K) : 0;
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return LATTICE_ERR_INVALID_ARG;
+    const Span ins[] = {xs, ys, span(w, (size_t)C * K * sw), span(bias, bias ? (size_t)C * sw : 0), span(state, state ? sb : 0),
+                        span(dstate_out, dstate_out ? sb : 0), span(lengths, lengths ? (size_t)B * 4 : 0)};
+    const Span outs[] = {span(dx, (size_t)B * T * C * sx), span(dw, dw ? (size_t)C * K * 4 : 0), span(dbias, dbias ? (size_t)C * 4 : 0),
+                         span(dstate, dstate ? sb : 0), span(workspace, need)};
+    if (clash(ins, 7, outs, 5, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
+    ConvArgs a;
+    conv_args(a, x, x_dtype, x_batch_stride, x_token_stride, w, bias, w_dtype, state, lengths, B, T, C, K, act);
+    a.dy = dy; a.ybs = dy_batch_stride; a.yts = dy_token_stride;
+    a.dx = dx; a.dw = dw; a.dbias = dbias;
+    a.dstate = K > 1 ? dstate : nullptr;
+    a.dstate_out = K > 1 ? dstate_out : nullptr;
+    a.parts = sums ? static_cast<float*>(workspace) : nullptr;
+    const size_t v = kConvBwdVec * sx;
+    const bool vec = C % kConvBwdVec == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && rows_vec(dy, sx, B, T, a.ybs, a.yts, v) &&
+                     aligned(dx, v) && aligned(state, v) && aligned(dstate, v) && aligned(dstate_out, v);
+    a.run = conv_run(B, T, C, true, vec);
+    a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvBwd, vec, static_cast<cudaStream_t>(stream)); });
+}
+
+lattice_status lattice_short_conv_step(const void* state, void* state_out, const void* x, lattice_dtype x_dtype,
+                                       long long x_batch_stride, const void* w, const void* bias, lattice_dtype w_dtype, void* y,
+                                       int B, int C, int K, lattice_act act, void* stream) {
+    lattice_status s = check_conv(x_dtype, w_dtype, B, 1, C, K, act);
+    if (s != LATTICE_OK) return s;
+    const size_t sx = type_size(x_dtype), sw = type_size(w_dtype), sb = (size_t)B * (K - 1) * C * sx;
+    Span xs;
+    if (!strided_span(x, sx, B, 1, C, x_batch_stride, 0, &xs)) return LATTICE_ERR_INVALID_ARG;
+    if (!x || !w || !y || (K > 1 && (!state || !state_out))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(x, sx) || !aligned(y, sx) || !aligned(state, sx) || !aligned(state_out, sx) || !aligned(w, sw) || !aligned(bias, sw))
+        return LATTICE_ERR_INVALID_ARG;
+    const Span ins[] = {xs, span(w, (size_t)C * K * sw), span(bias, bias ? (size_t)C * sw : 0), span(state, sb)};
+    const Span outs[] = {span(y, (size_t)B * C * sx), span(state_out, sb)};
+    if (clash(ins, 4, outs, 2, state, state_out)) return LATTICE_ERR_INVALID_ARG;
+    ConvArgs a;
+    conv_args(a, x, x_dtype, x_batch_stride, 0, w, bias, w_dtype, state, nullptr, B, 1, C, K, act);
+    a.y = y; a.state_out = state_out;
+    a.run = 8, a.runs = 1;
+    const bool vec = C % (kConvVecBytes / sx) == 0 && rows_vec(x, sx, B, 1, a.xbs, 0, kConvVecBytes) && aligned(y, kConvVecBytes) &&
+                     aligned(state, kConvVecBytes) && aligned(state_out, kConvVecBytes);
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvStep, vec, static_cast<cudaStream_t>(stream)); });
+}
+
+size_t lattice_selective_scan_marks_bytes(int B, int T, int E, int N) {
+    if (check_selective(LATTICE_F32, LATTICE_F32, B, T, E, N, 1) != LATTICE_OK) return 0;
+    return (size_t)B * ((T + (size_t)kSelMark - 1) / kSelMark) * E * N * 4;
+}
+
+size_t lattice_selective_scan_workspace_bytes(int B, int T, int E, int N, int G, int backward) {
+    if (check_selective(LATTICE_F32, LATTICE_F32, B, T, E, N, G) != LATTICE_OK) return 0;
+    return sel_space(sel_plan(B, T, E, N, G, backward != 0), B, T, E, N, G, backward != 0).bytes();
+}
+
+lattice_status lattice_selective_scan_fwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride, long long x_token_stride,
+                                          const void* dt, lattice_dtype dt_dtype, long long dt_batch_stride, long long dt_token_stride,
+                                          const float* A, const void* b, long long b_batch_stride, long long b_token_stride,
+                                          const void* c, long long c_batch_stride, long long c_token_stride, const float* skip,
+                                          const void* z, long long z_batch_stride, long long z_token_stride, const float* dt_bias,
+                                          int softplus, const float* h0, float* h_out, void* y, float* marks, const int* lengths,
+                                          void* workspace, size_t workspace_bytes, int B, int T, int E, int N, int G, void* stream) {
+    lattice_status s = check_selective(x_dtype, dt_dtype, B, T, E, N, G);
+    if (s != LATTICE_OK) return s;
+    SelArgs a;
+    SelInputs in;
+    s = sel_inputs(a, in, x, x_dtype, x_batch_stride, x_token_stride, dt, dt_dtype, dt_batch_stride, dt_token_stride, A, b,
+                   b_batch_stride, b_token_stride, c, c_batch_stride, c_token_stride, skip, z, z_batch_stride, z_token_stride, dt_bias,
+                   softplus, lengths, B, T, E, N, G);
+    if (s != LATTICE_OK) return s;
+    if (T > 0 && !y && !marks) return LATTICE_ERR_INVALID_ARG;
+    const size_t sx = type_size(x_dtype), nh = (size_t)B * E * N * 4;
+    const SelPlan plan = sel_plan(B, T, E, N, G, false);
+    const SelSpace space = sel_space(plan, B, T, E, N, G, false);
+    const size_t need = space.bytes();
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(h0, 4) || !aligned(h_out, 4) || !aligned(y, sx) || !aligned(marks, 16)) return LATTICE_ERR_INVALID_ARG;
+    in.s[in.n++] = span(h0, h0 ? nh : 0);
+    const Span outs[] = {span(h_out, h_out ? nh : 0), span(y, y ? (size_t)B * T * E * sx : 0),
+                         span(marks, marks ? lattice_selective_scan_marks_bytes(B, T, E, N) : 0), span(workspace, need)};
+    if (clash(in.s, in.n, outs, 4, h0, h_out)) return LATTICE_ERR_INVALID_ARG;
+    a.h0 = h0; a.h_out = h_out; a.y = y; a.marks = marks;
+    a.vec = a.vec && aligned(y, 2 * sx);
+    a.vec_n = a.vec_n && aligned(h0, 16) && aligned(h_out, 16);
+    sel_place(a, plan, space, workspace);
+    return with_x(x_dtype, [&](auto t) { return selective::launch_fwd<decltype(t)>(a, plan.S, static_cast<cudaStream_t>(stream)); });
+}
+
+lattice_status lattice_selective_scan_bwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride, long long x_token_stride,
+                                          const void* dt, lattice_dtype dt_dtype, long long dt_batch_stride, long long dt_token_stride,
+                                          const float* A, const void* b, long long b_batch_stride, long long b_token_stride,
+                                          const void* c, long long c_batch_stride, long long c_token_stride, const float* skip,
+                                          const void* z, long long z_batch_stride, long long z_token_stride, const float* dt_bias,
+                                          int softplus, const void* dy, long long dy_batch_stride, long long dy_token_stride,
+                                          const float* marks, const float* dh_T, void* dx, void* ddt, float* dA, void* db, void* dc,
+                                          float* dskip, void* dz, float* ddt_bias, float* dh0, const int* lengths, void* workspace,
+                                          size_t workspace_bytes, int B, int T, int E, int N, int G, void* stream) {
+    lattice_status s = check_selective(x_dtype, dt_dtype, B, T, E, N, G);
+    if (s != LATTICE_OK) return s;
+    SelArgs a;
+    SelInputs in;
+    s = sel_inputs(a, in, x, x_dtype, x_batch_stride, x_token_stride, dt, dt_dtype, dt_batch_stride, dt_token_stride, A, b,
+                   b_batch_stride, b_token_stride, c, c_batch_stride, c_token_stride, skip, z, z_batch_stride, z_token_stride, dt_bias,
+                   softplus, lengths, B, T, E, N, G);
+    if (s != LATTICE_OK) return s;
+    if (T > 0 && (!dy || !marks || !dx || !ddt || !db || !dc || (z && !dz))) return LATTICE_ERR_INVALID_ARG;
+    if (!dA || !dh0 || (!z && dz) || (dskip && !skip) || (ddt_bias && !dt_bias)) return LATTICE_ERR_INVALID_ARG;
+    const size_t sx = type_size(x_dtype), sd = type_size(dt_dtype), nh = (size_t)B * E * N * 4, nt = (size_t)B * T;
+    const SelPlan plan = sel_plan(B, T, E, N, G, true);
+    const SelSpace space = sel_space(plan, B, T, E, N, G, true);
+    const size_t need = space.bytes();
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return LATTICE_ERR_INVALID_ARG;
+    for (const void* p : {dy, (const void*)dx, (const void*)db, (const void*)dc, (const void*)dz})
+        if (!aligned(p, sx)) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(ddt, sd) || !aligned(marks, 16) || !aligned(dh_T, 4) || !aligned(dA, 4) || !aligned(dskip, 4) || !aligned(ddt_bias, 4) ||
+        !aligned(dh0, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    Span ys;
+    if (!strided_span(dy, sx, B, T, E, dy_batch_stride, dy_token_stride, &ys)) return LATTICE_ERR_INVALID_ARG;
+    const Span more[] = {ys, span(marks, lattice_selective_scan_marks_bytes(B, T, E, N)), span(dh_T, dh_T ? nh : 0)};
+    const Span outs[] = {span(dx, nt * E * sx), span(ddt, nt * E * sd), span(dz, dz ? nt * E * sx : 0), span(db, nt * G * N * sx),
+                         span(dc, nt * G * N * sx), span(dA, (size_t)E * N * 4), span(dskip, dskip ? (size_t)E * 4 : 0),
+                         span(ddt_bias, ddt_bias ? (size_t)E * 4 : 0), span(dh0, nh), span(workspace, need)};
+    if (clash(in.s, in.n, outs, 10, nullptr, nullptr) || clash(more, 3, outs, 10, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
+    a.dy = dy; a.ybs = dy_batch_stride; a.yts = dy_token_stride;
+    a.marks = const_cast<float*>(marks); a.dh_T = dh_T;
+    a.dx = dx; a.ddt = ddt; a.dz = dz; a.dh0 = dh0; a.db = db; a.dc = dc; a.dA = dA; a.dskip = dskip; a.ddt_bias = ddt_bias;
+    a.vec = a.vec && rows_vec(dy, sx, B, T, a.ybs, a.yts, 2 * sx) && aligned(dx, 2 * sx) && aligned(ddt, 2 * sd) && aligned(dz, 2 * sx);
+    a.vec_n = a.vec_n && aligned(dh_T, 16) && aligned(dh0, 16);
+    sel_place(a, plan, space, workspace);
+    return with_x(x_dtype, [&](auto t) { return selective::launch_bwd<decltype(t)>(a, static_cast<cudaStream_t>(stream)); });
+}
+
+lattice_status lattice_selective_step(const float* h, float* h_out, const void* x, lattice_dtype x_dtype, long long x_batch_stride,
+                                      const void* dt, lattice_dtype dt_dtype, long long dt_batch_stride, const float* A, const void* b,
+                                      long long b_batch_stride, const void* c, long long c_batch_stride, const float* skip,
+                                      const void* z, long long z_batch_stride, const float* dt_bias, int softplus, void* y, int B,
+                                      int E, int N, int G, void* stream) {
+    lattice_status s = check_selective(x_dtype, dt_dtype, B, 1, E, N, G);
+    if (s != LATTICE_OK) return s;
+    SelArgs a;
+    SelInputs in;
+    s = sel_inputs(a, in, x, x_dtype, x_batch_stride, 0, dt, dt_dtype, dt_batch_stride, 0, A, b, b_batch_stride, 0, c, c_batch_stride, 0,
+                   skip, z, z_batch_stride, 0, dt_bias, softplus, nullptr, B, 1, E, N, G);
+    if (s != LATTICE_OK) return s;
+    const size_t sx = type_size(x_dtype), nh = (size_t)B * E * N * 4;
+    if (!h || !h_out || !y || !aligned(h, 4) || !aligned(h_out, 4) || !aligned(y, sx)) return LATTICE_ERR_INVALID_ARG;
+    in.s[in.n++] = span(h, nh);
+    const Span outs[] = {span(h_out, nh), span(y, (size_t)B * E * sx)};
+    if (clash(in.s, in.n, outs, 2, h, h_out)) return LATTICE_ERR_INVALID_ARG;
+    a.h0 = h; a.h_out = h_out; a.y = y;
+    a.vec_n = a.vec_n && aligned(h, 16) && aligned(h_out, 16);
+    return with_x(x_dtype, [&](auto t) { return selective::launch_step<decltype(t)>(a, static_cast<cudaStream_t>(stream)); });
+}
+
+lattice_status lattice_layer_norm_fwd(const void* x, lattice_dtype x_dtype, long long x_stride, const void* residual,
+                                      lattice_dtype residual_dtype, long long residual_stride, const void* w, const void* b,
+                                      lattice_dtype w_dtype, void* r_out, void* n_out, lattice_dtype dtype, long long N, int G, int D,
+                                      float eps, void* stream) {
+    if (!residual) residual_dtype = x_dtype;
+    NormArgs a;
+    lattice_status s = check_norm(a, x, x_dtype, x_stride, nullptr, 0, residual, residual_dtype, residual_stride, w, b, w_dtype, dtype,
+                                  N, G, D, LATTICE_ACT_NONE, 1, 1.f, eps);
+    if (s != LATTICE_OK) return s;
+    if ((N > 0 && (!n_out || (residual && !r_out))) || (!residual && r_out) || !aligned(r_out, type_size(residual_dtype)) ||
+        !aligned(n_out, type_size(dtype)))
+        return LATTICE_ERR_INVALID_ARG;
+    if (N == 0) return LATTICE_OK;
+    const size_t n = (size_t)N * D, wb = (size_t)D * type_size(w_dtype);
+    Span sx, sr = {};
+    if (!group_span(x, x_dtype, N, G, D, x_stride, &sx) || !group_span(residual, residual_dtype, N, G, D, residual_stride, &sr))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!residual) sr = Span{};
+    const Span ins[] = {sx, sr, span(w, w ? wb : 0), span(b, b ? wb : 0)};
+    const Span outs[] = {span(r_out, r_out ? n * type_size(residual_dtype) : 0), span(n_out, n * type_size(dtype))};
+    if (clash(ins, 4, outs, 2, residual, r_out)) return LATTICE_ERR_INVALID_ARG;
+    a.r_out = r_out; a.n_out = n_out;
+    const bool vec = D % 8 == 0 && norm_rows_vec(x, x_dtype, N, G, x_stride) && norm_rows_vec(residual, residual_dtype, N, G, residual_stride) &&
+                     aligned(r_out, 16) && aligned(n_out, 16);
+    const bool shift = D % 8 != 0 && D + 7 <= kNormMaxD && norm_rows_shift(x, x_dtype, N, G, D, x_stride) &&
+                       norm_rows_shift(residual, residual_dtype, N, G, D, residual_stride) && aligned(r_out, 16) && aligned(n_out, 16);
+    use_unit(kLayerNormUnit, dtype);
+    return with_x(dtype, [&](auto t) {
+        return norm::launch_layer<decltype(t)>(false, a, vec ? kNormVec : shift ? kNormShift : kNormOdd, nullptr, static_cast<cudaStream_t>(stream));
+    });
+}
+
+size_t lattice_layer_norm_bwd_workspace_bytes(long long N, int D) { return lattice_block_norm_bwd_workspace_bytes(N, D); }
+
+lattice_status lattice_layer_norm_bwd(const void* r, lattice_dtype r_dtype, long long r_stride, const void* dn, long long dn_stride,
+                                      const void* dr, long long dr_stride, const void* w, lattice_dtype w_dtype, void* dr_out, void* dx,
+                                      lattice_dtype x_dtype, float* dw, float* db, void* workspace, size_t workspace_bytes,
+                                      lattice_dtype dtype, long long N, int G, int D, float eps, void* stream) {
+    if (!dx) x_dtype = r_dtype;
+    NormArgs a;
+    lattice_status s = check_norm(a, r, r_dtype, r_stride, nullptr, 0, nullptr, r_dtype, 0, w, nullptr, w_dtype, dtype, N, G, D,
+                                  LATTICE_ACT_NONE, 1, 1.f, eps);
+    if (s != LATTICE_OK) return s;
+    if (!type_ok(x_dtype) || dn_stride < 0 || dr_stride < 0) return LATTICE_ERR_INVALID_ARG;
+    if ((x_dtype != LATTICE_F32 && x_dtype != dtype) || dn_stride > kNormMaxStride || dr_stride > kNormMaxStride) return LATTICE_ERR_UNSUPPORTED;
+    if ((N > 0 && (!dn || !dr_out)) || (dw && !w)) return LATTICE_ERR_INVALID_ARG;
+    const bool sums = dw || db;
+    const size_t need = sums ? lattice_layer_norm_bwd_workspace_bytes(N, D) : 0;
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return LATTICE_ERR_INVALID_ARG;
+    if (!aligned(dn, type_size(dtype)) || !aligned(dr, type_size(r_dtype)) || !aligned(dr_out, type_size(r_dtype)) ||
+        !aligned(dx, type_size(x_dtype)) || !aligned(dw, 4) || !aligned(db, 4))
+        return LATTICE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        for (float* p : {dw, db}) {
+            cudaError_t e = p ? cudaMemsetAsync(p, 0, (size_t)D * 4, st) : cudaSuccess;
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        return LATTICE_OK;
+    }
+    const size_t n = (size_t)N * D;
+    Span sr, sdn, sdr = {};
+    if (!group_span(r, r_dtype, N, G, D, r_stride, &sr) || !group_span(dn, dtype, N, G, D, dn_stride, &sdn) ||
+        !group_span(dr, r_dtype, N, G, D, dr_stride, &sdr))
+        return LATTICE_ERR_INVALID_ARG;
+    if (!dr) sdr = Span{};
+    const Span ins[] = {sr, sdn, sdr, span(w, w ? (size_t)D * type_size(w_dtype) : 0)};
+    const Span outs[] = {span(dr_out, n * type_size(r_dtype)), span(dx, dx ? n * type_size(x_dtype) : 0),
+                         span(dw, dw ? (size_t)D * 4 : 0), span(db, db ? (size_t)D * 4 : 0), span(workspace, need)};
+    if (clash(ins, 4, outs, 5, nullptr, nullptr)) return LATTICE_ERR_INVALID_ARG;
+    a.dn = dn; a.dr = dr; a.dresidual = dr_out; a.dy = dx;
+    a.dns = (unsigned)dn_stride; a.drs = (unsigned)dr_stride;
+    a.parts = sums ? static_cast<float*>(workspace) : nullptr;
+    a.r32 = r_dtype == LATTICE_F32; a.y32 = x_dtype == LATTICE_F32;
+    const bool vec = D % 8 == 0 && norm_rows_vec(r, r_dtype, N, G, r_stride) && norm_rows_vec(dn, dtype, N, G, dn_stride) &&
+                     norm_rows_vec(dr, r_dtype, N, G, dr_stride) && aligned(dr_out, 16) && aligned(dx, 16);
+    const bool shift = D % 8 != 0 && D + 7 <= kNormMaxD && norm_rows_shift(r, r_dtype, N, G, D, r_stride) &&
+                       norm_rows_shift(dn, dtype, N, G, D, dn_stride) && norm_rows_shift(dr, r_dtype, N, G, D, dr_stride) &&
+                       aligned(dr_out, 16) && aligned(dx, 16);
+    int groups = 0;
+    use_unit(kLayerNormUnit, dtype);
+    s = with_x(dtype, [&](auto t) {
+        return norm::launch_layer<decltype(t)>(true, a, vec ? kNormVec : shift ? kNormShift : kNormOdd, &groups, st);
+    });
+    return s != LATTICE_OK || !sums ? s : launch_norm_dw(a, groups, dw, db, st);
+}
+
 lattice_status lattice_selftest_bounded_wait(unsigned long long limit_ns, void* stream) {
     if (limit_ns < 1 || limit_ns > 1000000000ull) return LATTICE_ERR_INVALID_ARG;
     bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns);
@@ -754,6 +1166,9 @@ lattice_status lattice_get_device_status(void* stream) {
                  {status_norm_f32, unit_used(kNormUnit, LATTICE_F32)},
                  {status_norm_bf16, unit_used(kNormUnit, LATTICE_BF16)},
                  {status_norm_f16, unit_used(kNormUnit, LATTICE_F16)},
+                 {status_lnorm_f32, unit_used(kLayerNormUnit, LATTICE_F32)},
+                 {status_lnorm_bf16, unit_used(kLayerNormUnit, LATTICE_BF16)},
+                 {status_lnorm_f16, unit_used(kLayerNormUnit, LATTICE_F16)},
                  {status_gated_fwd_f32, unit_used(kGatedFwdUnit, LATTICE_F32)},
                  {status_gated_fwd_bf16, unit_used(kGatedFwdUnit, LATTICE_BF16)},
                  {status_gated_fwd_f16, unit_used(kGatedFwdUnit, LATTICE_F16)},

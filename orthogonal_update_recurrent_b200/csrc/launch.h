@@ -61,9 +61,24 @@ template <class XT> lattice_status launch_bwd(GatedArgs a, int form, bool vec, c
 // (or null): how many rows of weight gradients the backward pass leaves in the workspace
 namespace norm {
 template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
+// tu_lnorm_*.cu: layer norm (y: x or backward r; w_post, w_pre: its weight and bias)
+template <class XT> lattice_status launch_layer(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
 }  // namespace norm
 int norm_parts(long long N, int D);  // at most so many
 lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st);
+
+// conv_*.cu: short convolution, a unit per type of x (no waits in it, and so no status word). vec: rows
+// can be read in vectors of as many channels as a thread has
+namespace conv {
+template <class XT> lattice_status launch(const ConvArgs& a, int what, bool vec, cudaStream_t st);
+}  // namespace conv
+
+// sel_fwd_*.cu, sel_bwd_*.cu: selective scan, a unit per type of x (no waits either). S: states per lane
+namespace selective {
+template <class XT> lattice_status launch_fwd(const SelArgs& a, int S, cudaStream_t st);
+template <class XT> lattice_status launch_step(const SelArgs& a, cudaStream_t st);
+template <class XT> lattice_status launch_bwd(const SelArgs& a, cudaStream_t st);
+}  // namespace selective
 
 // each unit's device status word (read, and zeroed when set)
 cudaError_t status_simt_exact(unsigned int* v);
@@ -74,6 +89,9 @@ cudaError_t status_tc(unsigned int* v);
 cudaError_t status_norm_f32(unsigned int* v);
 cudaError_t status_norm_bf16(unsigned int* v);
 cudaError_t status_norm_f16(unsigned int* v);
+cudaError_t status_lnorm_f32(unsigned int* v);
+cudaError_t status_lnorm_bf16(unsigned int* v);
+cudaError_t status_lnorm_f16(unsigned int* v);
 cudaError_t status_gated_fwd_f32(unsigned int* v);
 cudaError_t status_gated_fwd_bf16(unsigned int* v);
 cudaError_t status_gated_fwd_f16(unsigned int* v);

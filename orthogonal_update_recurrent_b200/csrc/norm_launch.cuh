@@ -47,13 +47,11 @@ struct Split {
 // 16384, backward: 543 us with a cluster of 4 for every 4 SMs, 316 us with as many as are held.)
 constexpr int kMaxDevices = 16;
 
-template <class F, bool SUB, bool BWD>  // names the kernel: all of them have one type
-lattice_status launch(const NormArgs& a, int* groups, cudaStream_t st) {
-    constexpr int mode = F::MODE, bytes_per_thread = BWD ? 128 : 64;
-    void (*k)(NormArgs);
-    if constexpr (BWD) k = norm_bwd_kernel<F, SUB>;
-    else k = norm_fwd_kernel<F, SUB>;
-    const Split split(a.D, BWD, mode);
+// Name: a type that names the kernel (all of them have one type).
+template <class Name>
+lattice_status launch_kernel(void (*k)(NormArgs), bool bwd, int mode, int bytes_per_thread, const NormArgs& a, int* groups,
+                             cudaStream_t st) {
+    const Split split(a.D, bwd, mode);
     const int threads = split.threads, smem = threads * bytes_per_thread;
     cudaError_t e;
     if (smem > 40 * 1024) {  // 48 KB with the static arrays
@@ -93,6 +91,14 @@ lattice_status launch(const NormArgs& a, int* groups, cudaStream_t st) {
     if (groups) *groups = (int)n;
     e = cudaLaunchKernelEx(&cfg, k, a);
     return e == cudaSuccess ? LATTICE_OK : cuda_fail(e);
+}
+
+template <class F, bool SUB, bool BWD>
+struct Kernel;
+template <class F, bool SUB, bool BWD>
+lattice_status launch(const NormArgs& a, int* groups, cudaStream_t st) {
+    if constexpr (BWD) return launch_kernel<Kernel<F, SUB, true>>(norm_bwd_kernel<F, SUB>, true, F::MODE, 128, a, groups, st);
+    else return launch_kernel<Kernel<F, SUB, false>>(norm_fwd_kernel<F, SUB>, false, F::MODE, 64, a, groups, st);
 }
 
 template <class F, bool SUB>

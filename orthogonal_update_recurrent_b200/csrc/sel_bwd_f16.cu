@@ -1,0 +1,8 @@
+// sel_bwd_f16.cu -- the selective scan's backward kernels for x of this type.
+#include "selective_launch.cuh"
+
+namespace lattice {
+
+template lattice_status selective::launch_bwd<__half>(const SelArgs& a, cudaStream_t st);
+
+}  // namespace lattice

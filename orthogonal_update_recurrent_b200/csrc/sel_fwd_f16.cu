@@ -1,0 +1,9 @@
+// sel_fwd_f16.cu -- the selective scan's forward and single-token kernels for x of this type.
+#include "selective_launch.cuh"
+
+namespace lattice {
+
+template lattice_status selective::launch_fwd<__half>(const SelArgs& a, int S, cudaStream_t st);
+template lattice_status selective::launch_step<__half>(const SelArgs& a, cudaStream_t st);
+
+}  // namespace lattice

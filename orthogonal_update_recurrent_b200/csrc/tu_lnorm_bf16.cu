@@ -1,0 +1,11 @@
+// tu_lnorm_bf16.cu -- the layer norm's kernels for calls of this type.
+#include "common.cuh"
+#include "lnorm_launch.cuh"
+
+namespace lattice {
+
+template lattice_status norm::launch_layer<__nv_bfloat16>(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
+
+cudaError_t status_lnorm_bf16(unsigned int* v) { return read_clear_module_status(v); }
+
+}  // namespace lattice
