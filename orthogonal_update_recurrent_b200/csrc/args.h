@@ -144,8 +144,8 @@ struct NormArgs {
 
 // short_conv.cuh: short causal convolution
 constexpr int kConvMaxK = 8;
-constexpr int kConvVecBytes = 16, kConvBwdVec = 4;  // forward: bytes, backward: channels per thread
-constexpr int kConvRun = 32, kConvBwdRun = 64, kConvMaxRuns = 1024;
+constexpr int kConvVec = 4;  // channels per thread, where vectors of as many can be read
+constexpr int kConvRun = 64, kConvBwdRun = 64, kConvMaxRuns = 1024;
 constexpr int kConvMaxSize = 1 << 30;  // channels, and tokens
 constexpr int kConvFwd = 0, kConvBwd = 1, kConvStep = 2;
 
@@ -181,7 +181,7 @@ struct SelArgs {
     long long xbs, xts, dbs, dts, zbs, zts, bbs, bts, cbs, cts, ybs, yts;  // batch and token strides; y: dy's
     int B, T, E, N, G, Eg;                         // Eg = E/G channels per group of b and c
     int tiles, nseg, seg, nmarks;                  // channel tiles per group; segments of the time axis, their tokens
-    bool dt32, softplus, vec, vec_n;               // vec: pairs of channels, vec_n: four states in one access
+    bool dt32, softplus, vec, vec_n;               // vec: sel_width() channels (one token: four of b and c too), vec_n: four states in one access
 };
 
 // Lanes that share a channel's states, 4 states each (2 in the forward pass where that fills the device better).
@@ -190,5 +190,9 @@ LATTICE_HD inline int sel_padded(int N) {
     while (np < N) np *= 2;
     return np;
 }
+
+// Channels that a thread reads and writes at once where a channel's states take so many lanes: as many as give every thread of
+// a CTA some.
+LATTICE_HD constexpr int sel_width(int lanes) { return lanes <= 4 ? 4 : lanes == 8 ? 2 : 1; }
 
 }  // namespace lattice

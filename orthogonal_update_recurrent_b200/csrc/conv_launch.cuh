@@ -9,19 +9,18 @@ namespace conv {
 
 template <class XT, int K>
 lattice_status run(ConvArgs a, int what, bool vec, cudaStream_t st) {
-    constexpr int VF = kConvVecBytes / (int)sizeof(XT), VB = kConvBwdVec;
-    const int V = !vec ? 1 : what == kConvBwd ? VB : VF;
+    const int V = vec ? kConvVec : 1;
     const long long ctas = ((long long)a.B * a.runs * (a.C / V) + 255) / 256;
     if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
     const unsigned n = (unsigned)ctas;
     if (what == kConvFwd) {
-        if (vec) fwd_kernel<XT, K, VF><<<n, 256, 0, st>>>(a);
+        if (vec) fwd_kernel<XT, K, kConvVec><<<n, 256, 0, st>>>(a);
         else fwd_kernel<XT, K, 1><<<n, 256, 0, st>>>(a);
     } else if (what == kConvStep) {
-        if (vec) step_kernel<XT, K, VF><<<n, 256, 0, st>>>(a);
+        if (vec) step_kernel<XT, K, kConvVec><<<n, 256, 0, st>>>(a);
         else step_kernel<XT, K, 1><<<n, 256, 0, st>>>(a);
     } else {
-        if (vec) bwd_kernel<XT, K, VB><<<n, 256, 0, st>>>(a);
+        if (vec) bwd_kernel<XT, K, kConvVec><<<n, 256, 0, st>>>(a);
         else bwd_kernel<XT, K, 1><<<n, 256, 0, st>>>(a);
         if (a.parts) {
             const lattice_status s = launch_status();

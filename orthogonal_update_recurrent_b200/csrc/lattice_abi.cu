@@ -277,7 +277,7 @@ lattice_status check_conv(lattice_dtype x_dtype, lattice_dtype w_dtype, int B, i
 // Tokens of a thread's run: kConvRun, fewer (whole eights) where the device would not be filled, more where the
 // backward pass would leave more than kConvMaxRuns rows of weight gradients per sequence.
 int conv_run(long long B, int T, int C, bool bwd, bool vec) {
-    const long long per = vec ? bwd ? kConvBwdVec : 8 : 1, lanes = B * ((C + per - 1) / per), want = (long long)sm_count() * 1024;
+    const long long per = vec ? kConvVec : 1, lanes = B * ((C + per - 1) / per), want = (long long)sm_count() * 1024;
     long long run = bwd ? kConvBwdRun : kConvRun;
     while (run > 8 && lanes * ((T + run - 1) / run) < want) run /= 2;
     while (bwd && run < (1 << 29) && (T + run - 1) / run > kConvMaxRuns) run *= 2;
@@ -374,10 +374,17 @@ lattice_status sel_inputs(SelArgs& a, SelInputs& in, const void* x, lattice_dtyp
     a.B = B; a.T = T; a.E = E; a.N = N; a.G = G; a.Eg = E / G;
     a.nmarks = (int)((T + (long long)kSelMark - 1) / kSelMark);
     a.dt32 = dt_dtype == LATTICE_F32; a.softplus = softplus != 0;
-    a.vec = a.Eg % 2 == 0 && rows_vec(x, sx, B, T, xbs, xts, 2 * sx) && rows_vec(dt, sd, B, T, dbs, dts, 2 * sd) &&
-            (!z || rows_vec(z, sx, B, T, zbs, zts, 2 * sx));
     a.vec_n = N % 4 == 0 && aligned(A, 16);
     return LATTICE_OK;
+}
+// Whether rows of channels and their outputs can be read and written in vectors of V, a sequence of each within 2^31 bytes
+bool sel_vec(const SelArgs& a, size_t sx, int V) {
+    const size_t sd = a.dt32 ? 4 : sx, bx = V * sx, bd = V * sd;
+    for (long long ts : {a.xts, a.dts, a.zts, a.bts, a.cts, a.yts, (long long)a.E})
+        if ((__int128)a.T * ts * 4 > 0x7fffffffLL) return false;
+    return a.Eg % V == 0 && rows_vec(a.x, sx, a.B, a.T, a.xbs, a.xts, bx) && rows_vec(a.dt, sd, a.B, a.T, a.dbs, a.dts, bd) &&
+           (!a.z || rows_vec(a.z, sx, a.B, a.T, a.zbs, a.zts, bx)) && (!a.dy || rows_vec(a.dy, sx, a.B, a.T, a.ybs, a.yts, bx)) &&
+           aligned(a.y, bx) && aligned(a.dx, bx) && aligned(a.dz, bx) && aligned(a.ddt, bd);
 }
 void sel_place(SelArgs& a, const SelPlan& p, const SelSpace& s, void* workspace) {
     a.tiles = p.tiles; a.nseg = p.nseg; a.seg = p.seg;
@@ -871,8 +878,9 @@ lattice_status lattice_short_conv_fwd(const void* x, lattice_dtype x_dtype, long
     conv_args(a, x, x_dtype, x_batch_stride, x_token_stride, w, bias, w_dtype, state, lengths, B, T, C, K, act);
     a.y = y;
     a.state_out = K > 1 ? state_out : nullptr;
-    const bool vec = C % (kConvVecBytes / sx) == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, kConvVecBytes) && aligned(y, kConvVecBytes) &&
-                     aligned(state, kConvVecBytes) && aligned(state_out, kConvVecBytes);
+    const size_t v = kConvVec * sx;
+    const bool vec = C % kConvVec == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && aligned(y, v) && aligned(state, v) &&
+                     aligned(state_out, v) && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw);
     a.run = conv_run(B, T, C, false, vec);
     a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
     return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvFwd, vec, static_cast<cudaStream_t>(stream)); });
@@ -914,8 +922,8 @@ lattice_status lattice_short_conv_bwd(const void* x, lattice_dtype x_dtype, long
     a.dstate = K > 1 ? dstate : nullptr;
     a.dstate_out = K > 1 ? dstate_out : nullptr;
     a.parts = sums ? static_cast<float*>(workspace) : nullptr;
-    const size_t v = kConvBwdVec * sx;
-    const bool vec = C % kConvBwdVec == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && rows_vec(dy, sx, B, T, a.ybs, a.yts, v) &&
+    const size_t v = kConvVec * sx;
+    const bool vec = C % kConvVec == 0 && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw) && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && rows_vec(dy, sx, B, T, a.ybs, a.yts, v) &&
                      aligned(dx, v) && aligned(state, v) && aligned(dstate, v) && aligned(dstate_out, v);
     a.run = conv_run(B, T, C, true, vec);
     a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
@@ -940,8 +948,9 @@ lattice_status lattice_short_conv_step(const void* state, void* state_out, const
     conv_args(a, x, x_dtype, x_batch_stride, 0, w, bias, w_dtype, state, nullptr, B, 1, C, K, act);
     a.y = y; a.state_out = state_out;
     a.run = 8, a.runs = 1;
-    const bool vec = C % (kConvVecBytes / sx) == 0 && rows_vec(x, sx, B, 1, a.xbs, 0, kConvVecBytes) && aligned(y, kConvVecBytes) &&
-                     aligned(state, kConvVecBytes) && aligned(state_out, kConvVecBytes);
+    const size_t v = kConvVec * sx;
+    const bool vec = C % kConvVec == 0 && rows_vec(x, sx, B, 1, a.xbs, 0, v) && aligned(y, v) && aligned(state, v) &&
+                     aligned(state_out, v) && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw);
     return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvStep, vec, static_cast<cudaStream_t>(stream)); });
 }
 
@@ -982,7 +991,7 @@ lattice_status lattice_selective_scan_fwd(const void* x, lattice_dtype x_dtype, 
                          span(marks, marks ? lattice_selective_scan_marks_bytes(B, T, E, N) : 0), span(workspace, need)};
     if (clash(in.s, in.n, outs, 4, h0, h_out)) return LATTICE_ERR_INVALID_ARG;
     a.h0 = h0; a.h_out = h_out; a.y = y; a.marks = marks;
-    a.vec = a.vec && aligned(y, 2 * sx);
+    a.vec = sel_vec(a, sx, sel_width(sel_padded(N) / plan.S));
     a.vec_n = a.vec_n && aligned(h0, 16) && aligned(h_out, 16);
     sel_place(a, plan, space, workspace);
     return with_x(x_dtype, [&](auto t) { return selective::launch_fwd<decltype(t)>(a, plan.S, static_cast<cudaStream_t>(stream)); });
@@ -1027,7 +1036,7 @@ lattice_status lattice_selective_scan_bwd(const void* x, lattice_dtype x_dtype, 
     a.dy = dy; a.ybs = dy_batch_stride; a.yts = dy_token_stride;
     a.marks = const_cast<float*>(marks); a.dh_T = dh_T;
     a.dx = dx; a.ddt = ddt; a.dz = dz; a.dh0 = dh0; a.db = db; a.dc = dc; a.dA = dA; a.dskip = dskip; a.ddt_bias = ddt_bias;
-    a.vec = a.vec && rows_vec(dy, sx, B, T, a.ybs, a.yts, 2 * sx) && aligned(dx, 2 * sx) && aligned(ddt, 2 * sd) && aligned(dz, 2 * sx);
+    a.vec = sel_vec(a, sx, sel_width(sel_padded(N) / 4));
     a.vec_n = a.vec_n && aligned(dh_T, 16) && aligned(dh0, 16);
     sel_place(a, plan, space, workspace);
     return with_x(x_dtype, [&](auto t) { return selective::launch_bwd<decltype(t)>(a, static_cast<cudaStream_t>(stream)); });
@@ -1052,6 +1061,7 @@ lattice_status lattice_selective_step(const float* h, float* h_out, const void* 
     if (clash(in.s, in.n, outs, 2, h, h_out)) return LATTICE_ERR_INVALID_ARG;
     a.h0 = h; a.h_out = h_out; a.y = y;
     a.vec_n = a.vec_n && aligned(h, 16) && aligned(h_out, 16);
+    a.vec = a.vec_n && rows_vec(b, sx, B, 1, b_batch_stride, 0, 4 * sx) && rows_vec(c, sx, B, 1, c_batch_stride, 0, 4 * sx);
     return with_x(x_dtype, [&](auto t) { return selective::launch_step<decltype(t)>(a, static_cast<cudaStream_t>(stream)); });
 }
 

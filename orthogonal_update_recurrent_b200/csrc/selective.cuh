@@ -45,99 +45,163 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-// Two neighbouring channels as read.
-template <class T>
-struct Pair {
-    uint32_t w[sizeof(T) / 2];
+// V neighbouring channels (1, 2 or 4) as read, of type T
+template <class T, int V>
+struct Raw {
+    static constexpr int W = sizeof(T) * V < 4 ? 1 : sizeof(T) * V / 4;
+    uint32_t w[W];
 };
-template <class T>
-__device__ __forceinline__ Pair<T> load2(const void* base, long long i, int n, bool vec) {
-    Pair<T> r;
-    if constexpr (sizeof(T) == 4) {
-        const uint32_t* p = static_cast<const uint32_t*>(base) + i;
-        if (vec && n == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            r.w[0] = v.x, r.w[1] = v.y;
-        } else {
-            r.w[0] = n > 0 ? p[0] : 0u;
-            r.w[1] = n > 1 ? p[1] : 0u;
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> none() {
+    Raw<T, V> r;
+#pragma unroll
+    for (int k = 0; k < Raw<T, V>::W; ++k) r.w[k] = 0u;
+    return r;
+}
+// n of them at p. VEC: n is 0 or V, and they can be read at once
+template <bool VEC, class T, int V>
+__device__ __forceinline__ Raw<T, V> load(const T* p, int n) {
+    Raw<T, V> r = none<T, V>();
+    if constexpr (VEC && V > 1) {
+        constexpr int W = Raw<T, V>::W;
+        if (n > 0) {
+            if constexpr (W == 4) {
+                const uint4 t = *reinterpret_cast<const uint4*>(p);
+                r.w[0] = t.x, r.w[W / 4] = t.y, r.w[W / 2] = t.z, r.w[W - 1] = t.w;
+            } else if constexpr (W == 2) {
+                const uint2 t = *reinterpret_cast<const uint2*>(p);
+                r.w[0] = t.x, r.w[W - 1] = t.y;
+            } else {
+                r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+            }
         }
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + i;
-        if (vec && n == 2) {
-            r.w[0] = *reinterpret_cast<const uint32_t*>(p);
-        } else {
-            r.w[0] = n > 0 ? p[0] : 0u;
-            if (n > 1) r.w[0] |= (uint32_t)p[1] << 16;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (v >= n) continue;
+            if constexpr (sizeof(T) == 4) r.w[v] = reinterpret_cast<const uint32_t*>(p)[v];
+            else r.w[v / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[v] << (16 * (v & 1));
         }
     }
     return r;
 }
-template <class T>
-__device__ __forceinline__ F2 value2(const Pair<T>& r) {
-    if constexpr (sizeof(T) == 4) {
-        return f2(__uint_as_float(r.w[0]), __uint_as_float(r.w[1]));
-    } else if constexpr (std::is_same<T, __half>::value) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r.w[0]));
-        return f2(v.x, v.y);
-    } else {
-        return f2(__uint_as_float(r.w[0] << 16), __uint_as_float(r.w[0] & 0xffff0000u));
-    }
-}
-template <class T>
-__device__ __forceinline__ void store2(void* base, long long i, F2 v, int n, bool vec) {
-    float a, b;
-    parts(v, a, b);
-    T* p = static_cast<T*>(base) + i;
-    if (vec && n == 2) {
+// pairs of their values; a single one has 0 beside it
+template <class T, int V>
+__device__ __forceinline__ void values(const Raw<T, V>& r, F2* f) {
+#pragma unroll
+    for (int k = 0; k < (V + 1) / 2; ++k) {
         if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float2*>(p) = make_float2(a, b);
+            f[k] = f2(__uint_as_float(r.w[2 * k]), V > 1 ? __uint_as_float(r.w[V > 1 ? 2 * k + 1 : 0]) : 0.f);
         } else if constexpr (std::is_same<T, __half>::value) {
-            *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r.w[k]));
+            f[k] = f2(v.x, v.y);
         } else {
-            *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+            f[k] = f2(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xffff0000u));
         }
-        return;
     }
-    if (n > 0) put(p, a);
-    if (n > 1) put(p + 1, b);
 }
-// dt: fp32 or XT
-template <class XT>
-__device__ __forceinline__ Pair<float> load_dt(const SelArgs& A, long long i, int n) {
-    if (sizeof(XT) == 4 || A.dt32) return load2<float>(A.dt, i, n, A.vec);
-    const Pair<XT> p = load2<XT>(A.dt, i, n, A.vec);
-    Pair<float> r;
-    r.w[0] = p.w[0], r.w[1] = 0u;
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 t = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&t);
+    } else {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&t);
+    }
+}
+template <bool VEC, class T, int V>
+__device__ __forceinline__ void store(T* p, const F2* f, int n) {
+    float v[V + 1];
+#pragma unroll
+    for (int k = 0; k < (V + 1) / 2; ++k) parts(f[k], v[2 * k], v[2 * k + 1]);
+    if constexpr (VEC && V > 1) {
+        if (n <= 0) return;
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[V - 2], v[V - 1]);
+            else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[V - 1]);
+        } else if constexpr (V == 4) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[V - 2], v[V - 1]));
+        } else {
+            *reinterpret_cast<uint32_t*>(p) = pack2<T>(v[0], v[1]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k < n) put(p + k, v[k]);
+    }
+}
+// Token t's entries of an array whose tokens are `ts` elements apart, from p on. VEC calls' arrays are less than 2^31 bytes
+// from the first to the last token, so that 32-bit offsets do.
+template <bool VEC, class T>
+__device__ __forceinline__ T* token(T* p, int t, long long ts) {
+    if constexpr (VEC) return reinterpret_cast<T*>(reinterpret_cast<unsigned long long>(p) + (unsigned)t * ((unsigned)ts * (unsigned)sizeof(T)));
+    else return p + t * ts;
+}
+// V channels of dt, which are fp32 or XT
+template <bool VEC, class XT, int V>
+__device__ __forceinline__ Raw<float, V> load_dt(const SelArgs& A, const void* p, int t, int n) {
+    if (sizeof(XT) == 4 || A.dt32) return load<VEC, float, V>(token<VEC>(static_cast<const float*>(p), t, A.dts), n);
+    const Raw<XT, V> v = load<VEC, XT, V>(token<VEC>(static_cast<const XT*>(p), t, A.dts), n);
+    Raw<float, V> r = none<float, V>();
+#pragma unroll
+    for (int k = 0; k < Raw<XT, V>::W; ++k) r.w[k] = v.w[k];
     return r;
 }
-template <class XT>
-__device__ __forceinline__ F2 value_dt(const SelArgs& A, const Pair<float>& r) {
+template <class XT, int V>
+__device__ __forceinline__ void values_dt(const SelArgs& A, const Raw<float, V>& r, F2* f) {
     if constexpr (sizeof(XT) == 2) {
         if (!A.dt32) {
-            Pair<XT> p;
-            p.w[0] = r.w[0];
-            return value2(p);
+            Raw<XT, V> p;
+#pragma unroll
+            for (int k = 0; k < Raw<XT, V>::W; ++k) p.w[k] = r.w[k];
+            values<XT, V>(p, f);
+            return;
         }
     }
-    return value2(r);
+    values<float, V>(r, f);
+}
+// where dt's entries of channel c of sequence b begin
+template <class XT>
+__device__ __forceinline__ const void* dt_at(const SelArgs& A, int b, int c) {
+    const long long i = b * A.dbs + c;
+    return sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(static_cast<const float*>(A.dt) + i)
+                                     : static_cast<const void*>(static_cast<const XT*>(A.dt) + i);
 }
 
 // exp(dt A) of two states, t = dt A log2(e). The approximate exponential's errors near 1 are not centred (mean
 // -2e-8 for t in [-1/2, -2^-8], measured), and a retention of R steps multiplies a mean error by R.
-// So -0.36 <= t <= 0 takes 1 + t q(t) instead, a minimax polynomial (1.6e-8, and 0 at t = 0) whose
-// last step rounds to nearest; below, R is at most 4. The integer comparison holds for negative t alone.
-constexpr float kNear = -0.36f;
-__device__ __forceinline__ F2 decay(F2 t) {
-    F2 p = fma2(f2(0.008524463512003422f), t, f2(0.055181119590997696f));
-    p = fma2(p, t, f2(0.24018850922584534f));
-    p = fma2(p, t, f2(0.6931458115577698f));
-    p = fma2(p, t, f2(1.f));
-    float t0, t1, p0, p1;
-    parts(t, t0, t1), parts(p, p0, p1);
-    const float e0 = ex2(t0), e1 = ex2(t1);
+// So -0.09 <= t <= 0 takes 1 + t q(t) instead, a minimax polynomial (6e-9, and 0 at t = 0) whose
+// last step rounds to nearest; below, R is at most 16. The integer comparison holds for negative t alone.
+constexpr float kNear = -0.09f;
+// of M pairs, step by step, so that no step waits for the one before it
+template <int M>
+__device__ __forceinline__ void decay(F2* t) {
+    F2 p[M];
+    float e[2 * M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) p[i] = fma2(f2(0.053866468369960785f), t[i], f2(0.24014140665531158f));
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        float t0, t1;
+        parts(t[i], t0, t1);
+        e[2 * i] = ex2(t0), e[2 * i + 1] = ex2(t1);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) p[i] = fma2(p[i], t[i], f2(0.6931459307670593f));
+#pragma unroll
+    for (int i = 0; i < M; ++i) p[i] = fma2(p[i], t[i], f2(1.f));
     const int near = __float_as_int(kNear);
-    return f2(__float_as_int(t0) <= near ? p0 : e0, __float_as_int(t1) <= near ? p1 : e1);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        float t0, t1, p0, p1;
+        parts(t[i], t0, t1), parts(p[i], p0, p1);
+        t[i] = f2(__float_as_int(t0) <= near ? p0 : e[2 * i], __float_as_int(t1) <= near ? p1 : e[2 * i + 1]);
+    }
+}
+__device__ __forceinline__ F2 decay(F2 t) {
+    decay<1>(&t);
+    return t;
 }
 
 // softplus(v) = max(v, 0) + log(1 + t), t = exp(-|v|), and its slope 1/(1 + exp(-v)). log(1 + t)/t is a
@@ -165,23 +229,24 @@ __device__ __forceinline__ F2 softplus(F2 v, F2* slope) {
 __device__ __forceinline__ F2 sigmoid(F2 z) {
     return each(each(mul2(z, f2(-kLog2e)), [](float n) { return 1.f + ex2(n); }), rcp);
 }
-// dt of two channels from what was read
-template <class XT>
-__device__ __forceinline__ F2 step_size(const SelArgs& A, const Pair<float>& raw, F2 bias, F2* slope) {
-    const F2 v = add2(value_dt<XT>(A, raw), bias);
-    if (A.softplus) return softplus(v, slope);
-    if (slope) *slope = f2(1.f);
-    return v;
+// dt of V channels from what was read
+template <class XT, int V>
+__device__ __forceinline__ void step_sizes(const SelArgs& A, const Raw<float, V>& raw, const F2* bias, F2* dt, F2* slope) {
+    values_dt<XT, V>(A, raw, dt);
+#pragma unroll
+    for (int k = 0; k < (V + 1) / 2; ++k) {
+        dt[k] = add2(dt[k], bias[k]);
+        if (A.softplus) dt[k] = softplus(dt[k], slope ? slope + k : nullptr);
+        else if (slope) slope[k] = f2(1.f);
+    }
 }
 __device__ __forceinline__ F2 low(ulonglong2 v) { return F2{v.x}; }
 __device__ __forceinline__ F2 high(ulonglong2 v) { return F2{v.y}; }
-__device__ __forceinline__ ulonglong2 both(F2 a, F2 b) { return make_ulonglong2(a.v, b.v); }
 __device__ __forceinline__ float total(F2 a) {
     float x, y;
     parts(a, x, y);
     return x + y;
 }
-__device__ __forceinline__ float total(F2 a, F2 b) { return total(add2(a, b)); }
 
 // v0 and v1 summed over two lanes that differ in `bit`: the lane without it keeps v0's sum.
 __device__ __forceinline__ float halve(float v0, float v1, int lane, int bit) {
@@ -190,14 +255,16 @@ __device__ __forceinline__ float halve(float v0, float v1, int lane, int bit) {
     return keep + __shfl_xor_sync(ALL, give, bit);
 }
 
-// Where a CTA works: a tile of CT channels of one group, one sequence, one segment of the time axis.
+// Where a CTA works: a tile of CT channels of one group, one sequence, one segment of the time axis. Its threads have two
+// tasks: the states of one channel on L lanes each, and V channels of the tile's tokens each, PI of them.
 template <int L>
 struct Place {
-    static constexpr int CH = 32 / L, CT = NW * CH, PAIRS = CT / 2, ROWS = NT / PAIRS;
-    static constexpr int PI = (TT + ROWS - 1) / ROWS;  // pairs per thread of a tile of tokens
-    static constexpr int CTP = CT + 8;                 // floats of a row of sums, rows apart in the banks
-    int b, s, ct, g, c0, cend, t0, t1, te;             // tokens t0..t1, te: up to the sequence's end
-    int lane, gl, cl, c, ch, cp, row;                  // states' lane, channel; the pair and first row of the thread
+    static constexpr int CH = 32 / L, CT = NW * CH, V = sel_width(L), P = (V + 1) / 2;
+    static constexpr int QUADS = CT / V, ROWS = NT / QUADS, PI = (TT + ROWS - 1) / ROWS;
+    static constexpr int CTP = CT + CH;              // floats from lane to lane of the sums over n: lanes apart in the banks
+    static constexpr int DW = CT + (V > 1 ? 2 * V : 0);  // a token's entries of dtu
+    int b, s, ct, g, c0, cend, t0, t1, te;           // tokens t0..t1, te: up to the sequence's end
+    int lane, gl, cl, c, ch, first, row;             // states' lane, channel; the V channels' first in the tile, and first row
     bool live;
     __device__ __forceinline__ Place(const SelArgs& A) {
         const int nt = A.G * A.tiles;
@@ -209,12 +276,62 @@ struct Place {
         t0 = s * A.seg, t1 = min(A.T, t0 + A.seg), te = max(t0, min(t1, len));
         lane = threadIdx.x & 31, gl = lane % L, cl = lane / L, c = (threadIdx.x >> 5) * CH + cl, ch = c0 + c;
         live = ch < cend;
-        cp = threadIdx.x % PAIRS, row = threadIdx.x / PAIRS;
+        first = threadIdx.x % QUADS * V, row = threadIdx.x / QUADS;
     }
-    __device__ __forceinline__ int pair() const { return c0 + 2 * cp; }
-    __device__ __forceinline__ int width() const { return min(2, max(0, cend - pair())); }  // channels of the pair
-    __device__ __forceinline__ long long seq() const { return b; }
+    __device__ __forceinline__ int column() const { return c0 + first; }
+    __device__ __forceinline__ int width() const { return min(V, max(0, cend - column())); }  // of the V channels, inside the group
+    // where channel c of a token stands in dtu: the V of a thread apart, so that neither writes nor reads meet in a bank
+    static __device__ __forceinline__ int entry(int c) { return c % V * (QUADS + (V > 1 ? 2 : 0)) + c / V; }
+    // the thread's entries: (d, d, u, u) of every channel
+    __device__ __forceinline__ void write(ulonglong2* dtu, int r, const F2* d, const F2* u) const {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float d0, d1, u0, u1;
+            parts(d[k / 2], d0, d1), parts(u[k / 2], u0, u1);
+            dtu[r * DW + k * (QUADS + (V > 1 ? 2 : 0)) + first / V] = make_ulonglong2(f2(k & 1 ? d1 : d0).v, f2(k & 1 ? u1 : u0).v);
+        }
+    }
 };
+// V floats of the thread's own channels in shared memory, [token][CT]
+template <int V>
+__device__ __forceinline__ void own_write(float* p, const F2* f) {
+    if constexpr (V == 4) *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(f[0].v, f[1].v);
+    else if constexpr (V == 2) *reinterpret_cast<unsigned long long*>(p) = f[0].v;
+    else {
+        float a, b;
+        parts(f[0], a, b);
+        *p = a;
+    }
+}
+template <int V>
+__device__ __forceinline__ void own_read(const float* p, F2* f) {
+    if constexpr (V == 4) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p);
+        f[0].v = t.x, f[1].v = t.y;
+    } else if constexpr (V == 2) {
+        f[0].v = *reinterpret_cast<const unsigned long long*>(p);
+    } else {
+        f[0] = f2(*p, 0.f);
+    }
+}
+// The sums over a channel's L lanes: [L][CTP] of a token, the thread's V channels
+template <int L>
+__device__ __forceinline__ void lane_sums(const float* p, F2* f) {
+    using P = Place<L>;
+    own_read<P::V>(p, f);
+#pragma unroll
+    for (int l = 1; l < L; ++l) {
+        F2 t[P::P];
+        own_read<P::V>(p + l * P::CTP, t);
+#pragma unroll
+        for (int k = 0; k < P::P; ++k) f[k] = add2(f[k], t[k]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_columns(const float* p, int at, int n, F2* f) {
+    const Raw<float, V> r = load<false, float, V>(p + at, p ? n : 0);
+    values<float, V>(r, f);
+}
 
 // S states of a channel, of p[N]; 0 past N
 template <int S>
@@ -262,40 +379,67 @@ __device__ __forceinline__ void read_vec(const float* p, F2* v) {
         v[0].v = *reinterpret_cast<const unsigned long long*>(p);
     }
 }
+// The decays and the writes u b of M tokens, from shared memory: du (dt, dt, u, u) and v (b) with their tokens' strides
+template <int M, int S>
+__device__ __forceinline__ void decays(const ulonglong2* du, int dstride, const float* v, int vstride, const F2* A2, F2 (*a)[S / 2],
+                                       F2 (*u)[S / 2]) {
+    constexpr int H = S / 2;
+    F2 t[M * H];
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        const ulonglong2 d = du[j * dstride];
+        read_vec<S>(v + j * vstride, u[j]);
+#pragma unroll
+        for (int k = 0; k < H; ++k) t[j * H + k] = mul2(low(d), A2[k]), u[j][k] = mul2(high(d), u[j][k]);
+    }
+    decay<M * H>(t);
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+#pragma unroll
+        for (int k = 0; k < H; ++k) a[j][k] = t[j * H + k];
+}
+// Four states' values of b or c of one token. VEC: N is a multiple of four and they can be read at once
+template <bool VEC, class XT>
+__device__ __forceinline__ void load_row(const XT* p, int n0, int N, float* v) {
+    F2 f[2];
+    values<XT, 4>(load<VEC, XT, 4>(p + n0, N - n0), f);
+    parts(f[0], v[0], v[1]), parts(f[1], v[2], v[3]);
+}
 // A tile's rows of b or c: NB elements of [TT][NP] per thread.
 template <int NP>
 struct Rows {
     static constexpr int NB = (TT * NP + NT - 1) / NT;
 };
-template <class XT, int NP>
-__device__ __forceinline__ void fetch_rows(const void* base, long long at, long long ts, int tb, int te, int N, XT* r) {
+template <bool VEC, class XT, int NP>
+__device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, int te, int N, XT* r) {
 #pragma unroll
     for (int k = 0; k < Rows<NP>::NB; ++k) {
         const int i = threadIdx.x + k * NT, t = i / NP, n = i % NP;
-        XT v = XT();
-        if (t < TT && tb + t < te && n < N) v = static_cast<const XT*>(base)[at + (tb + t) * ts + n];
-        r[k] = v;
+        r[k] = XT();
+        if ((TT * NP % NT == 0 || t < TT) && tb + t < te && n < N) r[k] = token<VEC>(p + n, tb + t, ts)[0];
     }
 }
 
 // ---- forward: all tokens of a segment, from the state that enters it
+// Between two barriers a CTA finishes the tile before, prepares the next one (in the other buffers) and works on its own.
 template <class XT, int L, int S>
 struct FwdShared {
-    static constexpr int NP = L * S, CT = Place<L>::CT, CTP = Place<L>::CTP;
-    ulonglong2 dtu[TT * CT];  // (dt, dt, u, u), u = dt x
-    float b[TT * NP], c[TT * NP];
-    float y[TT * CTP];
+    static constexpr int NP = L * S, CT = Place<L>::CT;
+    ulonglong2 dtu[2][TT * Place<L>::DW];        // (dt, dt, u, u), u = dt x
+    float gate[2][TT * CT], skip[2][TT * CT];    // silu(z) and skip x, for the thread that wrote them
+    float b[2][TT * NP], c[2][TT * NP];
+    float y[2][TT * L * Place<L>::CTP];          // the lanes' parts of the sums over n
 };
 
-template <class XT, int L, int S>
+template <class XT, int L, int S, bool VEC>
 __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
     using P = Place<L>;
-    constexpr int NP = L * S, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, H = S / 2;
+    constexpr int NP = L * S, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, H = S / 2, V = P::V, Q = P::P;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     FwdShared<XT, L, S>& sh = *reinterpret_cast<FwdShared<XT, L, S>*>(raw_shared);
     const P p(A);
     const int n0 = p.gl * S, pw = p.width();
-    F2 h[H], A2[H], bias = f2(0.f), skip = f2(0.f);
+    F2 h[H], A2[H], bias[Q], skip[Q];
     {
         float v[S] = {};
         if (p.live) load_states<S>(A.A + (long long)p.ch * A.N, n0, A.N, A.vec_n, v);
@@ -309,105 +453,122 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
         for (int k = 0; k < S; ++k) v[k] = 0.f;
         if (from && p.live) load_states<S>(from + (long long)p.ch * A.N, n0, A.N, A.vec_n, v);
         pack<S>(v, h);
-        if (A.dt_bias) bias = value2(load2<float>(A.dt_bias, p.pair(), pw, false));
-        if (A.skip) skip = value2(load2<float>(A.skip, p.pair(), pw, false));
+        load_columns<V>(A.dt_bias, p.column(), pw, bias);
+        load_columns<V>(A.skip, p.column(), pw, skip);
     }
-    const long long xat = p.b * A.xbs + p.pair(), dat = p.b * A.dbs + p.pair(), zat = p.b * A.zbs + p.pair(),
-                    bat = p.b * A.bbs + p.g * A.N, cat = p.b * A.cbs + p.g * A.N, yat = (long long)p.b * A.T * A.E + p.pair();
-    Pair<XT> rx[PI], rz[PI], kx[PI], kz[PI];
-    Pair<float> rd[PI];
+    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs + p.column(), *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
+             *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N, *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
+    const void* dp = dt_at<XT>(A, p.b, p.column());
+    XT* yp = static_cast<XT*>(A.y) + (long long)p.b * A.T * A.E + p.column();
+    Raw<XT, V> rx[PI], rz[PI];
+    Raw<float, V> rd[PI];
     XT rb[NB], rc[NB];
     auto fetch = [&](int tb) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load2<XT>(A.x, xat + t * A.xts, n, A.vec);
-            rd[k] = load_dt<XT>(A, dat + t * A.dts, n);
-            if (A.z) rz[k] = load2<XT>(A.z, zat + t * A.zts, n, A.vec);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, A.xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
+            if (A.z) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<XT, NP>(A.b, bat, A.bts, tb, p.te, A.N, rb);
-        fetch_rows<XT, NP>(A.c, cat, A.cts, tb, p.te, A.N, rc);
+        fetch_rows<VEC, XT, NP>(bp, A.bts, tb, p.te, A.N, rb);
+        fetch_rows<VEC, XT, NP>(cp, A.cts, tb, p.te, A.N, rc);
     };
-    auto finish = [&](int tb) {  // the tile's outputs
-#pragma unroll
-        for (int k = 0; k < PI; ++k) {
-            const int r = p.row + k * P::ROWS, t = tb + r;
-            if (r >= TT || t >= p.te) continue;
-            F2 y = *reinterpret_cast<const F2*>(sh.y + r * CTP + 2 * p.cp);
-            y = fma2(skip, value2(kx[k]), y);
-            if (A.z) {
-                const F2 z = value2(kz[k]);
-                y = mul2(y, mul2(z, sigmoid(z)));
-            }
-            store2<XT>(A.y, yat + (long long)t * A.E, y, pw, A.vec);
-        }
-    };
-    if (p.t0 < p.te) fetch(p.t0);
-    for (int tb = p.t0; tb < p.te; tb += TT) {
-        __syncthreads();
-        if (tb > p.t0 && A.y) finish(tb - TT);
+    auto prepare = [&](int tb, int buf) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS;
-            if (r >= TT) continue;
-            F2 dt = f2(0.f), u = f2(0.f);
-            if (tb + r < p.te) {
-                dt = step_size<XT>(A, rd[k], bias, nullptr);
-                u = mul2(dt, value2(rx[k]));
+            if (TT % P::ROWS != 0 && r >= TT) continue;
+            F2 dt[Q], x[Q], u[Q];
+            step_sizes<XT, V>(A, rd[k], bias, dt, nullptr);
+            values<XT, V>(rx[k], x);
+            const bool in = tb + r < p.te;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (!in) dt[q] = f2(0.f);
+                u[q] = mul2(dt[q], x[q]);  // rows behind the end were read as 0
             }
-            kx[k] = rx[k], kz[k] = rz[k];
-            float d0, d1, u0, u1;
-            parts(dt, d0, d1), parts(u, u0, u1);
-            sh.dtu[r * CT + 2 * p.cp] = both(f2(d0), f2(u0));
-            sh.dtu[r * CT + 2 * p.cp + 1] = both(f2(d1), f2(u1));
+            p.write(sh.dtu[buf], r, dt, u);
+            if (!A.y) continue;
+            if (A.skip) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) x[q] = mul2(x[q], skip[q]);
+                own_write<V>(sh.skip[buf] + r * CT + p.first, x);
+            }
+            if (A.z) {
+                values<XT, V>(rz[k], x);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) x[q] = mul2(x[q], sigmoid(x[q]));
+                own_write<V>(sh.gate[buf] + r * CT + p.first, x);
+            }
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             const int i = threadIdx.x + k * NT;
-            if (i < TT * NP) sh.b[i] = to_f(rb[k]), sh.c[i] = to_f(rc[k]);
+            if (i < TT * NP) sh.b[buf][i] = to_f(rb[k]), sh.c[buf][i] = to_f(rc[k]);
         }
-        if (tb + TT < p.te) fetch(tb + TT);
-        __syncthreads();
+    };
+    auto finish = [&](int tb, int buf) {  // the tile's outputs
+#pragma unroll
+        for (int k = 0; k < PI; ++k) {
+            const int r = p.row + k * P::ROWS, t = tb + r;
+            if (r >= TT || t >= p.te) continue;
+            F2 y[Q], f[Q];
+            lane_sums<L>(sh.y[buf] + r * L * CTP + p.first, y);
+            if (A.skip) {
+                own_read<V>(sh.skip[buf] + r * CT + p.first, f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) y[q] = add2(y[q], f[q]);
+            }
+            if (A.z) {
+                own_read<V>(sh.gate[buf] + r * CT + p.first, f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) y[q] = mul2(y[q], f[q]);
+            }
+            store<VEC, XT, V>(token<VEC>(yp, t, A.E), y, pw);
+        }
+    };
+    const int tiles = (p.te - p.t0 + TT - 1) / TT, entry = P::entry(p.c);
+    float* mark = A.marks + (((long long)p.b * A.nmarks + p.t0 / kSelMark) * A.E + p.ch) * A.N;
+    const bool marks = A.marks && p.live;
+    if (tiles > 0) fetch(p.t0), prepare(p.t0, 0);
+    if (tiles > 1) fetch(p.t0 + TT);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int tb = p.t0 + i * TT, buf = i & 1;
+        if (i > 0 && A.y) finish(tb - TT, buf ^ 1);
+        if (i + 1 < tiles) prepare(tb + TT, buf ^ 1);
+        if (i + 2 < tiles) fetch(tb + 2 * TT);
+        float* ys = sh.y[buf] + p.gl * CTP + p.c;
 #pragma unroll
         for (int q = 0; q < TT; q += 4) {
-            if (q % kSelMark == 0 && A.marks && tb + q < p.te && p.live) {
+            if (q % kSelMark == 0 && marks && tb + q < p.te) {
                 float v[S];
                 unpack<S>(h, v);
-                store_states<S>(A.marks + (((long long)p.b * A.nmarks + (tb + q) / kSelMark) * A.E + p.ch) * A.N, n0, A.N, A.vec_n, v);
+                store_states<S>(mark, n0, A.N, A.vec_n, v);
+                mark += (long long)A.E * A.N;
             }
-            float y[4];
+            F2 a[4][H], u[4][H];
+            decays<4, S>(sh.dtu[buf] + q * P::DW + entry, P::DW, sh.b[buf] + q * NP + n0, NP, A2, a, u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int t = q + j;
-                const ulonglong2 du = sh.dtu[t * CT + p.c];
-                F2 bv[H], cv[H];
-                read_vec<S>(sh.b + t * NP + n0, bv);
-                read_vec<S>(sh.c + t * NP + n0, cv);
-                F2 yy;
+                F2 cv[H], yy;
+                read_vec<S>(sh.c[buf] + (q + j) * NP + n0, cv);
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
-                    h[k] = fma2(decay(mul2(low(du), A2[k])), h[k], mul2(high(du), bv[k]));
+                    h[k] = fma2(a[j][k], h[k], u[j][k]);
                     yy = k ? fma2(h[k], cv[k], yy) : mul2(h[k], cv[k]);
                 }
-                y[j] = total(yy);
-            }
-            const float y01 = halve(y[0], y[1], p.lane, 1), y23 = halve(y[2], y[3], p.lane, 1);
-            if constexpr (L == 2) {
-                sh.y[(q + p.gl) * CTP + p.c] = y01;
-                sh.y[(q + 2 + p.gl) * CTP + p.c] = y23;
-            } else {
-                float v = halve(y01, y23, p.lane, 2);
-#pragma unroll
-                for (int o = 4; o < L; o *= 2) v += __shfl_xor_sync(ALL, v, o);
-                if (p.gl < 4) sh.y[(q + p.gl) * CTP + p.c] = v;
+                ys[(q + j) * L * CTP] = total(yy);
             }
         }
+        __syncthreads();
     }
     if (A.y) {
-        __syncthreads();
-        if (p.t0 < p.te) finish((p.te - 1 - p.t0) / TT * TT + p.t0);
+        if (tiles > 0) finish(p.t0 + (tiles - 1) * TT, (tiles - 1) & 1);
+        const F2 zero[Q] = {};
         for (int t = p.te + p.row; t < p.t1; t += P::ROWS)  // behind the sequence's end
-            store2<XT>(A.y, yat + (long long)t * A.E, f2(0.f), pw, A.vec);
+            store<VEC, XT, V>(token<VEC>(yp, t, A.E), zero, pw);
     }
     if (A.h_out && p.s == A.nseg - 1 && p.live) {
         float v[S];
@@ -419,21 +580,21 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
 // ---- a segment's state from 0 at its end (REV: the cotangent from 0 at its start) and the sum of its dt
 template <class XT, int L, int S>
 struct SegShared {
-    static constexpr int NP = L * S, CT = Place<L>::CT;
-    ulonglong2 dtu[TT * CT];  // (dt, dt, w, w), w = dt x or dy silu(z)
-    float v[TT * NP];         // b or c
-    float2 sum[NT];
+    static constexpr int NP = L * S;
+    ulonglong2 dtu[2][TT * Place<L>::DW];  // (dt, dt, w, w), w = dt x or dy silu(z)
+    float v[2][TT * NP];                   // b or c
+    float sum[NT * 4];
 };
 
-template <class XT, int L, int S, bool REV>
+template <class XT, int L, int S, bool REV, bool VEC>
 __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
     using P = Place<L>;
-    constexpr int NP = L * S, CT = P::CT, PI = P::PI, NB = Rows<NP>::NB, H = S / 2;
+    constexpr int NP = L * S, PI = P::PI, NB = Rows<NP>::NB, H = S / 2, V = P::V, Q = P::P;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     SegShared<XT, L, S>& sh = *reinterpret_cast<SegShared<XT, L, S>*>(raw_shared);
     const P p(A);
     const int n0 = p.gl * S, pw = p.width();
-    F2 h[H], A2[H], bias = f2(0.f), sum = f2(0.f);
+    F2 h[H], A2[H], bias[Q], sum[Q];
     {
         float v[S] = {};
         if (p.live) load_states<S>(A.A + (long long)p.ch * A.N, n0, A.N, A.vec_n, v);
@@ -442,72 +603,77 @@ __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
         pack<S>(v, A2);
 #pragma unroll
         for (int k = 0; k < H; ++k) h[k] = f2(0.f);
-        if (A.dt_bias) bias = value2(load2<float>(A.dt_bias, p.pair(), pw, false));
+        load_columns<V>(A.dt_bias, p.column(), pw, bias);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) sum[q] = f2(0.f);
     }
-    const void *src = REV ? A.dy : A.x, *vec = REV ? A.c : A.b;
-    const long long sts = REV ? A.yts : A.xts, sat = p.b * (REV ? A.ybs : A.xbs) + p.pair(), dat = p.b * A.dbs + p.pair(),
-                    zat = p.b * A.zbs + p.pair(), vts = REV ? A.cts : A.bts, vat = p.b * (REV ? A.cbs : A.bbs) + p.g * A.N;
+    const XT *xp = static_cast<const XT*>(REV ? A.dy : A.x) + p.b * (REV ? A.ybs : A.xbs) + p.column(),
+             *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
+             *vp = static_cast<const XT*>(REV ? A.c : A.b) + p.b * (REV ? A.cbs : A.bbs) + p.g * A.N;
+    const void* dp = dt_at<XT>(A, p.b, p.column());
+    const long long xts = REV ? A.yts : A.xts, vts = REV ? A.cts : A.bts;
     const bool gated = REV && A.z;
-    Pair<XT> rx[PI], rz[PI];
-    Pair<float> rd[PI];
+    Raw<XT, V> rx[PI], rz[PI];
+    Raw<float, V> rd[PI];
     XT rv[NB];
     auto fetch = [&](int tb) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load2<XT>(src, sat + t * sts, n, A.vec);
-            rd[k] = load_dt<XT>(A, dat + t * A.dts, n);
-            if (gated) rz[k] = load2<XT>(A.z, zat + t * A.zts, n, A.vec);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
+            if (gated) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<XT, NP>(vec, vat, vts, tb, p.te, A.N, rv);
+        fetch_rows<VEC, XT, NP>(vp, vts, tb, p.te, A.N, rv);
     };
-    const int tiles = (p.te - p.t0 + TT - 1) / TT;
-    auto base = [&](int i) { return p.t0 + (REV ? tiles - 1 - i : i) * TT; };
-    if (tiles) fetch(base(0));
-    for (int i = 0; i < tiles; ++i) {
-        const int tb = base(i);
-        __syncthreads();
+    auto prepare = [&](int tb, int buf) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS;
-            if (r >= TT) continue;
-            F2 dt = f2(0.f), w = f2(0.f);
-            if (tb + r < p.te) {
-                dt = step_size<XT>(A, rd[k], bias, nullptr);
-                w = value2(rx[k]);
-                if constexpr (!REV) {
-                    w = mul2(w, dt);
-                } else if (gated) {
-                    const F2 z = value2(rz[k]);
-                    w = mul2(w, mul2(z, sigmoid(z)));
-                }
+            if (TT % P::ROWS != 0 && r >= TT) continue;
+            F2 dt[Q], w[Q], z[Q];
+            step_sizes<XT, V>(A, rd[k], bias, dt, nullptr);
+            values<XT, V>(rx[k], w);
+            if (gated) values<XT, V>(rz[k], z);
+            const bool in = tb + r < p.te;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (!in) dt[q] = f2(0.f);
+                if constexpr (!REV) w[q] = mul2(w[q], dt[q]);
+                else if (gated) w[q] = mul2(w[q], mul2(z[q], sigmoid(z[q])));
+                sum[q] = add2(sum[q], dt[q]);
             }
-            sum = add2(sum, dt);
-            float d0, d1, w0, w1;
-            parts(dt, d0, d1), parts(w, w0, w1);
-            sh.dtu[r * CT + 2 * p.cp] = both(f2(d0), f2(w0));
-            sh.dtu[r * CT + 2 * p.cp + 1] = both(f2(d1), f2(w1));
+            p.write(sh.dtu[buf], r, dt, w);
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int j = threadIdx.x + k * NT;
-            if (j < TT * NP) sh.v[j] = to_f(rv[k]);
+            const int i = threadIdx.x + k * NT;
+            if (i < TT * NP) sh.v[buf][i] = to_f(rv[k]);
         }
-        if (i + 1 < tiles) fetch(base(i + 1));
+    };
+    const int tiles = (p.te - p.t0 + TT - 1) / TT, entry = P::entry(p.c);
+    auto base = [&](int i) { return p.t0 + (REV ? tiles - 1 - i : i) * TT; };
+    if (tiles > 0) fetch(base(0)), prepare(base(0), 0);
+    if (tiles > 1) fetch(base(1));
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int buf = i & 1;
+        if (i + 1 < tiles) prepare(base(i + 1), buf ^ 1);
+        if (i + 2 < tiles) fetch(base(i + 2));
+#pragma unroll
+        for (int i4 = 0; i4 < TT; i4 += 4) {
+            const int q = REV ? TT - 4 - i4 : i4;
+            F2 a[4][H], u[4][H];
+            decays<4, S>(sh.dtu[buf] + q * P::DW + entry, P::DW, sh.v[buf] + q * NP + n0, NP, A2, a, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    if constexpr (REV) h[k] = mul2(a[3 - j][k], add2(u[3 - j][k], h[k]));
+                    else h[k] = fma2(a[j][k], h[k], u[j][k]);
+                }
+        }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const int t = REV ? TT - 1 - j : j;
-            const ulonglong2 du = sh.dtu[t * CT + p.c];
-            F2 v[H];
-            read_vec<S>(sh.v + t * NP + n0, v);
-#pragma unroll
-            for (int k = 0; k < H; ++k) {
-                const F2 a = decay(mul2(low(du), A2[k]));
-                if constexpr (REV) h[k] = mul2(a, fma2(high(du), v[k], h[k]));
-                else h[k] = fma2(a, h[k], mul2(high(du), v[k]));
-            }
-        }
     }
     const long long at = (long long)(p.b * A.nseg + p.s) * A.E;
     if (p.live) {
@@ -515,17 +681,16 @@ __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
         unpack<S>(h, v);
         store_states<S>(A.seg_state + (at + p.ch) * A.N, n0, A.N, A.vec_n, v);
     }
-    float s0, s1;
-    parts(sum, s0, s1);
-    sh.sum[threadIdx.x] = make_float2(s0, s1);
+    own_write<V>(sh.sum + threadIdx.x * V, sum);
     __syncthreads();
     if (p.row == 0) {  // row by row, in order
         for (int r = 1; r < P::ROWS; ++r) {
-            const float2 o = sh.sum[r * P::PAIRS + p.cp];
-            s0 += o.x, s1 += o.y;
+            F2 o[Q];
+            own_read<V>(sh.sum + (r * P::QUADS + threadIdx.x) * V, o);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[q] = add2(sum[q], o[q]);
         }
-        if (pw > 0) A.seg_sum[at + p.pair()] = s0;
-        if (pw > 1) A.seg_sum[at + p.pair() + 1] = s1;
+        store<false, float, V>(A.seg_sum + at + p.column(), sum, pw);
     }
 }
 
@@ -547,54 +712,88 @@ __global__ void __launch_bounds__(256) join_kernel(const SelArgs A) {
     }
 }
 
-// ---- one token: 4 states per thread, L lanes per channel
-template <class XT, int L>
+// ---- one token: 4 states per thread, L lanes per channel, R sequences. What belongs to a channel is computed by one of its
+// lanes for each sequence: dt, x, the gate and the output of sequence k by lane k % L (of the first four). With R = 4 the lanes' sums
+// over n end with those lanes, and a state costs a fourth of the instructions around it.
+template <class XT, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) step_kernel(const SelArgs A) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = A.E;
-    const long long bc = i / L;
-    const int gl = (int)(i % L), n0 = gl * 4;
-    const bool live = bc < per * A.B;
-    const long long b = live ? bc / per : 0;
-    const int e = live ? (int)(bc - b * per) : 0, g = e / A.Eg;
-    float h[4] = {}, a[4] = {}, bv[4] = {}, cv[4] = {};
-    float x = 0.f, dt = 0.f;
-    if (live) {
-        load_states<4>(A.h0 + (b * A.E + e) * A.N, n0, A.N, A.vec_n, h);
-        load_states<4>(A.A + (long long)e * A.N, n0, A.N, A.vec_n, a);
-        const XT *pb = static_cast<const XT*>(A.b) + b * A.bbs + g * A.N, *pc = static_cast<const XT*>(A.c) + b * A.cbs + g * A.N;
+    constexpr int LR = L < R ? L : R, PR = R / LR;  // lanes with sequences of their own, and how many of these
+    const unsigned per = (unsigned)(((long long)A.E * L + 255) / 256), blk = blockIdx.x / per;  // CTAs per R sequences
+    const unsigned i = (blockIdx.x - blk * per) * 256u + threadIdx.x;
+    const int gl = (int)(i % L), n0 = gl * 4, lane = threadIdx.x & 31;
+    const bool in = i / L < (unsigned)A.E;
+    const int e = in ? (int)(i / L) : 0, g = A.G == 1 ? 0 : e / A.Eg;
+    const int b0 = (int)blk * R, most = A.B - 1;  // sequences past the last read the last one's
+    const int live = !in ? 0 : min(R, A.B - b0);
+    const long long EN = (long long)A.E * A.N, own = (long long)e * A.N;
+    float a[4], dt[PR], u[PR], x[PR], z[PR], h[R][4], bv[R][4], cv[R][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (n0 + k < A.N) bv[k] = to_f(pb[n0 + k]), cv[k] = to_f(pc[n0 + k]);
-        x = to_f(static_cast<const XT*>(A.x)[b * A.xbs + e]);
+    for (int k = 0; k < R; ++k) {
+        const long long b = min(b0 + k, most);
+        load_states<4>(A.h0 + b * EN + own, n0, A.N, VEC, h[k]);
+        load_row<VEC>(static_cast<const XT*>(A.b) + b * A.bbs + g * A.N, n0, A.N, bv[k]);
+        load_row<VEC>(static_cast<const XT*>(A.c) + b * A.cbs + g * A.N, n0, A.N, cv[k]);
+    }
+    load_states<4>(A.A + own, n0, A.N, VEC, a);
+    const float bias = A.dt_bias ? A.dt_bias[e] : 0.f, skip = A.skip ? A.skip[e] : 0.f;
+#pragma unroll
+    for (int j = 0; j < PR; ++j) {
+        const long long b = min(b0 + gl % LR + j * LR, most);
+        x[j] = to_f(static_cast<const XT*>(A.x)[b * A.xbs + e]);
+        z[j] = A.z ? to_f(static_cast<const XT*>(A.z)[b * A.zbs + e]) : 0.f;
         const long long di = b * A.dbs + e;
-        dt = sizeof(XT) == 4 || A.dt32 ? static_cast<const float*>(A.dt)[di] : to_f(static_cast<const XT*>(A.dt)[di]);
-        if (A.dt_bias) dt += A.dt_bias[e];
+        dt[j] = sizeof(XT) == 4 || A.dt32 ? static_cast<const float*>(A.dt)[di] : to_f(static_cast<const XT*>(A.dt)[di]);
+    }
+#pragma unroll
+    for (int j = 0; j < PR; ++j) {
+        dt[j] += bias;
         if (A.softplus) {
             float other;
-            parts(softplus(f2(dt), nullptr), dt, other);
+            parts(softplus(f2(dt[j], 0.f), nullptr), dt[j], other);
         }
+        u[j] = dt[j] * x[j];
     }
-    const float u = dt * x;
-    float y = 0.f;
+    const F2 a01 = f2(a[0] * kLog2e, a[1] * kLog2e), a23 = f2(a[2] * kLog2e, a[3] * kLog2e);
+    float y[R];
+    float* to = A.h_out + b0 * EN + own;
 #pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-        float a0, a1;
-        parts(decay(mul2(f2(dt * kLog2e), f2(a[k], a[k + 1]))), a0, a1);
-        h[k] = fmaf(a0, h[k], u * bv[k]);
-        h[k + 1] = fmaf(a1, h[k + 1], u * bv[k + 1]);
-        y = fmaf(h[k], cv[k], fmaf(h[k + 1], cv[k + 1], y));
+    for (int k = 0; k < R; ++k, to += EN) {
+        float d = dt[k / LR], v = u[k / LR];
+        if constexpr (LR > 1) {
+            d = __shfl_sync(ALL, d, (lane & ~(L - 1)) + k % LR);
+            v = __shfl_sync(ALL, v, (lane & ~(L - 1)) + k % LR);
+        }
+        F2 t[2] = {mul2(f2(d), a01), mul2(f2(d), a23)};
+        decay<2>(t);
+        const F2 h01 = fma2(t[0], f2(h[k][0], h[k][1]), mul2(f2(v), f2(bv[k][0], bv[k][1])));
+        const F2 h23 = fma2(t[1], f2(h[k][2], h[k][3]), mul2(f2(v), f2(bv[k][2], bv[k][3])));
+        y[k] = total(fma2(h23, f2(cv[k][2], cv[k][3]), mul2(h01, f2(cv[k][0], cv[k][1]))));
+        parts(h01, h[k][0], h[k][1]), parts(h23, h[k][2], h[k][3]);
+        if (k < live) store_states<4>(to, n0, A.N, VEC, h[k]);
     }
+    // the lanes' sums, each to the lane of its sequence
+    if constexpr (R == 4 && L > 1) {
+        y[0] = halve(y[0], y[1], lane, 1), y[2] = halve(y[2], y[3], lane, 1);
+        if constexpr (L == 2) {
+            y[1] = y[2];
+        } else {
+            y[0] = halve(y[0], y[2], lane, 2);
 #pragma unroll
-    for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(ALL, y, o);
-    if (!live) return;
-    store_states<4>(A.h_out + (b * A.E + e) * A.N, n0, A.N, A.vec_n, h);
-    if (gl) return;
-    if (A.skip) y = fmaf(A.skip[e], x, y);
-    if (A.z) {
-        const float z = to_f(static_cast<const XT*>(A.z)[b * A.zbs + e]);
-        y *= z * rcp(1.f + ex2(-z * kLog2e));
+            for (int o = 4; o < L; o *= 2) y[0] += __shfl_xor_sync(ALL, y[0], o);
+        }
+    } else if constexpr (R == 1) {
+#pragma unroll
+        for (int o = 1; o < L; o *= 2) y[0] += __shfl_xor_sync(ALL, y[0], o);
     }
-    put(static_cast<XT*>(A.y) + b * A.E + e, y);
+    if (gl >= LR) return;
+#pragma unroll
+    for (int j = 0; j < PR; ++j) {
+        const int k = gl + j * LR;
+        if (k >= live) continue;
+        if (A.skip) y[j] = fmaf(skip, x[j], y[j]);
+        if (A.z) y[j] *= z[j] * rcp(1.f + ex2(-z[j] * kLog2e));
+        put(static_cast<XT*>(A.y) + (long long)(b0 + k) * A.E + e, y[j]);
+    }
 }
 
 }  // namespace selective

@@ -20,10 +20,12 @@ struct BwdShared {
     static constexpr int NP = 4 * L, CT = Place<L>::CT, CTP = Place<L>::CTP;
     static constexpr int VAR = L <= 8 ? 4 : L == 16 ? 2 : 1;  // orders of a lane's four states
     static constexpr int VS = TT * NP + (NP < 32 ? NP : 0);   // from order to order, apart in the banks
-    ulonglong2 dtu[TT * CT];                                  // (dt, dt, u, u), u = dt x
-    F2 w[TT * CT];                                            // (w, w)
-    F2 x[TT * CT / 2], slope[TT * CT / 2], zf[TT * CT / 2];   // of pairs of channels, for the thread that wrote them
-    float y[TT * CTP], du[TT * CTP], dq[TT * CTP];            // sums over n
+    static constexpr int QS = CT + 8;
+    ulonglong2 dtu[TT * Place<L>::DW];                        // (dt, dt, u, u), u = dt x
+    F2 w[TT * Place<L>::DW];                                  // (w, w)
+    float x[TT * CT], slope[TT * CT], zf[TT * CT];            // for the thread that wrote them
+    float y[TT * L * CTP], du[TT * L * CTP];                  // the lanes' parts of the sums over n
+    float dq[TT * QS];                                        // a whole one
     float b[VAR * VS], c[VAR * VS];
     float sums[2][NW][TT * NP];                               // dc and db of the warps' channels
 };
@@ -44,38 +46,51 @@ __device__ __forceinline__ void reorder(float* v, int order) {
 }
 __device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Sums over the warp's channels of four states, token by token from the last: what add() has taken is written by the call
-// for which it has enough tokens.
+// Sums over the warp's channels of four states of dc and of db, token by token from the last: what add() has taken is written by
+// the call for which it has enough tokens. The two are added in pairs.
 template <int L>
 struct ChannelSums {
     static constexpr int NP = 4 * L;
-    float v1, r23, v3;
-    __device__ __forceinline__ void add(float* out, int t, const F2* f, int lane, int gl, int cl) {
-        float s[4];
-        parts(f[0], s[0], s[1]), parts(f[1], s[2], s[3]);
+    F2 v1, r23, v3;  // (dc, db)
+    static __device__ __forceinline__ F2 shfl(F2 v, int o) {
+        float a, b;
+        parts(v, a, b);
+        return f2(__shfl_xor_sync(ALL, a, o), __shfl_xor_sync(ALL, b, o));
+    }
+    static __device__ __forceinline__ F2 half(F2 v0, F2 v1, int lane, int bit) {  // halve() of both
+        float a0, b0, a1, b1;
+        parts(v0, a0, b0), parts(v1, a1, b1);
+        const bool up = lane & bit;
+        return add2(f2(up ? a1 : a0, up ? b1 : b0), shfl(f2(up ? a0 : a1, up ? b0 : b1), bit));
+    }
+    static __device__ __forceinline__ void put(float* dc, float* db, int at, F2 v) { parts(v, dc[at], db[at]); }
+    __device__ __forceinline__ void add(float* dc, float* db, int t, const F2* c, const F2* b, int lane, int gl, int cl) {
+        float c0, c1, b0, b1;
         if constexpr (L <= 8) {
-            s[0] += __shfl_xor_sync(ALL, s[2], 2 * L);
-            s[1] += __shfl_xor_sync(ALL, s[3], 2 * L);
-            s[0] += __shfl_xor_sync(ALL, s[1], L);
+            const F2 cs = add2(c[0], shfl(c[1], 2 * L)), bs = add2(b[0], shfl(b[1], 2 * L));
+            parts(cs, c0, c1), parts(bs, b0, b1);
+            const F2 s = add2(f2(c0, b0), shfl(f2(c1, b1), L));
             const int at = gl * 4 + (cl & 3);
             if constexpr (L == 8) {
-                out[t * NP + at] = s[0];
+                put(dc, db, t * NP + at, s);
             } else if constexpr (L == 4) {
-                if (t & 1) v1 = s[0];
-                else out[(t + (lane >> 4)) * NP + at] = halve(s[0], v1, lane, 16);
+                if (t & 1) v1 = s;
+                else put(dc, db, (t + (lane >> 4)) * NP + at, half(s, v1, lane, 16));
             } else {
-                if ((t & 3) == 3) v3 = s[0];
-                else if ((t & 3) == 2) r23 = halve(s[0], v3, lane, 8);
-                else if ((t & 3) == 1) v1 = s[0];
-                else out[(t + (lane >> 3)) * NP + at] = halve(halve(s[0], v1, lane, 8), r23, lane, 16);
+                if ((t & 3) == 3) v3 = s;
+                else if ((t & 3) == 2) r23 = half(s, v3, lane, 8);
+                else if ((t & 3) == 1) v1 = s;
+                else put(dc, db, (t + (lane >> 3)) * NP + at, half(half(s, v1, lane, 8), r23, lane, 16));
             }
         } else if constexpr (L == 16) {
-            s[0] += __shfl_xor_sync(ALL, s[1], 16);
-            s[2] += __shfl_xor_sync(ALL, s[3], 16);
-            out[t * NP + gl * 4 + cl] = s[0];
-            out[t * NP + gl * 4 + (2 ^ cl)] = s[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                parts(c[k], c0, c1), parts(b[k], b0, b1);
+                put(dc, db, t * NP + gl * 4 + (2 * k ^ cl), add2(f2(c0, b0), shfl(f2(c1, b1), 16)));
+            }
         } else {
-            *reinterpret_cast<float4*>(out + t * NP + gl * 4) = make_float4(s[0], s[1], s[2], s[3]);
+            *reinterpret_cast<ulonglong2*>(dc + t * NP + gl * 4) = make_ulonglong2(c[0].v, c[1].v);
+            *reinterpret_cast<ulonglong2*>(db + t * NP + gl * 4) = make_ulonglong2(b[0].v, b[1].v);
         }
     }
 };
@@ -105,17 +120,18 @@ struct StateSums {
     }
 };
 
-template <class XT, int L, bool GATE>
+template <class XT, int L, bool GATE, bool VEC>
 __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs A) {
     using P = Place<L>;
     using Sh = BwdShared<XT, L>;
-    constexpr int NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, VAR = Sh::VAR, VS = Sh::VS, SB = 8;
+    constexpr int NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, VAR = Sh::VAR, VS = Sh::VS, QS = Sh::QS, SB = 8,
+                  V = P::V, Q = P::P, DW = P::DW;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh& sh = *reinterpret_cast<Sh*>(raw_shared);
     const P p(A);
-    const int n0 = p.gl * 4, pw = p.width(), order = p.cl & (VAR - 1), warp = threadIdx.x >> 5;
+    const int n0 = p.gl * 4, pw = p.width(), order = p.cl & (VAR - 1), warp = threadIdx.x >> 5, entry = P::entry(p.c);
     const long long EN = (long long)A.E * A.N, own = (long long)p.ch * A.N, seg = (long long)p.b * A.nseg + p.s;
-    F2 g[2], A2[2], dA[2] = {f2(0.f), f2(0.f)}, bias = f2(0.f), skip = f2(0.f), dskip = f2(0.f), dbias = f2(0.f);
+    F2 g[2], A2[2], dA[2] = {f2(0.f), f2(0.f)}, bias[Q], skip[Q], dskip[Q], dbias[Q];
     {
         float v[4] = {};
         if (p.live) load_states<4>(A.A + own, n0, A.N, A.vec_n, v);
@@ -129,76 +145,91 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
         if (from && p.live) load_states<4>(from + own, n0, A.N, A.vec_n, v);
         reorder<VAR>(v, order);
         pack<4>(v, g);
-        if (A.dt_bias) bias = value2(load2<float>(A.dt_bias, p.pair(), pw, false));
-        if (A.skip) skip = value2(load2<float>(A.skip, p.pair(), pw, false));
+        load_columns<V>(A.dt_bias, p.column(), pw, bias);
+        load_columns<V>(A.skip, p.column(), pw, skip);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) dskip[q] = dbias[q] = f2(0.f);
     }
-    const long long xat = p.b * A.xbs + p.pair(), dat = p.b * A.dbs + p.pair(), zat = p.b * A.zbs + p.pair(),
-                    yat = p.b * A.ybs + p.pair(), bat = p.b * A.bbs + p.g * A.N, cat = p.b * A.cbs + p.g * A.N,
-                    oat = (long long)p.b * A.T * A.E + p.pair();
+    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs + p.column(), *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
+             *gp = static_cast<const XT*>(A.dy) + p.b * A.ybs + p.column(), *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N,
+             *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
+    const void* dp = dt_at<XT>(A, p.b, p.column());
+    const long long oat = (long long)p.b * A.T * A.E + p.column();
     const float* marks = A.marks + (long long)p.b * A.nmarks * EN + own;
-    auto put_dt = [&](long long i, F2 v, int n) {
-        if (sizeof(XT) == 4 || A.dt32) store2<float>(A.ddt, i, v, n, A.vec);
-        else store2<XT>(A.ddt, i, v, n, A.vec);
+    auto put_dt = [&](int t, const F2* v) {
+        if (sizeof(XT) == 4 || A.dt32) store<VEC, float, V>(token<VEC>(static_cast<float*>(A.ddt) + oat, t, A.E), v, pw);
+        else store<VEC, XT, V>(token<VEC>(static_cast<XT*>(A.ddt) + oat, t, A.E), v, pw);
     };
+    auto put_x = [&](void* to, int t, const F2* v) { store<VEC, XT, V>(token<VEC>(static_cast<XT*>(to) + oat, t, A.E), v, pw); };
     auto mark = [&](int t, F2* h) {  // the state before token t
         float v[4] = {};
         if (p.live && t < p.te) load_states<4>(marks + (long long)(t / kSelMark) * EN, n0, A.N, A.vec_n, v);
         reorder<VAR>(v, order);
         pack<4>(v, h);
     };
-    auto stage = [&](int tb) {
-        Pair<XT> rx[PI], rz[PI] = {}, ry[PI];
-        Pair<float> rd[PI];
-        XT rb[NB], rc[NB];
+    Raw<XT, V> rx[PI], rz[PI], ry[PI];
+    Raw<float, V> rd[PI];
+    XT rb[NB], rc[NB];
+    auto fetch = [&](int tb) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load2<XT>(A.x, xat + t * A.xts, n, A.vec);
-            rd[k] = load_dt<XT>(A, dat + t * A.dts, n);
-            ry[k] = load2<XT>(A.dy, yat + t * A.yts, n, A.vec);
-            if constexpr (GATE) rz[k] = load2<XT>(A.z, zat + t * A.zts, n, A.vec);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, A.xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
+            ry[k] = load<VEC, XT, V>(token<VEC>(gp, t, A.yts), n);
+            if constexpr (GATE) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<XT, NP>(A.b, bat, A.bts, tb, p.te, A.N, rb);
-        fetch_rows<XT, NP>(A.c, cat, A.cts, tb, p.te, A.N, rc);
-        if (tb > p.t0) {  // the next tile's lines are brought nearer
+        fetch_rows<VEC, XT, NP>(bp, A.bts, tb, p.te, A.N, rb);
+        fetch_rows<VEC, XT, NP>(cp, A.cts, tb, p.te, A.N, rc);
+    };
+    auto ahead = [&](int tb) {  // a tile's lines are brought nearer
 #pragma unroll
-            for (int k = 0; k < PI; ++k) {
-                const int r = p.row + k * P::ROWS, t = tb - TT + r;
-                if (r >= TT || pw == 0) continue;
-                const char *px = static_cast<const char*>(A.x) + (xat + t * A.xts) * (long long)sizeof(XT),
-                           *py = static_cast<const char*>(A.dy) + (yat + t * A.yts) * (long long)sizeof(XT),
-                           *pd = static_cast<const char*>(A.dt) + (dat + t * A.dts) * (long long)(A.dt32 ? 4 : sizeof(XT));
-                prefetch(px), prefetch(py), prefetch(pd);
-                if constexpr (GATE) prefetch(static_cast<const char*>(A.z) + (zat + t * A.zts) * (long long)sizeof(XT));
-            }
-            if (p.live && n0 < A.N)
-#pragma unroll
-                for (int t = 0; t < TT; t += kSelMark) prefetch(marks + (long long)((tb - TT + t) / kSelMark) * EN + n0);
+        for (int k = 0; k < PI; ++k) {
+            const int r = p.row + k * P::ROWS, t = tb + r;
+            if (r >= TT || pw == 0) continue;
+            prefetch(token<VEC>(xp, t, A.xts));
+            prefetch(token<VEC>(gp, t, A.yts));
+            prefetch(sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(token<VEC>(static_cast<const float*>(dp), t, A.dts))
+                                               : static_cast<const void*>(token<VEC>(static_cast<const XT*>(dp), t, A.dts)));
+            if constexpr (GATE) prefetch(token<VEC>(zp, t, A.zts));
         }
+        if (p.live && n0 < A.N)
+#pragma unroll
+            for (int t = 0; t < TT; t += kSelMark) prefetch(marks + (long long)((tb + t) / kSelMark) * EN + n0);
+    };
+    auto prepare = [&](int tb) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS;
-            if (r >= TT) continue;
-            F2 dt = f2(0.f), u = f2(0.f), w = f2(0.f), slope = f2(0.f), zf = f2(0.f), x = f2(0.f);
-            if (tb + r < p.te) {
-                dt = step_size<XT>(A, rd[k], bias, &slope);
-                x = value2(rx[k]);
-                u = mul2(dt, x);
-                w = value2(ry[k]);
-                if constexpr (GATE) {  // dy silu(z), dy silu'(z)
-                    const F2 z = value2(rz[k]), s = sigmoid(z), zs = mul2(z, s);
-                    zf = mul2(w, fma2(zs, fma2(s, f2(-1.f), f2(1.f)), s));
-                    w = mul2(w, zs);
+            if (TT % P::ROWS != 0 && r >= TT) continue;
+            F2 dt[Q], slope[Q], x[Q], u[Q], w[Q], z[Q];
+            step_sizes<XT, V>(A, rd[k], bias, dt, slope);
+            values<XT, V>(rx[k], x);
+            values<XT, V>(ry[k], w);
+            if constexpr (GATE) values<XT, V>(rz[k], z);
+            const bool in = tb + r < p.te;
+            const int at = r * CT + p.first;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (!in) dt[q] = f2(0.f);
+                u[q] = mul2(dt[q], x[q]);  // rows behind the end were read as 0
+                if constexpr (GATE) {      // dy silu(z), dy silu'(z)
+                    const F2 s = sigmoid(z[q]), zs = mul2(z[q], s);
+                    z[q] = mul2(w[q], fma2(zs, fma2(s, f2(-1.f), f2(1.f)), s));
+                    w[q] = mul2(w[q], zs);
                 }
+                dskip[q] = fma2(w[q], x[q], dskip[q]);
             }
-            float d0, d1, u0, u1, w0, w1;
-            parts(dt, d0, d1), parts(u, u0, u1), parts(w, w0, w1);
-            const int at = r * CT + 2 * p.cp;
-            sh.dtu[at] = both(f2(d0), f2(u0));
-            sh.dtu[at + 1] = both(f2(d1), f2(u1));
-            *reinterpret_cast<ulonglong2*>(sh.w + at) = both(f2(w0), f2(w1));
-            sh.x[at / 2] = x, sh.slope[at / 2] = slope;
-            if constexpr (GATE) sh.zf[at / 2] = zf;
+            p.write(sh.dtu, r, dt, u);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float w0, w1;
+                parts(w[v / 2], w0, w1);
+                sh.w[r * DW + P::entry(p.first + v)] = f2(v & 1 ? w1 : w0);
+            }
+            own_write<V>(sh.x + at, x);
+            own_write<V>(sh.slope + at, slope);
+            if constexpr (GATE) own_write<V>(sh.zf + at, z);
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -214,19 +245,36 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r;
             if (r >= TT || t >= p.te) continue;
-            const int at = r * CT + 2 * p.cp, st = r * CTP + 2 * p.cp;
-            const ulonglong2 p0 = sh.dtu[at], p1 = sh.dtu[at + 1], ww = *reinterpret_cast<const ulonglong2*>(sh.w + at);
-            float d0, d1, w0, w1, other;
-            parts(low(p0), d0, other), parts(low(p1), d1, other), parts(F2{ww.x}, w0, other), parts(F2{ww.y}, w1, other);
-            const F2 x = sh.x[at / 2], w = f2(w0, w1), du = *reinterpret_cast<const F2*>(sh.du + st);
-            const long long o = oat + (long long)t * A.E;
-            store2<XT>(A.dx, o, fma2(du, f2(d0, d1), mul2(skip, w)), pw, A.vec);
-            const F2 ddt = mul2(fma2(*reinterpret_cast<const F2*>(sh.dq + st), f2(kLn2), mul2(du, x)), sh.slope[at / 2]);
-            put_dt(o, ddt, pw);
-            dbias = add2(dbias, ddt);
-            dskip = fma2(w, x, dskip);
-            if constexpr (GATE)
-                store2<XT>(A.dz, o, mul2(fma2(skip, x, *reinterpret_cast<const F2*>(sh.y + st)), sh.zf[at / 2]), pw, A.vec);
+            const int at = r * CT + p.first;
+            F2 x[Q], du[Q], f[Q], e[Q];
+            lane_sums<L>(sh.du + r * L * CTP + p.first, du);
+            own_read<V>(sh.x + at, x);
+            own_read<V>(sh.slope + at, f);
+            own_read<V>(sh.dq + r * QS + p.first, e);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                e[q] = mul2(fma2(e[q], f2(kLn2), mul2(du[q], x[q])), f[q]);
+                dbias[q] = add2(dbias[q], e[q]);
+            }
+            put_dt(t, e);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {  // dt du + skip w
+                float d[2] = {}, w[2] = {}, other;
+#pragma unroll
+                for (int v = 0; v < (V > 1 ? 2 : 1); ++v) {
+                    const int i = r * DW + P::entry(p.first + 2 * q + v);
+                    parts(low(sh.dtu[i]), d[v], other), parts(sh.w[i], w[v], other);
+                }
+                e[q] = fma2(f2(d[0], d[1]), du[q], mul2(skip[q], f2(w[0], w[1])));
+            }
+            put_x(A.dx, t, e);
+            if constexpr (GATE) {
+                lane_sums<L>(sh.y + r * L * CTP + p.first, e);
+                own_read<V>(sh.zf + at, f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) e[q] = mul2(fma2(skip[q], x[q], e[q]), f[q]);
+                put_x(A.dz, t, e);
+            }
         }
         float* out = A.parts_bc + (((long long)p.ct * A.B + p.b) * A.T + tb) * 2 * A.N;
         for (int i = threadIdx.x; i < 2 * TT * NP; i += NT) {
@@ -242,44 +290,47 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
     for (int i = tiles - 1; i >= 0; --i) {
         const int tb = p.t0 + i * TT;
         __syncthreads();
+        fetch(tb);  // on its way while the tile behind is finished
+        if (i > 0) ahead(tb - TT);
         if (i + 1 < tiles) finish(tb + TT);
-        stage(tb);
+        prepare(tb);
         __syncthreads();
         F2 sA[2] = {f2(0.f), f2(0.f)};
-        StateSums<L> sy, sd, sq;
-        ChannelSums<L> sb, sc;
+        StateSums<L> sq;
+        ChannelSums<L> sc;
         const float *vb = sh.b + order * VS + n0, *vc = sh.c + order * VS + n0;
+        const ulonglong2* dtu = sh.dtu + entry;
+        const F2* ws = sh.w + entry;
+        float *ys = sh.y + p.gl * CTP + p.c, *dus = sh.du + p.gl * CTP + p.c;
 #pragma unroll 1
         for (int q = TT - SB; q >= 0; q -= SB) {
             F2 a[SB][2], hp[SB][2], h[2];
             mark(tb + q / kSelMark * kSelMark, h);
             if (kSelMark > SB && q) {
+                F2 u[SB][2];
+                decays<SB, 4>(dtu, DW, vb, NP, A2, a, u);
 #pragma unroll
-                for (int t = 0; t < SB; ++t) {
-                    const ulonglong2 du = sh.dtu[t * CT + p.c];
-                    F2 bv[2];
-                    read_vec<4>(vb + t * NP, bv);
+                for (int j = 0; j < SB; ++j)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) h[k] = fma2(decay(mul2(low(du), A2[k])), h[k], mul2(high(du), bv[k]));
-                }
+                    for (int k = 0; k < 2; ++k) h[k] = fma2(a[j][k], h[k], u[j][k]);
             }
 #pragma unroll
-            for (int j = 0; j < SB; ++j) {
-                const ulonglong2 du = sh.dtu[(q + j) * CT + p.c];
-                F2 bv[2];
-                read_vec<4>(vb + (q + j) * NP, bv);
+            for (int j4 = 0; j4 < SB; j4 += 4) {
+                F2 u[4][2];
+                decays<4, 4>(dtu + (q + j4) * DW, DW, vb + (q + j4) * NP, NP, A2, a + j4, u);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    hp[j][k] = h[k];
-                    a[j][k] = decay(mul2(low(du), A2[k]));
-                    h[k] = fma2(a[j][k], h[k], mul2(high(du), bv[k]));
-                }
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        hp[j4 + j][k] = h[k];
+                        h[k] = fma2(a[j4 + j][k], h[k], u[j][k]);
+                    }
             }
 #pragma unroll
             for (int j = SB - 1; j >= 0; --j) {
                 const int t = q + j;
-                const ulonglong2 du = sh.dtu[t * CT + p.c];
-                const F2 w = sh.w[t * CT + p.c];
+                const ulonglong2 du = dtu[t * DW];
+                const F2 w = ws[t * DW];
                 F2 bv[2], cv[2], dc[2], db[2], yy, dd, qq;
                 read_vec<4>(vb + t * NP, bv);
                 read_vec<4>(vc + t * NP, cv);
@@ -296,23 +347,22 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
                     sA[k] = fma2(ah, low(du), sA[k]);
                     h[k] = hp[j][k];
                 }
+                if constexpr (GATE) ys[t * L * CTP] = total(yy);
+                dus[t * L * CTP] = total(dd);
                 // j stands for t in the choice of what is handed on: q is a multiple of 4
-                if constexpr (GATE) sy.add(sh.y + q * CTP, CTP, j, total(yy), p.lane, p.gl, p.c);
-                sd.add(sh.du + q * CTP, CTP, j, total(dd), p.lane, p.gl, p.c);
-                sq.add(sh.dq + q * CTP, CTP, j, total(qq), p.lane, p.gl, p.c);
-                sc.add(sh.sums[0][warp] + q * NP, j, dc, p.lane, p.gl, p.cl);
-                sb.add(sh.sums[1][warp] + q * NP, j, db, p.lane, p.gl, p.cl);
+                sq.add(sh.dq + q * QS, QS, j, total(qq), p.lane, p.gl, p.c);
+                sc.add(sh.sums[0][warp] + q * NP, sh.sums[1][warp] + q * NP, j, dc, db, p.lane, p.gl, p.cl);
             }
         }
         dA[0] = add2(dA[0], sA[0]), dA[1] = add2(dA[1], sA[1]);  // tile by tile: short sums lose less
     }
     __syncthreads();
-    if (tiles) finish(p.t0);
+    if (tiles > 0) finish(p.t0);
+    const F2 zero[Q] = {};
     for (int t = p.te + p.row; t < p.t1; t += P::ROWS) {  // behind the sequence's end
-        const long long o = oat + (long long)t * A.E;
-        store2<XT>(A.dx, o, f2(0.f), pw, A.vec);
-        put_dt(o, f2(0.f), pw);
-        if constexpr (GATE) store2<XT>(A.dz, o, f2(0.f), pw, A.vec);
+        put_x(A.dx, t, zero);
+        put_dt(t, zero);
+        if constexpr (GATE) put_x(A.dz, t, zero);
     }
     if (p.live) {
         float v[4];
@@ -327,19 +377,22 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
     }
     // the sums over tokens per channel: row by row, in order
     __syncthreads();
-    float4* rows = reinterpret_cast<float4*>(raw_shared);
-    float s0, s1, k0, k1;
-    parts(dskip, s0, s1), parts(dbias, k0, k1);
-    rows[threadIdx.x] = make_float4(s0, s1, k0, k1);
+    float *s0 = reinterpret_cast<float*>(raw_shared), *s1 = s0 + NT * V;
+    own_write<V>(s0 + threadIdx.x * V, dskip);
+    own_write<V>(s1 + threadIdx.x * V, dbias);
     __syncthreads();
     if (p.row == 0) {
         for (int r = 1; r < P::ROWS; ++r) {
-            const float4 o = rows[r * P::PAIRS + p.cp];
-            s0 += o.x, s1 += o.y, k0 += o.z, k1 += o.w;
+            F2 o[Q];
+            own_read<V>(s0 + (r * P::QUADS + threadIdx.x) * V, o);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) dskip[q] = add2(dskip[q], o[q]);
+            own_read<V>(s1 + (r * P::QUADS + threadIdx.x) * V, o);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) dbias[q] = add2(dbias[q], o[q]);
         }
-        float* out = A.parts_ch + seg * 2 * A.E + p.pair();
-        if (pw > 0) out[0] = s0, out[A.E] = k0;
-        if (pw > 1) out[1] = s1, out[A.E + 1] = k1;
+        store<false, float, V>(A.parts_ch + seg * 2 * A.E + p.column(), dskip, pw);
+        store<false, float, V>(A.parts_ch + seg * 2 * A.E + A.E + p.column(), dbias, pw);
     }
 }
 

@@ -20,28 +20,33 @@ lattice_status start(K kernel, const SelArgs& a, size_t shared, long long ctas, 
 }
 inline long long ctas_of(const SelArgs& a) { return (long long)a.B * a.nseg * a.G * a.tiles; }
 
-template <class XT, int L, int S>
-lattice_status forward(const SelArgs& a, cudaStream_t st) {
+template <class XT, int L, int S, bool VEC>
+lattice_status forward_(const SelArgs& a, cudaStream_t st) {
     if (a.nseg > 1) {
-        lattice_status s = start(seg_kernel<XT, L, S, false>, a, sizeof(SegShared<XT, L, S>), ctas_of(a), st);
+        lattice_status s = start(seg_kernel<XT, L, S, false, VEC>, a, sizeof(SegShared<XT, L, S>), ctas_of(a), st);
         if (s != LATTICE_OK) return s;
         s = start(join_kernel<false>, a, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
         if (s != LATTICE_OK) return s;
     }
-    return start(fwd_kernel<XT, L, S>, a, sizeof(FwdShared<XT, L, S>), ctas_of(a), st);
+    return start(fwd_kernel<XT, L, S, VEC>, a, sizeof(FwdShared<XT, L, S>), ctas_of(a), st);
 }
 
-template <class XT, int L>
-lattice_status backward(const SelArgs& a, cudaStream_t st) {
+template <class XT, int L, int S>
+lattice_status forward(const SelArgs& a, cudaStream_t st) {
+    return a.vec ? forward_<XT, L, S, true>(a, st) : forward_<XT, L, S, false>(a, st);
+}
+
+template <class XT, int L, bool VEC>
+lattice_status backward_(const SelArgs& a, cudaStream_t st) {
     lattice_status s = LATTICE_OK;
     if (a.nseg > 1) {
-        s = start(seg_kernel<XT, L, 4, true>, a, sizeof(SegShared<XT, L, 4>), ctas_of(a), st);
+        s = start(seg_kernel<XT, L, 4, true, VEC>, a, sizeof(SegShared<XT, L, 4>), ctas_of(a), st);
         if (s != LATTICE_OK) return s;
         s = start(join_kernel<true>, a, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
         if (s != LATTICE_OK) return s;
     }
-    s = a.z ? start(bwd_kernel<XT, L, true>, a, sizeof(BwdShared<XT, L>), ctas_of(a), st)
-            : start(bwd_kernel<XT, L, false>, a, sizeof(BwdShared<XT, L>), ctas_of(a), st);
+    s = a.z ? start(bwd_kernel<XT, L, true, VEC>, a, sizeof(BwdShared<XT, L>), ctas_of(a), st)
+            : start(bwd_kernel<XT, L, false, VEC>, a, sizeof(BwdShared<XT, L>), ctas_of(a), st);
     if (s != LATTICE_OK) return s;
     if (a.T > 0) {
         s = start(shared_kernel<XT>, a, 0, ((long long)a.B * a.T * a.G * 2 * a.N + 255) / 256, st);
@@ -51,8 +56,17 @@ lattice_status backward(const SelArgs& a, cudaStream_t st) {
 }
 
 template <class XT, int L>
+lattice_status backward(const SelArgs& a, cudaStream_t st) {
+    return a.vec ? backward_<XT, L, true>(a, st) : backward_<XT, L, false>(a, st);
+}
+
+// Four sequences per thread where enough threads are left to fill the device with 16 warps per SM
+template <class XT, int L>
 lattice_status one_token(const SelArgs& a, cudaStream_t st) {
-    return start(step_kernel<XT, L>, a, 0, ((long long)a.B * a.E * L + 255) / 256, st);
+    auto ctas = [&](int R) { return (a.B + (long long)R - 1) / R * (((long long)a.E * L + 255) / 256); };
+    const bool many = ctas(4) >= 2 * sm_count();
+    if (a.vec) return many ? start(step_kernel<XT, L, 4, true>, a, 0, ctas(4), st) : start(step_kernel<XT, L, 1, true>, a, 0, ctas(1), st);
+    return many ? start(step_kernel<XT, L, 4, false>, a, 0, ctas(4), st) : start(step_kernel<XT, L, 1, false>, a, 0, ctas(1), st);
 }
 
 template <class XT>

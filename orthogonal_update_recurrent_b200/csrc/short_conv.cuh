@@ -6,13 +6,15 @@
 //   dx_s = sum_j w[K-1-j] e_{s+j},  dw[k] = sum_t e_t x_{t-K+1+k},  dbias = sum_t e_t
 //
 // HBM bounds it: x is read once and y written once. A thread has V neighbouring channels and
-// walks down a run of tokens with the last K-1 inputs in registers, loads of U tokens under way at
-// once; a run's K-1 first inputs are its neighbour's last ones and mostly come from the L2.
+// walks down a run of tokens with the last K-1 inputs in registers, loads of the next U tokens under way
+// at once; a run's K-1 first inputs are its neighbour's last ones and mostly come from the L2.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "args.h"
 #include "f32x2.cuh"
@@ -27,6 +29,28 @@ __device__ __forceinline__ void put(float& p, float v) { p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& p, float v) { p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half& p, float v) { p = __float2half_rn(v); }
 
+// A thread's V channels in H numbers: one, or pairs in packed instructions
+template <int V>
+struct Numbers {
+    using N = F2;
+    static constexpr int H = V / 2;
+};
+template <>
+struct Numbers<1> {
+    using N = float;
+    static constexpr int H = 1;
+};
+__device__ __forceinline__ float mad(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 mad(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ F2 add(F2 a, F2 b) { return add2(a, b); }
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-1.442695041f * v)); }
+__device__ __forceinline__ F2 sigmoid(F2 v) { return each(each(mul2(v, f2(-1.442695041f)), [](float n) { return 1.f + ex2(n); }), rcp); }
+__device__ __forceinline__ void fill(float& n, float v) { n = v; }
+__device__ __forceinline__ void fill(F2& n, float v) { n = f2(v); }
+
 template <class T, int V>
 struct alignas(sizeof(T) * V) Vec {
     T v[V];
@@ -36,16 +60,30 @@ __device__ __forceinline__ Vec<T, V> load(const void* p, long long i) {
     return *reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(p) + i);
 }
 template <class T, int V>
-__device__ __forceinline__ void store(void* p, long long i, const float* f) {
+__device__ __forceinline__ void store(void* p, long long i, const typename Numbers<V>::N* n) {
     Vec<T, V> r;
+    if constexpr (V == 1) {
+        put(r.v[0], n[0]);
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) put(r.v[v], f[v]);
+        for (int k = 0; k < V / 2; ++k) {
+            float a, b;
+            parts(n[k], a, b);
+            if constexpr (std::is_same<T, __half>::value) *reinterpret_cast<__half2*>(&r.v[2 * k]) = __floats2half2_rn(a, b);
+            else if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(&r.v[2 * k]) = __floats2bfloat162_rn(a, b);
+            else r.v[2 * k] = a, r.v[2 * k + 1] = b;
+        }
+    }
     *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(p) + i) = r;
 }
 template <class T, int V>
-__device__ __forceinline__ void values(const Vec<T, V>& r, float* f) {
+__device__ __forceinline__ void values(const Vec<T, V>& r, typename Numbers<V>::N* n) {
+    if constexpr (V == 1) {
+        n[0] = to_f(r.v[0]);
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = to_f(r.v[v]);
+        for (int k = 0; k < V / 2; ++k) n[k] = f2(to_f(r.v[2 * k]), to_f(r.v[2 * k + 1]));
+    }
 }
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> zeros() {
@@ -54,21 +92,40 @@ __device__ __forceinline__ Vec<T, V> zeros() {
     for (int v = 0; v < V; ++v) put(r.v[v], 0.f);
     return r;
 }
-template <class XT>
-__device__ __forceinline__ float weight(const ConvArgs& A, const void* p, long long i) {
-    return sizeof(XT) == 4 || A.w32 ? static_cast<const float*>(p)[i] : to_f(static_cast<const XT*>(p)[i]);
+// N consecutive weights, N a multiple of V, as vectors of V
+template <class T, int V, int N>
+__device__ __forceinline__ void weight_run(const void* p, long long i, float* f) {
+#pragma unroll
+    for (int k = 0; k < N; k += V) {
+        const Vec<T, V> r = load<T, V>(p, i + k);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[k + v] = to_f(r.v[v]);
+    }
 }
 // A thread's weights, from the oldest input's on, and bias
 template <class XT, int K, int V>
-__device__ __forceinline__ void weights(const ConvArgs& A, int c, float (*w)[V], float* bias) {
+__device__ __forceinline__ void weights(const ConvArgs& A, int c, typename Numbers<V>::N (*w)[Numbers<V>::H], typename Numbers<V>::N* bias) {
+    float f[K * V], g[V] = {};
+    if (sizeof(XT) == 4 || A.w32) {
+        weight_run<float, V, K * V>(A.w, (long long)c * K, f);
+        if (A.bias) weight_run<float, V, V>(A.bias, c, g);
+    } else {
+        weight_run<XT, V, K * V>(A.w, (long long)c * K, f);
+        if (A.bias) weight_run<XT, V, V>(A.bias, c, g);
+    }
+    if constexpr (V == 1) {
+        bias[0] = g[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+        for (int k = 0; k < K; ++k) w[k][0] = f[k];
+    } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][v] = weight<XT>(A, A.w, (long long)(c + v) * K + k);
-        bias[v] = A.bias ? weight<XT>(A, A.bias, c + v) : 0.f;
+        for (int h = 0; h < V / 2; ++h) {
+            bias[h] = f2(g[2 * h], g[2 * h + 1]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][h] = f2(f[2 * h * K + k], f[(2 * h + 1) * K + k]);
+        }
     }
 }
-__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-1.442695041f * v)); }
 
 // Who does what: V channels and a run of A.run tokens of one sequence per thread.
 template <int V>
@@ -92,74 +149,93 @@ __device__ __forceinline__ Vec<XT, V> input(const ConvArgs& A, int b, int c, int
 }
 
 template <class XT, int K, int V>
-__global__ void __launch_bounds__(256) fwd_kernel(const ConvArgs A) {
-    constexpr int U = 8;
+__global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) fwd_kernel(const ConvArgs A) {
+    using N = typename Numbers<V>::N;
+    constexpr int U = 4, H = Numbers<V>::H;
     const Place<V> p(A);
     if (!p.in) return;
-    float w[K][V], bias[V], win[K][V];  // win[k]: x_{t-K+1+k}
+    N w[K][H], bias[H], win[K][H];  // win[k]: x_{t-K+1+k}
     weights<XT, K, V>(A, p.c, w, bias);
     const int t0 = p.run * A.run, t1 = min(A.T, t0 + A.run), te = min(t1, p.len);
+    const bool tail = p.run == 0 && A.state_out;  // writes the state at the sequence's end
     Vec<XT, V> last[K > 1 ? K - 1 : 1];
-    if (p.run == 0 && A.state_out) {  // read before anything is written: the state may be updated in place
+    if (tail && p.len < K - 1) {  // part of the state itself: read before anything is written, which may be in place
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) last[j] = input<XT, K, V>(A, p.b, p.c, p.len - (K - 1) + j);
     }
+    if (t0 < te) {
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) {
-        if (t0 < te) values<XT, V>(input<XT, K, V>(A, p.b, p.c, t0 - (K - 1) + k), win[k]);
+        for (int k = 0; k < K - 1; ++k) values<XT, V>(input<XT, K, V>(A, p.b, p.c, t0 - (K - 1) + k), win[k]);
     }
-    const long long xat = p.b * A.xbs + p.c, yat = (long long)p.b * A.T * A.C + p.c;
-    for (int tb = t0; tb < te; tb += U) {
-        Vec<XT, V> r[U];
+    const XT* x = static_cast<const XT*>(A.x) + p.b * A.xbs + p.c + (long long)t0 * A.xts;
+    XT* y = static_cast<XT*>(A.y) + ((long long)p.b * A.T + t0) * A.C + p.c;
+    auto token = [&](const Vec<XT, V>& r) {
+        N s[H];
+        values<XT, V>(r, win[K - 1]);
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (tb + j < te) r[j] = load<XT, V>(A.x, xat + (tb + j) * A.xts);
+        for (int h = 0; h < H; ++h) {
+            s[h] = bias[h];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (tb + j >= te) break;
-            values<XT, V>(r[j], win[K - 1]);
-            float y[V];
+            for (int k = 0; k < K; ++k) s[h] = mad(w[k][h], win[k][h], s[h]);
+            if (A.silu) s[h] = mul(s[h], sigmoid(s[h]));
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float s = bias[v];
-#pragma unroll
-                for (int k = 0; k < K; ++k) s = fmaf(w[k][v], win[k][v], s);
-                y[v] = A.silu ? s * sigmoid(s) : s;
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) win[k][v] = win[k + 1][v];
-            }
-            store<XT, V>(A.y, yat + (long long)(tb + j) * A.C, y);
+            for (int k = 0; k < K - 1; ++k) win[k][h] = win[k + 1][h];
         }
-    }
-    const float none[V] = {};
-    for (int t = max(t0, te); t < t1; ++t) store<XT, V>(A.y, yat + (long long)t * A.C, none);  // behind the end
-    if (p.run == 0 && A.state_out) {
+        store<XT, V>(y, 0, s);
+        y += A.C;
+    };
+    int t = t0;
+    Vec<XT, V> r[U], next[U];  // U tokens' loads are under way while U tokens are worked on
+    auto fetch = [&](Vec<XT, V>* to) {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-            *reinterpret_cast<Vec<XT, V>*>(static_cast<XT*>(A.state_out) + ((long long)p.b * (K - 1) + j) * A.C + p.c) = last[j];
+        for (int j = 0; j < U; ++j) to[j] = load<XT, V>(x, j * A.xts);
+        x += U * A.xts;
+    };
+    if (t + U <= te) fetch(r);
+#pragma unroll 1
+    for (; t + U <= te; t += U) {
+        if (t + 2 * U <= te) fetch(next);
+#pragma unroll
+        for (int j = 0; j < U; ++j) token(r[j]), r[j] = next[j];
     }
+#pragma unroll 1
+    for (; t < te; ++t, x += A.xts) token(load<XT, V>(x, 0));
+    N zero[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) fill(zero[h], 0.f);
+#pragma unroll 1
+    for (t = max(t0, te); t < t1; ++t, y += A.C) store<XT, V>(y, 0, zero);  // behind the end
+    if (!tail) return;
+    if (p.len >= K - 1) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) last[j] = load<XT, V>(A.x, p.b * A.xbs + (long long)(p.len - (K - 1) + j) * A.xts + p.c);
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        *reinterpret_cast<Vec<XT, V>*>(static_cast<XT*>(A.state_out) + ((long long)p.b * (K - 1) + j) * A.C + p.c) = last[j];
 }
 
 // One token: the state's rows move up by one
 template <class XT, int K, int V>
 __global__ void __launch_bounds__(256) step_kernel(const ConvArgs A) {
+    using N = typename Numbers<V>::N;
+    constexpr int H = Numbers<V>::H;
     const Place<V> p(A);
     if (!p.in) return;
-    float w[K][V], bias[V], x[V], y[V];
+    N w[K][H], y[H], x[H];
     Vec<XT, V> r[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k] = input<XT, K, V>(A, p.b, p.c, k - (K - 1));
-    weights<XT, K, V>(A, p.c, w, bias);
-#pragma unroll
-    for (int v = 0; v < V; ++v) y[v] = bias[v];
+    weights<XT, K, V>(A, p.c, w, y);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         values<XT, V>(r[k], x);
 #pragma unroll
-        for (int v = 0; v < V; ++v) y[v] = fmaf(w[k][v], x[v], y[v]);
+        for (int h = 0; h < H; ++h) y[h] = mad(w[k][h], x[h], y[h]);
     }
+    if (A.silu)
 #pragma unroll
-    for (int v = 0; v < V; ++v) y[v] = A.silu ? y[v] * sigmoid(y[v]) : y[v];
+        for (int h = 0; h < H; ++h) y[h] = mul(y[h], sigmoid(y[h]));
     store<XT, V>(A.y, (long long)p.b * A.C + p.c, y);
 #pragma unroll
     for (int k = 1; k < K; ++k)
@@ -168,91 +244,124 @@ __global__ void __launch_bounds__(256) step_kernel(const ConvArgs A) {
 
 // A run's dx needs e of the K-1 tokens behind it, whose own inputs reach K-1 tokens back: x and dy of 2 (K-1)
 // and K-1 tokens are read twice. The weights' gradients are summed over the run and written as
-// one row [C][K+1] of the workspace per run.
+// one row [K+1][C] of the workspace per run.
 template <class XT, int K, int V>
-__global__ void __launch_bounds__(256) bwd_kernel(const ConvArgs A) {
-    constexpr int U = 4;
+__global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) bwd_kernel(const ConvArgs A) {
+    using N = typename Numbers<V>::N;
+    constexpr int U = 4, H = Numbers<V>::H;
     const Place<V> p(A);
     if (!p.in) return;
-    float w[K][V], bias[V], win[K][V], e[K][V] = {}, dw[K][V] = {}, db[V] = {};  // e[j]: e_{t-K+1+j}
+    N w[K][H], bias[H], win[K][H], e[K][H], dw[K][H], db[H], one, minus;  // e[j]: e_{t-K+1+j}
+    fill(one, 1.f), fill(minus, -1.f);
     weights<XT, K, V>(A, p.c, w, bias);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        fill(db[h], 0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) fill(e[k][h], 0.f), fill(dw[k][h], 0.f);
+    }
     const int t0 = p.run * A.run, t1 = min(A.T, t0 + A.run), te = min(t1, p.len);
-    const long long xat = p.b * A.xbs + p.c, gat = p.b * A.ybs + p.c, oat = (long long)p.b * A.T * A.C + p.c;
-    // what the final state's cotangent adds to input row s
-    auto state_part = [&](int s, float* f) {
-        const int j = s - (p.len - (K - 1));
-        if (!A.dstate_out || j < 0 || s >= p.len) return;
-        float d[V];
-        values<XT, V>(load<XT, V>(A.dstate_out, ((long long)p.b * (K - 1) + j) * A.C + p.c), d);
-#pragma unroll
-        for (int v = 0; v < V; ++v) f[v] += d[v];
-    };
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k)
-        if (t0 < te) values<XT, V>(input<XT, K, V>(A, p.b, p.c, t0 - (K - 1) + k), win[k]);
     const bool head = p.run == 0 && A.dstate;  // writes the gradients of the rows before the first token
-    const int end = t0 < te || head ? te + K - 1 : t0;
-    for (int tb = t0; tb < end; tb += U) {
-        Vec<XT, V> rx[U], rg[U];
+    if (t0 < te) {
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (tb + j < min(end, p.len)) rx[j] = load<XT, V>(A.x, xat + (tb + j) * A.xts), rg[j] = load<XT, V>(A.dy, gat + (tb + j) * A.yts);
+        for (int k = 0; k < K - 1; ++k) values<XT, V>(input<XT, K, V>(A, p.b, p.c, t0 - (K - 1) + k), win[k]);
+    }
+    const XT* x = static_cast<const XT*>(A.x) + p.b * A.xbs + p.c + (long long)t0 * A.xts;
+    const XT* dy = static_cast<const XT*>(A.dy) + p.b * A.ybs + p.c + (long long)t0 * A.yts;
+    XT* dx = static_cast<XT*>(A.dx) + ((long long)p.b * A.T + t0) * A.C + p.c;
+    // e of the next token, from its x and dy; SUM: it is one of the run's
+    auto forward = [&](const Vec<XT, V>& rx, const Vec<XT, V>& ry, bool sum) {
+        values<XT, V>(rx, win[K - 1]);
+        values<XT, V>(ry, e[K - 1]);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            if (A.silu) {
+                N s = bias[h];
+#pragma unroll
+                for (int k = 0; k < K; ++k) s = mad(w[k][h], win[k][h], s);
+                const N q = sigmoid(s);
+                e[K - 1][h] = mul(e[K - 1][h], mad(mul(s, q), mad(q, minus, one), q));
+            }
+            if (sum) {
+                db[h] = add(db[h], e[K - 1][h]);
+#pragma unroll
+                for (int k = 0; k < K; ++k) dw[k][h] = mad(e[K - 1][h], win[k][h], dw[k][h]);
+            }
+        }
+    };
+    // the gradient of the token K - 1 back
+    auto gradient = [&](N* d) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            d[h] = mul(w[K - 1][h], e[0][h]);
+#pragma unroll
+            for (int k = 1; k < K; ++k) d[h] = mad(w[K - 1 - k][h], e[k][h], d[h]);
+        }
+    };
+    auto shift = [&]() {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+            for (int h = 0; h < H; ++h) win[k][h] = win[k + 1][h], e[k][h] = e[k + 1][h];
+    };
+    // the token t = s + K - 1, one at a time, and what the ends of run and sequence need
+    auto careful = [&](int t) {
+        if (t < p.len) {
+            forward(load<XT, V>(x, 0), load<XT, V>(dy, 0), t < te);
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) fill(e[K - 1][h], 0.f);
+        }
+        x += A.xts, dy += A.yts;
+        const int s = t - (K - 1);
+        if (s >= t0 || head) {
+            N d[H], more[H];
+            gradient(d);
+            const int j = s - (p.len - (K - 1));  // the final state's row
+            if (A.dstate_out && j >= 0 && s < p.len) {
+                values<XT, V>(load<XT, V>(A.dstate_out, ((long long)p.b * (K - 1) + j) * A.C + p.c), more);
+#pragma unroll
+                for (int h = 0; h < H; ++h) d[h] = add(d[h], more[h]);
+            }
+            if (s >= t0) store<XT, V>(dx, 0, d), dx += A.C;
+            else store<XT, V>(A.dstate, ((long long)p.b * (K - 1) + K - 1 + s) * A.C + p.c, d);
+        }
+        shift();
+    };
+    const int end = t0 < te || head ? te + K - 1 : t0;
+    int t = t0;
+#pragma unroll 1
+    for (; t < min(end, t0 + K - 1); ++t) careful(t);
+    // tokens of the run whose K - 1 back are its own too, and no rows of the final state
+    const int whole = A.dstate_out ? min(te, p.len - (K - 1)) : te;
+    for (; t + U <= whole; t += U) {
+        Vec<XT, V> rx[U], ry[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) rx[j] = load<XT, V>(x, j * A.xts), ry[j] = load<XT, V>(dy, j * A.yts);
+        x += U * A.xts, dy += U * A.yts;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int t = tb + j;
-            if (t >= end) break;
-            if (t < p.len) {
-                values<XT, V>(rx[j], win[K - 1]);
-                values<XT, V>(rg[j], e[K - 1]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (A.silu) {
-                        float s = bias[v];
-#pragma unroll
-                        for (int k = 0; k < K; ++k) s = fmaf(w[k][v], win[k][v], s);
-                        const float q = sigmoid(s);
-                        e[K - 1][v] *= fmaf(s * q, 1.f - q, q);
-                    }
-                }
-                if (t < te) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        db[v] += e[K - 1][v];
-#pragma unroll
-                        for (int k = 0; k < K; ++k) dw[k][v] = fmaf(e[K - 1][v], win[k][v], dw[k][v]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[K - 1][v] = 0.f;
-            }
-            const int s = t - (K - 1);
-            if (s >= t0 || head) {
-                float d[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    d[v] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) d[v] = fmaf(w[K - 1 - k][v], e[k][v], d[v]);
-                }
-                state_part(s, d);
-                if (s >= t0) store<XT, V>(A.dx, oat + (long long)s * A.C, d);
-                else store<XT, V>(A.dstate, ((long long)p.b * (K - 1) + K - 1 + s) * A.C + p.c, d);
-            }
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[k][v] = win[k + 1][v], e[k][v] = e[k + 1][v];
+            N d[H];
+            forward(rx[j], ry[j], true);
+            gradient(d);
+            store<XT, V>(dx, 0, d);
+            dx += A.C;
+            shift();
         }
     }
-    const float none[V] = {};
-    for (int t = max(t0, te); t < t1; ++t) store<XT, V>(A.dx, oat + (long long)t * A.C, none);
+#pragma unroll 1
+    for (; t < end; ++t) careful(t);
+    N zero[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) fill(zero[h], 0.f);
+    dx = static_cast<XT*>(A.dx) + (long long)p.b * A.T * A.C + p.c;
+#pragma unroll 1
+    for (t = max(t0, te); t < t1; ++t) store<XT, V>(dx, (long long)t * A.C, zero);  // behind the end
     if (!A.parts) return;
-    float* out = A.parts + ((long long)p.b * A.runs + p.run) * (K + 1) * A.C + p.c;  // [K+1][C]
+    float* out = A.parts + ((long long)p.b * A.runs + p.run) * (K + 1) * A.C + p.c;
 #pragma unroll
-    for (int k = 0; k <= K; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) out[(long long)k * A.C + v] = k < K ? dw[k < K ? k : 0][v] : db[v];
+    for (int k = 0; k < K; ++k) store<float, V>(out, (long long)k * A.C, dw[k]);
+    store<float, V>(out, (long long)K * A.C, db);
 }
 
 // Column sums of [n][(K+1) C]: 32 columns and 32 slices of the rows per CTA, slices added up in order.
