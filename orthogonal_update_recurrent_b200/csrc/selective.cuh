@@ -240,8 +240,6 @@ __device__ __forceinline__ void step_sizes(const SelArgs& A, const Raw<float, V>
         else if (slope) slope[k] = f2(1.f);
     }
 }
-__device__ __forceinline__ F2 low(ulonglong2 v) { return F2{v.x}; }
-__device__ __forceinline__ F2 high(ulonglong2 v) { return F2{v.y}; }
 __device__ __forceinline__ float total(F2 a) {
     float x, y;
     parts(a, x, y);
@@ -262,7 +260,7 @@ struct Place {
     static constexpr int CH = 32 / L, CT = NW * CH, V = sel_width(L), P = (V + 1) / 2;
     static constexpr int QUADS = CT / V, ROWS = NT / QUADS, PI = (TT + ROWS - 1) / ROWS;
     static constexpr int CTP = CT + CH;              // floats from lane to lane of the sums over n: lanes apart in the banks
-    static constexpr int DW = CT + (V > 1 ? 2 * V : 0);  // a token's entries of dtu
+    static constexpr int DW = CT + (V > 1 ? 4 * V : 0);  // a token's entries of du
     int b, s, ct, g, c0, cend, t0, t1, te;           // tokens t0..t1, te: up to the sequence's end
     int lane, gl, cl, c, ch, first, row;             // states' lane, channel; the V channels' first in the tile, and first row
     bool live;
@@ -280,15 +278,16 @@ struct Place {
     }
     __device__ __forceinline__ int column() const { return c0 + first; }
     __device__ __forceinline__ int width() const { return min(V, max(0, cend - column())); }  // of the V channels, inside the group
-    // where channel c of a token stands in dtu: the V of a thread apart, so that neither writes nor reads meet in a bank
-    static __device__ __forceinline__ int entry(int c) { return c % V * (QUADS + (V > 1 ? 2 : 0)) + c / V; }
-    // the thread's entries: (d, d, u, u) of every channel
-    __device__ __forceinline__ void write(ulonglong2* dtu, int r, const F2* d, const F2* u) const {
+    // where channel c of a token stands in du: the V of a thread apart, so that neither writes nor reads meet in a bank
+    static constexpr int STEP = QUADS + (V > 1 ? 4 : 0);
+    static __device__ __forceinline__ int entry(int c) { return c % V * STEP + c / V; }
+    // the thread's entries: (d, u) of every channel
+    __device__ __forceinline__ void write(float2* du, int r, const F2* d, const F2* u) const {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             float d0, d1, u0, u1;
             parts(d[k / 2], d0, d1), parts(u[k / 2], u0, u1);
-            dtu[r * DW + k * (QUADS + (V > 1 ? 2 : 0)) + first / V] = make_ulonglong2(f2(k & 1 ? d1 : d0).v, f2(k & 1 ? u1 : u0).v);
+            du[r * DW + k * STEP + first / V] = make_float2(k & 1 ? d1 : d0, k & 1 ? u1 : u0);
         }
     }
 };
@@ -379,24 +378,43 @@ __device__ __forceinline__ void read_vec(const float* p, F2* v) {
         v[0].v = *reinterpret_cast<const unsigned long long*>(p);
     }
 }
-// The decays and the writes u b of M tokens, from shared memory: du (dt, dt, u, u) and v (b) with their tokens' strides
+// M tokens' (dt, u) and b as they stand in shared memory, with the tokens' strides, and from them the decays and the writes u b.
+// Read and worked on apart, so that the reads can go before the stores of the tokens before.
 template <int M, int S>
-__device__ __forceinline__ void decays(const ulonglong2* du, int dstride, const float* v, int vstride, const F2* A2, F2 (*a)[S / 2],
-                                       F2 (*u)[S / 2]) {
-    constexpr int H = S / 2;
-    F2 t[M * H];
+struct Tokens {
+    static constexpr int H = S / 2;
+    float2 du[M];
+    F2 u[M][H], a[M][H];
+    __device__ __forceinline__ void read(const float2* d, int dstride, const float* v, int vstride) {
 #pragma unroll
-    for (int j = 0; j < M; ++j) {
-        const ulonglong2 d = du[j * dstride];
-        read_vec<S>(v + j * vstride, u[j]);
-#pragma unroll
-        for (int k = 0; k < H; ++k) t[j * H + k] = mul2(low(d), A2[k]), u[j][k] = mul2(high(d), u[j][k]);
+        for (int j = 0; j < M; ++j) {
+            du[j] = d[j * dstride];
+            read_vec<S>(v + j * vstride, u[j]);
+        }
     }
-    decay<M * H>(t);
+    __device__ __forceinline__ void work(const F2* A2) {
+        F2 t[M * H];
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+#pragma unroll
+            for (int k = 0; k < H; ++k) t[j * H + k] = mul2(f2(du[j].x), A2[k]), u[j][k] = mul2(f2(du[j].y), u[j][k]);
+        decay<M * H>(t);
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+#pragma unroll
+            for (int k = 0; k < H; ++k) a[j][k] = t[j * H + k];
+    }
+};
+template <int M, int S>
+__device__ __forceinline__ void decays(const float2* du, int dstride, const float* v, int vstride, const F2* A2, F2 (*a)[S / 2],
+                                       F2 (*u)[S / 2]) {
+    Tokens<M, S> t;
+    t.read(du, dstride, v, vstride);
+    t.work(A2);
 #pragma unroll
     for (int j = 0; j < M; ++j)
 #pragma unroll
-        for (int k = 0; k < H; ++k) a[j][k] = t[j * H + k];
+        for (int k = 0; k < S / 2; ++k) a[j][k] = t.a[j][k], u[j][k] = t.u[j][k];
 }
 // Four states' values of b or c of one token. VEC: N is a multiple of four and they can be read at once
 template <bool VEC, class XT>
@@ -425,7 +443,7 @@ __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, in
 template <class XT, int L, int S>
 struct FwdShared {
     static constexpr int NP = L * S, CT = Place<L>::CT;
-    ulonglong2 dtu[2][TT * Place<L>::DW];        // (dt, dt, u, u), u = dt x
+    float2 du[2][TT * Place<L>::DW];             // (dt, u), u = dt x
     float gate[2][TT * CT], skip[2][TT * CT];    // silu(z) and skip x, for the thread that wrote them
     float b[2][TT * NP], c[2][TT * NP];
     float y[2][TT * L * Place<L>::CTP];          // the lanes' parts of the sums over n
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
                 if (!in) dt[q] = f2(0.f);
                 u[q] = mul2(dt[q], x[q]);  // rows behind the end were read as 0
             }
-            p.write(sh.dtu[buf], r, dt, u);
+            p.write(sh.du[buf], r, dt, u);
             if (!A.y) continue;
             if (A.skip) {
 #pragma unroll
@@ -540,26 +558,40 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
         if (i + 1 < tiles) prepare(tb + TT, buf ^ 1);
         if (i + 2 < tiles) fetch(tb + 2 * TT);
         float* ys = sh.y[buf] + p.gl * CTP + p.c;
+        const float2* du = sh.du[buf] + entry;
+        const float *vb = sh.b[buf] + n0, *vc = sh.c[buf] + n0;
+        F2 kept[TT / kSelMark][H];
+        Tokens<4, S> now, next;
+        now.read(du, P::DW, vb, NP);
+        now.work(A2);
 #pragma unroll
         for (int q = 0; q < TT; q += 4) {
-            if (q % kSelMark == 0 && marks && tb + q < p.te) {
-                float v[S];
-                unpack<S>(h, v);
-                store_states<S>(mark, n0, A.N, A.vec_n, v);
-                mark += (long long)A.E * A.N;
-            }
-            F2 a[4][H], u[4][H];
-            decays<4, S>(sh.dtu[buf] + q * P::DW + entry, P::DW, sh.b[buf] + q * NP + n0, NP, A2, a, u);
+            F2 cv[4][H];
+            if (q + 4 < TT) next.read(du + (q + 4) * P::DW, P::DW, vb + (q + 4) * NP, NP);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) read_vec<S>(vc + (q + j) * NP, cv[j]);
+            if (q + 4 < TT) next.work(A2);  // beside the chain below
+            if (q % kSelMark == 0)
+#pragma unroll
+                for (int k = 0; k < H; ++k) kept[q / kSelMark][k] = h[k];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                F2 cv[H], yy;
-                read_vec<S>(sh.c[buf] + (q + j) * NP + n0, cv);
+                F2 yy;
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
-                    h[k] = fma2(a[j][k], h[k], u[j][k]);
-                    yy = k ? fma2(h[k], cv[k], yy) : mul2(h[k], cv[k]);
+                    h[k] = fma2(now.a[j][k], h[k], now.u[j][k]);
+                    yy = k ? fma2(h[k], cv[j][k], yy) : mul2(h[k], cv[j][k]);
                 }
                 ys[(q + j) * L * CTP] = total(yy);
+            }
+            now = next;
+        }
+        if (marks) {
+#pragma unroll
+            for (int m = 0; m < TT / kSelMark; ++m, mark += (long long)A.E * A.N) {
+                float v[S];
+                unpack<S>(kept[m], v);
+                if (tb + m * kSelMark < p.te) store_states<S>(mark, n0, A.N, A.vec_n, v);
             }
         }
         __syncthreads();
@@ -581,7 +613,7 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
 template <class XT, int L, int S>
 struct SegShared {
     static constexpr int NP = L * S;
-    ulonglong2 dtu[2][TT * Place<L>::DW];  // (dt, dt, w, w), w = dt x or dy silu(z)
+    float2 du[2][TT * Place<L>::DW];       // (dt, w), w = dt x or dy silu(z)
     float v[2][TT * NP];                   // b or c
     float sum[NT * 4];
 };
@@ -643,7 +675,7 @@ __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
                 else if (gated) w[q] = mul2(w[q], mul2(z[q], sigmoid(z[q])));
                 sum[q] = add2(sum[q], dt[q]);
             }
-            p.write(sh.dtu[buf], r, dt, w);
+            p.write(sh.du[buf], r, dt, w);
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -660,18 +692,26 @@ __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
         const int buf = i & 1;
         if (i + 1 < tiles) prepare(base(i + 1), buf ^ 1);
         if (i + 2 < tiles) fetch(base(i + 2));
+        const float2* du = sh.du[buf] + entry;
+        const float* v = sh.v[buf] + n0;
+        Tokens<4, S> now, next;
+        now.read(du + (REV ? TT - 4 : 0) * P::DW, P::DW, v + (REV ? TT - 4 : 0) * NP, NP);
+        now.work(A2);
 #pragma unroll
         for (int i4 = 0; i4 < TT; i4 += 4) {
-            const int q = REV ? TT - 4 - i4 : i4;
-            F2 a[4][H], u[4][H];
-            decays<4, S>(sh.dtu[buf] + q * P::DW + entry, P::DW, sh.v[buf] + q * NP + n0, NP, A2, a, u);
+            const int q = REV ? TT - 8 - i4 : i4 + 4;
+            if (i4 + 4 < TT) {
+                next.read(du + q * P::DW, P::DW, v + q * NP, NP);
+                next.work(A2);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
-                    if constexpr (REV) h[k] = mul2(a[3 - j][k], add2(u[3 - j][k], h[k]));
-                    else h[k] = fma2(a[j][k], h[k], u[j][k]);
+                    if constexpr (REV) h[k] = mul2(now.a[3 - j][k], add2(now.u[3 - j][k], h[k]));
+                    else h[k] = fma2(now.a[j][k], h[k], now.u[j][k]);
                 }
+            now = next;
         }
         __syncthreads();
     }

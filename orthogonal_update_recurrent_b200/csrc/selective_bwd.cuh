@@ -21,10 +21,10 @@ struct BwdShared {
     static constexpr int VAR = L <= 8 ? 4 : L == 16 ? 2 : 1;  // orders of a lane's four states
     static constexpr int VS = TT * NP + (NP < 32 ? NP : 0);   // from order to order, apart in the banks
     static constexpr int QS = CT + 8;
-    ulonglong2 dtu[TT * Place<L>::DW];                        // (dt, dt, u, u), u = dt x
-    F2 w[TT * Place<L>::DW];                                  // (w, w)
+    float2 du[TT * Place<L>::DW];                             // (dt, u), u = dt x
+    float w[TT * Place<L>::DW];
     float x[TT * CT], slope[TT * CT], zf[TT * CT];            // for the thread that wrote them
-    float y[TT * L * CTP], du[TT * L * CTP];                  // the lanes' parts of the sums over n
+    float y[TT * L * CTP], g[TT * L * CTP];                   // y and du: the lanes' parts of the sums over n
     float dq[TT * QS];                                        // a whole one
     float b[VAR * VS], c[VAR * VS];
     float sums[2][NW][TT * NP];                               // dc and db of the warps' channels
@@ -220,12 +220,12 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
                 }
                 dskip[q] = fma2(w[q], x[q], dskip[q]);
             }
-            p.write(sh.dtu, r, dt, u);
+            p.write(sh.du, r, dt, u);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float w0, w1;
                 parts(w[v / 2], w0, w1);
-                sh.w[r * DW + P::entry(p.first + v)] = f2(v & 1 ? w1 : w0);
+                sh.w[r * DW + P::entry(p.first + v)] = v & 1 ? w1 : w0;
             }
             own_write<V>(sh.x + at, x);
             own_write<V>(sh.slope + at, slope);
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             if (r >= TT || t >= p.te) continue;
             const int at = r * CT + p.first;
             F2 x[Q], du[Q], f[Q], e[Q];
-            lane_sums<L>(sh.du + r * L * CTP + p.first, du);
+            lane_sums<L>(sh.g + r * L * CTP + p.first, du);
             own_read<V>(sh.x + at, x);
             own_read<V>(sh.slope + at, f);
             own_read<V>(sh.dq + r * QS + p.first, e);
@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             put_dt(t, e);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {  // dt du + skip w
-                float d[2] = {}, w[2] = {}, other;
+                float d[2] = {}, w[2] = {};
 #pragma unroll
                 for (int v = 0; v < (V > 1 ? 2 : 1); ++v) {
                     const int i = r * DW + P::entry(p.first + 2 * q + v);
-                    parts(low(sh.dtu[i]), d[v], other), parts(sh.w[i], w[v], other);
+                    d[v] = sh.du[i].x, w[v] = sh.w[i];
                 }
                 e[q] = fma2(f2(d[0], d[1]), du[q], mul2(skip[q], f2(w[0], w[1])));
             }
@@ -299,9 +299,9 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
         StateSums<L> sq;
         ChannelSums<L> sc;
         const float *vb = sh.b + order * VS + n0, *vc = sh.c + order * VS + n0;
-        const ulonglong2* dtu = sh.dtu + entry;
-        const F2* ws = sh.w + entry;
-        float *ys = sh.y + p.gl * CTP + p.c, *dus = sh.du + p.gl * CTP + p.c;
+        const float2* dtu = sh.du + entry;
+        const float* ws = sh.w + entry;
+        float *ys = sh.y + p.gl * CTP + p.c, *dus = sh.g + p.gl * CTP + p.c;
 #pragma unroll 1
         for (int q = TT - SB; q >= 0; q -= SB) {
             F2 a[SB][2], hp[SB][2], h[2];
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
 #pragma unroll
             for (int j = SB - 1; j >= 0; --j) {
                 const int t = q + j;
-                const ulonglong2 du = dtu[t * DW];
-                const F2 w = ws[t * DW];
+                const float2 d = dtu[t * DW];
+                const F2 dt = f2(d.x), u = f2(d.y), w = f2(ws[t * DW]);
                 F2 bv[2], cv[2], dc[2], db[2], yy, dd, qq;
                 read_vec<4>(vb + t * NP, bv);
                 read_vec<4>(vc + t * NP, cv);
@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
                     dc[k] = mul2(w, h[k]);
                     if constexpr (GATE) yy = k ? fma2(h[k], cv[k], yy) : mul2(h[k], cv[k]);
                     g[k] = fma2(w, cv[k], g[k]);
-                    db[k] = mul2(high(du), g[k]);
+                    db[k] = mul2(u, g[k]);
                     dd = k ? fma2(g[k], bv[k], dd) : mul2(g[k], bv[k]);
                     g[k] = mul2(a[j][k], g[k]);
                     const F2 ah = mul2(g[k], hp[j][k]);
                     qq = k ? fma2(ah, A2[k], qq) : mul2(ah, A2[k]);
-                    sA[k] = fma2(ah, low(du), sA[k]);
+                    sA[k] = fma2(ah, dt, sA[k]);
                     h[k] = hp[j][k];
                 }
                 if constexpr (GATE) ys[t * L * CTP] = total(yy);
