@@ -144,8 +144,9 @@ struct NormArgs {
 
 // short_conv.cuh: short causal convolution
 constexpr int kConvMaxK = 8;
-constexpr int kConvVec = 4;  // channels per thread, where vectors of as many can be read
-constexpr int kConvRun = 64, kConvBwdRun = 64, kConvMaxRuns = 1024;
+constexpr int kConvMostRun = 256;  // tokens of a thread's run, in eights
+// CTAs of 256 threads that an SM holds at once
+LATTICE_HD constexpr int conv_resident(bool bwd, int K) { return (bwd ? 2 : 3) - (K > 4); }
 constexpr int kConvMaxSize = 1 << 30;  // channels, and tokens
 constexpr int kConvFwd = 0, kConvBwd = 1, kConvStep = 2;
 

@@ -3,6 +3,6 @@
 
 namespace lattice {
 
-template lattice_status conv::launch<__half>(const ConvArgs& a, int what, bool vec, cudaStream_t st);
+template lattice_status conv::launch<__half>(const ConvArgs& a, int what, int V, cudaStream_t st);
 
 }  // namespace lattice

@@ -274,17 +274,37 @@ lattice_status check_conv(lattice_dtype x_dtype, lattice_dtype w_dtype, int B, i
     if (K > kConvMaxK || C > kConvMaxSize || T > kConvMaxSize) return LATTICE_ERR_UNSUPPORTED;
     return LATTICE_OK;
 }
-// Tokens of a thread's run: kConvRun, fewer (whole eights) where the device would not be filled, more where the
-// backward pass would leave more than kConvMaxRuns rows of weight gradients per sequence.
-int conv_run(long long B, int T, int C, bool bwd, bool vec) {
-    const long long per = vec ? kConvVec : 1, lanes = B * ((C + per - 1) / per), want = (long long)sm_count() * 1024;
-    long long run = bwd ? kConvBwdRun : kConvRun;
-    while (run > 8 && lanes * ((T + run - 1) / run) < want) run /= 2;
-    while (bwd && run < (1 << 29) && (T + run - 1) / run > kConvMaxRuns) run *= 2;
-    return (int)run;
+// Channels per thread: as many as every row, output and weight can be read and written in vectors of
+int conv_width(const ConvArgs& a, size_t sx, size_t sw) {
+    for (int V = 4; V > 1; V /= 2) {
+        const size_t v = V * sx;
+        if (a.C % V == 0 && rows_vec(a.x, sx, a.B, a.T, a.xbs, a.xts, v) && (!a.dy || rows_vec(a.dy, sx, a.B, a.T, a.ybs, a.yts, v)) &&
+            aligned(a.y, v) && aligned(a.state, v) && aligned(a.state_out, v) && aligned(a.dx, v) && aligned(a.dstate, v) &&
+            aligned(a.dstate_out, v) && aligned(a.w, V * sw) && aligned(a.bias, V * sw))
+            return V;
+    }
+    return 1;
 }
-size_t conv_workspace(int B, int T, int C, int K) {  // either width of a thread's channels
-    const int a = conv_run(B, T, C, true, true), b = conv_run(B, T, C, true, false), run = a < b ? a : b;
+// Tokens of a thread's run: those with which the waves of CTAs that the device holds at once take the fewest tokens one after
+// the other, the inputs that a run reads beside its own and its start (as long as some 8 tokens) among them. (8 x 4096 tokens of 2048 bf16
+// channels, 4 taps, forward: 1024 CTAs of 64 tokens, in 2.3 waves, 66 us.)
+int conv_run(long long B, int T, int C, int K, bool bwd, int V) {
+    const long long lanes = B * (C / V), held = (long long)sm_count() * conv_resident(bwd, K);
+    const int beside = (bwd ? 3 : 1) * (K - 1) + 8;
+    int best = 8;
+    long long least = -1;
+    for (int run = 8; run <= kConvMostRun; run += 8) {
+        const long long ctas = (lanes * ((T + (long long)run - 1) / run) + 255) / 256, cost = (ctas + held - 1) / held * (run + beside);
+        if (least < 0 || cost <= least) least = cost, best = run;
+    }
+    return best;
+}
+size_t conv_workspace(int B, int T, int C, int K) {  // for any width of a thread's channels
+    int run = kConvMostRun;
+    for (int V = 1; V <= 4; V *= 2) {
+        const int r = C % V ? run : conv_run(B, T, C, K, true, V);
+        run = r < run ? r : run;
+    }
     return (size_t)B * (((size_t)T + run - 1) / run) * (K + 1) * C * 4;
 }
 void conv_args(ConvArgs& a, const void* x, lattice_dtype x_dtype, long long xbs, long long xts, const void* w, const void* bias,
@@ -300,26 +320,34 @@ struct SelPlan {
     int S, tiles, nseg, seg;
 };
 long long sel_tiles(int Eg, int lanes) { return ((long long)Eg + kSelThreads / lanes - 1) / (kSelThreads / lanes); }
-// How the work is spread. A CTA has 256/L channels with N padded to L S states, and a whole sequence, which fills
-// the device from one CTA per SM on. With fewer: two states per lane instead of four (twice the CTAs, of half the work per
-// token), or the time axis in segments, whose states take a pass of their own and so twice the exponentials
-// (backward: half as many again). The cheapest of these, by the work on the fullest SM.
+// How the work is spread. A CTA has 256/L channels with N padded to L S states, and goes through its tokens alone. With few
+// CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose
+// states take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token and by
+// CTAs per SM, are what was measured (bf16, 16 states, gate; they hold for other N, whose CTAs have as many states), the cheapest
+// sum is taken: forward, 1024 / 2048 / 4096 / 6144 channels of 4096, 4096, 2048, 2048 tokens: four states 383 / 386 / 202 / 200 us,
+// two states 246 / 246 / 134 / 196, segments 88 / 142 / 143 / 200; backward, whole 1155 / 1201 / 627 / 637, segments
+// 190 / 304 / 331 / 429.
 SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
     const int np = sel_padded(N), Eg = E / G;
     const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4);
+    auto time = [&](long long ctas, double one, double two, double more) {
+        const long long per = (ctas + sm - 1) / sm;
+        return per == 1 ? one : per == 2 ? two : more * (double)per;
+    };
     SelPlan p = {4, (int)sel_tiles(Eg, np / 4), 1, T > 0 ? T : 1};
-    auto rounds = [&](long long ctas) { return (double)((ctas + sm - 1) / sm); };
-    double best = rounds(base);
+    double best = T * (bwd ? time(base, 0.30, 0.455, 0.23) : time(base, 0.098, 0.163, 0.0815));
     if (!bwd && np <= 32) {
         const long long tiles = sel_tiles(Eg, np / 2);
-        const double cost = 0.55 * rounds((long long)B * G * tiles);
-        if (cost < best) best = cost, p.S = 2, p.tiles = (int)tiles;
+        const double us = T * time((long long)B * G * tiles, 0.065, 0.107, 0.0515);
+        if (us < best) best = us, p.S = 2, p.tiles = (int)tiles;
     }
-    long long n = 2 * sm / base, most = T / (8 * kSelTile);
-    if (n > most) n = most;
-    if (n > 1 && (bwd ? 1.6 : 2.1) * rounds(base * n) / n < best) {
-        const long long tiles = ((long long)T + kSelTile - 1) / kSelTile, per = (tiles + n - 1) / n;
-        p = {4, (int)sel_tiles(Eg, np / 4), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
+    const long long tiles = ((long long)T + kSelTile - 1) / kSelTile;
+    long long n = 2 * sm / base;
+    if (n > tiles / 4) n = tiles / 4;
+    if (n > 1) {
+        const long long per = (tiles + n - 1) / n;
+        const double us = per * kSelTile * (bwd ? time(base * n, 0.37, 0.565, 0.29) : time(base * n, 0.168, 0.26, 0.13)) + (bwd ? 15 : 12);
+        if (us < best) p = {4, (int)sel_tiles(Eg, np / 4), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
     }
     return p;
 }
@@ -878,12 +906,10 @@ lattice_status lattice_short_conv_fwd(const void* x, lattice_dtype x_dtype, long
     conv_args(a, x, x_dtype, x_batch_stride, x_token_stride, w, bias, w_dtype, state, lengths, B, T, C, K, act);
     a.y = y;
     a.state_out = K > 1 ? state_out : nullptr;
-    const size_t v = kConvVec * sx;
-    const bool vec = C % kConvVec == 0 && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && aligned(y, v) && aligned(state, v) &&
-                     aligned(state_out, v) && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw);
-    a.run = conv_run(B, T, C, false, vec);
+    const int V = conv_width(a, sx, sw);
+    a.run = conv_run(B, T, C, K, false, V);
     a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
-    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvFwd, vec, static_cast<cudaStream_t>(stream)); });
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvFwd, V, static_cast<cudaStream_t>(stream)); });
 }
 
 size_t lattice_short_conv_bwd_workspace_bytes(int B, int T, int C, int K) {
@@ -922,12 +948,10 @@ lattice_status lattice_short_conv_bwd(const void* x, lattice_dtype x_dtype, long
     a.dstate = K > 1 ? dstate : nullptr;
     a.dstate_out = K > 1 ? dstate_out : nullptr;
     a.parts = sums ? static_cast<float*>(workspace) : nullptr;
-    const size_t v = kConvVec * sx;
-    const bool vec = C % kConvVec == 0 && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw) && rows_vec(x, sx, B, T, a.xbs, a.xts, v) && rows_vec(dy, sx, B, T, a.ybs, a.yts, v) &&
-                     aligned(dx, v) && aligned(state, v) && aligned(dstate, v) && aligned(dstate_out, v);
-    a.run = conv_run(B, T, C, true, vec);
+    const int V = conv_width(a, sx, sw);
+    a.run = conv_run(B, T, C, K, true, V);
     a.runs = T > a.run ? (int)((T + (long long)a.run - 1) / a.run) : 1;
-    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvBwd, vec, static_cast<cudaStream_t>(stream)); });
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvBwd, V, static_cast<cudaStream_t>(stream)); });
 }
 
 lattice_status lattice_short_conv_step(const void* state, void* state_out, const void* x, lattice_dtype x_dtype,
@@ -948,10 +972,8 @@ lattice_status lattice_short_conv_step(const void* state, void* state_out, const
     conv_args(a, x, x_dtype, x_batch_stride, 0, w, bias, w_dtype, state, nullptr, B, 1, C, K, act);
     a.y = y; a.state_out = state_out;
     a.run = 8, a.runs = 1;
-    const size_t v = kConvVec * sx;
-    const bool vec = C % kConvVec == 0 && rows_vec(x, sx, B, 1, a.xbs, 0, v) && aligned(y, v) && aligned(state, v) &&
-                     aligned(state_out, v) && aligned(w, kConvVec * sw) && aligned(bias, kConvVec * sw);
-    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvStep, vec, static_cast<cudaStream_t>(stream)); });
+    const int V = conv_width(a, sx, sw);
+    return with_x(x_dtype, [&](auto t) { return conv::launch<decltype(t)>(a, kConvStep, V, static_cast<cudaStream_t>(stream)); });
 }
 
 size_t lattice_selective_scan_marks_bytes(int B, int T, int E, int N) {

@@ -67,10 +67,10 @@ template <class XT> lattice_status launch_layer(bool bwd, NormArgs a, int mode, 
 int norm_parts(long long N, int D);  // at most so many
 lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st);
 
-// conv_*.cu: short convolution, a unit per type of x (no waits in it, and so no status word). vec: rows
-// can be read in vectors of as many channels as a thread has
+// conv_*.cu: short convolution, a unit per type of x (no waits in it, and so no status word). V: channels
+// per thread, 4, 2 or 1, as many as rows can be read in vectors of
 namespace conv {
-template <class XT> lattice_status launch(const ConvArgs& a, int what, bool vec, cudaStream_t st);
+template <class XT> lattice_status launch(const ConvArgs& a, int what, int V, cudaStream_t st);
 }  // namespace conv
 
 // sel_fwd_*.cu, sel_bwd_*.cu: selective scan, a unit per type of x (no waits either). S: states per lane

@@ -127,6 +127,43 @@ __device__ __forceinline__ void weights(const ConvArgs& A, int c, typename Numbe
     }
 }
 
+// The thread's next D tokens of one array on their way through shared memory, in groups of U: cp.async needs no registers, and
+// since every thread reads what it copied itself, no barrier. Pieces of less than 4 bytes (one 16-bit channel per
+// thread) cannot be copied so; they are loaded U tokens ahead of the work.
+template <class T, int V, int U, int D>
+struct Ahead {
+    static constexpr bool RING = sizeof(T) * V >= 4;
+    static constexpr int BYTES = RING ? D * 256 * (int)sizeof(T) * V : 16;
+    uint32_t slot;
+    Vec<T, V> next[RING ? 1 : U];
+    __device__ __forceinline__ explicit Ahead(const Vec<T, V>* ring) {
+        slot = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
+    }
+    // group g's U tokens, of which `n` are there, the first at p
+    __device__ __forceinline__ void fetch(int g, const T* p, long long ts, int n) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (j >= n) continue;
+            if constexpr (RING) {
+                const uint32_t to = slot + ((g * U + j) % D) * 256 * (uint32_t)sizeof(Vec<T, V>);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p + j * ts), "n"((int)sizeof(Vec<T, V>)) : "memory");
+            } else {
+                next[j] = load<T, V>(p, j * ts);
+            }
+        }
+    }
+    __device__ __forceinline__ void take(int g, const Vec<T, V>* ring, Vec<T, V>* r) const {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if constexpr (RING) r[j] = ring[((g * U + j) % D) * 256 + threadIdx.x];
+            else r[j] = next[j];
+        }
+    }
+};
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Who does what: V channels and a run of A.run tokens of one sequence per thread.
 template <int V>
 struct Place {
@@ -149,7 +186,7 @@ __device__ __forceinline__ Vec<XT, V> input(const ConvArgs& A, int b, int c, int
 }
 
 template <class XT, int K, int V>
-__global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) fwd_kernel(const ConvArgs A) {
+__global__ void __launch_bounds__(256, conv_resident(false, K)) fwd_kernel(const ConvArgs A) {
     using N = typename Numbers<V>::N;
     constexpr int U = 4, H = Numbers<V>::H;
     const Place<V> p(A);
@@ -246,9 +283,11 @@ __global__ void __launch_bounds__(256) step_kernel(const ConvArgs A) {
 // and K-1 tokens are read twice. The weights' gradients are summed over the run and written as
 // one row [K+1][C] of the workspace per run.
 template <class XT, int K, int V>
-__global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) bwd_kernel(const ConvArgs A) {
+__global__ void __launch_bounds__(256, conv_resident(true, K)) bwd_kernel(const ConvArgs A) {
     using N = typename Numbers<V>::N;
-    constexpr int U = 4, H = Numbers<V>::H;
+    constexpr int U = 2, H = Numbers<V>::H, D = sizeof(XT) * V > 8 ? 4 : 8;
+    using Q = Ahead<XT, V, U, D>;
+    __shared__ __align__(16) Vec<XT, V> ring[Q::RING ? 2 * D * 256 : 1];
     const Place<V> p(A);
     if (!p.in) return;
     N w[K][H], bias[H], win[K][H], e[K][H], dw[K][H], db[H], one, minus;  // e[j]: e_{t-K+1+j}
@@ -334,20 +373,38 @@ __global__ void __launch_bounds__(256, K <= 4 ? 2 : 1) bwd_kernel(const ConvArgs
     for (; t < min(end, t0 + K - 1); ++t) careful(t);
     // tokens of the run whose K - 1 back are its own too, and no rows of the final state
     const int whole = A.dstate_out ? min(te, p.len - (K - 1)) : te;
-    for (; t + U <= whole; t += U) {
-        Vec<XT, V> rx[U], ry[U];
+    const int n = whole - t;
+    if (n >= U) {
+        Q qx(ring), qy(ring + (Q::RING ? D * 256 : 0));
+        constexpr int G = Q::RING ? D / U - 1 : 1;  // groups ahead
+        const int groups = n / U;
 #pragma unroll
-        for (int j = 0; j < U; ++j) rx[j] = load<XT, V>(x, j * A.xts), ry[j] = load<XT, V>(dy, j * A.yts);
-        x += U * A.xts, dy += U * A.yts;
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            N d[H];
-            forward(rx[j], ry[j], true);
-            gradient(d);
-            store<XT, V>(dx, 0, d);
-            dx += A.C;
-            shift();
+        for (int g = 0; g < G; ++g) {
+            const int m = g < groups ? U : 0;
+            qx.fetch(g, x + g * U * A.xts, A.xts, m), qy.fetch(g, dy + g * U * A.yts, A.yts, m), commit();
         }
+#pragma unroll 1
+        for (int g = 0; g < groups; ++g) {
+            Vec<XT, V> rx[U], ry[U];
+            const int m = g + G < groups ? U : 0;
+            if constexpr (!Q::RING) qx.take(g, ring, rx), qy.take(g, ring, ry);
+            qx.fetch(g + G, x + G * U * A.xts, A.xts, m), qy.fetch(g + G, dy + G * U * A.yts, A.yts, m), commit();
+            if constexpr (Q::RING) {
+                wait<G>();
+                qx.take(g, ring, rx), qy.take(g, ring + D * 256, ry);
+            }
+            x += U * A.xts, dy += U * A.yts;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                N d[H];
+                forward(rx[j], ry[j], true);
+                gradient(d);
+                store<XT, V>(dx, 0, d);
+                dx += A.C;
+                shift();
+            }
+        }
+        t += groups * U;
     }
 #pragma unroll 1
     for (; t < end; ++t) careful(t);
