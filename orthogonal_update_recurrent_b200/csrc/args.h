@@ -165,7 +165,6 @@ struct ConvArgs {
 // selective.cuh: selective state space scan
 constexpr int kSelTile = 16;     // tokens that a CTA stages at once
 constexpr int kSelMark = 8;      // tokens between the states that the forward pass leaves for the backward pass
-constexpr int kSelThreads = 256;
 constexpr int kSelMaxN = 128;
 constexpr int kSelMaxSize = 1 << 30;  // channels, and tokens
 

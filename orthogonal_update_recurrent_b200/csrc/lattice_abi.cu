@@ -317,10 +317,17 @@ void conv_args(ConvArgs& a, const void* x, lattice_dtype x_dtype, long long xbs,
 
 // ---- selective scan
 struct SelPlan {
-    int S, tiles, nseg, seg;
+    int S, W, tiles, nseg, seg;
 };
-long long sel_tiles(int Eg, int lanes) { return ((long long)Eg + kSelThreads / lanes - 1) / (kSelThreads / lanes); }
-// How the work is spread. A CTA has 256/L channels with N padded to L S states, and goes through its tokens alone. With few
+// Channel tiles of a group: W warps of 32/lanes channels each
+long long sel_tiles(int Eg, int lanes, int W) {
+    const int per = W * (32 / lanes);
+    return ((long long)Eg + per - 1) / per;
+}
+// Warps of a CTA: 8, or 2 where 8 would leave a quarter of them without channels more than 2 would (20 sequences of 49370 tokens at most,
+// 12 channels, 16 states: forward and backward 2966 us with 8 warps).
+int sel_warps(int Eg, int lanes) { return 3 * sel_tiles(Eg, lanes, 8) * 4 > 4 * sel_tiles(Eg, lanes, 2) ? 2 : 8; }
+// How the work is spread. A CTA has 256/L channels (64/L) with N padded to L S states, and goes through its tokens alone. With few
 // CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose
 // states take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token and by
 // CTAs per SM, are what was measured (bf16, 16 states, gate; they hold for other N, whose CTAs have as many states), the cheapest
@@ -328,26 +335,27 @@ long long sel_tiles(int Eg, int lanes) { return ((long long)Eg + kSelThreads / l
 // two states 246 / 246 / 134 / 196, segments 88 / 142 / 143 / 200; backward, whole 1155 / 1201 / 627 / 637, segments
 // 190 / 304 / 331 / 429.
 SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
-    const int np = sel_padded(N), Eg = E / G;
-    const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4);
-    auto time = [&](long long ctas, double one, double two, double more) {
-        const long long per = (ctas + sm - 1) / sm;
+    const int np = sel_padded(N), Eg = E / G, W = sel_warps(Eg, np / 4), unit = 8 / W;  // CTAs that count as one of 8 warps
+    const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4, W);
+    auto time = [&](long long ctas, int u, double one, double two, double more) {
+        const long long per = (ctas + sm * u - 1) / (sm * u);
         return per == 1 ? one : per == 2 ? two : more * (double)per;
     };
-    SelPlan p = {4, (int)sel_tiles(Eg, np / 4), 1, T > 0 ? T : 1};
-    double best = T * (bwd ? time(base, 0.30, 0.455, 0.23) : time(base, 0.098, 0.163, 0.0815));
+    SelPlan p = {4, W, (int)sel_tiles(Eg, np / 4, W), 1, T > 0 ? T : 1};
+    double best = T * (bwd ? time(base, unit, 0.30, 0.455, 0.23) : time(base, unit, 0.098, 0.163, 0.0815));
     if (!bwd && np <= 32) {
-        const long long tiles = sel_tiles(Eg, np / 2);
-        const double us = T * time((long long)B * G * tiles, 0.065, 0.107, 0.0515);
-        if (us < best) best = us, p.S = 2, p.tiles = (int)tiles;
+        const int W2 = sel_warps(Eg, np / 2);
+        const long long tiles = sel_tiles(Eg, np / 2, W2);
+        const double us = T * time((long long)B * G * tiles, 8 / W2, 0.065, 0.107, 0.0515);
+        if (us < best) best = us, p.S = 2, p.W = W2, p.tiles = (int)tiles;
     }
     const long long tiles = ((long long)T + kSelTile - 1) / kSelTile;
-    long long n = 2 * sm / base;
+    long long n = 2 * sm * unit / base;
     if (n > tiles / 4) n = tiles / 4;
     if (n > 1) {
         const long long per = (tiles + n - 1) / n;
-        const double us = per * kSelTile * (bwd ? time(base * n, 0.37, 0.565, 0.29) : time(base * n, 0.168, 0.26, 0.13)) + (bwd ? 15 : 12);
-        if (us < best) p = {4, (int)sel_tiles(Eg, np / 4), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
+        const double us = per * kSelTile * (bwd ? time(base * n, unit, 0.37, 0.565, 0.29) : time(base * n, unit, 0.168, 0.26, 0.13)) + (bwd ? 15 : 12);
+        if (us < best) p = {4, W, (int)sel_tiles(Eg, np / 4, W), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
     }
     return p;
 }
@@ -1016,7 +1024,7 @@ lattice_status lattice_selective_scan_fwd(const void* x, lattice_dtype x_dtype, 
     a.vec = sel_vec(a, sx, sel_width(sel_padded(N) / plan.S));
     a.vec_n = a.vec_n && aligned(h0, 16) && aligned(h_out, 16);
     sel_place(a, plan, space, workspace);
-    return with_x(x_dtype, [&](auto t) { return selective::launch_fwd<decltype(t)>(a, plan.S, static_cast<cudaStream_t>(stream)); });
+    return with_x(x_dtype, [&](auto t) { return selective::launch_fwd<decltype(t)>(a, plan.S, plan.W, static_cast<cudaStream_t>(stream)); });
 }
 
 lattice_status lattice_selective_scan_bwd(const void* x, lattice_dtype x_dtype, long long x_batch_stride, long long x_token_stride,
@@ -1061,7 +1069,7 @@ lattice_status lattice_selective_scan_bwd(const void* x, lattice_dtype x_dtype, 
     a.vec = sel_vec(a, sx, sel_width(sel_padded(N) / 4));
     a.vec_n = a.vec_n && aligned(dh_T, 16) && aligned(dh0, 16);
     sel_place(a, plan, space, workspace);
-    return with_x(x_dtype, [&](auto t) { return selective::launch_bwd<decltype(t)>(a, static_cast<cudaStream_t>(stream)); });
+    return with_x(x_dtype, [&](auto t) { return selective::launch_bwd<decltype(t)>(a, plan.W, static_cast<cudaStream_t>(stream)); });
 }
 
 lattice_status lattice_selective_step(const float* h, float* h_out, const void* x, lattice_dtype x_dtype, long long x_batch_stride,

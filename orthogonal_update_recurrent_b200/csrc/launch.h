@@ -73,11 +73,12 @@ namespace conv {
 template <class XT> lattice_status launch(const ConvArgs& a, int what, int V, cudaStream_t st);
 }  // namespace conv
 
-// sel_fwd_*.cu, sel_bwd_*.cu: selective scan, a unit per type of x (no waits either). S: states per lane
+// sel_fwd_*.cu, sel_bwd_*.cu: selective scan, a unit per type of x (no waits either). S: states per
+// lane; W: warps of a CTA, 8 or 2
 namespace selective {
-template <class XT> lattice_status launch_fwd(const SelArgs& a, int S, cudaStream_t st);
+template <class XT> lattice_status launch_fwd(const SelArgs& a, int S, int W, cudaStream_t st);
 template <class XT> lattice_status launch_step(const SelArgs& a, cudaStream_t st);
-template <class XT> lattice_status launch_bwd(const SelArgs& a, cudaStream_t st);
+template <class XT> lattice_status launch_bwd(const SelArgs& a, int W, cudaStream_t st);
 }  // namespace selective
 
 // each unit's device status word (read, and zeroed when set)

@@ -3,6 +3,6 @@
 
 namespace lattice {
 
-template lattice_status selective::launch_bwd<__nv_bfloat16>(const SelArgs& a, cudaStream_t st);
+template lattice_status selective::launch_bwd<__nv_bfloat16>(const SelArgs& a, int W, cudaStream_t st);
 
 }  // namespace lattice

@@ -3,7 +3,7 @@
 
 namespace lattice {
 
-template lattice_status selective::launch_fwd<float>(const SelArgs& a, int S, cudaStream_t st);
+template lattice_status selective::launch_fwd<float>(const SelArgs& a, int S, int W, cudaStream_t st);
 template lattice_status selective::launch_step<float>(const SelArgs& a, cudaStream_t st);
 
 }  // namespace lattice

@@ -16,7 +16,7 @@
 // 2 (measured); the layout keeps every state's work on those units at about the exponential's 8.
 //
 // Layout: a channel's states are split over L lanes, S (4 or 2) each, so a warp has 32/L channels and a
-// CTA 8 warps. y's sum over n is a shuffle over L lanes, for four tokens at once (each lane
+// CTA 8 warps (2 for few channels). y's sum over n is a shuffle over L lanes, for four tokens at once (each lane
 // hands half of its tokens on per step). What belongs to a channel and not to its states (softplus, dt x, the
 // gate, the skip) is computed once per (token, channel) by the CTA, 16 tokens at a time, and passed on through
 // shared memory.
@@ -34,7 +34,7 @@
 namespace lattice {
 namespace selective {
 
-constexpr int TT = kSelTile, NT = kSelThreads, NW = NT / 32;
+constexpr int TT = kSelTile;
 constexpr unsigned ALL = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -254,10 +254,11 @@ __device__ __forceinline__ float halve(float v0, float v1, int lane, int bit) {
 }
 
 // Where a CTA works: a tile of CT channels of one group, one sequence, one segment of the time axis. Its threads have two
-// tasks: the states of one channel on L lanes each, and V channels of the tile's tokens each, PI of them.
-template <int L>
+// tasks: the states of one channel on L lanes each, and V channels of the tile's tokens each, PI of them. W warps: 8, or 2 where a group
+// has few channels.
+template <int L, int W>
 struct Place {
-    static constexpr int CH = 32 / L, CT = NW * CH, V = sel_width(L), P = (V + 1) / 2;
+    static constexpr int NT = 32 * W, CH = 32 / L, CT = W * CH, V = sel_width(L), P = (V + 1) / 2;
     static constexpr int QUADS = CT / V, ROWS = NT / QUADS, PI = (TT + ROWS - 1) / ROWS;
     static constexpr int CTP = CT + CH;              // floats from lane to lane of the sums over n: lanes apart in the banks
     static constexpr int DW = CT + (V > 1 ? 4 * V : 0);  // a token's entries of du
@@ -314,9 +315,9 @@ __device__ __forceinline__ void own_read(const float* p, F2* f) {
     }
 }
 // The sums over a channel's L lanes: [L][CTP] of a token, the thread's V channels
-template <int L>
+template <int L, int W>
 __device__ __forceinline__ void lane_sums(const float* p, F2* f) {
-    using P = Place<L>;
+    using P = Place<L, W>;
     own_read<P::V>(p, f);
 #pragma unroll
     for (int l = 1; l < L; ++l) {
@@ -424,14 +425,15 @@ __device__ __forceinline__ void load_row(const XT* p, int n0, int N, float* v) {
     parts(f[0], v[0], v[1]), parts(f[1], v[2], v[3]);
 }
 // A tile's rows of b or c: NB elements of [TT][NP] per thread.
-template <int NP>
+template <int NP, int W>
 struct Rows {
-    static constexpr int NB = (TT * NP + NT - 1) / NT;
+    static constexpr int NT = 32 * W, NB = (TT * NP + NT - 1) / NT;
 };
-template <bool VEC, class XT, int NP>
+template <bool VEC, class XT, int NP, int W>
 __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, int te, int N, XT* r) {
+    constexpr int NT = 32 * W;
 #pragma unroll
-    for (int k = 0; k < Rows<NP>::NB; ++k) {
+    for (int k = 0; k < Rows<NP, W>::NB; ++k) {
         const int i = threadIdx.x + k * NT, t = i / NP, n = i % NP;
         r[k] = XT();
         if ((TT * NP % NT == 0 || t < TT) && tb + t < te && n < N) r[k] = token<VEC>(p + n, tb + t, ts)[0];
@@ -440,21 +442,21 @@ __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, in
 
 // ---- forward: all tokens of a segment, from the state that enters it
 // Between two barriers a CTA finishes the tile before, prepares the next one (in the other buffers) and works on its own.
-template <class XT, int L, int S>
+template <class XT, int L, int S, int W>
 struct FwdShared {
-    static constexpr int NP = L * S, CT = Place<L>::CT;
-    float2 du[2][TT * Place<L>::DW];             // (dt, u), u = dt x
+    static constexpr int NP = L * S, CT = Place<L, W>::CT;
+    float2 du[2][TT * Place<L, W>::DW];             // (dt, u), u = dt x
     float gate[2][TT * CT], skip[2][TT * CT];    // silu(z) and skip x, for the thread that wrote them
     float b[2][TT * NP], c[2][TT * NP];
-    float y[2][TT * L * Place<L>::CTP];          // the lanes' parts of the sums over n
+    float y[2][TT * L * Place<L, W>::CTP];          // the lanes' parts of the sums over n
 };
 
-template <class XT, int L, int S, bool VEC>
-__global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
-    using P = Place<L>;
-    constexpr int NP = L * S, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, H = S / 2, V = P::V, Q = P::P;
+template <class XT, int L, int S, int W, bool VEC>
+__global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
+    using P = Place<L, W>;
+    constexpr int NT = P::NT, NP = L * S, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, H = S / 2, V = P::V, Q = P::P;
     extern __shared__ __align__(16) unsigned char raw_shared[];
-    FwdShared<XT, L, S>& sh = *reinterpret_cast<FwdShared<XT, L, S>*>(raw_shared);
+    FwdShared<XT, L, S, W>& sh = *reinterpret_cast<FwdShared<XT, L, S, W>*>(raw_shared);
     const P p(A);
     const int n0 = p.gl * S, pw = p.width();
     F2 h[H], A2[H], bias[Q], skip[Q];
@@ -489,8 +491,8 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
             rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
             if (A.z) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<VEC, XT, NP>(bp, A.bts, tb, p.te, A.N, rb);
-        fetch_rows<VEC, XT, NP>(cp, A.cts, tb, p.te, A.N, rc);
+        fetch_rows<VEC, XT, NP, W>(bp, A.bts, tb, p.te, A.N, rb);
+        fetch_rows<VEC, XT, NP, W>(cp, A.cts, tb, p.te, A.N, rc);
     };
     auto prepare = [&](int tb, int buf) {
 #pragma unroll
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
             const int r = p.row + k * P::ROWS, t = tb + r;
             if (r >= TT || t >= p.te) continue;
             F2 y[Q], f[Q];
-            lane_sums<L>(sh.y[buf] + r * L * CTP + p.first, y);
+            lane_sums<L, W>(sh.y[buf] + r * L * CTP + p.first, y);
             if (A.skip) {
                 own_read<V>(sh.skip[buf] + r * CT + p.first, f);
 #pragma unroll
@@ -610,20 +612,20 @@ __global__ void __launch_bounds__(NT, 2) fwd_kernel(const SelArgs A) {
 }
 
 // ---- a segment's state from 0 at its end (REV: the cotangent from 0 at its start) and the sum of its dt
-template <class XT, int L, int S>
+template <class XT, int L, int S, int W>
 struct SegShared {
     static constexpr int NP = L * S;
-    float2 du[2][TT * Place<L>::DW];       // (dt, w), w = dt x or dy silu(z)
+    float2 du[2][TT * Place<L, W>::DW];       // (dt, w), w = dt x or dy silu(z)
     float v[2][TT * NP];                   // b or c
-    float sum[NT * 4];
+    float sum[32 * W * 4];
 };
 
-template <class XT, int L, int S, bool REV, bool VEC>
-__global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
-    using P = Place<L>;
-    constexpr int NP = L * S, PI = P::PI, NB = Rows<NP>::NB, H = S / 2, V = P::V, Q = P::P;
+template <class XT, int L, int S, int W, bool REV, bool VEC>
+__global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
+    using P = Place<L, W>;
+    constexpr int NT = P::NT, NP = L * S, PI = P::PI, NB = Rows<NP, W>::NB, H = S / 2, V = P::V, Q = P::P;
     extern __shared__ __align__(16) unsigned char raw_shared[];
-    SegShared<XT, L, S>& sh = *reinterpret_cast<SegShared<XT, L, S>*>(raw_shared);
+    SegShared<XT, L, S, W>& sh = *reinterpret_cast<SegShared<XT, L, S, W>*>(raw_shared);
     const P p(A);
     const int n0 = p.gl * S, pw = p.width();
     F2 h[H], A2[H], bias[Q], sum[Q];
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(NT, 2) seg_kernel(const SelArgs A) {
             rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
             if (gated) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<VEC, XT, NP>(vp, vts, tb, p.te, A.N, rv);
+        fetch_rows<VEC, XT, NP, W>(vp, vts, tb, p.te, A.N, rv);
     };
     auto prepare = [&](int tb, int buf) {
 #pragma unroll

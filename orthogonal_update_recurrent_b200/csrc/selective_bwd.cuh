@@ -15,19 +15,19 @@
 namespace lattice {
 namespace selective {
 
-template <class XT, int L>
+template <class XT, int L, int W>
 struct BwdShared {
-    static constexpr int NP = 4 * L, CT = Place<L>::CT, CTP = Place<L>::CTP;
+    static constexpr int NP = 4 * L, CT = Place<L, W>::CT, CTP = Place<L, W>::CTP;
     static constexpr int VAR = L <= 8 ? 4 : L == 16 ? 2 : 1;  // orders of a lane's four states
     static constexpr int VS = TT * NP + (NP < 32 ? NP : 0);   // from order to order, apart in the banks
     static constexpr int QS = CT + 8;
-    float2 du[TT * Place<L>::DW];                             // (dt, u), u = dt x
-    float w[TT * Place<L>::DW];
+    float2 du[TT * Place<L, W>::DW];                             // (dt, u), u = dt x
+    float w[TT * Place<L, W>::DW];
     float x[TT * CT], slope[TT * CT], zf[TT * CT];            // for the thread that wrote them
     float y[TT * L * CTP], g[TT * L * CTP];                   // y and du: the lanes' parts of the sums over n
     float dq[TT * QS];                                        // a whole one
     float b[VAR * VS], c[VAR * VS];
-    float sums[2][NW][TT * NP];                               // dc and db of the warps' channels
+    float sums[2][W][TT * NP];                               // dc and db of the warps' channels
 };
 
 // the lane's states from register order to memory order, and back
@@ -120,11 +120,11 @@ struct StateSums {
     }
 };
 
-template <class XT, int L, bool GATE, bool VEC>
-__global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs A) {
-    using P = Place<L>;
-    using Sh = BwdShared<XT, L>;
-    constexpr int NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP>::NB, VAR = Sh::VAR, VS = Sh::VS, QS = Sh::QS, SB = 8,
+template <class XT, int L, int W, bool GATE, bool VEC>
+__global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_kernel(const SelArgs A) {
+    using P = Place<L, W>;
+    using Sh = BwdShared<XT, L, W>;
+    constexpr int NT = P::NT, NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, VAR = Sh::VAR, VS = Sh::VS, QS = Sh::QS, SB = 8,
                   V = P::V, Q = P::P, DW = P::DW;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh& sh = *reinterpret_cast<Sh*>(raw_shared);
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             ry[k] = load<VEC, XT, V>(token<VEC>(gp, t, A.yts), n);
             if constexpr (GATE) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
         }
-        fetch_rows<VEC, XT, NP>(bp, A.bts, tb, p.te, A.N, rb);
-        fetch_rows<VEC, XT, NP>(cp, A.cts, tb, p.te, A.N, rc);
+        fetch_rows<VEC, XT, NP, W>(bp, A.bts, tb, p.te, A.N, rb);
+        fetch_rows<VEC, XT, NP, W>(cp, A.cts, tb, p.te, A.N, rc);
     };
     auto ahead = [&](int tb) {  // a tile's lines are brought nearer
 #pragma unroll
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             if (r >= TT || t >= p.te) continue;
             const int at = r * CT + p.first;
             F2 x[Q], du[Q], f[Q], e[Q];
-            lane_sums<L>(sh.g + r * L * CTP + p.first, du);
+            lane_sums<L, W>(sh.g + r * L * CTP + p.first, du);
             own_read<V>(sh.x + at, x);
             own_read<V>(sh.slope + at, f);
             own_read<V>(sh.dq + r * QS + p.first, e);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             }
             put_x(A.dx, t, e);
             if constexpr (GATE) {
-                lane_sums<L>(sh.y + r * L * CTP + p.first, e);
+                lane_sums<L, W>(sh.y + r * L * CTP + p.first, e);
                 own_read<V>(sh.zf + at, f);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) e[q] = mul2(fma2(skip[q], x[q], e[q]), f[q]);
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
             if (n >= A.N || tb + t >= p.te) continue;
             float v = sh.sums[kind][0][j];
 #pragma unroll
-            for (int q = 1; q < NW; ++q) v += sh.sums[kind][q][j];
+            for (int q = 1; q < W; ++q) v += sh.sums[kind][q][j];
             out[(long long)t * 2 * A.N + kind * A.N + n] = v;
         }
     };
@@ -396,34 +396,46 @@ __global__ void __launch_bounds__(NT, L == 32 ? 1 : 2) bwd_kernel(const SelArgs 
     }
 }
 
-// db and dc from the channel tiles' sums, in their order
+// db and dc from the channel tiles' sums, in their order. A CTA has kSharedTokens tokens of a sequence; its threads stand for the 2 N
+// values of a token's group, padded to a power of two, and as many groups at once as are left.
+constexpr int kSharedTokens = 64;
 template <class XT>
-__global__ void __launch_bounds__(256) shared_kernel(const SelArgs A) {
-    const int n2 = 2 * A.N;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, rows = (long long)A.B * A.T;
-    if (i >= rows * A.G * n2) return;
-    const long long r = i / n2, bt = r / A.G;
-    const int m = (int)(i - r * n2), g = (int)(r - bt * A.G), b = (int)(bt / A.T), kind = m >= A.N, n = m - kind * A.N;
-    const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
-    float v = 0.f;
-    if (bt - (long long)b * A.T < len) {
-        const float* from = A.parts_bc + ((long long)g * A.tiles * rows + bt) * n2 + m;
+__global__ void __launch_bounds__(256) shared_kernel(const SelArgs A, int width) {
+    const int n2 = 2 * A.N, per = (A.T + kSharedTokens - 1) / kSharedTokens, b = blockIdx.x / per, t0 = (blockIdx.x - b * per) * kSharedTokens;
+    const int m = threadIdx.x & (width - 1), kind = m >= A.N, n = m - kind * A.N, step = 256 / width;
+    if (m >= n2) return;
+    const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T, rows = min(kSharedTokens, A.T - t0) * A.G;
+    const long long all = (long long)A.B * A.T * n2, bt0 = (long long)b * A.T + t0;
+    XT* to = static_cast<XT*>(kind ? A.db : A.dc) + bt0 * A.G * A.N + n;
+    for (int r = threadIdx.x / width; r < rows; r += step) {
+        const int t = A.G == 1 ? r : r / A.G, g = r - t * A.G;
+        float v = 0.f;
+        if (t0 + t < len) {
+            const float* from = A.parts_bc + (long long)g * A.tiles * all + (bt0 + t) * n2 + m;
 #pragma unroll 8
-        for (int k = 0; k < A.tiles; ++k) v += from[k * rows * n2];
+            for (int k = 0; k < A.tiles; ++k) v += from[k * all];
+        }
+        put(to + (long long)r * A.N, v);
     }
-    put(static_cast<XT*>(kind ? A.db : A.dc) + r * A.N + n, v);
 }
 
-// dA, dskip and ddt_bias from the segments' sums, in their order
-inline __global__ void __launch_bounds__(256) weights_kernel(const SelArgs A) {
-    const long long EN = (long long)A.E * A.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= EN + 2 * A.E) return;
-    const bool ch = i >= EN;
+// dA, dskip and ddt_bias from the sequences' and segments' sums: 32 columns and 32 slices of these per CTA, slices added up in order
+inline __global__ void __launch_bounds__(1024) weights_kernel(const SelArgs A) {
+    __shared__ float sum[32][33];
+    const long long EN = (long long)A.E * A.N;
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const long long i = (long long)blockIdx.x * 32 + lane;
+    const bool in = i < EN + 2 * A.E, ch = i >= EN;
     const float* from = ch ? A.parts_ch + (i - EN) : A.parts_A + i;
     const long long step = ch ? 2 * A.E : EN;
     float v = 0.f;
+    if (in)
 #pragma unroll 4
-    for (int k = 0; k < A.B * A.nseg; ++k) v += from[k * step];
+        for (int k = slice; k < A.B * A.nseg; k += 32) v += from[k * step];
+    sum[slice][lane] = v;
+    __syncthreads();
+    if (slice || !in) return;
+    for (int k = 1; k < 32; ++k) v += sum[k][lane];
     if (!ch) A.dA[i] = v;
     else if (i - EN < A.E) {
         if (A.dskip) A.dskip[i - EN] = v;
