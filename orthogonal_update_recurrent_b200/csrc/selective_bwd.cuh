@@ -396,15 +396,14 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
     }
 }
 
-// db and dc from the channel tiles' sums, in their order. A CTA has kSharedTokens tokens of a sequence; its threads stand for the 2 N
+// db and dc from the channel tiles' sums, in their order. A CTA has `tokens` of a sequence; its threads stand for the 2 N
 // values of a token's group, padded to a power of two, and as many groups at once as are left.
-constexpr int kSharedTokens = 64;
 template <class XT>
-__global__ void __launch_bounds__(256) shared_kernel(const SelArgs A, int width) {
-    const int n2 = 2 * A.N, per = (A.T + kSharedTokens - 1) / kSharedTokens, b = blockIdx.x / per, t0 = (blockIdx.x - b * per) * kSharedTokens;
+__global__ void __launch_bounds__(256) shared_kernel(const SelArgs A, int width, int tokens) {
+    const int n2 = 2 * A.N, per = (A.T + tokens - 1) / tokens, b = blockIdx.x / per, t0 = (blockIdx.x - b * per) * tokens;
     const int m = threadIdx.x & (width - 1), kind = m >= A.N, n = m - kind * A.N, step = 256 / width;
     if (m >= n2) return;
-    const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T, rows = min(kSharedTokens, A.T - t0) * A.G;
+    const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T, rows = min(tokens, A.T - t0) * A.G;
     const long long all = (long long)A.B * A.T * n2, bt0 = (long long)b * A.T + t0;
     XT* to = static_cast<XT*>(kind ? A.db : A.dc) + bt0 * A.G * A.N + n;
     for (int r = threadIdx.x / width; r < rows; r += step) {

@@ -51,9 +51,12 @@ lattice_status backward(const SelArgs& a, cudaStream_t st) {
     if (a.T > 0) {
         int width = 2;
         while (width < 2 * a.N) width *= 2;
-        const long long ctas = (long long)a.B * ((a.T + kSharedTokens - 1) / kSharedTokens);
+        long long tokens = (long long)a.B * a.T / (16 * sm_count());  // several CTAs per SM, none with more than 64 tokens
+        const int least = 256 / width / a.G;
+        tokens = tokens > 64 ? 64 : tokens < least ? least : tokens < 1 ? 1 : tokens;
+        const long long ctas = a.B * ((a.T + tokens - 1) / tokens);
         if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
-        shared_kernel<XT><<<(unsigned)ctas, 256, 0, st>>>(a, width);
+        shared_kernel<XT><<<(unsigned)ctas, 256, 0, st>>>(a, width, (int)tokens);
         s = launch_status();
         if (s != LATTICE_OK) return s;
     }
