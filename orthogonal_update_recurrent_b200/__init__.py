@@ -788,6 +788,8 @@ def _conv_args(x, w, bias, act: str, lead: int, lengths):
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a tensor [C, K]")
     K = w.shape[1]
+    if w.numel() > _INT_MAX:
+        _fits("the convolution's taps", K)
     _rows(w, "w", torch.Size((shape[-1], K)), 0, _XZ[x.dtype], device)
     if bias is not None:
         _whole(bias, "bias", shape[-1:], (w.dtype,), device)
@@ -908,10 +910,14 @@ def _sel_args(x, dt, A, b, c, skip, z, dt_bias, lead: int, lengths):
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a tensor [E, N]")
     E, N = shape[-1], A.shape[1]
+    if A.numel() > _INT_MAX:
+        _fits("the selective scan's states", N)
     _rows(A, "A", torch.Size((E, N)), 0, _F32_ONLY, device)
     if not isinstance(b, torch.Tensor) or b.dim() not in (lead + 1, lead + 2):
         raise ValueError("b must be a tensor [B, T, N] or [B, T, G, N] (one token: without T)")
     G = b.shape[lead] if b.dim() == lead + 2 else 1
+    if G < 1 or E % G:
+        raise ValueError(f"{E} channels do not make {G} groups")
     rows = shape[:lead] + ((G, N) if b.dim() == lead + 2 else (N,))
     bs = _rows(b, "b", rows, lead, same, device)
     cs = _rows(c, "c", rows, lead, same, device)
@@ -919,8 +925,6 @@ def _sel_args(x, dt, A, b, c, skip, z, dt_bias, lead: int, lengths):
     _whole(dt_bias, "dt_bias", shape[-1:], _F32_ONLY, device)
     if lengths is not None:
         _whole(lengths, "lengths", shape[:1], (torch.int32,), device)
-    if G < 1 or E % G:
-        raise ValueError(f"{E} channels do not make {G} groups")
     return xs, ds, bs, cs, zs, N, G
 
 
