@@ -1127,7 +1127,10 @@ lattice_status lattice_layer_norm_fwd(const void* x, lattice_dtype x_dtype, long
     });
 }
 
-size_t lattice_layer_norm_bwd_workspace_bytes(long long N, int D) { return lattice_block_norm_bwd_workspace_bytes(N, D); }
+size_t lattice_layer_norm_bwd_workspace_bytes(long long N, int D) {
+    if (N < 0 || N > 0x7fffffffLL || D < 1 || D > kNormMaxD) return 0;
+    return (size_t)layer_parts(N, D) * 2 * D * 4;
+}
 
 lattice_status lattice_layer_norm_bwd(const void* r, lattice_dtype r_dtype, long long r_stride, const void* dn, long long dn_stride,
                                       const void* dr, long long dr_stride, const void* w, lattice_dtype w_dtype, void* dr_out, void* dx,

@@ -65,6 +65,7 @@ template <class XT> lattice_status launch_norm(bool bwd, NormArgs a, int mode, i
 template <class XT> lattice_status launch_layer(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st);
 }  // namespace norm
 int norm_parts(long long N, int D);  // at most so many
+int layer_parts(long long N, int D);
 lattice_status launch_norm_dw(const NormArgs& a, int groups, float* dw_post, float* dw_pre, cudaStream_t st);
 
 // conv_*.cu: short convolution, a unit per type of x (no waits in it, and so no status word). V: channels

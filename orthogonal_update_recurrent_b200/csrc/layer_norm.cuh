@@ -10,7 +10,10 @@
 // HBM bounds both. Rows are read, summed and kept in registers as in the norms after and before a
 // block (block_norm.cuh, whose threads, columns and row sums these kernels use). The mean is taken
 // first and the variance from the differences, which loses nothing where the mean is large; the
-// second sum costs an exchange more, during which the next row is on its way.
+// second sum costs an exchange more, during which the next row is on its way. What is left is bound by
+// those exchanges, so both directions keep 1024 threads' rows at once per SM, 64 registers each. (One exchange of
+// differences from the row's first element, a second one where that cancels, was slower: 32768 rows of 2048 bf16, no residual,
+// forward 62 -> 84 us.)
 #pragma once
 #include "block_norm.cuh"
 
@@ -138,7 +141,8 @@ layer_fwd_kernel(const NormArgs A) {
 
 // dresidual: d r in r's type; dy: d r in the call's type (may be null)
 template <class F, bool SUB>
-__global__ void __launch_bounds__(SUB ? 256 : kBwdThreads, SUB ? 2 : 1) layer_bwd_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(SUB ? 256 : F::V == 8 ? kFwdThreads : kFwdOddThreads, SUB ? (F::MODE == kVec || !F::RES ? 4 : 2) : 1)
+layer_bwd_kernel(const NormArgs A) {
     using XT = typename F::XT;
     constexpr int MODE = F::MODE, V = F::V, NV = 8 / V;
     extern __shared__ __align__(16) ulonglong2 own[];

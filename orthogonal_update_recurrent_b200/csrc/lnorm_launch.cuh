@@ -12,7 +12,8 @@ struct LayerKernel;
 
 template <class F, bool SUB>
 lattice_status run_layer(bool bwd, const NormArgs& a, int* groups, cudaStream_t st) {
-    if (bwd) return launch_kernel<LayerKernel<F, SUB, true>>(layer_bwd_kernel<F, SUB>, true, F::MODE, 96, a, groups, st);
+    // both have the threads of a forward pass
+    if (bwd) return launch_kernel<LayerKernel<F, SUB, true>>(layer_bwd_kernel<F, SUB>, false, F::MODE, 96, a, groups, st);
     return launch_kernel<LayerKernel<F, SUB, false>>(layer_fwd_kernel<F, SUB>, false, F::MODE, 64, a, groups, st);
 }
 template <class T, bool SUB, bool RES, bool Y32, bool R32>
@@ -34,7 +35,7 @@ lattice_status run_layer_types(bool bwd, const NormArgs& a, int mode, int* group
 }
 template <class T>
 lattice_status launch_layer(bool bwd, NormArgs a, int mode, int* groups, cudaStream_t st) {
-    const Split split(a.D, bwd, mode);
+    const Split split(a.D, false, mode);
     a.tpr = split.tpr;
     a.K = split.K;
     const bool res = bwd ? a.dr != nullptr : a.residual != nullptr;

@@ -42,6 +42,15 @@ struct Split {
     }
 };
 
+// Rows of the workspace that a backward pass of N rows leaves at most (bwd: which Split its kernels have).
+inline int parts(long long N, int D, bool bwd) {
+    const Split vec(D, bwd, kVec), shift(D, bwd, kShift), odd(D, bwd, kOdd);
+    long long n = vec.groups(N);
+    const long long o = odd.groups(N), m = D % 8 != 0 && D + 7 <= kNormMaxD ? shift.whole_periods(shift.groups(N), N, D) : n;
+    n = m > n ? m : n;
+    return (int)(o > n ? o : n);
+}
+
 // The grid is what the device holds at once, or fewer: it is asked once per kernel, CTA size and
 // device. (Clusters lie within a GPC, which may hold fewer than its SMs would: 4096 rows of
 // 16384, backward: 543 us with a cluster of 4 for every 4 SMs, 316 us with as many as are held.)
