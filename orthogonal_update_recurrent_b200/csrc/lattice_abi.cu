@@ -324,9 +324,12 @@ long long sel_tiles(int Eg, int lanes, int W) {
     const int per = W * (32 / lanes);
     return ((long long)Eg + per - 1) / per;
 }
-// Warps of a CTA: 8, or 2 where 8 would leave a quarter of them without channels more than 2 would (20 sequences of 49370 tokens at most,
-// 12 channels, 16 states: forward and backward 2966 us with 8 warps).
-int sel_warps(int Eg, int lanes) { return 3 * sel_tiles(Eg, lanes, 8) * 4 > 4 * sel_tiles(Eg, lanes, 2) ? 2 : 8; }
+// Warps of a CTA: 8, or 2 where 8 would leave so many more of them without channels that it pays: a warp of two takes 1.1 times a
+// warp of eight's time, backward, with its share of the sums over channels, 1.7 times (mid-size layer: 636 and 698 us, 1713 and 2886 us; 20
+// sequences of 49370 tokens at most, 12 channels, 16 states, forward and backward: 2966 us with 8 warps, 880 us with 2).
+int sel_warps(int Eg, int lanes, bool bwd) {
+    return (double)sel_tiles(Eg, lanes, 8) * 4 > (bwd ? 1.7 : 1.1) * (double)sel_tiles(Eg, lanes, 2) ? 2 : 8;
+}
 // How the work is spread. A CTA has 256/L channels (64/L) with N padded to L S states, and goes through its tokens alone. With few
 // CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose
 // states take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token and by
@@ -335,7 +338,7 @@ int sel_warps(int Eg, int lanes) { return 3 * sel_tiles(Eg, lanes, 8) * 4 > 4 * 
 // two states 246 / 246 / 134 / 196, segments 88 / 142 / 143 / 200; backward, whole 1155 / 1201 / 627 / 637, segments
 // 190 / 304 / 331 / 429.
 SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
-    const int np = sel_padded(N), Eg = E / G, W = sel_warps(Eg, np / 4), unit = 8 / W;  // CTAs that count as one of 8 warps
+    const int np = sel_padded(N), Eg = E / G, W = sel_warps(Eg, np / 4, bwd), unit = 8 / W;  // CTAs that count as one of 8 warps
     const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4, W);
     auto time = [&](long long ctas, int u, double one, double two, double more) {
         const long long per = (ctas + sm * u - 1) / (sm * u);
@@ -344,7 +347,7 @@ SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
     SelPlan p = {4, W, (int)sel_tiles(Eg, np / 4, W), 1, T > 0 ? T : 1};
     double best = T * (bwd ? time(base, unit, 0.30, 0.455, 0.23) : time(base, unit, 0.098, 0.163, 0.0815));
     if (!bwd && np <= 32) {
-        const int W2 = sel_warps(Eg, np / 2);
+        const int W2 = sel_warps(Eg, np / 2, false);
         const long long tiles = sel_tiles(Eg, np / 2, W2);
         const double us = T * time((long long)B * G * tiles, 8 / W2, 0.065, 0.107, 0.0515);
         if (us < best) best = us, p.S = 2, p.W = W2, p.tiles = (int)tiles;
@@ -417,7 +420,7 @@ lattice_status sel_inputs(SelArgs& a, SelInputs& in, const void* x, lattice_dtyp
 bool sel_vec(const SelArgs& a, size_t sx, int V) {
     const size_t sd = a.dt32 ? 4 : sx, bx = V * sx, bd = V * sd;
     for (long long ts : {a.xts, a.dts, a.zts, a.bts, a.cts, a.yts, (long long)a.E})
-        if ((__int128)a.T * ts * 4 > 0x7fffffffLL) return false;
+        if (((__int128)a.T * ts + a.E + (long long)a.G * a.N) * 4 > 0x7fffffffLL) return false;
     return a.Eg % V == 0 && rows_vec(a.x, sx, a.B, a.T, a.xbs, a.xts, bx) && rows_vec(a.dt, sd, a.B, a.T, a.dbs, a.dts, bd) &&
            (!a.z || rows_vec(a.z, sx, a.B, a.T, a.zbs, a.zts, bx)) && (!a.dy || rows_vec(a.dy, sx, a.B, a.T, a.ybs, a.yts, bx)) &&
            aligned(a.y, bx) && aligned(a.dx, bx) && aligned(a.dz, bx) && aligned(a.ddt, bd);

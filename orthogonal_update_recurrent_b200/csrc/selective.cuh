@@ -131,18 +131,18 @@ __device__ __forceinline__ void store(T* p, const F2* f, int n) {
             if (k < n) put(p + k, v[k]);
     }
 }
-// Token t's entries of an array whose tokens are `ts` elements apart, from p on. VEC calls' arrays are less than 2^31 bytes
-// from the first to the last token, so that 32-bit offsets do.
+// Column c of token t of an array whose tokens are `ts` elements apart, from p on (the same for the whole CTA). VEC calls' arrays
+// are less than 2^31 bytes from the first to the last token, so that 32-bit offsets do.
 template <bool VEC, class T>
-__device__ __forceinline__ T* token(T* p, int t, long long ts) {
-    if constexpr (VEC) return reinterpret_cast<T*>(reinterpret_cast<unsigned long long>(p) + (unsigned)t * ((unsigned)ts * (unsigned)sizeof(T)));
-    else return p + t * ts;
+__device__ __forceinline__ T* token(T* p, int c, int t, long long ts) {
+    if constexpr (VEC) return reinterpret_cast<T*>(reinterpret_cast<unsigned long long>(p) + ((unsigned)t * (unsigned)ts + (unsigned)c) * (unsigned)sizeof(T));
+    else return p + (t * ts + c);
 }
 // V channels of dt, which are fp32 or XT
 template <bool VEC, class XT, int V>
-__device__ __forceinline__ Raw<float, V> load_dt(const SelArgs& A, const void* p, int t, int n) {
-    if (sizeof(XT) == 4 || A.dt32) return load<VEC, float, V>(token<VEC>(static_cast<const float*>(p), t, A.dts), n);
-    const Raw<XT, V> v = load<VEC, XT, V>(token<VEC>(static_cast<const XT*>(p), t, A.dts), n);
+__device__ __forceinline__ Raw<float, V> load_dt(const SelArgs& A, const void* p, int c, int t, int n) {
+    if (sizeof(XT) == 4 || A.dt32) return load<VEC, float, V>(token<VEC>(static_cast<const float*>(p), c, t, A.dts), n);
+    const Raw<XT, V> v = load<VEC, XT, V>(token<VEC>(static_cast<const XT*>(p), c, t, A.dts), n);
     Raw<float, V> r = none<float, V>();
 #pragma unroll
     for (int k = 0; k < Raw<XT, V>::W; ++k) r.w[k] = v.w[k];
@@ -161,12 +161,11 @@ __device__ __forceinline__ void values_dt(const SelArgs& A, const Raw<float, V>&
     }
     values<float, V>(r, f);
 }
-// where dt's entries of channel c of sequence b begin
+// where dt's entries of sequence b begin
 template <class XT>
-__device__ __forceinline__ const void* dt_at(const SelArgs& A, int b, int c) {
-    const long long i = b * A.dbs + c;
-    return sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(static_cast<const float*>(A.dt) + i)
-                                     : static_cast<const void*>(static_cast<const XT*>(A.dt) + i);
+__device__ __forceinline__ const void* dt_at(const SelArgs& A, int b) {
+    return sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(static_cast<const float*>(A.dt) + b * A.dbs)
+                                     : static_cast<const void*>(static_cast<const XT*>(A.dt) + b * A.dbs);
 }
 
 // exp(dt A) of two states, t = dt A log2(e). The approximate exponential's errors near 1 are not centred (mean
@@ -436,7 +435,7 @@ __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, in
     for (int k = 0; k < Rows<NP, W>::NB; ++k) {
         const int i = threadIdx.x + k * NT, t = i / NP, n = i % NP;
         r[k] = XT();
-        if ((TT * NP % NT == 0 || t < TT) && tb + t < te && n < N) r[k] = token<VEC>(p + n, tb + t, ts)[0];
+        if ((TT * NP % NT == 0 || t < TT) && tb + t < te && n < N) r[k] = *token<VEC>(p, n, tb + t, ts);
     }
 }
 
@@ -476,10 +475,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
         load_columns<V>(A.dt_bias, p.column(), pw, bias);
         load_columns<V>(A.skip, p.column(), pw, skip);
     }
-    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs + p.column(), *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
+    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs, *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
              *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N, *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
-    const void* dp = dt_at<XT>(A, p.b, p.column());
-    XT* yp = static_cast<XT*>(A.y) + (long long)p.b * A.T * A.E + p.column();
+    const void* dp = dt_at<XT>(A, p.b);
+    XT* yp = static_cast<XT*>(A.y) + (long long)p.b * A.T * A.E;
     Raw<XT, V> rx[PI], rz[PI];
     Raw<float, V> rd[PI];
     XT rb[NB], rc[NB];
@@ -487,9 +486,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, A.xts), n);
-            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
-            if (A.z) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, p.column(), t, A.xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, p.column(), t, n);
+            if (A.z) rz[k] = load<VEC, XT, V>(token<VEC>(zp, p.column(), t, A.zts), n);
         }
         fetch_rows<VEC, XT, NP, W>(bp, A.bts, tb, p.te, A.N, rb);
         fetch_rows<VEC, XT, NP, W>(cp, A.cts, tb, p.te, A.N, rc);
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
 #pragma unroll
                 for (int q = 0; q < Q; ++q) y[q] = mul2(y[q], f[q]);
             }
-            store<VEC, XT, V>(token<VEC>(yp, t, A.E), y, pw);
+            store<VEC, XT, V>(token<VEC>(yp, p.column(), t, A.E), y, pw);
         }
     };
     const int tiles = (p.te - p.t0 + TT - 1) / TT, entry = P::entry(p.c);
@@ -602,7 +601,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
         if (tiles > 0) finish(p.t0 + (tiles - 1) * TT, (tiles - 1) & 1);
         const F2 zero[Q] = {};
         for (int t = p.te + p.row; t < p.t1; t += P::ROWS)  // behind the sequence's end
-            store<VEC, XT, V>(token<VEC>(yp, t, A.E), zero, pw);
+            store<VEC, XT, V>(token<VEC>(yp, p.column(), t, A.E), zero, pw);
     }
     if (A.h_out && p.s == A.nseg - 1 && p.live) {
         float v[S];
@@ -641,10 +640,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) sum[q] = f2(0.f);
     }
-    const XT *xp = static_cast<const XT*>(REV ? A.dy : A.x) + p.b * (REV ? A.ybs : A.xbs) + p.column(),
-             *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
+    const XT *xp = static_cast<const XT*>(REV ? A.dy : A.x) + p.b * (REV ? A.ybs : A.xbs),
+             *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
              *vp = static_cast<const XT*>(REV ? A.c : A.b) + p.b * (REV ? A.cbs : A.bbs) + p.g * A.N;
-    const void* dp = dt_at<XT>(A, p.b, p.column());
+    const void* dp = dt_at<XT>(A, p.b);
     const long long xts = REV ? A.yts : A.xts, vts = REV ? A.cts : A.bts;
     const bool gated = REV && A.z;
     Raw<XT, V> rx[PI], rz[PI];
@@ -654,9 +653,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, xts), n);
-            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
-            if (gated) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, p.column(), t, xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, p.column(), t, n);
+            if (gated) rz[k] = load<VEC, XT, V>(token<VEC>(zp, p.column(), t, A.zts), n);
         }
         fetch_rows<VEC, XT, NP, W>(vp, vts, tb, p.te, A.N, rv);
     };

@@ -4,7 +4,7 @@
 // before every kSelMark-th token; from it a thread recomputes 8 tokens' states, keeps them and their decays in
 // registers, and goes back through them with the cotangent g.
 //
-// Sums over a channel's states (y, du, and ddt's part) are shuffles over its L lanes as in the forward pass. Sums
+// Sums over a channel's states (y, du, and ddt's part) are taken as in the forward pass, over many lanes by shuffles. Sums
 // over channels (db, dc) are shuffles over the warp's channels; a lane names its four states so that what it
 // keeps and what it hands on have the same registers in all lanes (register r stands for state r ^ (channel & 3)),
 // which takes the selects out of the first two steps; shared memory adds the warps up, the workspace the CTAs. All in a
@@ -20,14 +20,17 @@ struct BwdShared {
     static constexpr int NP = 4 * L, CT = Place<L, W>::CT, CTP = Place<L, W>::CTP;
     static constexpr int VAR = L <= 8 ? 4 : L == 16 ? 2 : 1;  // orders of a lane's four states
     static constexpr int VS = TT * NP + (NP < 32 ? NP : 0);   // from order to order, apart in the banks
-    static constexpr int QS = CT + 8;
+    // The lanes' sums over n stand side by side for few lanes, whole for many: floats of a token
+    static constexpr bool PARTS = L == 4 || L == 8;  // (two lanes' parts would leave one CTA per SM)
+    static constexpr int WHOLE = CT + 8, ROW = PARTS ? L * CTP : WHOLE;
     float2 du[TT * Place<L, W>::DW];                             // (dt, u), u = dt x
     float w[TT * Place<L, W>::DW];
     float x[TT * CT], slope[TT * CT], zf[TT * CT];            // for the thread that wrote them
-    float y[TT * L * CTP], g[TT * L * CTP];                   // y and du: the lanes' parts of the sums over n
-    float dq[TT * QS];                                        // a whole one
+    float y[TT * ROW], g[TT * ROW], q[TT * WHOLE];            // the sums over n of y, du and (always whole) ddt's part
     float b[VAR * VS], c[VAR * VS];
     float sums[2][W][TT * NP];                               // dc and db of the warps' channels
+    // for the threads' channels, what is added up over the tiles too: in registers they would cost spills
+    float bias[CT], skip[CT], dskip[32 * W * Place<L, W>::V], dbias[32 * W * Place<L, W>::V];
 };
 
 // the lane's states from register order to memory order, and back
@@ -94,7 +97,7 @@ struct ChannelSums {
         }
     }
 };
-// Sums over a channel's lanes of one value, four tokens at a time from the last; out: [TT][CTP].
+// Sums over a channel's lanes of one value, four tokens at a time from the last; out: [.][stride]
 template <int L>
 struct StateSums {
     float v1, v3, r23;
@@ -106,12 +109,12 @@ struct StateSums {
         } else if ((t & 3) == 1) {
             v1 = s;
         } else {
-            const float r01 = halve(s, v1, lane, 1);
+            float v = halve(s, v1, lane, 1);
             if constexpr (L == 2) {
-                out[(t + gl) * stride + c] = r01;
+                out[(t + gl) * stride + c] = v;
                 out[(t + 2 + gl) * stride + c] = r23;
             } else {
-                float v = halve(r01, r23, lane, 2);
+                v = halve(v, r23, lane, 2);
 #pragma unroll
                 for (int o = 4; o < L; o *= 2) v += __shfl_xor_sync(ALL, v, o);
                 if (gl < 4) out[(t + gl) * stride + c] = v;
@@ -124,14 +127,14 @@ template <class XT, int L, int W, bool GATE, bool VEC>
 __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_kernel(const SelArgs A) {
     using P = Place<L, W>;
     using Sh = BwdShared<XT, L, W>;
-    constexpr int NT = P::NT, NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, VAR = Sh::VAR, VS = Sh::VS, QS = Sh::QS, SB = 8,
+    constexpr int NT = P::NT, NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, VAR = Sh::VAR, VS = Sh::VS, ROW = Sh::ROW, WHOLE = Sh::WHOLE, SB = 8,
                   V = P::V, Q = P::P, DW = P::DW;
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh& sh = *reinterpret_cast<Sh*>(raw_shared);
     const P p(A);
     const int n0 = p.gl * 4, pw = p.width(), order = p.cl & (VAR - 1), warp = threadIdx.x >> 5, entry = P::entry(p.c);
     const long long EN = (long long)A.E * A.N, own = (long long)p.ch * A.N, seg = (long long)p.b * A.nseg + p.s;
-    F2 g[2], A2[2], dA[2] = {f2(0.f), f2(0.f)}, bias[Q], skip[Q], dskip[Q], dbias[Q];
+    F2 g[2], A2[2], dA[2] = {f2(0.f), f2(0.f)};
     {
         float v[4] = {};
         if (p.live) load_states<4>(A.A + own, n0, A.N, A.vec_n, v);
@@ -145,22 +148,27 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
         if (from && p.live) load_states<4>(from + own, n0, A.N, A.vec_n, v);
         reorder<VAR>(v, order);
         pack<4>(v, g);
-        load_columns<V>(A.dt_bias, p.column(), pw, bias);
-        load_columns<V>(A.skip, p.column(), pw, skip);
+        F2 f[Q];
+        load_columns<V>(A.dt_bias, p.column(), pw, f);
+        if (p.row == 0) own_write<V>(sh.bias + p.first, f);
+        load_columns<V>(A.skip, p.column(), pw, f);
+        if (p.row == 0) own_write<V>(sh.skip + p.first, f);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) dskip[q] = dbias[q] = f2(0.f);
+        for (int q = 0; q < Q; ++q) f[q] = f2(0.f);
+        own_write<V>(sh.dskip + threadIdx.x * V, f);
+        own_write<V>(sh.dbias + threadIdx.x * V, f);
     }
-    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs + p.column(), *zp = static_cast<const XT*>(A.z) + p.b * A.zbs + p.column(),
-             *gp = static_cast<const XT*>(A.dy) + p.b * A.ybs + p.column(), *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N,
+    const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs, *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
+             *gp = static_cast<const XT*>(A.dy) + p.b * A.ybs, *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N,
              *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
-    const void* dp = dt_at<XT>(A, p.b, p.column());
-    const long long oat = (long long)p.b * A.T * A.E + p.column();
+    const void* dp = dt_at<XT>(A, p.b);
+    const long long oat = (long long)p.b * A.T * A.E;
     const float* marks = A.marks + (long long)p.b * A.nmarks * EN + own;
     auto put_dt = [&](int t, const F2* v) {
-        if (sizeof(XT) == 4 || A.dt32) store<VEC, float, V>(token<VEC>(static_cast<float*>(A.ddt) + oat, t, A.E), v, pw);
-        else store<VEC, XT, V>(token<VEC>(static_cast<XT*>(A.ddt) + oat, t, A.E), v, pw);
+        if (sizeof(XT) == 4 || A.dt32) store<VEC, float, V>(token<VEC>(static_cast<float*>(A.ddt) + oat, p.column(), t, A.E), v, pw);
+        else store<VEC, XT, V>(token<VEC>(static_cast<XT*>(A.ddt) + oat, p.column(), t, A.E), v, pw);
     };
-    auto put_x = [&](void* to, int t, const F2* v) { store<VEC, XT, V>(token<VEC>(static_cast<XT*>(to) + oat, t, A.E), v, pw); };
+    auto put_x = [&](void* to, int t, const F2* v) { store<VEC, XT, V>(token<VEC>(static_cast<XT*>(to) + oat, p.column(), t, A.E), v, pw); };
     auto mark = [&](int t, F2* h) {  // the state before token t
         float v[4] = {};
         if (p.live && t < p.te) load_states<4>(marks + (long long)(t / kSelMark) * EN, n0, A.N, A.vec_n, v);
@@ -174,10 +182,10 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r, n = r < TT && t < p.te ? pw : 0;
-            rx[k] = load<VEC, XT, V>(token<VEC>(xp, t, A.xts), n);
-            rd[k] = load_dt<VEC, XT, V>(A, dp, t, n);
-            ry[k] = load<VEC, XT, V>(token<VEC>(gp, t, A.yts), n);
-            if constexpr (GATE) rz[k] = load<VEC, XT, V>(token<VEC>(zp, t, A.zts), n);
+            rx[k] = load<VEC, XT, V>(token<VEC>(xp, p.column(), t, A.xts), n);
+            rd[k] = load_dt<VEC, XT, V>(A, dp, p.column(), t, n);
+            ry[k] = load<VEC, XT, V>(token<VEC>(gp, p.column(), t, A.yts), n);
+            if constexpr (GATE) rz[k] = load<VEC, XT, V>(token<VEC>(zp, p.column(), t, A.zts), n);
         }
         fetch_rows<VEC, XT, NP, W>(bp, A.bts, tb, p.te, A.N, rb);
         fetch_rows<VEC, XT, NP, W>(cp, A.cts, tb, p.te, A.N, rc);
@@ -187,17 +195,20 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r;
             if (r >= TT || pw == 0) continue;
-            prefetch(token<VEC>(xp, t, A.xts));
-            prefetch(token<VEC>(gp, t, A.yts));
-            prefetch(sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(token<VEC>(static_cast<const float*>(dp), t, A.dts))
-                                               : static_cast<const void*>(token<VEC>(static_cast<const XT*>(dp), t, A.dts)));
-            if constexpr (GATE) prefetch(token<VEC>(zp, t, A.zts));
+            prefetch(token<VEC>(xp, p.column(), t, A.xts));
+            prefetch(token<VEC>(gp, p.column(), t, A.yts));
+            prefetch(sizeof(XT) == 4 || A.dt32 ? static_cast<const void*>(token<VEC>(static_cast<const float*>(dp), p.column(), t, A.dts))
+                                               : static_cast<const void*>(token<VEC>(static_cast<const XT*>(dp), p.column(), t, A.dts)));
+            if constexpr (GATE) prefetch(token<VEC>(zp, p.column(), t, A.zts));
         }
         if (p.live && n0 < A.N)
 #pragma unroll
             for (int t = 0; t < TT; t += kSelMark) prefetch(marks + (long long)((tb + t) / kSelMark) * EN + n0);
     };
     auto prepare = [&](int tb) {
+        F2 bias[Q], dskip[Q];
+        own_read<V>(sh.bias + p.first, bias);
+        own_read<V>(sh.dskip + threadIdx.x * V, dskip);
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS;
@@ -231,6 +242,7 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
             own_write<V>(sh.slope + at, slope);
             if constexpr (GATE) own_write<V>(sh.zf + at, z);
         }
+        own_write<V>(sh.dskip + threadIdx.x * V, dskip);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             const int i = threadIdx.x + k * NT;
@@ -240,17 +252,24 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
             for (int v = 0; v < VAR; ++v) sh.b[v * VS + (i ^ v)] = vb, sh.c[v * VS + (i ^ v)] = vc;
         }
     };
+    auto whole = [&](const float* rows, int r, F2* f) {  // the thread's channels' sums over n
+        if constexpr (Sh::PARTS) lane_sums<L, W>(rows + r * ROW + p.first, f);
+        else own_read<V>(rows + r * ROW + p.first, f);
+    };
     auto finish = [&](int tb) {  // the tile's outputs
+        F2 skip[Q], dbias[Q];
+        own_read<V>(sh.skip + p.first, skip);
+        own_read<V>(sh.dbias + threadIdx.x * V, dbias);
 #pragma unroll
         for (int k = 0; k < PI; ++k) {
             const int r = p.row + k * P::ROWS, t = tb + r;
             if (r >= TT || t >= p.te) continue;
             const int at = r * CT + p.first;
             F2 x[Q], du[Q], f[Q], e[Q];
-            lane_sums<L, W>(sh.g + r * L * CTP + p.first, du);
+            whole(sh.g, r, du);
             own_read<V>(sh.x + at, x);
             own_read<V>(sh.slope + at, f);
-            own_read<V>(sh.dq + r * QS + p.first, e);
+            own_read<V>(sh.q + r * WHOLE + p.first, e);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 e[q] = mul2(fma2(e[q], f2(kLn2), mul2(du[q], x[q])), f[q]);
@@ -269,13 +288,14 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
             }
             put_x(A.dx, t, e);
             if constexpr (GATE) {
-                lane_sums<L, W>(sh.y + r * L * CTP + p.first, e);
+                whole(sh.y, r, e);
                 own_read<V>(sh.zf + at, f);
 #pragma unroll
                 for (int q = 0; q < Q; ++q) e[q] = mul2(fma2(skip[q], x[q], e[q]), f[q]);
                 put_x(A.dz, t, e);
             }
         }
+        own_write<V>(sh.dbias + threadIdx.x * V, dbias);
         float* out = A.parts_bc + (((long long)p.ct * A.B + p.b) * A.T + tb) * 2 * A.N;
         for (int i = threadIdx.x; i < 2 * TT * NP; i += NT) {
             const int kind = i / (TT * NP), j = i - kind * TT * NP, t = j / NP, n = j % NP;
@@ -296,12 +316,12 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
         prepare(tb);
         __syncthreads();
         F2 sA[2] = {f2(0.f), f2(0.f)};
-        StateSums<L> sq;
+        StateSums<L> sy, sg, sq;
         ChannelSums<L> sc;
         const float *vb = sh.b + order * VS + n0, *vc = sh.c + order * VS + n0;
         const float2* dtu = sh.du + entry;
         const float* ws = sh.w + entry;
-        float *ys = sh.y + p.gl * CTP + p.c, *dus = sh.g + p.gl * CTP + p.c;
+        float *ys = sh.y + p.gl * CTP + p.c, *gs = sh.g + p.gl * CTP + p.c;  // the lane's parts
 #pragma unroll 1
         for (int q = TT - SB; q >= 0; q -= SB) {
             F2 a[SB][2], hp[SB][2], h[2];
@@ -347,10 +367,15 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
                     sA[k] = fma2(ah, dt, sA[k]);
                     h[k] = hp[j][k];
                 }
-                if constexpr (GATE) ys[t * L * CTP] = total(yy);
-                dus[t * L * CTP] = total(dd);
                 // j stands for t in the choice of what is handed on: q is a multiple of 4
-                sq.add(sh.dq + q * QS, QS, j, total(qq), p.lane, p.gl, p.c);
+                if constexpr (Sh::PARTS) {
+                    if constexpr (GATE) ys[t * ROW] = total(yy);
+                    gs[t * ROW] = total(dd);
+                } else {
+                    if constexpr (GATE) sy.add(sh.y + q * ROW, ROW, j, total(yy), p.lane, p.gl, p.c);
+                    sg.add(sh.g + q * ROW, ROW, j, total(dd), p.lane, p.gl, p.c);
+                }
+                sq.add(sh.q + q * WHOLE, WHOLE, j, total(qq), p.lane, p.gl, p.c);
                 sc.add(sh.sums[0][warp] + q * NP, sh.sums[1][warp] + q * NP, j, dc, db, p.lane, p.gl, p.cl);
             }
         }
@@ -375,19 +400,16 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
             store_states<4>(A.dh0 + p.b * EN + own, n0, A.N, A.vec_n, v);
         }
     }
-    // the sums over tokens per channel: row by row, in order
     __syncthreads();
-    float *s0 = reinterpret_cast<float*>(raw_shared), *s1 = s0 + NT * V;
-    own_write<V>(s0 + threadIdx.x * V, dskip);
-    own_write<V>(s1 + threadIdx.x * V, dbias);
-    __syncthreads();
-    if (p.row == 0) {
+    if (p.row == 0) {  // the sums over tokens per channel: row by row, in order
+        F2 dskip[Q], dbias[Q], o[Q];
+        own_read<V>(sh.dskip + threadIdx.x * V, dskip);
+        own_read<V>(sh.dbias + threadIdx.x * V, dbias);
         for (int r = 1; r < P::ROWS; ++r) {
-            F2 o[Q];
-            own_read<V>(s0 + (r * P::QUADS + threadIdx.x) * V, o);
+            own_read<V>(sh.dskip + (r * P::QUADS + threadIdx.x) * V, o);
 #pragma unroll
             for (int q = 0; q < Q; ++q) dskip[q] = add2(dskip[q], o[q]);
-            own_read<V>(s1 + (r * P::QUADS + threadIdx.x) * V, o);
+            own_read<V>(sh.dbias + (r * P::QUADS + threadIdx.x) * V, o);
 #pragma unroll
             for (int q = 0; q < Q; ++q) dbias[q] = add2(dbias[q], o[q]);
         }
