@@ -165,6 +165,7 @@ struct ConvArgs {
 // selective.cuh: selective state space scan
 constexpr int kSelTile = 16;     // tokens that a CTA stages at once
 constexpr int kSelMark = 8;      // tokens between the states that the forward pass leaves for the backward pass
+constexpr int kSelFold = 32;     // segments that a CTA goes through itself for the state that enters its own
 constexpr int kSelMaxN = 128;
 constexpr int kSelMaxSize = 1 << 30;  // channels, and tokens
 
@@ -181,6 +182,7 @@ struct SelArgs {
     long long xbs, xts, dbs, dts, zbs, zts, bbs, bts, cbs, cts, ybs, yts;  // batch and token strides; y: dy's
     int B, T, E, N, G, Eg;                         // Eg = E/G channels per group of b and c
     int tiles, nseg, seg, nmarks;                  // channel tiles per group; segments of the time axis, their tokens
+    bool joined;                                   // seg_state holds what enters the segments (join_kernel), not their own states
     bool dt32, softplus, vec, vec_n;               // vec: sel_width() channels (one token: four of b and c too), vec_n: four states in one access
 };
 

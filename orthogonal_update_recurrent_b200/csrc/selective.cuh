@@ -439,6 +439,31 @@ __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, in
     }
 }
 
+// The state that enters the CTA's segment (REV: the cotangent that enters it from behind), of the thread's S states as they stand in
+// memory: the sequence's own, then through the segments before it, each with its own state from 0 and the sum of its steps; or, where there are
+// many segments, as join_kernel has left it.
+template <int L, int W, int S, bool REV>
+__device__ __forceinline__ void entering(const SelArgs& A, const Place<L, W>& p, int n0, const float* a2, float* h) {
+    const long long EN = (long long)A.E * A.N, own = (long long)p.ch * A.N;
+#pragma unroll
+    for (int k = 0; k < S; ++k) h[k] = 0.f;
+    if (!p.live) return;
+    const float* first = REV ? A.dh_T : A.h0;
+    if (A.joined) load_states<S>(A.seg_state + ((long long)p.b * A.nseg + p.s) * EN + own, n0, A.N, A.vec_n, h);
+    else if (first) load_states<S>(first + p.b * EN + own, n0, A.N, A.vec_n, h);
+    if (A.joined || A.nseg == 1) return;
+    const int n = REV ? A.nseg - 1 - p.s : p.s;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const long long at = (long long)p.b * A.nseg + (REV ? A.nseg - 1 - i : i);
+        const float sum = A.seg_sum[at * A.E + p.ch];
+        float v[S];
+        load_states<S>(A.seg_state + at * EN + own, n0, A.N, A.vec_n, v);
+#pragma unroll
+        for (int k = 0; k < S; ++k) h[k] = fmaf(ex2(a2[k] * sum), h[k], v[k]);
+    }
+}
+
 // ---- forward: all tokens of a segment, from the state that enters it
 // Between two barriers a CTA finishes the tile before, prepares the next one (in the other buffers) and works on its own.
 template <class XT, int L, int S, int W>
@@ -465,13 +490,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
 #pragma unroll
         for (int k = 0; k < S; ++k) v[k] *= kLog2e;
         pack<S>(v, A2);
-        const float* from = A.nseg > 1 ? A.seg_state + ((long long)(p.b * A.nseg + p.s) * A.E) * A.N
-                            : A.h0   ? A.h0 + (long long)p.b * A.E * A.N
-                                     : nullptr;
-#pragma unroll
-        for (int k = 0; k < S; ++k) v[k] = 0.f;
-        if (from && p.live) load_states<S>(from + (long long)p.ch * A.N, n0, A.N, A.vec_n, v);
-        pack<S>(v, h);
+        float e[S];
+        entering<L, W, S, false>(A, p, n0, v, e);
+        pack<S>(e, h);
         load_columns<V>(A.dt_bias, p.column(), pw, bias);
         load_columns<V>(A.skip, p.column(), pw, skip);
     }
@@ -735,7 +756,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
     }
 }
 
-// The states that enter the segments (REV: the cotangents that enter them from behind), in place.
+// The states that enter the segments (REV: the cotangents that enter them from behind), in place: for more than kSelFold segments, which
+// take longer to go through than a launch.
 template <bool REV>
 __global__ void __launch_bounds__(256) join_kernel(const SelArgs A) {
     const long long per = (long long)A.E * A.N, i = (long long)blockIdx.x * 256 + threadIdx.x;

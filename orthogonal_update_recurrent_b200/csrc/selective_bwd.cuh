@@ -138,16 +138,14 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
     {
         float v[4] = {};
         if (p.live) load_states<4>(A.A + own, n0, A.N, A.vec_n, v);
-        reorder<VAR>(v, order);
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] *= kLog2e;
-        pack<4>(v, A2);
-        const float* from = A.nseg > 1 ? A.seg_state + seg * EN : A.dh_T ? A.dh_T + p.b * EN : nullptr;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = 0.f;
-        if (from && p.live) load_states<4>(from + own, n0, A.N, A.vec_n, v);
+        float e[4];
+        entering<L, W, 4, true>(A, p, n0, v, e);
         reorder<VAR>(v, order);
-        pack<4>(v, g);
+        pack<4>(v, A2);
+        reorder<VAR>(e, order);
+        pack<4>(e, g);
         F2 f[Q];
         load_columns<V>(A.dt_bias, p.column(), pw, f);
         if (p.row == 0) own_write<V>(sh.bias + p.first, f);
@@ -418,10 +416,35 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
     }
 }
 
-// db and dc from the channel tiles' sums, in their order. A CTA has `tokens` of a sequence; its threads stand for the 2 N
-// values of a token's group, padded to a power of two, and as many groups at once as are left.
+// What the CTAs have left in the workspace, in one launch. The first `most` CTAs: db and dc from the channel tiles' sums, in their order. Such a
+// CTA has `tokens` of a sequence; its threads stand for the 2 N values of a token's group, padded to a power of two (width), and as many
+// groups at once as are left. The others: dA, dskip and ddt_bias from the sequences' and segments' sums, 32 columns and 8 slices of these
+// per CTA, slices added up in order.
 template <class XT>
-__global__ void __launch_bounds__(256) shared_kernel(const SelArgs A, int width, int tokens) {
+__global__ void __launch_bounds__(256) sums_kernel(const SelArgs A, int width, int tokens, int most) {
+    if ((int)blockIdx.x >= most) {
+        __shared__ float sum[8][33];
+        const long long EN = (long long)A.E * A.N, i = (long long)((int)blockIdx.x - most) * 32 + (threadIdx.x & 31);
+        const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+        const bool in = i < EN + 2 * A.E, ch = i >= EN;
+        const float* from = ch ? A.parts_ch + (i - EN) : A.parts_A + i;
+        const long long step = ch ? 2 * A.E : EN;
+        float v = 0.f;
+        if (in)
+#pragma unroll 4
+            for (int k = slice; k < A.B * A.nseg; k += 8) v += from[k * step];
+        sum[slice][lane] = v;
+        __syncthreads();
+        if (slice || !in) return;
+        for (int k = 1; k < 8; ++k) v += sum[k][lane];
+        if (!ch) A.dA[i] = v;
+        else if (i - EN < A.E) {
+            if (A.dskip) A.dskip[i - EN] = v;
+        } else if (A.ddt_bias) {
+            A.ddt_bias[i - EN - A.E] = v;
+        }
+        return;
+    }
     const int n2 = 2 * A.N, per = (A.T + tokens - 1) / tokens, b = blockIdx.x / per, t0 = (blockIdx.x - b * per) * tokens;
     const int m = threadIdx.x & (width - 1), kind = m >= A.N, n = m - kind * A.N, step = 256 / width;
     if (m >= n2) return;
@@ -437,31 +460,6 @@ __global__ void __launch_bounds__(256) shared_kernel(const SelArgs A, int width,
             for (int k = 0; k < A.tiles; ++k) v += from[k * all];
         }
         put(to + (long long)r * A.N, v);
-    }
-}
-
-// dA, dskip and ddt_bias from the sequences' and segments' sums: 32 columns and 32 slices of these per CTA, slices added up in order
-inline __global__ void __launch_bounds__(1024) weights_kernel(const SelArgs A) {
-    __shared__ float sum[32][33];
-    const long long EN = (long long)A.E * A.N;
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const long long i = (long long)blockIdx.x * 32 + lane;
-    const bool in = i < EN + 2 * A.E, ch = i >= EN;
-    const float* from = ch ? A.parts_ch + (i - EN) : A.parts_A + i;
-    const long long step = ch ? 2 * A.E : EN;
-    float v = 0.f;
-    if (in)
-#pragma unroll 4
-        for (int k = slice; k < A.B * A.nseg; k += 32) v += from[k * step];
-    sum[slice][lane] = v;
-    __syncthreads();
-    if (slice || !in) return;
-    for (int k = 1; k < 32; ++k) v += sum[k][lane];
-    if (!ch) A.dA[i] = v;
-    else if (i - EN < A.E) {
-        if (A.dskip) A.dskip[i - EN] = v;
-    } else if (A.ddt_bias) {
-        A.ddt_bias[i - EN - A.E] = v;
     }
 }
 

@@ -25,7 +25,7 @@ lattice_status forward(const SelArgs& a, cudaStream_t st) {
     if (a.nseg > 1) {
         lattice_status s = start(seg_kernel<XT, L, S, W, false, VEC>, a, 32 * W, sizeof(SegShared<XT, L, S, W>), ctas_of(a), st);
         if (s != LATTICE_OK) return s;
-        s = start(join_kernel<false>, a, 256, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
+        if (a.joined) s = start(join_kernel<false>, a, 256, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
         if (s != LATTICE_OK) return s;
     }
     return start(fwd_kernel<XT, L, S, W, VEC>, a, 32 * W, sizeof(FwdShared<XT, L, S, W>), ctas_of(a), st);
@@ -42,25 +42,21 @@ lattice_status backward(const SelArgs& a, cudaStream_t st) {
     if (a.nseg > 1) {
         s = start(seg_kernel<XT, L, 4, W, true, VEC>, a, 32 * W, sizeof(SegShared<XT, L, 4, W>), ctas_of(a), st);
         if (s != LATTICE_OK) return s;
-        s = start(join_kernel<true>, a, 256, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
+        if (a.joined) s = start(join_kernel<true>, a, 256, 0, ((long long)a.B * a.E * a.N + 255) / 256, st);
         if (s != LATTICE_OK) return s;
     }
     s = a.z ? start(bwd_kernel<XT, L, W, true, VEC>, a, 32 * W, sizeof(BwdShared<XT, L, W>), ctas_of(a), st)
             : start(bwd_kernel<XT, L, W, false, VEC>, a, 32 * W, sizeof(BwdShared<XT, L, W>), ctas_of(a), st);
     if (s != LATTICE_OK) return s;
-    if (a.T > 0) {
-        int width = 2;
-        while (width < 2 * a.N) width *= 2;
-        long long tokens = (long long)a.B * a.T / (16 * sm_count());  // several CTAs per SM, none with more than 64 tokens
-        const int least = 256 / width / a.G;
-        tokens = tokens > 64 ? 64 : tokens < least ? least : tokens < 1 ? 1 : tokens;
-        const long long ctas = a.B * ((a.T + tokens - 1) / tokens);
-        if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
-        shared_kernel<XT><<<(unsigned)ctas, 256, 0, st>>>(a, width, (int)tokens);
-        s = launch_status();
-        if (s != LATTICE_OK) return s;
-    }
-    return start(weights_kernel, a, 1024, 0, ((long long)a.E * a.N + 2 * a.E + 31) / 32, st);
+    int width = 2;
+    while (width < 2 * a.N) width *= 2;
+    long long tokens = (long long)a.B * a.T / (16 * sm_count());  // several CTAs per SM, none with more than 64 tokens
+    const int least = 256 / width / a.G;
+    tokens = tokens > 64 ? 64 : tokens < least ? least : tokens < 1 ? 1 : tokens;
+    const long long most = a.T > 0 ? a.B * ((a.T + tokens - 1) / tokens) : 0, ctas = most + ((long long)a.E * a.N + 2 * a.E + 31) / 32;
+    if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
+    sums_kernel<XT><<<(unsigned)ctas, 256, 0, st>>>(a, width, (int)tokens, (int)most);
+    return launch_status();
 }
 template <class XT, int L>
 lattice_status backward(const SelArgs& a, int W, cudaStream_t st) {
