@@ -21,7 +21,7 @@ lattice_status run(const ConvArgs& a, int what, cudaStream_t st) {
         if (a.parts) {
             const lattice_status s = launch_status();
             if (s != LATTICE_OK) return s;
-            weights_kernel<<<(unsigned)(((long long)(K + 1) * a.C + 31) / 32), 1024, 0, st>>>(a, a.B * a.runs);
+            weights_kernel<<<(unsigned)(((long long)(K + 1) * a.C + 31) / 32), 1024, 0, st>>>(a, (long long)a.B * a.runs);
         }
     }
     return launch_status();

@@ -427,7 +427,7 @@ bool sel_vec(const SelArgs& a, size_t sx, int V) {
 }
 void sel_place(SelArgs& a, const SelPlan& p, const SelSpace& s, void* workspace) {
     a.tiles = p.tiles; a.nseg = p.nseg; a.seg = p.seg;
-    a.joined = p.nseg > kSelFold;
+    a.joined = p.nseg > kSelFold || (p.nseg > 1 && a.h0 && a.h0 == a.h_out);  // in place: h0 is read before any CTA writes
     float* w = static_cast<float*>(workspace);
     if (p.nseg > 1) a.seg_state = w, a.seg_sum = w + s.state;
     if (s.A) a.parts_A = w + s.state + s.sum, a.parts_ch = a.parts_A + s.A, a.parts_bc = a.parts_ch + s.ch;

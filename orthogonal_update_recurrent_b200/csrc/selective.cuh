@@ -439,9 +439,13 @@ __device__ __forceinline__ void fetch_rows(const XT* p, long long ts, int tb, in
     }
 }
 
+// A segment's own state and what is left of the one that entered it. The decays of a segment together may be past the largest number where
+// A or dt has the other sign; a state of 0 stays 0 all the same.
+__device__ __forceinline__ float pass_on(float h, float keep, float own) { return h == 0.f ? own : fmaf(keep, h, own); }
+
 // The state that enters the CTA's segment (REV: the cotangent that enters it from behind), of the thread's S states as they stand in
 // memory: the sequence's own, then through the segments before it, each with its own state from 0 and the sum of its steps; or, where there are
-// many segments, as join_kernel has left it.
+// many segments or the final state overwrites h0, as join_kernel has left it.
 template <int L, int W, int S, bool REV>
 __device__ __forceinline__ void entering(const SelArgs& A, const Place<L, W>& p, int n0, const float* a2, float* h) {
     const long long EN = (long long)A.E * A.N, own = (long long)p.ch * A.N;
@@ -460,7 +464,7 @@ __device__ __forceinline__ void entering(const SelArgs& A, const Place<L, W>& p,
         float v[S];
         load_states<S>(A.seg_state + at * EN + own, n0, A.N, A.vec_n, v);
 #pragma unroll
-        for (int k = 0; k < S; ++k) h[k] = fmaf(ex2(a2[k] * sum), h[k], v[k]);
+        for (int k = 0; k < S; ++k) h[k] = pass_on(h[k], ex2(a2[k] * sum), v[k]);
     }
 }
 
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) fwd_kernel(const SelArgs A) {
         load_columns<V>(A.skip, p.column(), pw, skip);
     }
     const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs, *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
-             *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N, *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
+             *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + (long long)p.g * A.N, *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + (long long)p.g * A.N;
     const void* dp = dt_at<XT>(A, p.b);
     XT* yp = static_cast<XT*>(A.y) + (long long)p.b * A.T * A.E;
     Raw<XT, V> rx[PI], rz[PI];
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
     }
     const XT *xp = static_cast<const XT*>(REV ? A.dy : A.x) + p.b * (REV ? A.ybs : A.xbs),
              *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
-             *vp = static_cast<const XT*>(REV ? A.c : A.b) + p.b * (REV ? A.cbs : A.bbs) + p.g * A.N;
+             *vp = static_cast<const XT*>(REV ? A.c : A.b) + p.b * (REV ? A.cbs : A.bbs) + (long long)p.g * A.N;
     const void* dp = dt_at<XT>(A, p.b);
     const long long xts = REV ? A.yts : A.xts, vts = REV ? A.cts : A.bts;
     const bool gated = REV && A.z;
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) seg_kernel(const SelArgs A) {
 }
 
 // The states that enter the segments (REV: the cotangents that enter them from behind), in place: for more than kSelFold segments, which
-// take longer to go through than a launch.
+// take longer to go through than a launch, and for a final state that overwrites h0, which CTAs still to come could not read any more.
 template <bool REV>
 __global__ void __launch_bounds__(256) join_kernel(const SelArgs A) {
     const long long per = (long long)A.E * A.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -769,9 +773,9 @@ __global__ void __launch_bounds__(256) join_kernel(const SelArgs A) {
     for (int k = 0; k < A.nseg; ++k) {
         const long long at = b * A.nseg + (REV ? A.nseg - 1 - k : k);
         float* p = A.seg_state + at * per + en;
-        const float own = *p, keep = exp2f(a * A.seg_sum[at * A.E + e]);
+        const float own = *p, keep = ex2(a * A.seg_sum[at * A.E + e]);
         *p = h;
-        h = fmaf(keep, h, own);
+        h = pass_on(h, keep, own);
     }
 }
 
@@ -782,9 +786,9 @@ template <class XT, int L, int R, bool VEC>
 __global__ void __launch_bounds__(256) step_kernel(const SelArgs A) {
     constexpr int LR = L < R ? L : R, PR = R / LR;  // lanes with sequences of their own, and how many of these
     const unsigned per = (unsigned)(((long long)A.E * L + 255) / 256), blk = blockIdx.x / per;  // CTAs per R sequences
-    const unsigned i = (blockIdx.x - blk * per) * 256u + threadIdx.x;
-    const int gl = (int)(i % L), n0 = gl * 4, lane = threadIdx.x & 31;
-    const bool in = i / L < (unsigned)A.E;
+    const long long i = (long long)(blockIdx.x - blk * per) * 256 + threadIdx.x;
+    const int gl = (int)(threadIdx.x % L), n0 = gl * 4, lane = threadIdx.x & 31;
+    const bool in = i / L < A.E;
     const int e = in ? (int)(i / L) : 0, g = A.G == 1 ? 0 : e / A.Eg;
     const int b0 = (int)blk * R, most = A.B - 1;  // sequences past the last read the last one's
     const int live = !in ? 0 : min(R, A.B - b0);
@@ -794,8 +798,8 @@ __global__ void __launch_bounds__(256) step_kernel(const SelArgs A) {
     for (int k = 0; k < R; ++k) {
         const long long b = min(b0 + k, most);
         load_states<4>(A.h0 + b * EN + own, n0, A.N, VEC, h[k]);
-        load_row<VEC>(static_cast<const XT*>(A.b) + b * A.bbs + g * A.N, n0, A.N, bv[k]);
-        load_row<VEC>(static_cast<const XT*>(A.c) + b * A.cbs + g * A.N, n0, A.N, cv[k]);
+        load_row<VEC>(static_cast<const XT*>(A.b) + b * A.bbs + (long long)g * A.N, n0, A.N, bv[k]);
+        load_row<VEC>(static_cast<const XT*>(A.c) + b * A.cbs + (long long)g * A.N, n0, A.N, cv[k]);
     }
     load_states<4>(A.A + own, n0, A.N, VEC, a);
     const float bias = A.dt_bias ? A.dt_bias[e] : 0.f, skip = A.skip ? A.skip[e] : 0.f;

@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
         own_write<V>(sh.dbias + threadIdx.x * V, f);
     }
     const XT *xp = static_cast<const XT*>(A.x) + p.b * A.xbs, *zp = static_cast<const XT*>(A.z) + p.b * A.zbs,
-             *gp = static_cast<const XT*>(A.dy) + p.b * A.ybs, *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + p.g * A.N,
-             *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + p.g * A.N;
+             *gp = static_cast<const XT*>(A.dy) + p.b * A.ybs, *bp = static_cast<const XT*>(A.b) + p.b * A.bbs + (long long)p.g * A.N,
+             *cp = static_cast<const XT*>(A.c) + p.b * A.cbs + (long long)p.g * A.N;
     const void* dp = dt_at<XT>(A, p.b);
     const long long oat = (long long)p.b * A.T * A.E;
     const float* marks = A.marks + (long long)p.b * A.nmarks * EN + own;

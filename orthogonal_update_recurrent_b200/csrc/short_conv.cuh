@@ -422,14 +422,14 @@ __global__ void __launch_bounds__(256, conv_resident(true, K)) bwd_kernel(const 
 }
 
 // Column sums of [n][(K+1) C]: 32 columns and 32 slices of the rows per CTA, slices added up in order.
-inline __global__ void __launch_bounds__(1024) weights_kernel(const ConvArgs A, int n) {
+inline __global__ void __launch_bounds__(1024) weights_kernel(const ConvArgs A, long long n) {
     __shared__ float sum[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const long long cols = (long long)(A.K + 1) * A.C, c = (long long)blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < cols)
 #pragma unroll 4
-        for (int i = slice; i < n; i += 32) t += A.parts[i * cols + c];
+        for (long long i = slice; i < n; i += 32) t += A.parts[i * cols + c];
     sum[slice][lane] = t;
     __syncthreads();
     if (slice || c >= cols) return;

@@ -237,3 +237,28 @@ def test_without_marks_and_marks_alone(L):
     marks = L.selective_scan_marks(t["x"], 16)
     y2, h2 = L.selective_scan_fwd(*args, h0=t["h0"], marks=marks)
     assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(marks[:, 0], t["h0"])
+
+
+@pytest.mark.parametrize("T", [900, 5000])
+def test_state_in_place_over_segments(L, T):
+    """The final state over the initial one, which all segments' entering states need: the same as into another place."""
+    t = make(1, T, 24, 16)
+    args, how = [t[k] for k in ("x", "dt", "A", "b", "c")], {"skip": t["skip"], "z": t["z"], "dt_bias": t["dt_bias"] - 5}  # long memory
+    assert L.lib().lattice_selective_scan_workspace_bytes(1, T, 24, 16, 1, 0) > 0
+    y, h = L.selective_scan_fwd(*args, h0=t["h0"], **how)
+    state = t["h0"].clone()
+    y2, h2 = L.selective_scan_fwd(*args, h0=state, h_out=state, **how)
+    assert h2 is state and torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def test_growing_states_over_segments(L):
+    """A > 0, whose growth over a segment is past the largest number, on states and cotangents that are 0 there."""
+    t = make(1, 900, 12, 16, softplus=False, h0=False)
+    t["A"] = -t["A"]
+    t["x"][:, :-5], t["dy"][:, 5:] = 0.0, 0.0
+    got = call(L, t)
+    how = {k: t[k] for k in ("x", "dt", "A", "b", "c", "skip", "z", "dt_bias", "softplus", "h0", "lengths", "dy", "dh_T")}
+    want, mag = R.selective(**how), R.selective(**how, mag=True)
+    for k in ("y", "h_T", "dx", "dz", "ddt", "db", "dc", "dA"):  # 5 steps remembered: 2 * 10 * 5 + 2 * 16 + 64 + 900 / 16
+        assert torch.isfinite(got[k]).all(), k
+        R.close(got[k], want[k], mag[k], 253, k)
