@@ -319,47 +319,48 @@ void conv_args(ConvArgs& a, const void* x, lattice_dtype x_dtype, long long xbs,
 struct SelPlan {
     int S, W, tiles, nseg, seg;
 };
-// Channel tiles of a group: W warps of 32/lanes channels each
+// Channel tiles of a group
 long long sel_tiles(int Eg, int lanes, int W) {
     const int per = W * (32 / lanes);
     return ((long long)Eg + per - 1) / per;
 }
-// Warps of a CTA: 8, or 2 where 8 would leave so many more of them without channels that it pays: a warp of two takes 1.1 times a
-// warp of eight's time, backward, with its share of the sums over channels, 1.7 times (mid-size layer: 636 and 698 us, 1713 and 2886 us; 20
-// sequences of 49370 tokens at most, 12 channels, 16 states, forward and backward: 2966 us with 8 warps, 880 us with 2).
+// Warps of a CTA: 8, or 2 where 8 would leave so many more of them without channels that it pays: a warp of two takes 1.1 times the time,
+// backward, with its share of the sums over channels, 1.7 times (mid-size layer: 636 and 698 us, 1713 and 2886 us; 20 sequences of 49370
+// tokens at most, 12 channels, 16 states, forward and backward: 2966 us with 8 warps, 880 us with 2).
 int sel_warps(int Eg, int lanes, bool bwd) {
     return (double)sel_tiles(Eg, lanes, 8) * 4 > (bwd ? 1.7 : 1.1) * (double)sel_tiles(Eg, lanes, 2) ? 2 : 8;
 }
-// How the work is spread. A CTA has 256/L channels (64/L) with N padded to L S states, and goes through its tokens alone. With few
-// CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose
-// states take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token and by
-// CTAs per SM, are what was measured (bf16, 16 states, gate; they hold for other N, whose CTAs have as many states), the cheapest
-// sum is taken: forward, 1024 / 2048 / 4096 / 6144 channels of 4096, 4096, 2048, 2048 tokens: four states 383 / 386 / 202 / 200 us,
-// two states 246 / 246 / 134 / 196, segments 88 / 142 / 143 / 200; backward, whole 1155 / 1201 / 627 / 637, segments
-// 190 / 304 / 331 / 429.
+// How the work is spread. A CTA has 256/L channels (64/L for few channels) with N padded to L S states, and goes through its tokens alone.
+// With few CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose states
+// take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token of a CTA's and by CTAs per
+// SM, are what was measured (bf16, 16 states, gate; they hold for other N, whose CTAs have as many states); the cheapest is taken. Forward,
+// 1024 / 2048 / 4096 / 8192 / 16384 channels of 4096, 4096, 2048, 2048, 2048 tokens: four states 430 / 435 / 238 / 238 / 355 us, two states
+// 297 / 297 / 167 / 240 / 427, segments 111 / 170 / 181 / 312; backward, whole 1155 / 1201 / 627 / 637 / 865, segments 188 / 303 / 329 / 589.
 SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
-    const int np = sel_padded(N), Eg = E / G, W = sel_warps(Eg, np / 4, bwd), unit = 8 / W;  // CTAs that count as one of 8 warps
-    const long long sm = sm_count(), base = (long long)B * G * sel_tiles(Eg, np / 4, W);
-    auto time = [&](long long ctas, int u, double one, double two, double more) {
-        const long long per = (ctas + sm * u - 1) / (sm * u);
-        return per == 1 ? one : per == 2 ? two : more * (double)per;
+    const int np = sel_padded(N), Eg = E / G;
+    const long long sm = sm_count(), tiles = ((long long)T + kSelTile - 1) / kSelTile;
+    const double whole[2][3] = {{0.11, 0.165, 0.08}, {0.30, 0.39, 0.205}}, split[2][3] = {{0.168, 0.26, 0.13}, {0.37, 0.565, 0.29}},
+                 two[3] = {0.072, 0.117, 0.052};  // one CTA per SM, two, and each of more
+    SelPlan p = {};
+    double best = -1;
+    auto offer = [&](int S, bool segments, const double* us) {
+        const int W = sel_warps(Eg, np / S, bwd), unit = 8 / W;  // CTAs that count as one of 8 warps' channels
+        const long long ct = sel_tiles(Eg, np / S, W), base = (long long)B * G * ct;
+        long long n = 1, tokens = T;
+        if (segments) {
+            n = 2 * sm * unit / base;
+            if (n > tiles / 4) n = tiles / 4;
+            if (n <= 1) return;
+            tokens = (tiles + n - 1) / n * kSelTile;
+            n = (T + tokens - 1) / tokens;
+        }
+        const long long per = (base * n + sm * unit - 1) / (sm * unit);
+        const double time = (double)tokens * (per <= 2 ? us[per - 1] : us[2] * (double)per) + (segments ? 15 : 0);
+        if (best < 0 || time < best) best = time, p = {S, W, (int)ct, (int)n, (int)(tokens > 0 ? tokens : 1)};
     };
-    SelPlan p = {4, W, (int)sel_tiles(Eg, np / 4, W), 1, T > 0 ? T : 1};
-    double best = T * (bwd ? time(base, unit, 0.30, 0.455, 0.23) : time(base, unit, 0.098, 0.163, 0.0815));
-    if (!bwd && np <= 32) {
-        const int W2 = sel_warps(Eg, np / 2, false);
-        const long long tiles = sel_tiles(Eg, np / 2, W2);
-        const double us = T * time((long long)B * G * tiles, 8 / W2, 0.065, 0.107, 0.0515);
-        if (us < best) best = us, p.S = 2, p.W = W2, p.tiles = (int)tiles;
-    }
-    const long long tiles = ((long long)T + kSelTile - 1) / kSelTile;
-    long long n = 2 * sm * unit / base;
-    if (n > tiles / 4) n = tiles / 4;
-    if (n > 1) {
-        const long long per = (tiles + n - 1) / n;
-        const double us = per * kSelTile * (bwd ? time(base * n, unit, 0.37, 0.565, 0.29) : time(base * n, unit, 0.168, 0.26, 0.13)) + (bwd ? 15 : 12);
-        if (us < best) p = {4, W, (int)sel_tiles(Eg, np / 4, W), (int)((tiles + per - 1) / per), (int)(per * kSelTile)};
-    }
+    offer(4, false, whole[bwd]);
+    offer(4, true, split[bwd]);
+    if (!bwd && np <= 32) offer(2, false, two);
     return p;
 }
 // Floats of the workspace's parts, each a multiple of 4: the segments' states and sums, and backward the CTAs' sums
