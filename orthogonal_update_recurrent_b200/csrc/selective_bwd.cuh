@@ -4,11 +4,16 @@
 // before every kSelMark-th token; from it a thread recomputes 8 tokens' states, keeps them and their decays in
 // registers, and goes back through them with the cotangent g.
 //
-// Sums over a channel's states (y, du, and ddt's part) are taken as in the forward pass, over many lanes by shuffles. Sums
+// Sums over a channel's states (y, du) are taken as in the forward pass or, where the lanes' parts would take too much shared memory,
+// by shuffles, four tokens at once (each lane hands half of its tokens on per step), and ddt's part always. Sums
 // over channels (db, dc) are shuffles over the warp's channels; a lane names its four states so that what it
 // keeps and what it hands on have the same registers in all lanes (register r stands for state r ^ (channel & 3)),
 // which takes the selects out of the first two steps; shared memory adds the warps up, the workspace the CTAs. All in a
 // fixed order.
+//
+// Mid-size layer (8 x 4096 tokens of 2048 bf16 channels, 16 states, gate): 1575 us, of which HBM would need 225, and 48 us for the sums
+// over the channel tiles. A token costs a warp 116 instructions for 128 states: 58 % of the issue slots; shared memory and shuffles keep
+// their pipe busy 65 % of the time, at 16 warps per SM (127 registers: 8 tokens' states and decays).
 #pragma once
 #include "selective.cuh"
 

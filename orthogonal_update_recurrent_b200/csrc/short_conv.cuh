@@ -7,7 +7,11 @@
 //
 // HBM bounds it: x is read once and y written once. A thread has V neighbouring channels and
 // walks down a run of tokens with the last K-1 inputs in registers, loads of the next U tokens under way
-// at once; a run's K-1 first inputs are its neighbour's last ones and mostly come from the L2.
+// at once; a run's K-1 first inputs are its neighbour's last ones and mostly come from the L2. The mid-size layer (8 x 4096 tokens of
+// 2048 bf16 channels, 4 taps) takes 53.5 us forward, 5.0 TB/s of what has to move, with the special function units 59 % busy (the SiLU's
+// exponential and reciprocal); backward 108 us, 3.7 TB/s, where a token's 117 instructions bind at 16 warps per SM (a thread's 128 registers
+// hold weights, window, slopes and sums; copies through shared memory keep loads out of them). One token of 256 sequences of
+// 4096 channels takes 5 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -228,10 +232,17 @@ __global__ void __launch_bounds__(256, conv_resident(false, K)) fwd_kernel(const
         for (int j = 0; j < U; ++j) to[j] = load<XT, V>(x, j * A.xts);
         x += U * A.xts;
     };
+    // The U tokens after those are brought into the L2, which takes no registers (mid-size layer 55.9 -> 53.5 us; 2051 channels,
+    // call included, 113 -> 102 us). With more taps a token's arithmetic hides the way, and they cost more than they give (8 taps: 89 -> 97 us).
+    auto ahead = [&]() {
+#pragma unroll
+        for (int j = 0; j < U; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + j * A.xts));
+    };
     if (t + U <= te) fetch(r);
 #pragma unroll 1
     for (; t + U <= te; t += U) {
         if (t + 2 * U <= te) fetch(next);
+        if (K <= 4 && t + 3 * U <= te) ahead();
 #pragma unroll
         for (int j = 0; j < U; ++j) token(r[j]), r[j] = next[j];
     }
