@@ -336,9 +336,9 @@ def time_calls(torch, f, steps, warmup, flush=None):
 
 
 def layer_ops(torch, L, w: LI.Workload, device, flush, pk) -> dict:
-    """The gated recurrence and the block norms on a workload's shape (bf16, logit gates):
-    what a layer of this size runs beside the state scan. Bytes count every input read
-    once and every output written once."""
+    """The gated recurrence, the block norms, the layer norm, the short convolution (4 taps) and the
+    selective scan (16 states) on a workload's shape (bf16, logit gates): what a layer of this
+    size runs beside the state scan. Bytes count every input read once and every output written once."""
     gen = torch.Generator(device=device)
     gen.manual_seed(w.seed)
     n = lambda *s, dt=torch.bfloat16: torch.randn(s, generator=gen, device=device).to(dt)  # noqa: E731
@@ -364,6 +364,20 @@ def layer_ops(torch, L, w: LI.Workload, device, flush, pk) -> dict:
     dr, dn = n(w.B, w.T, w.H * w.d, dt=torch.float32), dy.flatten(-2)
     add("residual_norms_bwd", lambda: L.block_norm_bwd(u, wD, residual=res, w_pre=wD, dr=dr, dn=dn), els * 18,
         "norm_bwd_kernel")
+    r, _ = L.layer_norm_fwd(u, wD, wD, residual=res)
+    add("layer_norm", lambda: L.layer_norm_fwd(u, wD, wD, residual=res), els * 12, "layer_fwd_kernel")
+    add("layer_norm_bwd", lambda: L.layer_norm_bwd(r, dn, wD, wD, dr=dr, x_dtype=u.dtype), els * 16, "layer_bwd_kernel")
+    del res, dr, r
+    taps, N = torch.randn(w.H * w.d, 4, generator=gen, device=device) / 2, 16
+    add("short_conv", lambda: L.short_conv_fwd(u, taps, wD), els * 4, "conv::fwd_kernel")
+    add("short_conv_bwd", lambda: L.short_conv_bwd(u, taps, dn, wD), els * 6, "conv::bwd_kernel")
+    dt, gate, b, c = n(w.B, w.T, w.H * w.d), n(w.B, w.T, w.H * w.d), n(w.B, w.T, N), n(w.B, w.T, N)
+    A, states = -torch.arange(1., N + 1, device=device).expand(w.H * w.d, N).contiguous(), L.selective_scan_marks(u, N)
+    call, how = (u, dt, A, b, c), {"z": gate, "dt_bias": wD - 5}
+    rows, kept = 2 * (b.numel() + c.numel()), 4 * states.numel()
+    add("selective_scan", lambda: L.selective_scan_fwd(*call, wD, marks=states, **how), els * 8 + rows + kept, "selective::fwd_kernel")
+    add("selective_scan_bwd", lambda: L.selective_scan_bwd(*call, dn, states, wD, **how), els * 14 + 2 * rows + kept,
+        "selective::bwd_kernel")
     return out
 
 
@@ -803,7 +817,7 @@ def main():
                 extra[name] = ent
                 del tn
                 torch.cuda.empty_cache()
-            # the gated recurrence and the norms around a block, on the mid-size layer
+            # the operators around a block, on the mid-size layer
             extra["layer_ops_mid_layer"] = layer_ops(torch, L, LI.WORKLOADS["mid_layer"], device, flush, pk)
             torch.cuda.empty_cache()
             # chunk-form variants and the backward pass on the small training shape
