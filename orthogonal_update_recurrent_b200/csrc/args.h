@@ -193,6 +193,10 @@ LATTICE_HD inline int sel_padded(int N) {
     return np;
 }
 
+// Columns whose sums over sequences and segments the backward pass takes: dA's, then dskip's and ddt_bias's. In 64 bits: 2 E alone
+// passes an int at the largest E.
+LATTICE_HD inline long long sel_columns(int E, int N) { return (N + 2LL) * E; }
+
 // Channels that a thread reads and writes at once where a channel's states take so many lanes: as many as give every thread of
 // a CTA some.
 LATTICE_HD constexpr int sel_width(int lanes) { return lanes <= 4 ? 4 : lanes == 8 ? 2 : 1; }

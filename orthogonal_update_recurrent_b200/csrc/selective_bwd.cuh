@@ -431,9 +431,9 @@ __global__ void __launch_bounds__(256) sums_kernel(const SelArgs A, int width, i
         __shared__ float sum[8][33];
         const long long EN = (long long)A.E * A.N, i = (long long)((int)blockIdx.x - most) * 32 + (threadIdx.x & 31);
         const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-        const bool in = i < EN + 2 * A.E, ch = i >= EN;
+        const bool in = i < sel_columns(A.E, A.N), ch = i >= EN;
         const float* from = ch ? A.parts_ch + (i - EN) : A.parts_A + i;
-        const long long step = ch ? 2 * A.E : EN;
+        const long long step = ch ? 2LL * A.E : EN;
         float v = 0.f;
         if (in)
 #pragma unroll 4

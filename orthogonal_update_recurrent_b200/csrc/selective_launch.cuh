@@ -53,7 +53,7 @@ lattice_status backward(const SelArgs& a, cudaStream_t st) {
     long long tokens = (long long)a.B * a.T / (16 * sm_count());  // several CTAs per SM, none with more than 64 tokens
     const int least = 256 / width / a.G;
     tokens = tokens > 64 ? 64 : tokens < least ? least : tokens < 1 ? 1 : tokens;
-    const long long most = a.T > 0 ? a.B * ((a.T + tokens - 1) / tokens) : 0, ctas = most + ((long long)a.E * a.N + 2 * a.E + 31) / 32;
+    const long long most = a.T > 0 ? a.B * ((a.T + tokens - 1) / tokens) : 0, ctas = most + (sel_columns(a.E, a.N) + 31) / 32;
     if (ctas > 0x7fffffffLL) return LATTICE_ERR_UNSUPPORTED;
     sums_kernel<XT><<<(unsigned)ctas, 256, 0, st>>>(a, width, (int)tokens, (int)most);
     return launch_status();

@@ -1,6 +1,9 @@
 """What the short convolution, the selective scan and the layer norm refuse, on the host: every call below fails its checks
 before any CUDA call (none could run here), through the C ABI and the binding; and what the host computes for them."""
 import ctypes
+import os
+import re
+import subprocess
 
 import pytest
 import torch
@@ -201,3 +204,19 @@ def test_binding_rejects_host_tensors():
             f()
     with pytest.raises(TypeError):
         L.layer_norm_bwd(x, None)
+
+
+def test_scan_columns_of_the_largest_call(tmp_path):
+    """The columns that the scan's backward pass adds up last, by the rule that its launch and its kernel use, where 2 E is no int."""
+    main = tmp_path / "columns.cpp"
+    main.write_text('#include <stdio.h>\n#include "args.h"\n'
+                    'int main() { using namespace lattice; printf("%d %lld %lld", kSelMaxSize, sel_columns(kSelMaxSize, 2),'
+                    ' sel_columns(kSelMaxSize, kSelMaxN)); }\n')
+    subprocess.run(["g++", "-std=c++17", "-I", B.CSRC, "-o", str(tmp_path / "columns"), str(main)], check=True)
+    out = subprocess.run([str(tmp_path / "columns")], check=True, capture_output=True, text=True).stdout
+    E = 1 << 30
+    assert [int(v) for v in out.split()] == [E, 4 * E, 130 * E]
+    for name in ("selective_launch.cuh", "selective_bwd.cuh"):  # the only rule for them there
+        with open(os.path.join(B.CSRC, name)) as f:
+            text = f.read()
+        assert "sel_columns(" in text and not re.search(r"\b2 \* [Aa]\.E\b(?! \+ (A\.E \+ )?p\.column)", text), name

@@ -262,3 +262,29 @@ def test_growing_states_over_segments(L):
     for k in ("y", "h_T", "dx", "dz", "ddt", "db", "dc", "dA"):  # 5 steps remembered: 2 * 10 * 5 + 2 * 16 + 64 + 900 / 16
         assert torch.isfinite(got[k]).all(), k
         R.close(got[k], want[k], mag[k], 253, k)
+
+
+def test_most_channels(L):
+    """The largest E: one token of 2^30 channels with one state each, some 60 GB, whose gradients per channel are checked at both ends and
+    in the middle."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    E, N = 1 << 30, 1
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    n = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda").normal_(generator=gen)  # noqa: E731
+    t = {"x": n(1, 1, E), "dt": n(1, 1, E), "A": n(E, N, dtype=torch.float32).abs_().neg_(), "b": n(1, 1, N), "c": n(1, 1, N),
+         "skip": n(E, dtype=torch.float32), "dt_bias": n(E, dtype=torch.float32), "dy": n(1, 1, E)}
+    args = [t[k] for k in ("x", "dt", "A", "b", "c")]
+    marks = L.selective_scan_marks(t["x"], N)
+    y, h_T = L.selective_scan_fwd(*args, t["skip"], dt_bias=t["dt_bias"], marks=marks)
+    got = L.selective_scan_bwd(*args, t["dy"], marks, t["skip"], dt_bias=t["dt_bias"])
+    got.update(y=y, h_T=h_T)
+    for lo in (0, E // 2, E - 1000):
+        of = {k: slice(lo, lo + 1000) for k in ("x", "dt", "dy", "y", "dx", "ddt", "A", "dA", "skip", "dskip", "dt_bias", "ddt_bias", "h_T", "dh0")}
+        cut = lambda k, v: v[of[k]] if v.shape[0] == E else v[..., of[k], :] if k in ("h_T", "dh0") else v[..., of[k]]  # noqa: E731
+        how = {k: cut(k, v) if k in of else v for k, v in t.items()}
+        want, mag = R.selective(**how), R.selective(**how, mag=True)
+        for k in ("y", "h_T", "dx", "ddt", "dA", "dskip", "ddt_bias", "dh0"):  # one step remembered: 2 * 10 + 2 * 1 + 64
+            R.close(cut(k, got[k]), want[k], mag[k], 86, k)
+    del t, args, marks, y, h_T, got, how, want, mag
+    torch.cuda.empty_cache()
