@@ -288,3 +288,25 @@ def test_most_channels(L):
             R.close(cut(k, got[k]), want[k], mag[k], 86, k)
     del t, args, marks, y, h_T, got, how, want, mag
     torch.cuda.empty_cache()
+
+
+def test_more_segments_than_a_cta_goes_through(L):
+    """More than 32 segments, whose entering states and cotangents a launch of its own joins: both directions against the 64-bit form, with
+    states from before, cotangents from behind, an end inside a segment, and a memory of several segments (dt |A| from 2.5e-3 to 0.085)."""
+    B, T, E, N = 2, 3000, 24, 16
+    t = make(B, T, E, N, gate=False, softplus=False, lengths=[T, 1111], seed=6)
+    t["dt"] = 0.05 + (t["dt"] - 0.01) * 0.25
+    t["A"], t["h0"], t["dh_T"] = t["A"] / 10, 30 * t["h0"], 30 * t["dh_T"]
+    row = E * N + E  # a segment's states and sum of steps; backward as much for dA's parts, 2 E for two sums, and db's and dc's per CTA of 16
+    ws = L.lib().lattice_selective_scan_workspace_bytes
+    assert ws(B, T, E, N, 1, 0) > 4 * B * 32 * row and ws(B, T, E, N, 1, 1) > 4 * (B * 32 * (2 * row + E) + 2 * B * T * 2 * N)
+    got = check(L, t)
+    how = {k: t[k] for k in ("x", "dt", "A", "b", "c", "skip", "z", "dt_bias", "softplus", "h0", "lengths", "dy", "dh_T")}
+    mag = R.selective(**how, mag=True)
+    # the bounds tell a state or cotangent that was not handed on: 8 segments of 64 tokens from where it enters
+    without, at = R.selective(**{**how, "h0": None}), slice(512, 520)
+    with pytest.raises(AssertionError):
+        R.close(got["y"][:1, at], without["y"][:1, at], mag["y"][:1, at], 5000 + N + 16, "y")
+    without, at = R.selective(**{**how, "dh_T": None}), slice(T - 520, T - 512)
+    with pytest.raises(AssertionError):
+        R.close(got["dx"][:1, at], without["dx"][:1, at], mag["dx"][:1, at], 10000 + 2 * N + 32, "dx")
