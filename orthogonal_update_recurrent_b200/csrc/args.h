@@ -137,7 +137,7 @@ struct NormArgs {
     long long N;
     int G, D, tpr, K;                                       // threads per row and CTA, CTAs per row
     int act;
-    float scale, eps, inv_d;
+    float scale, eps, inv_d, inv_d_rest;                    // 1/D rounded, and what that lacks
     bool post;
     bool y32, r32, w32;                                     // fp32, else the call's type: y; residual, r and dr; weights
 };

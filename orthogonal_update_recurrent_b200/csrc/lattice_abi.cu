@@ -246,7 +246,7 @@ lattice_status check_norm(NormArgs& a, const void* y, lattice_dtype y_dtype, lon
     a.y = y; a.gate = gate; a.residual = residual; a.w_post = w_post; a.w_pre = w_pre;
     a.ys = (unsigned)ys; a.gs = (unsigned)gs; a.rs = (unsigned)rs;
     a.N = N; a.G = G; a.D = D; a.act = (int)act;
-    a.scale = scale; a.eps = eps; a.inv_d = 1.f / (float)D;
+    a.scale = scale; a.eps = eps; a.inv_d = 1.f / (float)D; a.inv_d_rest = (float)(1. / D - (double)a.inv_d);
     a.post = post != 0;
     a.y32 = y_dtype == LATTICE_F32; a.r32 = r_dtype == LATTICE_F32; a.w32 = w_dtype == LATTICE_F32;
     return LATTICE_OK;

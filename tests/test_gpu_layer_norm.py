@@ -134,3 +134,17 @@ def test_runs_the_same_on_every_call(L):
     t = make(900, 520, "bf16", rdtype="f32")
     a, b = check(L, t), check(L, t)
     assert torch.equal(a[1], b[1]) and all(torch.equal(a[2][k], b[2][k]) for k in a[2])
+
+
+@pytest.mark.parametrize("D", [41, 1000, 1203, 3584, 7168])
+@pytest.mark.parametrize("wide", [0, 1])
+@pytest.mark.parametrize("value", [3.0, 1000.0])
+def test_constant_rows_have_no_deviation(L, D, wide, value):
+    """Sums of equal whole numbers below 2^24 are exact, and so must their mean be: nothing is left for 1/sqrt(eps) = 316 to raise. Forward the
+    bias alone, backward no gradient of the weight, and none of the rows where the cotangent is constant too."""
+    t = make(5, D, "f32", residual=False, seed=D)
+    t["x"] = torch.full((5, D + wide), value, device="cuda")[:, :D]
+    _, n = L.layer_norm_fwd(t["x"], t["w"], t["b"])
+    assert torch.equal(n, t["b"].expand(5, D))
+    assert not L.layer_norm_bwd(t["x"], t["dn"], t["w"], t["b"])["dw"].any()
+    assert not L.layer_norm_bwd(t["x"], torch.full((5, D), 3.0, device="cuda"))["dr"].any()
