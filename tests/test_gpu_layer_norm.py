@@ -148,3 +148,26 @@ def test_constant_rows_have_no_deviation(L, D, wide, value):
     assert torch.equal(n, t["b"].expand(5, D))
     assert not L.layer_norm_bwd(t["x"], t["dn"], t["w"], t["b"])["dw"].any()
     assert not L.layer_norm_bwd(t["x"], torch.full((5, D), 3.0, device="cuda"))["dr"].any()
+
+
+@pytest.mark.parametrize("D", [41, 1500, 1504])
+def test_large_means_to_first_order(L, D):
+    """A mean of 1000 against a deviation of 1. The mean is off by the roundings of its sum, d = 22 units (20 additions, 1/D, and itself) of the
+    mean magnitude, and the differences by that and no more (they are exact), all of a row's alike; the variance to second order only. So n
+    moves by rho d w, and dr by rho^2 d (|mean(m xhat)| + |xhat| |mean m|), beside the 64 units of its own terms. Zeros would not pass."""
+    t = make(9, D, "f32", mean=1000.0, residual=False, seed=D)
+    _, n = L.layer_norm_fwd(t["x"], t["w"], t["b"])
+    got = L.layer_norm_bwd(t["x"], t["dn"], t["w"], t["b"])["dr"]
+    want, _ = R.layer(t["x"], t["w"], t["b"], dn=t["dn"])
+    r, w, m = t["x"].double(), t["w"].double(), t["dn"].double() * t["w"].double()
+    mean = lambda v: v.mean(-1, keepdim=True)  # noqa: E731
+    u = r - mean(r)
+    rho = 1 / torch.sqrt(mean(u * u) + 1e-5)
+    xhat, unit = u * rho, 2.0 ** -24
+    d = 22 * unit * mean(r.abs())
+    tol = rho * d * w.abs() + 64 * unit * ((xhat * w).abs() + t["b"].double().abs())
+    assert ((n.double() - want["n"]).abs() <= tol).all()
+    tol = 64 * unit * rho * (m.abs() + mean(m.abs()) + xhat.abs() * mean((m * xhat).abs()))
+    tol = tol + rho * rho * d * (mean(m * xhat).abs() + (xhat.abs() + rho * d) * mean(m).abs())
+    assert ((got.double() - want["dr"]).abs() <= tol).all()
+    assert (want["dr"].abs() > tol).double().mean() > 0.9
