@@ -213,17 +213,18 @@ __device__ __forceinline__ F2 decay(F2 t) {
 }
 
 // softplus(v) = max(v, 0) + log(1 + t), t = exp(-|v|), and its slope 1/(1 + exp(-v)). log(1 + t)/t is a
-// polynomial of degree 9 (minimax on [0, 1], relative error 5e-9), so small steps keep their relative accuracy.
+// polynomial of degree 9 (minimax on [0, 1] with 1 at t = 0, rounded one coefficient after the other and refitted: relative error 5.3e-9,
+// mean 6e-11), so small steps keep their relative accuracy.
 __device__ __forceinline__ F2 softplus(F2 v, F2* slope) {
     const F2 t = each(v, [](float a) { return ex2(-fabsf(a) * kLog2e); });
-    F2 p = fma2(f2(-0.003244034f), t, f2(0.019851461f));
-    p = fma2(p, t, f2(-0.05695953f));
-    p = fma2(p, t, f2(0.10603654f));
-    p = fma2(p, t, f2(-0.15305592f));
-    p = fma2(p, t, f2(0.19675939f));
-    p = fma2(p, t, f2(-0.24954134f));
-    p = fma2(p, t, f2(0.33329964f));
-    p = fma2(p, t, f2(-0.49999902f));
+    F2 p = fma2(f2(-0.0032910742f), t, f2(0.02008846f));
+    p = fma2(p, t, f2(-0.057460483f));
+    p = fma2(p, t, f2(0.10661371f));
+    p = fma2(p, t, f2(-0.15344977f));
+    p = fma2(p, t, f2(0.19692121f));
+    p = fma2(p, t, f2(-0.2495802f));
+    p = fma2(p, t, f2(0.33330464f));
+    p = fma2(p, t, f2(-0.4999993f));
     p = fma2(p, t, f2(1.f));
     if (slope) {
         const F2 r = each(add2(t, f2(1.f)), rcp), s = mul2(t, r);
