@@ -179,8 +179,8 @@ __device__ __forceinline__ const void* dt_at(const SelArgs& A, int b) {
 
 // exp(dt A) of two states, t = dt A log2(e). The approximate exponential's errors near 1 are not centred (mean
 // -2e-8 for t in [-1/2, -2^-8], measured), and a retention of R steps multiplies a mean error by R.
-// So -0.09 <= t <= 0 takes 1 + t q(t) instead, a minimax polynomial (6e-9, and 0 at t = 0) whose
-// last step rounds to nearest; below, R is at most 16. The integer comparison holds for negative t alone.
+// So -0.09 <= t <= 0 takes 1 + t q(t) instead, a minimax polynomial (6.7e-9, 1e-11 on the mean, and 0 at
+// t = 0) whose last step rounds to nearest; below, R is at most 16. The integer comparison holds for negative t alone.
 constexpr float kNear = -0.09f;
 // of M pairs, step by step, so that no step waits for the one before it
 template <int M>

@@ -31,3 +31,12 @@ def test_softplus():
     assert len(c) == 10 and c[-1] == 1.0
     e = error(c, t, np.log1p(t) / t)
     assert np.abs(e).max() <= 5.4e-9 and abs(e.mean()) <= 1e-10
+
+
+def test_decay():
+    near = float(np.float32(re.search(r"kNear = (-[0-9.]+)f", SOURCE).group(1)))
+    t = np.linspace(near, 0, 200001)
+    c = coefficients("void decay(")
+    assert len(c) == 4 and c[-1] == 1.0
+    e = error(c, t, np.exp2(t))
+    assert np.abs(e).max() <= 6.7e-9 and abs(e.mean()) <= 1e-10
