@@ -132,8 +132,9 @@ template <class XT, int L, int W, bool GATE, bool VEC>
 __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_kernel(const SelArgs A) {
     using P = Place<L, W>;
     using Sh = BwdShared<XT, L, W>;
-    constexpr int NT = P::NT, NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, VAR = Sh::VAR, VS = Sh::VS, ROW = Sh::ROW, WHOLE = Sh::WHOLE, SB = 8,
+    constexpr int NT = P::NT, NP = Sh::NP, CT = P::CT, CTP = P::CTP, PI = P::PI, NB = Rows<NP, W>::NB, VAR = Sh::VAR, VS = Sh::VS, ROW = Sh::ROW, WHOLE = Sh::WHOLE, SB = kSelMark,
                   V = P::V, Q = P::P, DW = P::DW;
+    static_assert(SB % 4 == 0 && TT % SB == 0, "tokens between marks: whole groups of the sums, whole parts of a tile");
     extern __shared__ __align__(16) unsigned char raw_shared[];
     Sh& sh = *reinterpret_cast<Sh*>(raw_shared);
     const P p(A);
@@ -328,15 +329,7 @@ __global__ void __launch_bounds__(32 * W, L == 32 && W == 8 ? 1 : 16 / W) bwd_ke
 #pragma unroll 1
         for (int q = TT - SB; q >= 0; q -= SB) {
             F2 a[SB][2], hp[SB][2], h[2];
-            mark(tb + q / kSelMark * kSelMark, h);
-            if (kSelMark > SB && q) {
-                F2 u[SB][2];
-                decays<SB, 4>(dtu, DW, vb, NP, A2, a, u);
-#pragma unroll
-                for (int j = 0; j < SB; ++j)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) h[k] = fma2(a[j][k], h[k], u[j][k]);
-            }
+            mark(tb + q, h);
 #pragma unroll
             for (int j4 = 0; j4 < SB; j4 += 4) {
                 F2 u[4][2];
