@@ -393,7 +393,8 @@ _INT_MAX = 0x7fffffff
 
 
 def _fits(what: str, *sizes):
-    """Refuses sizes that are no C int: ctypes would cut them off."""
+    """Refuses sizes that are no C int: ctypes would cut them off. (Asked where a tensor's elements are that many, or
+    none: then one axis of length 0 hides what the others are.)"""
     if max(sizes) > _INT_MAX:
         raise LatticeError(ERR_UNSUPPORTED, what)
 
@@ -402,7 +403,7 @@ def _gated_args(x, z, lead: int, lengths, gate: str, write: str):
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 2:
         raise ValueError("x must be a tensor [B, T, H, d] (one token: [B, H, d])")
     shape, device = x.shape, x.device
-    if x.numel() > _INT_MAX:
+    if not 0 < x.numel() <= _INT_MAX:
         _fits("the gated recurrence's sizes", *shape)
     xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
     per_head = isinstance(z, torch.Tensor) and z.dim() == lead + 1
@@ -558,7 +559,7 @@ def _norm_args(y, w_post, gate, residual, w_pre, act, dtype):
     if not isinstance(y, torch.Tensor) or not y.is_cuda or y.dim() < 1:
         raise TypeError("y must be a CUDA tensor [..., D]")
     shape, dev = y.shape, y.device
-    if y.numel() > _INT_MAX:
+    if not 0 < y.numel() <= _INT_MAX:
         _fits("the norm's sizes", *shape[-2:])
     if dtype is None:
         dtype = gate.dtype if isinstance(gate, torch.Tensor) else y.dtype
@@ -782,7 +783,7 @@ def _conv_args(x, w, bias, act: str, lead: int, lengths):
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
         raise ValueError("x must be a tensor [B, T, C] (one token: [B, C])")
     shape, device = x.shape, x.device
-    if x.numel() > _INT_MAX:
+    if not 0 < x.numel() <= _INT_MAX:
         _fits("the convolution's sizes", *shape)
     xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
@@ -901,7 +902,7 @@ def _sel_args(x, dt, A, b, c, skip, z, dt_bias, lead: int, lengths):
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
         raise ValueError("x must be a tensor [B, T, E] (one token: [B, E])")
     shape, device = x.shape, x.device
-    if x.numel() > _INT_MAX:
+    if not 0 < x.numel() <= _INT_MAX:
         _fits("the selective scan's sizes", *shape)
     xs = _rows(x, "x", shape, lead, _FLOATS, device) if x.is_cuda else _like(x, "x", shape, _FLOATS, device)
     same = (x.dtype,)

@@ -220,3 +220,14 @@ def test_scan_columns_of_the_largest_call(tmp_path):
         with open(os.path.join(B.CSRC, name)) as f:
             text = f.read()
         assert "sel_columns(" in text and not re.search(r"\b2 \* [Aa]\.E\b(?! \+ (A\.E \+ )?p\.column)", text), name
+
+
+def test_binding_rejects_sizes_that_are_no_int_beside_an_axis_of_0():
+    """No tokens, so no elements, of more sequences than an int counts: cut off, they would be one sequence, and the states of the others
+    would come back unwritten."""
+    many = (1 << 32) + 1
+    x, w, A, b = torch.empty(many, 0, 1), torch.empty(1, 2), torch.empty(1, 1), torch.empty(many, 0, 1)
+    for f in (lambda: L.short_conv_fwd(x, w), lambda: L.short_conv_bwd(x, w, x), lambda: L.selective_scan_fwd(x, x, A, b, b),
+              lambda: L.selective_scan_bwd(x, x, A, b, b, x, b), lambda: L.gated_scan_fwd(x[..., None], x[..., None])):
+        with pytest.raises(L.LatticeError):
+            f()

@@ -171,3 +171,11 @@ def test_large_means_to_first_order(L, D):
     tol = tol + rho * rho * d * (mean(m * xhat).abs() + (xhat.abs() + rho * d) * mean(m).abs())
     assert ((got.double() - want["dr"]).abs() <= tol).all()
     assert (want["dr"].abs() > tol).double().mean() > 0.9
+
+
+def test_no_rows_of_more_columns_than_an_int_counts(L):
+    """Cut off to an int, 2^32 + 16 columns would be 16."""
+    x = torch.empty((0, (1 << 32) + 16), device="cuda")
+    for f in (lambda: L.layer_norm_fwd(x), lambda: L.layer_norm_bwd(x, x), lambda: L.block_norm_fwd(x)):
+        with pytest.raises(L.LatticeError):
+            f()
