@@ -186,7 +186,8 @@ struct SelArgs {
     bool dt32, softplus, vec, vec_n;               // vec: sel_width() channels (one token: four of b and c too), vec_n: four states in one access
 };
 
-// Lanes that share a channel's states, 4 states each (2 in the forward pass where that fills the device better).
+// A channel's states as its lanes have them, 4 each (2 in the forward pass where that fills the device better): the power of two, 8 at
+// least, that holds N.
 LATTICE_HD inline int sel_padded(int N) {
     int np = 8;
     while (np < N) np *= 2;

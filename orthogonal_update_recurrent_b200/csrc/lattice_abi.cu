@@ -325,17 +325,23 @@ long long sel_tiles(int Eg, int lanes, int W) {
     return ((long long)Eg + per - 1) / per;
 }
 // Warps of a CTA: 8, or 2 where 8 would leave so many more of them without channels that it pays: a warp of two takes 1.1 times the time,
-// backward, with its share of the sums over channels, 1.7 times (mid-size layer: 636 and 698 us, 1713 and 2886 us; 20 sequences of 49370
-// tokens at most, 12 channels, 16 states, forward and backward: 2966 us with 8 warps, 880 us with 2).
+// backward, with its share of the sums over channels, 1.5 times (mid-size layer: 614 and 672 us, 1635 and 2446 us; 20 sequences of 49370
+// tokens, 12 channels, 16 states: 916 us with 8 warps and 283 us with 2, backward 1822 and 742 us). Backward, two have to be ahead by 1.7:
+// from 1.5 on (groups of 65 to 80 channels at 16 states, 33 to 40 at 32) neither is always. 72 channels, 32 sequences of 2048 tokens, 74 of
+// 1024, 148 of 1024, 300 of 512: 522 / 276 / 429 / 520 us with 8 and 489 / 314 / 425 / 498 us with 2; 36 channels, 32 states: 563 and 635 us.
 int sel_warps(int Eg, int lanes, bool bwd) {
     return (double)sel_tiles(Eg, lanes, 8) * 4 > (bwd ? 1.7 : 1.1) * (double)sel_tiles(Eg, lanes, 2) ? 2 : 8;
 }
 // How the work is spread. A CTA has 256/L channels (64/L for few channels) with N padded to L S states, and goes through its tokens alone.
 // With few CTAs the device is filled by two states per lane instead of four (twice the CTAs), or by segments of the time axis, whose states
 // take a pass of their own (its exponentials are the forward pass's again). The times below, in us per token of a CTA's and by CTAs per
-// SM, are what was measured (bf16, 16 states, gate; they hold for other N, whose CTAs have as many states); the cheapest is taken. Forward,
+// SM, are what was measured with CTAs of 8 warps (bf16, 16 states, gate); the cheapest is taken. Forward,
 // 1024 / 2048 / 4096 / 8192 / 16384 channels of 4096, 4096, 2048, 2048, 2048 tokens: four states 430 / 435 / 238 / 238 / 355 us, two states
 // 297 / 297 / 167 / 240 / 427, segments 111 / 170 / 181 / 312; backward, whole 1155 / 1201 / 627 / 637 / 865, segments 188 / 303 / 329 / 589.
+// They stand for the other forms too, whose CTAs have as many states, and are right there as long as an SM holds as many of them. Backward it
+// does not always: of CTAs with 65 to 128 states per channel one instead of two (4 x 2048 tokens of 256 channels, 128 states: two segments
+// are taken, 941 us, whole sequences 839 us), of CTAs of two warps 4 to 7 instead of 8 (16 x 2048 tokens, two groups of 6 channels: 32
+// segments are taken, 87 us, 24 segments 78 us).
 SelPlan sel_plan(int B, int T, int E, int N, int G, bool bwd) {
     const int np = sel_padded(N), Eg = E / G;
     const long long sm = sm_count(), tiles = ((long long)T + kSelTile - 1) / kSelTile;

@@ -13,7 +13,7 @@
 // second sum costs an exchange more, during which the next row is on its way. What is left is bound by
 // those exchanges, so both directions keep 1024 threads' rows at once per SM, 64 registers each. (One exchange of
 // differences from the row's first element, a second one where that cancels, was slower: 32768 rows of 2048 bf16, no residual,
-// forward 62 -> 84 us.) 32768 rows of 2048, bf16 with residual and r in fp32: 131 us forward, 6.1 TB/s; backward 183 us, 5.9 TB/s, and 4 us for
+// forward 62 -> 84 us.) 32768 rows of 2048, bf16 with residual and r in fp32: 131 us forward, 6.1 TB/s; backward 185 us, 5.8 TB/s, and 4 us for
 // the weights' sums.
 #pragma once
 #include "block_norm.cuh"

@@ -15,10 +15,11 @@
 // every 8.1 cycles, its multiply-adds every 1.1 (packed pairs: 2.2), its shuffles every 4.1 and its selects every
 // 2 (measured); the layout keeps every state's work on those units at about the exponential's 8.
 //
-// Mid-size layer (8 x 4096 tokens of 2048 bf16 channels, 16 states, gate): 640 us, 1.7e12 states per second, 0.37 of the rate of the
-// exponentials alone. A token costs a warp 48 instructions for 128 states, its share of the staging included, 58 % of the issue slots at 3.5
-// warps per scheduler; shared memory returns data 58 % of the time, the exponentials' units are busy 46 %, and a warp's own latencies fill
-// the rest. One sequence of 65536 tokens of 1024 channels: 545 us, and 390 us for its 18 segments' states (seg_kernel).
+// Mid-size layer (8 x 4096 tokens of 2048 bf16 channels, 16 states, gate): 640 us with the backward pass's marks (614 us without),
+// 1.7e12 states per second, 0.37 of the rate of the exponentials alone. A token costs a warp 48 instructions for 128 states, its share of the
+// staging included, 58 % of the issue slots at 3.5 warps per scheduler; shared memory returns data 58 % of the time, the exponentials' units are
+// busy 46 %, and a warp's own latencies fill the rest. One sequence of 65536 tokens of 1024 channels: 545 us, and 390 us for its 18
+// segments' states (seg_kernel).
 // One token of 256 sequences of 4096 channels, 137 MB of states: 27 us (step_kernel; reads and writes bind).
 //
 // Tried: two channels per lane, which share what is read of b and c, on half the threads (694 us; backward 1590 us, as fast as

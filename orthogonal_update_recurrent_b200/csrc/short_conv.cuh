@@ -193,7 +193,7 @@ template <class XT, int K, int V>
 __global__ void __launch_bounds__(256, conv_resident(false, K)) fwd_kernel(const ConvArgs A) {
     using N = typename Numbers<V>::N;
     // Tokens whose loads are under way at once: two of 16 bytes do beside the lines brought nearer, with fewer spills (8 x 4096 tokens of 1024
-    // fp32 channels, 3 taps: 51.5 -> 48.6 us); without those lines four (8 taps: 52.7 us, with two 62.3 us).
+    // fp32 channels, 3 taps: 51.5 -> 48.6 us); without those lines four (5 to 8 taps: 50, 50, 50 and 53 us, with two 60, 60, 61 and 63 us).
     constexpr int U = sizeof(XT) * V > 8 && K <= 4 ? 2 : 4, H = Numbers<V>::H;
     const Place<V> p(A);
     if (!p.in) return;
@@ -235,7 +235,10 @@ __global__ void __launch_bounds__(256, conv_resident(false, K)) fwd_kernel(const
         x += U * A.xts;
     };
     // The U tokens after those are brought into the L2, which takes no registers (mid-size layer 55.9 -> 53.5 us; 2051 channels,
-    // call included, 113 -> 102 us). With more taps a token's arithmetic hides the way, and they cost more than they give (8 taps: 89 -> 97 us).
+    // call included, 113 -> 102 us). With more taps a token's arithmetic hides the way, and they cost more than
+    // they give (8 x 4096 tokens, 5 to 8 taps: 2048 bf16 channels 62.5, 63.5, 65 and 69.5 us, with them 64.5, 67.5, 71 and 77 us; 1024 fp32
+    // channels 50 to 53 us, with them 50 to 55 us), but for single 16-bit elements (2051 channels: 92, 92, 123 and 124 us, with them 85, 95, 104
+    // and 102 us), which are not told apart.
     auto ahead = [&]() {
 #pragma unroll
         for (int j = 0; j < U; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + j * A.xts));
